@@ -171,8 +171,9 @@ ar_status ar_fused_reduce_rmsnorm(ar_ctx* ctx, const ar_fused_args* args, void* 
  * Read and clear the context's device status word.  The staged variants wait on their
  * shared-memory copies (and, in the cluster form, on the peer CTAs' totals) with a bound
  * (about a second); if a wait ever runs out, the kernel stops early, its outputs are
- * incomplete, and it records code 1 here.  0 means no wait
- * has run out since the last read.  Synchronises the device (a blocking copy): call it
+ * incomplete, and it records code 1 here.  The attention block's calls record code 2 for an
+ * index in device memory that was out of range (the last code stays).  0 means neither
+ * has happened since the last read.  Synchronises the device (a blocking copy): call it
  * outside graph capture, e.g. after a batch of calls.  No counterpart on the pages.
  */
 ar_status ar_device_status(ar_ctx* ctx, int* code);
@@ -248,6 +249,184 @@ ar_status ar_fused_reduce_rmsnorm_host(ar_ctx* ctx, const ar_fused_args* args, v
 #define AR_NOALLOC_SCRATCH_BYTES 256
 ar_status ar_fused_reduce_rmsnorm_noalloc(const ar_fused_args* args, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The attention block between two fused calls of a tensor-parallel inference step: plan the
+ * step's cache slots, normalise and rotate the heads and write the cache, attend over it.
+ *
+ * Common to the three: request lengths, tables and slots are device memory, so the host need
+ * not know them and a captured graph follows them; the host-side arguments (counts, strides,
+ * capacities) bound every access.  An index read from device memory that lies outside those
+ * bounds is never followed: it is dropped as each call describes, and code 2 is left in the
+ * context's status word (ar_device_status).  The calls allocate nothing, do not synchronise,
+ * can be captured, and use no memory but the arguments' (and the status word).
+ *
+ * A paged cache is [num_blocks, page_size, kv_heads, head_dim] with unit stride in head_dim
+ * and any strides (in elements) otherwise, so other orders of the first three dimensions are
+ * the same call.  Slot s is token s % page_size of block s / page_size.
+ * ------------------------------------------------------------------------------------- */
+
+#define AR_MAX_REQUESTS 8192
+#define AR_MAX_ROPE_AXES 4
+#define AR_MAX_HEAD_DIM 256
+
+/* ar_paged_plan refusals, info[2] */
+enum { AR_PLAN_OK = 0, AR_PLAN_NO_BLOCKS = 1, AR_PLAN_TABLE_FULL = 2, AR_PLAN_TOO_MANY_TOKENS = 3, AR_PLAN_BAD_LENGTH = 4 };
+
+/*
+ * Block tables and slot maps of one step.  Request r has cached_lens[r] tokens in the cache,
+ * whose blocks are the first ceil(cached / page_size) entries of its table row, and
+ * new_lens[r] tokens that this step adds (0: it waits).  Blocks it lacks come off the end of
+ * free_blocks[0 .. *free_count), in the order of the requests, and are appended to its row.
+ *
+ *   cu_q[r]      new tokens of the requests before r; cu_q[requests] the step's tokens
+ *   seq_lens[r]  cached_lens[r] + new_lens[r]
+ *   positions[t] place of token t in its request;  0 for t >= cu_q[requests]
+ *   slots[t]     its cache slot;                  -1 for t >= cu_q[requests]
+ *   *free_count_out  the free blocks left (free_blocks itself is not changed)
+ *   info[0..3]   tokens, blocks taken, refusal (AR_PLAN_*, the largest that applies), blocks needed
+ *
+ * A step is planned whole or not at all.  Where the blocks do not suffice, a row has too few
+ * columns, the tokens exceed max_tokens, or a length or count is negative or a count above its
+ * capacity, info[2] says which, the table and the free count stay, cu_q is all 0, every slot
+ * -1 and seq_lens the cached lengths (negative ones 0): the step's other calls then do nothing.
+ */
+typedef struct {
+  int requests;               /* 0..AR_MAX_REQUESTS */
+  int page_size;              /* 1..65536 tokens a block */
+  int64_t max_tokens;         /* length of slots and positions, 0..2^30 */
+  int64_t free_capacity;      /* length of free_blocks, 0..2^31-1 */
+  int64_t table_cols;         /* columns of block_table, 0..2^31-1 */
+  int64_t table_stride;       /* elements between its rows, >= table_cols (0: table_cols) */
+  const int32_t* cached_lens; /* device [requests] */
+  const int32_t* new_lens;    /* device [requests] */
+  const int32_t* free_blocks; /* device [free_capacity] */
+  const int32_t* free_count;  /* device [1] */
+  int32_t* block_table;       /* device [requests, table_cols], updated in place */
+  int32_t* cu_q;              /* device [requests + 1] */
+  int32_t* seq_lens;          /* device [requests] */
+  int64_t* slots;             /* device [max_tokens] */
+  int32_t* positions;         /* device [max_tokens] */
+  int32_t* free_count_out;    /* device [1]; not free_count itself: give two in turn */
+  int32_t* info;              /* device [4] */
+} ar_paged_plan_args;
+
+/* No output may overlap an input or another output (AR_ERR_OVERLAP). */
+ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* args, void* stream);
+
+/*
+ * RMSNorm of each q and k head, rotation by the position, and the write to the paged cache, in
+ * one pass.  For a head x of head_dim elements (fp32 inside, one rounding at the end):
+ *
+ *   y = x * rsqrt(mean(x^2) + eps) * w'       w' = w or (1 + w); y = x where the weight is NULL
+ *   frequency i < rot_dim / 2 turns the pair (a, b) of y by theta = position[axis(i)] * inv_freq[i]:
+ *     a' = a cos theta - b sin theta,  b' = b cos theta + a sin theta
+ *   pairs != 0: (y[2i], y[2i + 1]); else (y[i], y[i + rot_dim / 2]); y[rot_dim ..) stays
+ *
+ * theta is reduced exactly enough for any int32 position (64-bit fixed-point turns).  With
+ * several position axes, sections[a] frequencies belong to axis a (their sum is rot_dim / 2):
+ * one section after another, or, with `dealt`, dealt to the axes in turn, an axis dropping out
+ * when its section is full.
+ *
+ * q_out and k_out may be exactly q and k (same strides) or NULL (nothing stored; q_out may be
+ * NULL only with q_heads 0, k_out only with a cache).  With a cache, token t's k and its
+ * unchanged v are written at slots[t]; slot -1 (padding) writes neither, a slot below -1 or at or
+ * above num_blocks * page_size is dropped and leaves code 2.  Rows q_out and k_out are written for
+ * every token.  Equal slots in one call: which token stays is not defined.
+ */
+typedef struct {
+  int64_t tokens;                       /* >= 0 */
+  int q_heads, kv_heads;                /* >= 0, not both 0 */
+  int head_dim;                         /* 1..AR_MAX_HEAD_DIM */
+  ar_dtype dtype;                       /* AR_DTYPE_BF16 or AR_DTYPE_F16: all tensors below but inv_freq */
+  const void* q;                        /* device [tokens, q_heads, head_dim], unit last stride */
+  const void* k;                        /* device [tokens, kv_heads, head_dim] */
+  const void* v;                        /* the same; used with a cache only */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  void* q_out;
+  void* k_out;
+  int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+  const void* q_weight;                 /* device [head_dim] or NULL: no norm of q */
+  const void* k_weight;                 /* device [head_dim] or NULL: no norm of k */
+  float eps;                            /* finite, >= 0 */
+  int gemma;                            /* != 0: w' = 1 + w */
+  int rot_dim;                          /* 0 (no rotation) or even, at most head_dim */
+  int pairs;                            /* != 0: adjacent pairs, else halves */
+  int axes;                             /* 1..AR_MAX_ROPE_AXES (with rot_dim 0: ignored) */
+  int sections[AR_MAX_ROPE_AXES];       /* frequencies of each axis (axes = 1: ignored) */
+  int dealt;
+  const int32_t* positions;             /* device [axes, tokens] */
+  int64_t position_stride;              /* elements between the axes' rows (0: tokens) */
+  const float* inv_freq;                /* device fp32 [rot_dim / 2], radians a position */
+  void* k_cache;                        /* both or neither */
+  void* v_cache;
+  int64_t k_block_stride, k_page_stride, k_cache_head_stride;  /* elements between blocks, tokens of a block, heads */
+  int64_t v_block_stride, v_page_stride, v_cache_head_stride;
+  int64_t num_blocks;
+  int page_size;                        /* 1..65536 */
+  const int64_t* slots;                 /* device [tokens], with a cache */
+} ar_qk_norm_rope_args;
+
+ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* args, void* stream);
+
+/*
+ * Attention of the requests' new tokens over the paged cache (which holds them already).
+ * Request r owns rows cu_q[r] .. cu_q[r+1] of q and out, n of them, the last n of its
+ * len = seq_lens[r] cached tokens: row i of the request has position p = len - n + i.
+ * q head h reads cache head h / (q_heads / kv_heads).
+ *
+ *   s(i, j)  = scale * q_i . k_j;  with softcap c > 0: c * tanh(s / c);  with slopes: - slopes[h] * |p - j|
+ *   visible  = j < len and (j < prefix_lens[r] or ((not causal or j <= p) and (window = 0 or j > p - window)))
+ *   out_i    = sum_j softmax_j(s(i, j)) v_j over the visible j;  lse = log sum_j exp(s(i, j))
+ *
+ * A row that sees nothing gives 0 and lse -inf.  Rows of out and lse outside
+ * cu_q[0] .. cu_q[requests] are left as they are.  What the cache holds at or behind a
+ * request's length is never used, NaN and infinities included; k may hold them wherever it is
+ * not visible; v must be finite at the tokens of a request (a token that one row does not see
+ * shares matrix products with rows that do).
+ * A block number outside the cache reads as zeros and leaves code 2; lengths are cut to what
+ * the table's columns hold, and row ranges to the tokens, likewise with code 2.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to dtype for the
+ * second product, which is summed in fp32.
+ *
+ * workspace: ar_paged_attention_workspace(args) bytes of device memory, 16-byte aligned, for
+ * the parts of rows whose keys were split over SMs.  Its contents need no preparation; calls
+ * that may run at the same time need one each.
+ */
+typedef struct {
+  int64_t tokens;                       /* rows of q, out and lse, >= 0 */
+  int requests;                         /* 0..AR_MAX_REQUESTS */
+  int q_heads, kv_heads;                /* >= 1, q_heads a multiple of kv_heads */
+  int head_dim;                         /* 1..AR_MAX_HEAD_DIM */
+  ar_dtype dtype;                       /* AR_DTYPE_BF16 or AR_DTYPE_F16 */
+  const void* q;                        /* device [tokens, q_heads, head_dim], unit last stride */
+  void* out;                            /* the same shape */
+  int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+  float* lse;                           /* device [tokens, q_heads] or NULL */
+  const void* k_cache;
+  const void* v_cache;
+  int64_t k_block_stride, k_page_stride, k_head_stride;
+  int64_t v_block_stride, v_page_stride, v_head_stride;
+  int64_t num_blocks;
+  int page_size;                        /* 1..65536 */
+  const int32_t* block_table;           /* device [requests, table_cols] */
+  int64_t table_cols, table_stride;     /* table_stride >= table_cols (0: table_cols) */
+  const int32_t* cu_q;                  /* device [requests + 1], not decreasing */
+  const int32_t* seq_lens;              /* device [requests] */
+  float scale;                          /* finite */
+  int causal;
+  int window;                           /* >= 0; 0: no window */
+  float softcap;                        /* finite, >= 0; 0: no cap */
+  const float* slopes;                  /* device fp32 [q_heads] or NULL */
+  const int32_t* prefix_lens;           /* device [requests] or NULL */
+  void* workspace;
+  size_t workspace_bytes;
+} ar_paged_attention_args;
+
+ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* args, void* stream);
+
+/* Bytes of workspace that calls with this head_dim and dtype need (whatever their lengths). */
+ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_args* args, size_t* bytes);
+
 /* Static description of a status code. */
 const char* ar_status_string(ar_status s);
 
@@ -259,7 +438,8 @@ const char* ar_last_error(const ar_ctx* ctx);
  * 4-6 partials run by the staged fused kernel on the array viewed as rows, without residual
  * or norm), "reduce_rows", "fused_row_vec", "fused_cluster_vec", "fused_staged",
  * "fused_staged_cluster" (rows longer than 8192 elements split over a cluster of staged CTAs),
- * "fused_scalar", "fused_cluster_scalar", "fused_batch", "fused_batch_sequential" or "none"
+ * "fused_scalar", "fused_cluster_scalar", "fused_batch", "fused_batch_sequential", "paged_plan",
+ * "qk_norm_rope_vec", "qk_norm_rope_scalar", "paged_attention_mma", "paged_attention_tma" or "none"
  * (empty call). */
 const char* ar_last_variant(const ar_ctx* ctx);
 

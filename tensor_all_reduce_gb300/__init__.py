@@ -6,14 +6,16 @@ the C ABI (``ar_init``, ``ar_reduce_sum``, ``ar_fused_reduce_rmsnorm``,
 ``ar_fused_reduce_rmsnorm_noalloc``, ``ar_destroy`` ...) take raw pointers and sizes exactly
 as the C functions do; the ``Context`` methods (``reduce_sum``, ``fused_reduce_rmsnorm``,
 ``fused_reduce_rmsnorm_batch``, ``fused_reduce_rmsnorm_host``) marshal torch tensors into
-those calls.  Every step of the computation runs in the library's CUDA kernels: there is no
+those calls.  The attention block between two fused calls is ``ar_paged_plan``,
+``ar_qk_norm_rope`` and ``ar_paged_attention`` (methods ``paged_plan``, ``qk_norm_rope``,
+``paged_attention``).  Every step of the computation runs in the library's CUDA kernels: there is no
 Python or PyTorch compute path, and using the package without a built ``libar.so`` raises.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libar.so")
@@ -52,6 +54,15 @@ AR_INFO_L2_BYTES = 1
 AR_INFO_REDUCE_TILE_PACKS = 2
 AR_INFO_DEVICE = 3
 
+AR_MAX_REQUESTS = 8192
+AR_MAX_ROPE_AXES = 4
+AR_MAX_HEAD_DIM = 256
+AR_PLAN_OK = 0
+AR_PLAN_NO_BLOCKS = 1
+AR_PLAN_TABLE_FULL = 2
+AR_PLAN_TOO_MANY_TOKENS = 3
+AR_PLAN_BAD_LENGTH = 4
+
 
 class ArFusedArgs(ctypes.Structure):
     _fields_ = [
@@ -75,6 +86,73 @@ class ArFusedArgs(ctypes.Structure):
         ("ld_in", ctypes.c_int64),
         ("ld_out", ctypes.c_int64),
     ]
+
+
+def _fields(text):
+    """ctypes fields from "type name name ..." lines: i int, l int64, f float, z size_t, p pointer."""
+    kinds = {"i": ctypes.c_int, "l": ctypes.c_int64, "f": ctypes.c_float, "z": ctypes.c_size_t, "p": ctypes.c_void_p}
+    return [(name, kinds[kind]) for kind, *names in map(str.split, text.strip().splitlines()) for name in names]
+
+
+class ArPagedPlanArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        i requests page_size
+        l max_tokens free_capacity table_cols table_stride
+        p cached_lens new_lens free_blocks free_count block_table cu_q seq_lens slots positions free_count_out info
+    """)
+
+
+class ArQkNormRopeArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        l tokens
+        i q_heads kv_heads head_dim dtype
+        p q k v
+        l q_token_stride q_head_stride k_token_stride k_head_stride v_token_stride v_head_stride
+        p q_out k_out
+        l q_out_token_stride q_out_head_stride k_out_token_stride k_out_head_stride
+        p q_weight k_weight
+        f eps
+        i gemma rot_dim pairs axes
+    """) + [("sections", ctypes.c_int * AR_MAX_ROPE_AXES)] + _fields("""
+        i dealt
+        p positions
+        l position_stride
+        p inv_freq k_cache v_cache
+        l k_block_stride k_page_stride k_cache_head_stride v_block_stride v_page_stride v_cache_head_stride num_blocks
+        i page_size
+        p slots
+    """)
+
+
+class ArPagedAttentionArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        l tokens
+        i requests q_heads kv_heads head_dim dtype
+        p q out
+        l q_token_stride q_head_stride out_token_stride out_head_stride
+        p lse k_cache v_cache
+        l k_block_stride k_page_stride k_head_stride v_block_stride v_page_stride v_head_stride num_blocks
+        i page_size
+        p block_table
+        l table_cols table_stride
+        p cu_q seq_lens
+        f scale
+        i causal window
+        f softcap
+        p slopes prefix_lens workspace
+        z workspace_bytes
+    """)
+
+
+class PagedPlan(NamedTuple):
+    """One step's plan (see ar_paged_plan): device tensors."""
+    block_table: object
+    cu_q: object
+    seq_lens: object
+    slots: object
+    positions: object
+    free_count: object
+    info: object
 
 
 class ArError(RuntimeError):
@@ -114,7 +192,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ar_get_info.argtypes = [vp, c_int, ctypes.POINTER(i64)]
     lib.ar_device_status.argtypes = [vp, ctypes.POINTER(c_int)]
     lib.ar_fused_reduce_rmsnorm_batch.argtypes = [vp, ctypes.POINTER(ArFusedArgs), c_int, vp]
-    for f in ("ar_init", "ar_destroy", "ar_reduce_sum", "ar_fused_reduce_rmsnorm", "ar_set_option",
+    lib.ar_paged_plan.argtypes = [vp, ctypes.POINTER(ArPagedPlanArgs), vp]
+    lib.ar_qk_norm_rope.argtypes = [vp, ctypes.POINTER(ArQkNormRopeArgs), vp]
+    lib.ar_paged_attention.argtypes = [vp, ctypes.POINTER(ArPagedAttentionArgs), vp]
+    lib.ar_paged_attention_workspace.argtypes = [vp, ctypes.POINTER(ArPagedAttentionArgs),
+                                                 ctypes.POINTER(ctypes.c_size_t)]
+    for f in ("ar_paged_plan", "ar_qk_norm_rope", "ar_paged_attention", "ar_paged_attention_workspace",
+              "ar_init", "ar_destroy", "ar_reduce_sum", "ar_fused_reduce_rmsnorm", "ar_set_option",
               "ar_get_info", "ar_device_status", "ar_fused_reduce_rmsnorm_batch", "ar_fused_reduce_rmsnorm_host",
               "ar_fused_reduce_rmsnorm_noalloc"):
         getattr(lib, f).restype = c_int
@@ -228,6 +312,37 @@ def ar_fused_reduce_rmsnorm_batch(ctx: int, calls: Sequence[ArFusedArgs], stream
     return st
 
 
+def ar_paged_plan(ctx: int, args: ArPagedPlanArgs, stream: Optional[int] = None, raise_on_error: bool = True) -> int:
+    st = load_library().ar_paged_plan(ctx, ctypes.byref(args), stream)
+    if raise_on_error:
+        _check(ctx, st, "ar_paged_plan")
+    return st
+
+
+def ar_qk_norm_rope(ctx: int, args: ArQkNormRopeArgs, stream: Optional[int] = None, raise_on_error: bool = True) -> int:
+    st = load_library().ar_qk_norm_rope(ctx, ctypes.byref(args), stream)
+    if raise_on_error:
+        _check(ctx, st, "ar_qk_norm_rope")
+    return st
+
+
+def ar_paged_attention(ctx: int, args: ArPagedAttentionArgs, stream: Optional[int] = None,
+                       raise_on_error: bool = True) -> int:
+    st = load_library().ar_paged_attention(ctx, ctypes.byref(args), stream)
+    if raise_on_error:
+        _check(ctx, st, "ar_paged_attention")
+    return st
+
+
+def ar_paged_attention_workspace(ctx: int, args: ArPagedAttentionArgs) -> int:
+    """Bytes of workspace for calls with the head size and element type of `args`."""
+    n = ctypes.c_size_t()
+    st = load_library().ar_paged_attention_workspace(ctx, ctypes.byref(args), ctypes.byref(n))
+    if st != AR_OK:
+        raise ArError(st, "ar_paged_attention_workspace")
+    return n.value
+
+
 def make_fused_args(partials: Sequence[int], residual_in: Optional[int], residual_out: Optional[int],
                     weight: Optional[int], out: Optional[int], eps: float, gemma: bool, quant: bool,
                     q_out: Optional[int], scale_out: Optional[int], m: int, h: int, dtype: int,
@@ -294,12 +409,53 @@ def _row_stride(tensors, m, h, dtype, what, host: bool = False) -> int:
     return h if ld is None else ld
 
 
+def _flat(t, dtype, n, device, what) -> Optional[int]:
+    """Address of a contiguous CUDA tensor of `n` elements (None: any number) on `device`."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.get_device() != device or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor on cuda:{device}"
+                         + ("" if n is None else f" with {n} elements"))
+    return t.data_ptr()
+
+
+def _heads(t, tokens, heads, dim, dtype, device, what):
+    """(address, token stride, head stride) of a [tokens, heads, dim] tensor with unit last stride."""
+    if t.shape != (tokens, heads, dim) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{what} must be a [{tokens}, {heads}, {dim}] {dtype} tensor on cuda:{device}")
+    ts, hs, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    return t.data_ptr(), ts, hs
+
+
+def _cache(t, heads, dim, dtype, device, what):
+    """(address, block, token, head stride, blocks, page) of a [blocks, page, heads, dim] cache."""
+    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{what} must be a [blocks, page, {heads}, {dim}] {dtype} tensor on cuda:{device}")
+    bs, ps, hs, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    return t.data_ptr(), bs, ps, hs, t.shape[0], t.shape[1]
+
+
+def _table(t, requests, device):
+    """(address, columns, row stride) of a [requests, columns] int32 block table."""
+    import torch
+    if t.dim() != 2 or t.shape[0] != requests or t.dtype != torch.int32 or t.get_device() != device or \
+            (t.shape[1] > 1 and t.stride(1) != 1) or (requests > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"block_table must be a [{requests}, columns] int32 tensor on cuda:{device}, "
+                         "unit stride in its rows")
+    return t.data_ptr(), t.shape[1], t.stride(0) if requests > 1 else 0
+
+
 class Context:
     """Owns one ar_ctx for a device; torch-tensor front end of the C ABI."""
 
     def __init__(self, device: int = 0):
         self.device = device
         self.handle = ar_init(device)
+        self._workspace_bytes = {}
 
     def close(self):
         if self.handle:
@@ -433,3 +589,180 @@ class Context:
             results.append((out, ro, q, sc))
         ar_fused_reduce_rmsnorm_batch(self.handle, args, _stream(stream))
         return results
+
+    # ---- the attention block ------------------------------------------------
+
+    def _raw_stream(self, stream) -> int:
+        import torch
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if stream.device.index != self.device:
+            raise ValueError(f"the stream belongs to another device than cuda:{self.device}")
+        return stream.cuda_stream
+
+    def _empty(self, shape, dtype, stream):
+        """An output on this device that belongs to `stream` (None: the current one)."""
+        import torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
+
+    def paged_plan(self, cached_lens, new_lens, free_blocks, free_count, block_table, page_size: int,
+                   max_tokens: Optional[int] = None, cu_q=None, seq_lens=None, slots=None, positions=None,
+                   free_count_out=None, info=None, stream=None) -> PagedPlan:
+        """Block tables and slot maps of one step from int32 length tensors (see ar_paged_plan).
+        `block_table` [requests, columns] is updated in place; the others are returned, allocated
+        where not given.  `max_tokens` is the length of slots and positions (needed unless one of
+        them is given); free_count_out must not be free_count itself."""
+        import torch
+        dev, i32, r = self.device, torch.int32, cached_lens.numel()
+        if max_tokens is None:
+            given = slots if slots is not None else positions
+            if given is None:
+                raise ValueError("max_tokens, slots or positions must be given")
+            max_tokens = given.numel()
+        if cu_q is None:
+            cu_q = self._empty((r + 1,), i32, stream)
+        if seq_lens is None:
+            seq_lens = self._empty((r,), i32, stream)
+        if slots is None:
+            slots = self._empty((max_tokens,), torch.int64, stream)
+        if positions is None:
+            positions = self._empty((max_tokens,), i32, stream)
+        if free_count_out is None:
+            free_count_out = self._empty((1,), i32, stream)
+        if info is None:
+            info = self._empty((4,), i32, stream)
+        table, cols, stride = _table(block_table, r, dev)
+        args = ArPagedPlanArgs(
+            r, page_size, max_tokens, free_blocks.numel(), cols, stride,
+            _flat(cached_lens, i32, r, dev, "cached_lens"), _flat(new_lens, i32, r, dev, "new_lens"),
+            _flat(free_blocks, i32, None, dev, "free_blocks"), _flat(free_count, i32, 1, dev, "free_count"),
+            table, _flat(cu_q, i32, r + 1, dev, "cu_q"), _flat(seq_lens, i32, r, dev, "seq_lens"),
+            _flat(slots, torch.int64, max_tokens, dev, "slots"), _flat(positions, i32, max_tokens, dev, "positions"),
+            _flat(free_count_out, i32, 1, dev, "free_count_out"), _flat(info, i32, 4, dev, "info"))
+        ar_paged_plan(self.handle, args, self._raw_stream(stream))
+        return PagedPlan(block_table, cu_q, seq_lens, slots, positions, free_count_out, info)
+
+    def qk_norm_rope(self, q, k, v, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     gemma: bool = False, pairs: bool = False, sections: Optional[Sequence[int]] = None,
+                     dealt: bool = False, k_cache=None, v_cache=None, slots=None, q_out=None, k_out=None,
+                     want_k_out: bool = True, stream=None):
+        """RMSNorm of each q and k head (where its weight is given), rotation by `positions`
+        ([tokens] or [axes, tokens] int32) with the fp32 frequencies `inv_freq` (None: none), and
+        the write of k and v to the paged cache at `slots` (see ar_qk_norm_rope).  q, k, v are
+        [tokens, heads, head_dim] and may be views of one packed projection; q or k may be None.
+        Returns (q_out, k_out); with a cache, want_k_out=False leaves k_out out (None)."""
+        import torch
+        dev = self.device
+        x0 = q if q is not None else k
+        if x0 is None:
+            raise ValueError("q or k must be given")
+        n, _, d = x0.shape
+        dt = x0.dtype
+        if dt not in (torch.bfloat16, torch.float16):
+            raise ValueError("q, k and v must be bfloat16 or float16")
+        hq, hk = (0 if q is None else q.shape[1]), (0 if k is None else k.shape[1])
+        none = (None, 0, 0)
+        qa = _heads(q, n, hq, d, dt, dev, "q") if hq else none
+        ka = _heads(k, n, hk, d, dt, dev, "k") if hk else none
+        if hq and q_out is None:
+            q_out = self._empty((n, hq, d), dt, stream)
+        if hk and k_out is None and (want_k_out or k_cache is None):
+            k_out = self._empty((n, hk, d), dt, stream)
+        qo = _heads(q_out, n, hq, d, dt, dev, "q_out") if hq else none
+        ko = _heads(k_out, n, hk, d, dt, dev, "k_out") if hk and k_out is not None else none
+        half = 0 if inv_freq is None else inv_freq.numel()
+        axes, pos, pos_stride = 1, None, 0
+        if half:
+            if positions.dtype != torch.int32 or positions.get_device() != dev or positions.dim() not in (1, 2) or \
+                    positions.shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
+                raise ValueError(f"positions must be a [{n}] or [axes, {n}] int32 tensor on cuda:{dev}, unit stride")
+            pos = positions.data_ptr()
+            if positions.dim() == 2:
+                axes = positions.shape[0]
+                pos_stride = positions.stride(0) if axes > 1 else 0
+            if not 1 <= axes <= AR_MAX_ROPE_AXES:
+                raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
+            if axes > 1 and (sections is None or len(sections) != axes):
+                raise ValueError("sections must name the frequencies of each position axis")
+        sec = (ctypes.c_int * AR_MAX_ROPE_AXES)(*(sections if axes > 1 else ()))
+        kc = vc = (None, 0, 0, 0, 0, 1)
+        va, slot = none, None
+        if (k_cache is None) != (v_cache is None):
+            raise ValueError("k_cache and v_cache are given together")
+        if k_cache is not None:
+            if v is None or slots is None:
+                raise ValueError("a cache needs v and slots")
+            va = _heads(v, n, hk, d, dt, dev, "v")
+            kc = _cache(k_cache, hk, d, dt, dev, "k_cache")
+            vc = _cache(v_cache, hk, d, dt, dev, "v_cache")
+            if kc[4:] != vc[4:]:
+                raise ValueError("k_cache and v_cache must have the same blocks and page size")
+            slot = _flat(slots, torch.int64, n, dev, "slots")
+        args = ArQkNormRopeArgs(
+            n, hq, hk, d, AR_DTYPE_BF16 if dt == torch.bfloat16 else AR_DTYPE_F16, qa[0], ka[0], va[0],
+            qa[1], qa[2], ka[1], ka[2], va[1], va[2], qo[0], ko[0], qo[1], qo[2], ko[1], ko[2],
+            _flat(q_weight, dt, d, dev, "q_weight"), _flat(k_weight, dt, d, dev, "k_weight"), eps, gemma, 2 * half,
+            pairs, axes, sec, dealt, pos, pos_stride, _flat(inv_freq, torch.float32, half, dev, "inv_freq"),
+            kc[0], vc[0], kc[1], kc[2], kc[3], vc[1], vc[2], vc[3], kc[4], kc[5], slot)
+        ar_qk_norm_rope(self.handle, args, self._raw_stream(stream))
+        return q_out, k_out
+
+    def paged_attention(self, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: Optional[float] = None,
+                        causal: bool = True, window: int = 0, softcap: float = 0.0, slopes=None, prefix_lens=None,
+                        out=None, lse=None, want_lse: bool = False, workspace=None, stream=None):
+        """Attention of the requests' new tokens q [tokens, q_heads, head_dim] over the paged
+        cache [blocks, page, kv_heads, head_dim] (see ar_paged_attention); scale defaults to
+        head_dim ** -0.5.  Returns (out, lse); lse [tokens, q_heads] fp32 is None unless given or
+        wanted.  Rows of no request are not written.  `workspace` (uint8, from
+        paged_attention_workspace) is allocated where not given; calls that may run at the
+        same time need one each."""
+        import torch
+        dev = self.device
+        n, hq, d = q.shape
+        dt = q.dtype
+        if dt not in (torch.bfloat16, torch.float16):
+            raise ValueError("q must be bfloat16 or float16")
+        code = AR_DTYPE_BF16 if dt == torch.bfloat16 else AR_DTYPE_F16
+        r, hk = seq_lens.numel(), k_cache.shape[2]
+        if hk < 1 or hq % hk:
+            raise ValueError("q_heads must be a multiple of kv_heads")
+        if out is None:
+            out = self._empty((n, hq, d), dt, stream)
+        if lse is None and want_lse:
+            lse = self._empty((n, hq), torch.float32, stream)
+        if workspace is None:
+            workspace = self._empty((self._attention_workspace(d, code),), torch.uint8, stream)
+        qa = _heads(q, n, hq, d, dt, dev, "q")
+        oa = _heads(out, n, hq, d, dt, dev, "out")
+        kc = _cache(k_cache, hk, d, dt, dev, "k_cache")
+        vc = _cache(v_cache, hk, d, dt, dev, "v_cache")
+        if kc[4:] != vc[4:]:
+            raise ValueError("k_cache and v_cache must have the same blocks and page size")
+        table, cols, stride = _table(block_table, r, dev)
+        args = ArPagedAttentionArgs(
+            n, r, hq, hk, d, code, qa[0], oa[0], qa[1], qa[2], oa[1], oa[2],
+            _flat(lse, torch.float32, n * hq, dev, "lse"), kc[0], vc[0], kc[1], kc[2], kc[3], vc[1], vc[2], vc[3],
+            kc[4], kc[5], table, cols, stride, _flat(cu_q, torch.int32, r + 1, dev, "cu_q"),
+            _flat(seq_lens, torch.int32, r, dev, "seq_lens"), d ** -0.5 if scale is None else scale, causal, window,
+            softcap, _flat(slopes, torch.float32, hq, dev, "slopes"),
+            _flat(prefix_lens, torch.int32, r, dev, "prefix_lens"),
+            _flat(workspace, torch.uint8, None, dev, "workspace"), workspace.numel())
+        ar_paged_attention(self.handle, args, self._raw_stream(stream))
+        return out, lse
+
+    def _attention_workspace(self, head_dim: int, code: int) -> int:
+        key = (head_dim, code)
+        n = self._workspace_bytes.get(key)
+        if n is None:
+            n = self._workspace_bytes[key] = ar_paged_attention_workspace(
+                self.handle, ArPagedAttentionArgs(head_dim=head_dim, dtype=code))
+        return n
+
+    def paged_attention_workspace(self, head_dim: int, dtype):
+        """A workspace for paged_attention calls with this head size and element type, of any lengths."""
+        import torch
+        code = {torch.bfloat16: AR_DTYPE_BF16, torch.float16: AR_DTYPE_F16}[dtype]
+        return self._empty((self._attention_workspace(head_dim, code),), torch.uint8, None)

@@ -1,0 +1,282 @@
+// Work division of the paged attention kernels.
+//
+// An item is a tile of ROWS consecutive query rows of one request and one key head (rows are
+// the request's new tokens times the q heads that share the key head, token-major), with the
+// tiles of KT keys that some row of it can see.  All (item, key tile) pairs of the call stand in
+// one sequence, request by request, query tile by query tile, head by head, and every CTA of a
+// resident grid takes an equal, contiguous span of it.  So one rule serves single tokens over
+// long caches, chunks, and both in one batch, and the lengths may stay in device memory.
+//
+// A CTA that covers an item's tiles whole writes the output.  Otherwise it leaves the unnormalised
+// sum, maximum and weight sum of its part in the workspace: a CTA's span touches at most one
+// item that began before it (slot 0) and one that ends after it (slot 1).  A second small
+// kernel joins the parts in the order of the spans, so results do not depend on timing.
+#pragma once
+
+#include "ar_common.cuh"
+#include "ar_serve.h"
+
+namespace ar {
+
+constexpr int kHeaderInts = 8;  // flags (1: there, 2: the item ends here), first row of the request, rows of the request, query tile, head
+constexpr int kThere = 1, kEnds = 2;
+
+struct Request {
+  int q0, n, len, prefix;  // first row of q, new tokens, keys, keys that every row sees
+};
+
+__device__ __forceinline__ Request load_request(const AttnParams& p, int r) {
+  Request q;
+  const int a = p.cu_q[r], b = p.cu_q[r + 1];
+  const int most = (int)p.tokens;
+  q.q0 = min(max(a, 0), most);
+  q.n = min(max(b, q.q0), most) - q.q0;
+  const int len = p.seq_lens[r];
+  q.len = min(max(len, 0), p.max_len);
+  q.prefix = p.prefix ? min(max(p.prefix[r], 0), q.len) : 0;
+  if (a < 0 || b < a || b > most || q.len != len) *p.status = kStatusBadIndex;
+  return q;
+}
+
+// Key tiles of a query tile: [0, pre), then [lo, hi).
+struct TileRange {
+  int pre, lo, hi;
+  __device__ __forceinline__ int count() const { return max(pre + max(hi - lo, 0), 1); }  // an empty row is one masked tile
+  __device__ __forceinline__ int tile(int i) const { return i < pre ? i : lo + (i - pre); }
+};
+
+template <int ROWS, int KT>
+__device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Request& q, int qt) {
+  const int64_t row0 = (int64_t)qt * ROWS;
+  const int64_t rows = (int64_t)q.n * p.group;
+  const int t0 = (int)row0 / p.group, t1 = (int)(min(row0 + ROWS, rows) - 1) / p.group;
+  const int p0 = q.len - q.n + t0, p1 = q.len - q.n + t1;  // may be negative: rows that see no key
+  const int high = p.causal ? min(max(p1 + 1, 0), q.len) : q.len;
+  const int low = p.window ? max(p0 - p.window + 1, 0) : 0;  // |p0| and window are at most 2^30
+  TileRange t;
+  t.pre = (q.prefix + KT - 1) / KT;
+  t.lo = max(low / KT, t.pre);
+  t.hi = (high + KT - 1) / KT;
+  return t;
+}
+
+struct Cursor {  // a place in the sequence
+  int r, qt, h, tile;
+};
+
+// One item as a CTA walks over it.
+struct Item {
+  Request q;
+  int rows;  // rows of the request (new tokens times group)
+  int r, qt, h;
+  TileRange range;
+  int begin, end;  // tiles of this CTA's part
+  bool first, last;  // the part holds the item's first, last tile
+};
+
+struct SpanShared {
+  long long warp_sum[32];
+  long long offset;
+  Cursor at;
+  long long tiles;  // tiles of this CTA's span
+};
+
+// The CTA's span: where it starts and how many tiles it has.  All threads take part.
+template <int ROWS, int KT, int THREADS>
+__device__ void find_span(const AttnParams& p, SpanShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int WARPS = THREADS / 32;
+  auto request_tiles = [&](int r, bool there) -> long long {  // key tiles of each thread's request, over its query tiles and heads
+    Request q = {0, 0, 0, 0};
+    if (there) q = load_request(p, r);
+    const int nqt = (int)(((int64_t)q.n * p.group + ROWS - 1) / ROWS);
+    long long mine = 0;
+    if (nqt == 1) mine = tile_range<ROWS, KT>(p, q, 0).count();
+    for (unsigned many = __ballot_sync(0xffffffffu, nqt > 1); many; many &= many - 1) {  // the warp together
+      const int src = __ffs(many) - 1;
+      Request o;
+      o.q0 = 0;
+      o.n = __shfl_sync(0xffffffffu, q.n, src);
+      o.len = __shfl_sync(0xffffffffu, q.len, src);
+      o.prefix = __shfl_sync(0xffffffffu, q.prefix, src);
+      const int m = __shfl_sync(0xffffffffu, nqt, src);
+      long long s = 0;
+      for (int t = lane; t < m; t += 32) s += tile_range<ROWS, KT>(p, o, t).count();
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      if (lane == src) mine = s;
+    }
+    return mine * p.kv_heads;
+  };
+  long long before = 0, mine = 0, excl = 0;
+  auto scan = [&](int base) {  // `mine` and its exclusive prefix over all requests; adds the chunk to `before`
+    const int r = base + (int)threadIdx.x;
+    mine = request_tiles(r, r < p.requests);
+    long long s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) sh.warp_sum[warp] = s;
+    __syncthreads();
+    excl = before + s - mine;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) excl += sh.warp_sum[w];
+      before += sh.warp_sum[w];
+    }
+    __syncthreads();
+  };
+  for (int base = 0; base < p.requests; base += THREADS) scan(base);
+  const long long total = before;
+  const long long s0 = total * blockIdx.x / gridDim.x, s1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (threadIdx.x == 0) {
+    sh.tiles = s1 - s0;
+    sh.at = {0, 0, 0, 0};
+    sh.offset = 0;
+  }
+  __syncthreads();
+  const bool one = p.requests <= THREADS;
+  before = 0;
+  for (int base = 0; base < p.requests; base += THREADS) {
+    if (!one) scan(base);
+    if (s1 > s0 && mine > 0 && excl <= s0 && s0 < excl + mine) {
+      sh.at.r = base + (int)threadIdx.x;
+      sh.offset = s0 - excl;
+    }
+  }
+  __syncthreads();
+  if (s1 > s0 && warp == 0) {  // the query tile within the request
+    const Request q = load_request(p, sh.at.r);
+    const int nqt = (int)(((int64_t)q.n * p.group + ROWS - 1) / ROWS);
+    long long left = sh.offset;
+    for (int base = 0; base < nqt; base += 32) {
+      const int t = base + lane;
+      const int c = t < nqt ? tile_range<ROWS, KT>(p, q, t).count() : 0;
+      const long long own = (long long)c * p.kv_heads;
+      long long s = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, s > left);
+      if (over) {
+        if (lane == __ffs(over) - 1) {
+          const long long in = left - (s - own);
+          sh.at.qt = t;
+          sh.at.h = (int)(in / c);
+          sh.at.tile = (int)(in - (long long)sh.at.h * c);
+        }
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, s, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// Walks the items of a span; every role of a CTA walks for itself.
+template <int ROWS, int KT>
+struct Walk {
+  Cursor at;
+  long long left;
+  Request q;
+
+  __device__ __forceinline__ Walk(const AttnParams& p, const SpanShared& sh) : at(sh.at), left(sh.tiles) {
+    if (left > 0) q = load_request(p, at.r);
+  }
+
+  __device__ __forceinline__ bool next(const AttnParams& p, Item& it) {
+    if (left <= 0) return false;
+    const int rows = q.n * p.group;
+    it.q = q;
+    it.rows = rows;
+    it.r = at.r;
+    it.qt = at.qt;
+    it.h = at.h;
+    it.range = tile_range<ROWS, KT>(p, q, at.qt);
+    const int n = it.range.count();
+    it.begin = at.tile;
+    it.end = (int)min((long long)n, at.tile + left);
+    it.first = it.begin == 0;
+    it.last = it.end == n;
+    left -= max(it.end - it.begin, 1);
+    at.tile = 0;
+    if (++at.h == p.kv_heads) {
+      at.h = 0;
+      if ((int64_t)++at.qt * ROWS >= rows) {
+        at.qt = 0;
+        if (left > 0) {  // a request with rows follows
+          q.n = 0;
+          while (q.n == 0 && ++at.r < p.requests) q = load_request(p, at.r);
+          if (q.n == 0) left = 0;
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// What a row of the item sees and how its scores are bent.
+struct RowView {
+  int pos;     // position of the query
+  int see_lo;  // keys [see_lo, see_hi) besides the prefix
+  int see_hi;
+  float slope;  // slope * log2(e)
+};
+
+__device__ __forceinline__ RowView row_view(const AttnParams& p, const Item& it, int row) {
+  RowView v;
+  const int t = row / p.group, g = row - t * p.group;
+  v.pos = it.q.len - it.q.n + t;
+  v.see_hi = p.causal ? min(v.pos + 1, it.q.len) : it.q.len;
+  v.see_lo = p.window ? v.pos - p.window + 1 : 0;
+  v.slope = p.slopes && row < it.rows ? p.slopes[it.h * p.group + g] * 1.4426950408889634f : 0.0f;
+  if (row >= it.rows) v.see_hi = 0;
+  return v;
+}
+
+// (row, key) visible: rows behind the item's end have see_hi 0 and no outputs.
+__device__ __forceinline__ bool visible(const Item& it, const RowView& v, int key) {
+  return key < it.q.prefix || (key < v.see_hi && key >= v.see_lo);
+}
+
+// Score in log2 units from the raw product.
+__device__ __forceinline__ float bend(const AttnParams& p, const RowView& v, float dot, int key) {
+  float s = dot * p.scale_log2;
+  if (p.cap_log2 > 0.0f) s = p.cap_log2 * tanhf(s);
+  if (p.slopes) s -= v.slope * (float)abs(v.pos - key);
+  return s;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Block and place in it of a key; -1 for a block number outside the cache.
+__device__ __forceinline__ int64_t block_of(const AttnParams& p, int r, int key, int& in_page) {
+  const int j = key / p.page;
+  in_page = key - j * p.page;
+  const int b = p.table[(int64_t)r * p.table_stride + j];
+  if (b < 0 || b >= p.num_blocks) {
+    *p.status = kStatusBadIndex;
+    return -1;
+  }
+  return b;
+}
+
+__device__ __forceinline__ void write_header(const AttnParams& p, int slot, int flags, const Item* it) {
+  int* h = p.headers + ((int64_t)blockIdx.x * 2 + slot) * kHeaderInts;
+  h[0] = flags;
+  if (it) {
+    h[1] = it->q.q0;
+    h[2] = it->rows;
+    h[3] = it->qt;
+    h[4] = it->h;
+  }
+}
+
+}  // namespace ar

@@ -1,0 +1,307 @@
+// Paged attention, general form: any head size up to 256, page size, stride and alignment.
+//
+// One CTA of four warps takes 64 query rows (16 a warp) against tiles of 64 keys: scores and
+// the weighted sum by 16 x 8 x 16 matrix instructions on tiles in shared memory, the softmax's
+// running maximum and sum in registers, each key and value read once an item.  Keys are gathered
+// row by row through the block table, so pages may end anywhere in a tile.
+#include "ar_attn.cuh"
+
+namespace ar {
+namespace {
+
+constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
+template <int DT>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (DT == kBF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One row of head_dim elements into shared memory, the rest of the padded row zero; src NULL: zeros.
+template <int DP>
+__device__ __forceinline__ void fill_row(const AttnParams& p, uint16_t* dst, const uint16_t* src, int part, int parts) {
+  for (int c = part; c < DP / 8; c += parts) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const int e = c * 8;
+    if (src && e < p.head_dim) {
+      if (p.vec) {
+        v = ld_keep(src + e);
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = e + i < p.head_dim ? ld_u16(src + e + i) : 0;
+        v = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + e) = v;
+  }
+}
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ AttnParams p) {
+  constexpr int LD = DP + 8;  // 16 bytes of padding: the eight rows of a matrix load fall into different banks
+  extern __shared__ __align__(16) uint16_t smem[];
+  uint16_t* sq = smem;
+  uint16_t* sk = sq + kRows * LD;
+  uint16_t* sv = sk + kKeys * LD;
+  __shared__ SpanShared span;
+  pdl_wait_and_release();
+  find_span<kRows, kKeys, kThreads>(p, span);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool wrote[2] = {false, false};
+  Walk<kRows, kKeys> walk(p, span);
+  Item it;
+  while (walk.next(p, it)) {
+    __syncthreads();
+    for (int r = threadIdx.x >> 2; r < kRows; r += kThreads / 4) {
+      const int row = it.qt * kRows + r;
+      const uint16_t* src = nullptr;
+      if (row < it.rows) {
+        const int t = row / p.group, g = row - t * p.group;
+        src = static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * p.group + g) * p.q_hs;
+      }
+      fill_row<DP>(p, sq + r * LD, src, threadIdx.x & 3, 4);
+    }
+    // the two rows of this lane
+    RowView view[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) view[i] = row_view(p, it, it.qt * kRows + warp * 16 + (lane >> 2) + i * 8);
+    float o[DP / 8][4];
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    for (int ti = it.begin; ti < it.end; ++ti) {
+      const int key0 = it.range.tile(ti) * kKeys;
+      __syncthreads();
+      for (int r = threadIdx.x >> 2; r < kKeys; r += kThreads / 4) {
+        const int key = key0 + r;
+        const uint16_t *k = nullptr, *v = nullptr;
+        if (key < it.q.len) {
+          int off;
+          const int64_t b = block_of(p, it.r, key, off);
+          if (b >= 0) {
+            k = static_cast<const uint16_t*>(p.k) + b * p.k_bs + off * p.k_ps + it.h * p.k_hs;
+            v = static_cast<const uint16_t*>(p.v) + b * p.v_bs + off * p.v_ps + it.h * p.v_hs;
+          }
+        }
+        fill_row<DP>(p, sk + r * LD, k, threadIdx.x & 3, 4);
+        fill_row<DP>(p, sv + r * LD, v, threadIdx.x & 3, 4);
+      }
+      __syncthreads();
+
+      float s[kKeys / 8][4];
+#pragma unroll
+      for (int i = 0; i < kKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        uint32_t a[4];
+        ldsm4(a, smem_u32(sq + (warp * 16 + (lane & 15)) * LD + kk * 16 + (lane >> 4) * 8));
+#pragma unroll
+        for (int j = 0; j < kKeys / 16; ++j) {
+          uint32_t b[4];
+          ldsm4(b, smem_u32(sk + (j * 16 + (lane >> 4) * 8 + (lane & 7)) * LD + kk * 16 + ((lane >> 3) & 1) * 8));
+          mma<DT>(s[2 * j], a, b[0], b[1]);
+          mma<DT>(s[2 * j + 1], a, b[2], b[3]);
+        }
+      }
+      // scores in log2 units; what a row does not see is -inf whatever the product gave
+      float top[2] = {m[0], m[1]};
+#pragma unroll
+      for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + j * 8 + (lane & 3) * 2 + (e & 1);
+          const RowView& w = view[e >> 1];
+          s[j][e] = visible(it, w, key) ? bend(p, w, s[j][e], key) : -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
+        }
+      float base[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        base[i] = top[i] == -INFINITY ? 0.0f : top[i];
+        const float shrink = ex2(m[i] - base[i]);  // m = -inf: 0
+        m[i] = top[i];
+        l[i] *= shrink;
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          o[j][2 * i] *= shrink;
+          o[j][2 * i + 1] *= shrink;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[j][e] = ex2(s[j][e] - base[e >> 1]);
+          l[e >> 1] += s[j][e];
+        }
+      // weights rounded to the 16-bit type for the second product; their sum l is of the unrounded ones
+#pragma unroll
+      for (int kk = 0; kk < kKeys / 16; ++kk) {
+        const uint32_t a[4] = {pack2<DT>(s[2 * kk][0], s[2 * kk][1]), pack2<DT>(s[2 * kk][2], s[2 * kk][3]),
+                               pack2<DT>(s[2 * kk + 1][0], s[2 * kk + 1][1]), pack2<DT>(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+#pragma unroll
+        for (int j = 0; j < DP / 16; ++j) {
+          uint32_t b[4];
+          ldsm4t(b, smem_u32(sv + (kk * 16 + (lane & 15)) * LD + j * 16 + (lane >> 4) * 8));
+          mma<DT>(o[2 * j], a, b[0], b[1]);
+          mma<DT>(o[2 * j + 1], a, b[2], b[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    const bool whole = it.first && it.last;
+    const int slot = it.first ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int local = warp * 16 + (lane >> 2) + i * 8, row = it.qt * kRows + local;
+      if (row >= it.rows) continue;
+      if (whole) {
+        const int t = row / p.group, head = it.h * p.group + row - t * p.group;
+        const float inv = l[i] > 0.0f ? 1.0f / l[i] : 0.0f;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          const int e = j * 8 + (lane & 3) * 2;
+          if (p.vec) {
+            if (e < p.head_dim) *reinterpret_cast<uint32_t*>(dst + e) = pack2<DT>(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+          } else {
+            if (e < p.head_dim) st_u16(dst + e, round1<DT>(o[j][2 * i] * inv));
+            if (e + 1 < p.head_dim) st_u16(dst + e + 1, round1<DT>(o[j][2 * i + 1] * inv));
+          }
+        }
+        if (p.lse && (lane & 3) == 0)
+          p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l[i] > 0.0f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+      } else {
+        const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + local;
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          const int e = j * 8 + (lane & 3) * 2;
+          if (e < p.part_dim) *reinterpret_cast<float2*>(p.part_o + at * p.part_dim + e) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+        }
+        if ((lane & 3) == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[i], l[i]);
+      }
+    }
+    if (!whole) {
+      wrote[slot] = true;
+      if (threadIdx.x == 0) write_header(p, slot, kThere | (it.last ? kEnds : 0), &it);
+    }
+  }
+  if (threadIdx.x == 0)
+    for (int s = 0; s < 2; ++s)
+      if (!wrote[s]) write_header(p, s, 0, nullptr);
+}
+
+// Joins the parts of the items that more than one span holds: block (c, y) serves rows
+// [8 y, 8 y + 8) of the item that begins in span c and does not end there.
+template <int DT>
+__global__ void __launch_bounds__(128) attn_combine(const __grid_constant__ AttnParams p) {
+  __shared__ int sh_end;
+  pdl_wait_and_release();
+  const int c = blockIdx.x;
+  const int* h = p.headers + ((int64_t)c * 2 + 1) * kHeaderInts;
+  if (!(h[0] & kThere)) return;
+  const int q0 = h[1], rows = h[2], qt = h[3], head0 = h[4] * p.group;
+  const int row_base = qt * p.tile_rows;
+  if (row_base + (int)blockIdx.y * 8 >= rows) return;
+  if (threadIdx.x == 0) sh_end = p.spans;
+  __syncthreads();
+  for (int i = c + 1 + (int)threadIdx.x; i < p.spans; i += 128)
+    if (p.headers[(int64_t)i * 2 * kHeaderInts] & kEnds) {
+      atomicMin(&sh_end, i);
+      break;
+    }
+  __syncthreads();
+  const int end = min(sh_end, p.spans - 1);  // the chain: slot 1 of span c, slot 0 of spans c + 1 .. end
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto place = [&](int i, int local) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.tile_rows + local; };
+  for (int k = 0; k < 2; ++k) {
+    const int local = blockIdx.y * 8 + warp * 2 + k, row = row_base + local;
+    if (row >= rows) continue;
+    float top = -INFINITY;
+    for (int i = c + lane; i <= end; i += 32) top = fmaxf(top, p.part_ml[place(i, local) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f;
+    for (int i = c + lane; i <= end; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + place(i, local) * 2);
+      l += ex2(ml.x - base) * ml.y;
+    }
+    l = warp_sum(l);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int t = row / p.group, head = head0 + row - t * p.group;
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+    for (int e = lane * 4; e < p.part_dim; e += 128) {
+      float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int i = c; i <= end; ++i) {
+        const int64_t at = place(i, local);
+        const float w = ex2(p.part_ml[at * 2] - base);
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * p.part_dim + e);
+        a[0] += w * v.x;
+        a[1] += w * v.y;
+        a[2] += w * v.z;
+        a[3] += w * v.w;
+      }
+      if (p.vec) {
+        if (e < p.head_dim) st_v2(dst + e, make_uint2(pack2<DT>(a[0] * inv, a[1] * inv), pack2<DT>(a[2] * inv, a[3] * inv)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e + j < p.head_dim) st_u16(dst + e + j, round1<DT>(a[j] * inv));
+      }
+    }
+    if (p.lse && lane == 0)
+      p.lse[(int64_t)(q0 + t) * p.q_heads + head] = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int DT>
+const void* mma_of(int dp) {
+  switch (dp) {
+    case 64: return reinterpret_cast<const void*>(&attn_mma<DT, 64>);
+    case 128: return reinterpret_cast<const void*>(&attn_mma<DT, 128>);
+    case 256: return reinterpret_cast<const void*>(&attn_mma<DT, 256>);
+  }
+  return nullptr;
+}
+
+}  // namespace
+
+const void* attn_mma_kernel(bool bf16, int padded_dim) { return bf16 ? mma_of<kBF16>(padded_dim) : mma_of<kF16>(padded_dim); }
+
+const void* attn_combine_kernel(bool bf16) {
+  return bf16 ? reinterpret_cast<const void*>(&attn_combine<kBF16>) : reinterpret_cast<const void*>(&attn_combine<kF16>);
+}
+
+}  // namespace ar

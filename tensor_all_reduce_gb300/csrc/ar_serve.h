@@ -1,0 +1,103 @@
+// Kernel parameters and entries of the attention block's operators (paged plan, per-head norm
+// with rotation, paged attention), shared by their kernels and the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ar.h"
+
+namespace ar {
+
+constexpr int kStatusBadIndex = 2;  // status word: an index in device memory was out of range
+
+struct PlanParams {
+  int requests, page;
+  int64_t max_tokens, free_capacity, table_cols, table_stride;
+  const int32_t* cached;
+  const int32_t* fresh;
+  const int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* table;
+  int32_t* cu_q;
+  int32_t* seq_lens;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* free_count_out;
+  int32_t* info;
+};
+
+struct HeadRows {  // [tokens, heads, head_dim] with unit last stride
+  const void* in;
+  void* out;  // NULL: not stored
+  int64_t in_ts, in_hs, out_ts, out_hs;
+  const void* weight;  // NULL: no norm
+  int heads;
+};
+
+struct RopeParams {
+  int64_t tokens;
+  int head_dim;
+  HeadRows q, k;
+  const void* v;
+  int64_t v_ts, v_hs;
+  float eps, inv_dim;
+  int gemma, half, pairs, axes, dealt;  // half: frequencies, rot_dim / 2
+  int sections[AR_MAX_ROPE_AXES];
+  const int32_t* positions;
+  int64_t pos_stride;
+  const float* inv_freq;
+  void* k_cache;
+  void* v_cache;
+  int64_t kc_bs, kc_ps, kc_hs, vc_bs, vc_ps, vc_hs;  // strides: block, token of a block, head
+  int64_t num_slots;
+  int page;
+  const int64_t* slots;
+  int* status;
+};
+
+struct AttnParams {
+  int64_t tokens;
+  int requests, q_heads, kv_heads, group, head_dim;
+  const void* q;
+  void* out;
+  int64_t q_ts, q_hs, o_ts, o_hs;
+  float* lse;
+  const void* k;
+  const void* v;
+  int64_t k_bs, k_ps, k_hs, v_bs, v_ps, v_hs;
+  int64_t num_blocks;
+  int page;
+  const int32_t* table;
+  int64_t table_stride;
+  int max_len;  // keys that a table row can name, at most 2^30
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  float scale_log2;  // scale * log2(e); with a cap, scale / cap
+  float cap_log2;    // cap * log2(e), 0: no cap
+  int causal, window;
+  const float* slopes;
+  const int32_t* prefix;
+  int vec;  // 16-byte loads of q and the cache, 16-byte stores of out
+  // workspace: the partial results of the spans that begin or end inside an item
+  int spans, tile_rows, part_dim;  // CTAs, rows of an item, floats of a partial row
+  int* headers;
+  float* part_o;
+  float* part_ml;
+  int* status;
+  long long wait_cycles;
+};
+
+const void* plan_kernel();
+const void* rope_kernel(bool bf16, bool vec);
+const void* attn_mma_kernel(bool bf16, int padded_dim);
+const void* attn_combine_kernel(bool bf16);
+
+// Dynamic shared memory of the general attention kernel: 64 query rows, keys and values each,
+// padded by 16 bytes.
+inline size_t attn_mma_smem(int padded_dim) { return (size_t)3 * 64 * (padded_dim + 8) * 2; }
+
+// Function attributes, module loading and occupancies for all of the above, once per context.
+cudaError_t serve_prepare(ar_ctx* ctx);
+
+}  // namespace ar

@@ -1,0 +1,438 @@
+// C ABI of the attention block's operators: argument validation, choice of the kernel, launch.
+//
+// As in ar_api.cu, validation precedes any use of the context, and nothing here allocates or
+// synchronises.
+#include <math.h>
+#include <string.h>
+
+#include "ar.h"
+#include "ar_common.cuh"
+#include "ar_ctx.h"
+#include "ar_launch.h"
+#include "ar_serve.h"
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+
+// A strided array as the bytes it spans: `rows` rows of `span` bytes, `stride` bytes apart.
+struct Extent {
+  const void* p;
+  int64_t span, stride, rows;
+  bool empty() const { return !p || span <= 0 || rows <= 0; }
+  int64_t bytes() const { return (rows - 1) * stride + span; }
+};
+
+Extent flat(const void* p, int64_t bytes) { return {p, bytes, bytes, 1}; }
+
+// Whether two arrays share a byte.  Arrays of one row stride may lie side by side in each row
+// (q, k and v of a packed projection, k and v of one cache tensor).
+bool overlap(const Extent& a, const Extent& b) {
+  if (a.empty() || b.empty()) return false;
+  if (!overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
+  if (a.stride != b.stride || a.rows < 2 || b.rows < 2) return true;
+  const int64_t s = a.stride;
+  int64_t d = (int64_t)(addr(b.p) - addr(a.p)) % s;  // b's row start within a's row
+  if (d < 0) d += s;
+  return !(d >= a.span && d + b.span <= s);
+}
+
+struct Checker {
+  Extent in[24], out[8];
+  int ni = 0, no = 0;
+  void read(const Extent& e) { if (!e.empty()) in[ni++] = e; }
+  void write(const Extent& e) { if (!e.empty()) out[no++] = e; }
+  // `alias[o]`: index + 1 of the input that output o is exactly
+  bool ok(const int* alias = nullptr) const {
+    for (int o = 0; o < no; ++o) {
+      for (int i = 0; i < ni; ++i)
+        if (!(alias && alias[o] == i + 1) && overlap(out[o], in[i])) return false;
+      for (int q = o + 1; q < no; ++q)
+        if (overlap(out[o], out[q])) return false;
+    }
+    return true;
+  }
+};
+
+// Non-negative strides of [outer, inner, dim] that keep rows and heads apart.
+bool strides_ok(int64_t outer, int64_t os, int64_t inner, int64_t is, int64_t dim) {
+  constexpr int64_t most = (int64_t)1 << 40;
+  if (os < 0 || is < 0 || os > most || is > most) return false;
+  if (inner > 1 && is < dim) return false;
+  if (outer > 1 && os < dim) return false;
+  return true;
+}
+
+int64_t span3(int64_t b, int64_t bs, int64_t c, int64_t cs, int64_t d) {
+  return (b - 1) * bs + (c - 1) * cs + d;
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* a, void* stream) {
+  if (!a) return AR_ERR_INVALID_ARG;
+  const int64_t i31 = 0x7fffffff;
+  if (a->requests < 0 || a->requests > AR_MAX_REQUESTS || a->page_size < 1 || a->page_size > 65536 || a->max_tokens < 0 ||
+      a->max_tokens > kMaxRows || a->free_capacity < 0 || a->free_capacity > i31 || a->table_cols < 0 || a->table_cols > i31 ||
+      a->table_stride < 0 || (a->table_stride && a->table_stride < a->table_cols) || a->table_stride > ((int64_t)1 << 40))
+    return AR_ERR_INVALID_ARG;
+  const int64_t ts = a->table_stride ? a->table_stride : a->table_cols;
+  const int64_t r = a->requests;
+  if (!a->cu_q || !a->free_count || !a->free_count_out || !a->info || (a->free_capacity && !a->free_blocks) ||
+      (a->max_tokens && (!a->slots || !a->positions)) ||
+      (r && (!a->cached_lens || !a->new_lens || !a->seq_lens || (a->table_cols && !a->block_table))))
+    return AR_ERR_INVALID_ARG;
+  if (!aligned(a->cached_lens, 4) || !aligned(a->new_lens, 4) || !aligned(a->free_blocks, 4) || !aligned(a->free_count, 4) ||
+      !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) || !aligned(a->seq_lens, 4) || !aligned(a->slots, 8) ||
+      !aligned(a->positions, 4) || !aligned(a->free_count_out, 4) || !aligned(a->info, 4))
+    return AR_ERR_ALIGNMENT;
+  Checker c;
+  c.read(flat(a->cached_lens, r * 4));
+  c.read(flat(a->new_lens, r * 4));
+  c.read(flat(a->free_blocks, a->free_capacity * 4));
+  c.read(flat(a->free_count, 4));
+  c.write({a->block_table, a->table_cols * 4, ts * 4, r});
+  c.write(flat(a->cu_q, (r + 1) * 4));
+  c.write(flat(a->seq_lens, r * 4));
+  c.write(flat(a->slots, a->max_tokens * 8));
+  c.write(flat(a->positions, a->max_tokens * 4));
+  c.write(flat(a->free_count_out, 4));
+  c.write(flat(a->info, 16));
+  if (!c.ok()) return AR_ERR_OVERLAP;
+  if (!ctx) return AR_ERR_NOT_INITIALIZED;
+
+  ar::PlanParams p;
+  p.requests = a->requests;
+  p.page = a->page_size;
+  p.max_tokens = a->max_tokens;
+  p.free_capacity = a->free_capacity;
+  p.table_cols = a->table_cols;
+  p.table_stride = ts;
+  p.cached = a->cached_lens;
+  p.fresh = a->new_lens;
+  p.free_blocks = a->free_blocks;
+  p.free_count = a->free_count;
+  p.table = a->block_table;
+  p.cu_q = a->cu_q;
+  p.seq_lens = a->seq_lens;
+  p.slots = a->slots;
+  p.positions = a->positions;
+  p.free_count_out = a->free_count_out;
+  p.info = a->info;
+  // a CTA for every 512 tokens, one an SM at most
+  int64_t grid = (a->max_tokens + 511) / 512;
+  if (grid > ctx->sm_count) grid = ctx->sm_count;
+  if (grid < 1) grid = 1;
+  DeviceGuard g(ctx->device);
+  void* args[1] = {&p};
+  const ar_status st = launch(ctx, ar::plan_kernel(), (unsigned)grid, 512, 1, args, (size_t)(r ? r : 1) * 8, stream);
+  if (st == AR_OK) ctx->last_variant = "paged_plan";
+  return st;
+}
+
+ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stream) {
+  if (!a) return AR_ERR_INVALID_ARG;
+  const bool cache = a->k_cache || a->v_cache;
+  if (a->tokens < 0 || a->q_heads < 0 || a->kv_heads < 0 || a->q_heads + (int64_t)a->kv_heads < 1 || a->q_heads > 65536 ||
+      a->kv_heads > 65536 || a->head_dim < 1 || a->head_dim > AR_MAX_HEAD_DIM || a->tokens > kMaxRows ||
+      (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
+    return AR_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.0f) || isinf(a->eps)) return AR_ERR_INVALID_ARG;
+  if (a->rot_dim < 0 || a->rot_dim > a->head_dim || (a->rot_dim & 1)) return AR_ERR_INVALID_ARG;
+  const int half = a->rot_dim / 2;
+  if (half) {
+    if (a->axes < 1 || a->axes > AR_MAX_ROPE_AXES || a->position_stride < 0 ||
+        (a->position_stride && a->axes > 1 && a->position_stride < a->tokens) || a->position_stride > ((int64_t)1 << 40))
+      return AR_ERR_INVALID_ARG;
+    if (a->axes > 1) {
+      int sum = 0;
+      for (int i = 0; i < a->axes; ++i) {
+        if (a->sections[i] < 0 || a->sections[i] > half) return AR_ERR_INVALID_ARG;
+        sum += a->sections[i];
+      }
+      if (sum != half) return AR_ERR_INVALID_ARG;
+    }
+  }
+  const int64_t n = a->tokens, d = a->head_dim, hq = a->q_heads, hk = a->kv_heads;
+  if (cache && (!a->k_cache || !a->v_cache || !hk || a->num_blocks < 0 || a->page_size < 1 || a->page_size > 65536 ||
+                a->num_blocks > ((int64_t)1 << 40) / a->page_size))
+    return AR_ERR_INVALID_ARG;
+  if (n == 0) {
+    if (!ctx) return AR_ERR_NOT_INITIALIZED;
+    ctx->last_variant = "none";
+    return AR_OK;
+  }
+  if ((hq && (!a->q || !a->q_out)) || (hk && (!a->k || (!a->k_out && !cache))) || (half && (!a->positions || !a->inv_freq)) ||
+      (cache && (!a->v || !a->slots)))
+    return AR_ERR_INVALID_ARG;
+  const bool k_out = hk && a->k_out;
+  if ((hq && (!strides_ok(n, a->q_token_stride, hq, a->q_head_stride, d) || !strides_ok(n, a->q_out_token_stride, hq, a->q_out_head_stride, d))) ||
+      (hk && !strides_ok(n, a->k_token_stride, hk, a->k_head_stride, d)) ||
+      (k_out && !strides_ok(n, a->k_out_token_stride, hk, a->k_out_head_stride, d)) ||
+      (cache && (!strides_ok(n, a->v_token_stride, hk, a->v_head_stride, d) ||
+                 !strides_ok(a->num_blocks, a->k_block_stride, a->page_size, a->k_page_stride, d) ||
+                 !strides_ok(a->num_blocks, a->v_block_stride, a->page_size, a->v_page_stride, d) ||
+                 !strides_ok(1, 0, hk, a->k_cache_head_stride, d) || !strides_ok(1, 0, hk, a->v_cache_head_stride, d))))
+    return AR_ERR_INVALID_ARG;
+  const void* two[] = {hq ? a->q : nullptr, hq ? a->q_out : nullptr, hk ? a->k : nullptr, k_out ? a->k_out : nullptr, a->q_weight, a->k_weight,
+                       cache ? a->v : nullptr, a->k_cache, a->v_cache};
+  for (const void* x : two)
+    if (!aligned(x, 2)) return AR_ERR_ALIGNMENT;
+  if ((half && (!aligned(a->positions, 4) || !aligned(a->inv_freq, 4))) || (cache && !aligned(a->slots, 8))) return AR_ERR_ALIGNMENT;
+
+  Checker c;
+  int alias[4] = {0, 0, 0, 0};
+  auto heads = [&](const void* p, int64_t ts, int64_t h, int64_t hs) { return Extent{p, ((h - 1) * hs + d) * 2, ts * 2, n}; };
+  if (hq) c.read(heads(a->q, a->q_token_stride, hq, a->q_head_stride));
+  const int qi = c.ni;
+  if (hk) c.read(heads(a->k, a->k_token_stride, hk, a->k_head_stride));
+  const int ki = c.ni;
+  if (cache) c.read(heads(a->v, a->v_token_stride, hk, a->v_head_stride));
+  if (hq) c.read(flat(a->q_weight, d * 2));
+  if (hk) c.read(flat(a->k_weight, d * 2));
+  if (half) {
+    const int64_t ps = a->position_stride ? a->position_stride : n;
+    c.read({a->positions, n * 4, ps * 4, a->axes});
+    c.read(flat(a->inv_freq, half * 4));
+  }
+  if (cache) c.read(flat(a->slots, n * 8));
+  if (hq) {
+    if (a->q_out == a->q && a->q_out_token_stride == a->q_token_stride && a->q_out_head_stride == a->q_head_stride) alias[c.no] = qi;
+    c.write(heads(a->q_out, a->q_out_token_stride, hq, a->q_out_head_stride));
+  }
+  if (k_out) {
+    if (a->k_out == a->k && a->k_out_token_stride == a->k_token_stride && a->k_out_head_stride == a->k_head_stride) alias[c.no] = ki;
+    c.write(heads(a->k_out, a->k_out_token_stride, hk, a->k_out_head_stride));
+  }
+  if (cache && a->num_blocks) {
+    const int64_t pg = a->page_size;
+    c.write({a->k_cache, span3(pg, a->k_page_stride, hk, a->k_cache_head_stride, d) * 2, a->k_block_stride * 2, a->num_blocks});
+    c.write({a->v_cache, span3(pg, a->v_page_stride, hk, a->v_cache_head_stride, d) * 2, a->v_block_stride * 2, a->num_blocks});
+  }
+  if (!c.ok(alias)) return AR_ERR_OVERLAP;
+  if (!ctx) return AR_ERR_NOT_INITIALIZED;
+
+  ar::RopeParams p;
+  memset(&p, 0, sizeof(p));
+  p.tokens = n;
+  p.head_dim = a->head_dim;
+  p.q = {a->q, hq ? a->q_out : nullptr, a->q_token_stride, a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride, a->q_weight, a->q_heads};
+  p.k = {a->k, k_out ? a->k_out : nullptr, a->k_token_stride, a->k_head_stride, a->k_out_token_stride, a->k_out_head_stride, a->k_weight, a->kv_heads};
+  p.v = a->v;
+  p.v_ts = a->v_token_stride;
+  p.v_hs = a->v_head_stride;
+  p.eps = a->eps;
+  p.inv_dim = (float)(1.0 / (double)d);
+  p.gemma = a->gemma != 0;
+  p.half = half;
+  p.pairs = a->pairs != 0;
+  p.axes = half ? a->axes : 1;
+  p.dealt = a->dealt != 0;
+  for (int i = 0; i < AR_MAX_ROPE_AXES; ++i) p.sections[i] = i < p.axes ? a->sections[i] : 0;
+  p.positions = a->positions;
+  p.pos_stride = a->position_stride ? a->position_stride : n;
+  p.inv_freq = a->inv_freq;
+  p.k_cache = a->k_cache;
+  p.v_cache = a->v_cache;
+  p.kc_bs = a->k_block_stride;
+  p.kc_ps = a->k_page_stride;
+  p.kc_hs = a->k_cache_head_stride;
+  p.vc_bs = a->v_block_stride;
+  p.vc_ps = a->v_page_stride;
+  p.vc_hs = a->v_cache_head_stride;
+  p.page = cache ? a->page_size : 1;
+  p.num_slots = cache ? a->num_blocks * a->page_size : 0;
+  p.slots = a->slots;
+  p.status = ctx->d_status;
+  const int64_t warps = n * (hq + hk * (cache ? 2 : 1));
+  int64_t grid = (warps + 7) / 8;
+  if (grid > ctx->sm_count * 8) grid = ctx->sm_count * 8;
+  DeviceGuard g(ctx->device);
+  void* args[1] = {&p};
+  const ar_status st = launch(ctx, ar::rope_kernel(a->dtype == AR_DTYPE_BF16, false), (unsigned)grid, 256, 1, args, 0, stream);
+  if (st == AR_OK) ctx->last_variant = "qk_norm_rope_scalar";
+  return st;
+}
+
+}  // extern "C"
+
+namespace {
+
+int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+constexpr int kMmaRows = 64;
+
+struct Workspace {
+  int64_t ml, o, bytes;  // offsets of the statistics and the sums behind the headers
+};
+
+Workspace workspace_of(int64_t spans, int64_t rows, int64_t part_dim) {
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  Workspace w;
+  w.ml = up(spans * 2 * 8 * 4);
+  w.o = w.ml + up(spans * 2 * rows * 8);
+  w.bytes = w.o + up(spans * 2 * rows * part_dim * 4);
+  return w;
+}
+
+int mma_spans(const ar_ctx* ctx, bool bf16, int dp) {
+  return ctx->sm_count * ctx->attn_mma_per_sm[bf16][dp == 64 ? 0 : dp == 128 ? 1 : 2];
+}
+
+int part_dim(int d) { return (d + 3) / 4 * 4; }
+
+int64_t workspace_need(const ar_ctx* ctx, bool bf16, int d) {
+  return workspace_of(mma_spans(ctx, bf16, padded_dim(d)), kMmaRows, part_dim(d)).bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_args* a, size_t* bytes) {
+  if (!a || !bytes || a->head_dim < 1 || a->head_dim > AR_MAX_HEAD_DIM || (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
+    return AR_ERR_INVALID_ARG;
+  if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  *bytes = (size_t)workspace_need(ctx, a->dtype == AR_DTYPE_BF16, a->head_dim);
+  return AR_OK;
+}
+
+ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void* stream) {
+  if (!a) return AR_ERR_INVALID_ARG;
+  if (a->tokens < 0 || a->requests < 0 || a->requests > AR_MAX_REQUESTS || a->q_heads < 1 || a->kv_heads < 1 || a->q_heads % a->kv_heads ||
+      a->q_heads > 65536 || a->head_dim < 1 || a->head_dim > AR_MAX_HEAD_DIM || (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
+    return AR_ERR_INVALID_ARG;
+  if (!isfinite(a->scale) || !isfinite(a->softcap) || a->softcap < 0.0f || a->window < 0) return AR_ERR_INVALID_ARG;
+  if (a->page_size < 1 || a->page_size > 65536 || a->num_blocks < 0 || a->num_blocks > ((int64_t)1 << 40) / a->page_size || a->table_cols < 0 ||
+      a->table_cols > 0x7fffffff || a->table_stride < 0 || (a->table_stride && a->table_stride < a->table_cols) ||
+      a->table_stride > ((int64_t)1 << 40))
+    return AR_ERR_INVALID_ARG;
+  const int64_t n = a->tokens, d = a->head_dim, hq = a->q_heads, hk = a->kv_heads, r = a->requests, pg = a->page_size;
+  if (n > kMaxRows || n * (hq / hk) > kMaxRows) return AR_ERR_UNSUPPORTED;
+  if (n == 0 || r == 0) {
+    if (!ctx) return AR_ERR_NOT_INITIALIZED;
+    ctx->last_variant = "none";
+    return AR_OK;
+  }
+  if (!a->q || !a->out || !a->cu_q || !a->seq_lens || (a->table_cols && !a->block_table) || (a->num_blocks && (!a->k_cache || !a->v_cache)) ||
+      !a->workspace)
+    return AR_ERR_INVALID_ARG;
+  if (!strides_ok(n, a->q_token_stride, hq, a->q_head_stride, d) || !strides_ok(n, a->out_token_stride, hq, a->out_head_stride, d) ||
+      !strides_ok(a->num_blocks, a->k_block_stride, pg, a->k_page_stride, d) || !strides_ok(a->num_blocks, a->v_block_stride, pg, a->v_page_stride, d) ||
+      !strides_ok(1, 0, hk, a->k_head_stride, d) || !strides_ok(1, 0, hk, a->v_head_stride, d))
+    return AR_ERR_INVALID_ARG;
+  if (!aligned(a->q, 2) || !aligned(a->out, 2) || !aligned(a->lse, 4) || !aligned(a->k_cache, 2) || !aligned(a->v_cache, 2) ||
+      !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) || !aligned(a->seq_lens, 4) || !aligned(a->slopes, 4) ||
+      !aligned(a->prefix_lens, 4) || !aligned(a->workspace, 16))
+    return AR_ERR_ALIGNMENT;
+  const int64_t ts = a->table_stride ? a->table_stride : a->table_cols;
+  Checker c;
+  c.read({a->q, ((hq - 1) * a->q_head_stride + d) * 2, a->q_token_stride * 2, n});
+  c.read({a->k_cache, span3(pg, a->k_page_stride, hk, a->k_head_stride, d) * 2, a->k_block_stride * 2, a->num_blocks});
+  c.read({a->v_cache, span3(pg, a->v_page_stride, hk, a->v_head_stride, d) * 2, a->v_block_stride * 2, a->num_blocks});
+  c.read({a->block_table, a->table_cols * 4, ts * 4, r});
+  c.read(flat(a->cu_q, (r + 1) * 4));
+  c.read(flat(a->seq_lens, r * 4));
+  c.read(flat(a->slopes, hq * 4));
+  c.read(flat(a->prefix_lens, r * 4));
+  c.write({a->out, ((hq - 1) * a->out_head_stride + d) * 2, a->out_token_stride * 2, n});
+  c.write(flat(a->lse, n * hq * 4));
+  c.write(flat(a->workspace, (int64_t)a->workspace_bytes));
+  if (!c.ok()) return AR_ERR_OVERLAP;
+  if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  const bool bf16 = a->dtype == AR_DTYPE_BF16;
+  if ((int64_t)a->workspace_bytes < workspace_need(ctx, bf16, a->head_dim)) return AR_ERR_INVALID_ARG;
+
+  ar::AttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.tokens = n;
+  p.requests = a->requests;
+  p.q_heads = a->q_heads;
+  p.kv_heads = a->kv_heads;
+  p.group = a->q_heads / a->kv_heads;
+  p.head_dim = a->head_dim;
+  p.q = a->q;
+  p.out = a->out;
+  p.q_ts = a->q_token_stride;
+  p.q_hs = a->q_head_stride;
+  p.o_ts = a->out_token_stride;
+  p.o_hs = a->out_head_stride;
+  p.lse = a->lse;
+  p.k = a->k_cache;
+  p.v = a->v_cache;
+  p.k_bs = a->k_block_stride;
+  p.k_ps = a->k_page_stride;
+  p.k_hs = a->k_head_stride;
+  p.v_bs = a->v_block_stride;
+  p.v_ps = a->v_page_stride;
+  p.v_hs = a->v_head_stride;
+  p.num_blocks = a->num_blocks;
+  p.page = a->page_size;
+  p.table = a->block_table;
+  p.table_stride = ts;
+  const int64_t room = a->table_cols * pg;
+  p.max_len = (int)(room < kMaxRows ? room : kMaxRows);
+  p.cu_q = a->cu_q;
+  p.seq_lens = a->seq_lens;
+  p.causal = a->causal != 0;
+  p.window = a->window >= kMaxRows ? 0 : a->window;  // no length reaches it
+  const double log2e = 1.4426950408889634;
+  p.cap_log2 = (float)(a->softcap * log2e);
+  p.scale_log2 = (float)(a->softcap > 0.0f ? (double)a->scale / a->softcap : a->scale * log2e);
+  p.slopes = a->slopes;
+  p.prefix = a->prefix_lens;
+  auto eight = [](int64_t x) { return x % 8 == 0; };
+  p.vec = eight(d) && eight(a->q_token_stride) && eight(a->q_head_stride) && eight(a->out_token_stride) && eight(a->out_head_stride) &&
+          eight(a->k_block_stride) && eight(a->k_page_stride) && eight(a->k_head_stride) && eight(a->v_block_stride) &&
+          eight(a->v_page_stride) && eight(a->v_head_stride) && aligned(a->q, 16) && aligned(a->out, 16) && aligned(a->k_cache, 16) &&
+          aligned(a->v_cache, 16) && ctx->force_variant != 4;
+  p.status = ctx->d_status;
+  p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
+
+  const int dp = padded_dim(a->head_dim);
+  p.spans = mma_spans(ctx, bf16, dp);
+  p.tile_rows = kMmaRows;
+  p.part_dim = part_dim(a->head_dim);
+  const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
+  char* base = static_cast<char*>(a->workspace);
+  p.headers = reinterpret_cast<int*>(base);
+  p.part_ml = reinterpret_cast<float*>(base + w.ml);
+  p.part_o = reinterpret_cast<float*>(base + w.o);
+  DeviceGuard g(ctx->device);
+  void* args[1] = {&p};
+  ar_status st = launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
+  if (st != AR_OK) return st;
+  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, (unsigned)(p.tile_rows / 8)), 128, 1, args, 0, stream);
+  if (st == AR_OK) ctx->last_variant = "paged_attention_mma";
+  return st;
+}
+
+}  // extern "C"
+
+namespace ar {
+
+cudaError_t serve_prepare(ar_ctx* ctx) {
+  cudaError_t e = cudaSuccess;
+  cudaFuncAttributes fa;
+  auto keep = [&](cudaError_t x) {
+    if (e == cudaSuccess) e = x;
+  };
+  keep(cudaFuncGetAttributes(&fa, plan_kernel()));
+  keep(cudaFuncSetAttribute(plan_kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, AR_MAX_REQUESTS * 8));
+  for (int b = 0; b < 2; ++b) {
+    for (int v = 0; v < 2; ++v) keep(cudaFuncGetAttributes(&fa, rope_kernel(b, v)));
+    keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
+    for (int i = 0; i < 3; ++i) {
+      const int dp = 64 << i;
+      const void* f = attn_mma_kernel(b, dp);
+      keep(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_mma_smem(dp)));
+      keep(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctx->attn_mma_per_sm[b][i], f, 128, attn_mma_smem(dp)));
+      if (ctx->attn_mma_per_sm[b][i] < 1) ctx->attn_mma_per_sm[b][i] = 1;
+    }
+  }
+  return e;
+}
+
+}  // namespace ar
