@@ -129,7 +129,9 @@ __device__ void find_span(const AttnParams& p, SpanShared& sh) {
   };
   for (int base = 0; base < p.requests; base += THREADS) scan(base);
   const long long total = before;
-  const long long s0 = total * blockIdx.x / gridDim.x, s1 = total * (blockIdx.x + 1) / gridDim.x;
+  // spans with tiles stand side by side: with fewer tiles than CTAs the first ones take one each
+  auto start = [&](long long b) { return total >= gridDim.x ? total * b / gridDim.x : min(b, total); };
+  const long long s0 = start(blockIdx.x), s1 = start(blockIdx.x + 1);
   if (threadIdx.x == 0) {
     sh.tiles = s1 - s0;
     sh.at = {0, 0, 0, 0};
