@@ -246,13 +246,30 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   p.num_slots = cache ? a->num_blocks * a->page_size : 0;
   p.slots = a->slots;
   p.status = ctx->d_status;
-  const int64_t warps = n * (hq + hk * (cache ? 2 : 1));
-  int64_t grid = (warps + 7) / 8;
-  if (grid > ctx->sm_count * 8) grid = ctx->sm_count * 8;
+  // the vector form: every row on a 16-byte boundary
+  auto row = [](const void* q, int64_t ts, int64_t hs) { return aligned(q, 16) && ts % 8 == 0 && hs % 8 == 0; };
+  bool vec = d % 8 == 0 && ctx->force_variant != 4;
+  if (hq) vec = vec && row(a->q, a->q_token_stride, a->q_head_stride) && row(a->q_out, a->q_out_token_stride, a->q_out_head_stride) && aligned(a->q_weight, 16);
+  if (hk) vec = vec && row(a->k, a->k_token_stride, a->k_head_stride) && aligned(a->k_weight, 16);
+  if (k_out) vec = vec && row(a->k_out, a->k_out_token_stride, a->k_out_head_stride);
+  if (cache)
+    vec = vec && row(a->v, a->v_token_stride, a->v_head_stride) && row(a->k_cache, a->k_page_stride, a->k_cache_head_stride) &&
+          row(a->v_cache, a->v_page_stride, a->v_cache_head_stride) && a->k_block_stride % 8 == 0 && a->v_block_stride % 8 == 0;
+  const bool bf16 = a->dtype == AR_DTYPE_BF16;
   DeviceGuard g(ctx->device);
-  void* args[1] = {&p};
-  const ar_status st = launch(ctx, ar::rope_kernel(a->dtype == AR_DTYPE_BF16, false), (unsigned)grid, 256, 1, args, 0, stream);
-  if (st == AR_OK) ctx->last_variant = "qk_norm_rope_scalar";
+  ar_status st;
+  if (vec) {
+    ar::RopeGrid rg = ar::rope_vec_grid(p, ctx->sm_count);
+    void* args[3] = {&p, &rg.step, &rg.split};
+    st = launch(ctx, ar::rope_vec_kernel(bf16, p.head_dim, half, p.pairs), rg.ctas, 256, 1, args, 0, stream);
+  } else {
+    const int64_t warps = n * (hq + hk * (cache ? 2 : 1));
+    int64_t grid = (warps + 7) / 8;
+    if (grid > ctx->sm_count * 8) grid = ctx->sm_count * 8;
+    void* args[1] = {&p};
+    st = launch(ctx, ar::rope_scalar_kernel(bf16), (unsigned)grid, 256, 1, args, 0, stream);
+  }
+  if (st == AR_OK) ctx->last_variant = vec ? "qk_norm_rope_vec" : "qk_norm_rope_scalar";
   return st;
 }
 
@@ -422,7 +439,9 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
   keep(cudaFuncGetAttributes(&fa, plan_kernel()));
   keep(cudaFuncSetAttribute(plan_kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, AR_MAX_REQUESTS * 8));
   for (int b = 0; b < 2; ++b) {
-    for (int v = 0; v < 2; ++v) keep(cudaFuncGetAttributes(&fa, rope_kernel(b, v)));
+    keep(cudaFuncGetAttributes(&fa, rope_scalar_kernel(b)));
+    for (int d = 64; d <= 256; d *= 2)
+      for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0)));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int i = 0; i < 3; ++i) {
       const int dp = 64 << i;

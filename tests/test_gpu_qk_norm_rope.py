@@ -210,6 +210,38 @@ def test_tiny_and_huge_values(ctx):
     check(ctx, x)
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("d, rot", [(128, 64), (80, 40), (33, 32)])
+def test_an_infinity_stays_in_its_pair(ctx, pairs, d, rot):
+    """Without a norm an infinity reaches its own pair only; an element that does not turn keeps it."""
+    x = make(9, 2, 1, d, "bf16", rot, norm=False)
+    x["q"][3, 1, rot:] = float("inf")
+    x["q"][4, 0, 5] = float("inf")
+    g = on_gpu(x)
+    qo = ctx.qk_norm_rope(g["q"], None, None, g["pos"][0], g["freq"], pairs=pairs)[0].cpu()
+    other = 4 if pairs else 5 + rot // 2
+    bad = ~torch.isfinite(qo)
+    want = torch.zeros_like(bad)
+    want[3, 1, rot:] = True
+    want[4, 0, 5] = want[4, 0, other] = True
+    assert torch.equal(bad, want) and (qo[3, 1, rot:] == float("inf")).all()
+
+
+@pytest.mark.parametrize("hq, hk, d", [(48, 8, 128), (5, 3, 64), (9, 2, 256), (16, 16, 80)])
+def test_both_forms_agree(ctx, hq, hk, d):
+    """The vector form and the general one, each within the bound, at sizes that share heads and tokens differently."""
+    import tensor_all_reduce_gb300 as tar
+    for tokens in (1, 3, 160, 1900):
+        x = make(tokens, hq, hk, d, "bf16", d, seed=tokens)
+        for option, name in ((0, "qk_norm_rope_vec"), (4, "qk_norm_rope_scalar")):
+            ctx.set_option(tar.AR_OPT_FORCE_VARIANT, option)
+            try:
+                check(ctx, x)
+                assert ctx.last_variant == name
+            finally:
+                ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 0)
+
+
 def test_streams_and_graph(ctx):
     x = on_gpu(make(50, 4, 2, 128, "bf16", 128))
     s = torch.cuda.Stream()
