@@ -446,7 +446,8 @@ const char* ar_last_variant(const ar_ctx* ctx);
 /* Tuning and test overrides (0 = automatic for each, except AR_OPT_PDL).  Values outside
  * the documented range return AR_ERR_INVALID_ARG. */
 typedef enum {
-  AR_OPT_FORCE_VARIANT = 0,  /* 0 auto, 1 row, 2 cluster, 3 staged, 4 scalar (tail) */
+  AR_OPT_FORCE_VARIANT = 0,  /* 0 auto, 1 row, 2 cluster, 3 staged, 4 scalar (tail); the attention
+                                block's calls know 0 and 4 (their general forms), others count as 0 */
   AR_OPT_CLUSTER_SIZE = 1,   /* 0 auto, else 1, 2, 4, 8 or 16 CTAs per row (with
                                 AR_OPT_FORCE_VARIANT = 3 and 2..8: the staged cluster form) */
   AR_OPT_PACKS_PER_THREAD = 2, /* 0 auto, else 1, 2 or 4 16-byte packs per thread (1 or 2 in
@@ -460,7 +461,8 @@ typedef enum {
                                 complete before it reads memory); 0: ordinary stream order */
   AR_OPT_WAIT_CYCLES = 6,    /* bound of one staged-kernel wait in SM clock cycles (1e3..8e9);
                                 0 (the default): 2e9, about a second */
-  AR_OPT_TEST_STALL = 7,     /* test hook, 0 (the default) or 1: the staged kernels arm each CTA's
+  AR_OPT_TEST_STALL = 7,     /* test hook, 0 (the default) or 1: the staged kernels, and the tensor-core
+                                attention kernel, arm each CTA's
                                 first stage without issuing its copies, so that wait runs out and
                                 the call ends early with code 1 in the status word (exercises the
                                 failure path; outputs are then incomplete) */

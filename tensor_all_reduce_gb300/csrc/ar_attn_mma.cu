@@ -221,10 +221,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
       if (!wrote[s]) write_header(p, s, 0, nullptr);
 }
 
-// Joins the parts of the items that more than one span holds: block (c, y) serves rows
-// [8 y, 8 y + 8) of the item that begins in span c and does not end there.
+// Joins the parts of the items that more than one span holds: block (c, y) serves, a warp a row,
+// every gridDim.y-th group of 8 rows of the item that begins in span c and does not end there.
 template <int DT>
-__global__ void __launch_bounds__(128) attn_combine(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ AttnParams p) {
   __shared__ int sh_end;
   pdl_wait_and_release();
   const int c = blockIdx.x;
@@ -232,10 +232,11 @@ __global__ void __launch_bounds__(128) attn_combine(const __grid_constant__ Attn
   if (!(h[0] & kThere)) return;
   const int q0 = h[1], rows = h[2], qt = h[3], head0 = h[4] * p.group;
   const int row_base = qt * p.tile_rows;
-  if (row_base + (int)blockIdx.y * 8 >= rows) return;
+  const int local_rows = min(rows - row_base, p.tile_rows);
+  if ((int)blockIdx.y * 8 >= local_rows) return;
   if (threadIdx.x == 0) sh_end = p.spans;
   __syncthreads();
-  for (int i = c + 1 + (int)threadIdx.x; i < p.spans; i += 128)
+  for (int i = c + 1 + (int)threadIdx.x; i < p.spans; i += 256)
     if (p.headers[(int64_t)i * 2 * kHeaderInts] & kEnds) {
       atomicMin(&sh_end, i);
       break;
@@ -244,9 +245,8 @@ __global__ void __launch_bounds__(128) attn_combine(const __grid_constant__ Attn
   const int end = min(sh_end, p.spans - 1);  // the chain: slot 1 of span c, slot 0 of spans c + 1 .. end
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto place = [&](int i, int local) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.tile_rows + local; };
-  for (int k = 0; k < 2; ++k) {
-    const int local = blockIdx.y * 8 + warp * 2 + k, row = row_base + local;
-    if (row >= rows) continue;
+  for (int local = blockIdx.y * 8 + warp; local < local_rows; local += gridDim.y * 8) {
+    const int row = row_base + local;
     float top = -INFINITY;
     for (int i = c + lane; i <= end; i += 32) top = fmaxf(top, p.part_ml[place(i, local) * 2]);
 #pragma unroll

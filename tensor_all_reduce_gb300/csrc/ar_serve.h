@@ -2,6 +2,7 @@
 // with rotation, paged attention), shared by their kernels and the C ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -85,6 +86,9 @@ struct AttnParams {
   float* part_o;
   float* part_ml;
   int* status;
+  // the tensor-core form
+  int box_rows;  // keys of one copy: the largest power of two, at most 128, that divides the page
+  int stall;     // test hook: the first copy is not issued, so that its wait runs out
   long long wait_cycles;
 };
 
@@ -103,6 +107,14 @@ const void* attn_combine_kernel(bool bf16);
 // Dynamic shared memory of the general attention kernel: 64 query rows, keys and values each,
 // padded by 16 bytes.
 inline size_t attn_mma_smem(int padded_dim) { return (size_t)3 * 64 * (padded_dim + 8) * 2; }
+
+const void* attn_tma_kernel(bool bf16, int padded_dim, bool ext);  // padded_dim 64 or 128; ext: cap, bias or a scale that is not positive
+size_t attn_tma_smem(int padded_dim);
+
+// Tensor map of a cache [blocks, page, heads, dim] (strides in elements) with boxes of box_rows
+// tokens by 64 elements; `encode` is the driver's cuTensorMapEncodeTiled.
+bool attn_tensor_map(void* encode, CUtensorMap* map, const void* base, bool bf16, int64_t dim, int64_t page, int64_t heads, int64_t blocks,
+                     int64_t page_stride, int64_t head_stride, int64_t block_stride, int box_rows);
 
 // Function attributes, module loading and occupancies for all of the above, once per context.
 cudaError_t serve_prepare(ar_ctx* ctx);

@@ -279,7 +279,7 @@ namespace {
 
 int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-constexpr int kMmaRows = 64;
+constexpr int kMmaRows = 64, kTmaRows = 256;
 
 struct Workspace {
   int64_t ml, o, bytes;  // offsets of the statistics and the sums behind the headers
@@ -301,7 +301,9 @@ int mma_spans(const ar_ctx* ctx, bool bf16, int dp) {
 int part_dim(int d) { return (d + 3) / 4 * 4; }
 
 int64_t workspace_need(const ar_ctx* ctx, bool bf16, int d) {
-  return workspace_of(mma_spans(ctx, bf16, padded_dim(d)), kMmaRows, part_dim(d)).bytes;
+  const int64_t general = workspace_of(mma_spans(ctx, bf16, padded_dim(d)), kMmaRows, part_dim(d)).bytes;
+  const int64_t tma = workspace_of(ctx->sm_count, kTmaRows, part_dim(d)).bytes;
+  return d <= 128 && tma > general ? tma : general;
 }
 
 }  // namespace
@@ -408,9 +410,23 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.status = ctx->d_status;
   p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
 
+  // The tensor-core form takes aligned rows of up to 128 elements and pages that whole groups of
+  // 8 keys (the swizzle's period) fill; the general form the rest.
   const int dp = padded_dim(a->head_dim);
-  p.spans = mma_spans(ctx, bf16, dp);
-  p.tile_rows = kMmaRows;
+  int box = 1;
+  while (box < 128 && pg % (box * 2) == 0) box *= 2;
+  bool tma = p.vec && dp <= 128 && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
+  CUtensorMap kmap, vmap;
+  if (tma) {
+    p.box_rows = box;
+    p.stall = ctx->test_stall;
+    tma = ar::attn_tensor_map(ctx->encode_tensor_map, &kmap, a->k_cache, bf16, d, pg, hk, a->num_blocks, a->k_page_stride, a->k_head_stride,
+                              a->k_block_stride, box) &&
+          ar::attn_tensor_map(ctx->encode_tensor_map, &vmap, a->v_cache, bf16, d, pg, hk, a->num_blocks, a->v_page_stride, a->v_head_stride,
+                              a->v_block_stride, box);
+  }
+  p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp);
+  p.tile_rows = tma ? kTmaRows : kMmaRows;
   p.part_dim = part_dim(a->head_dim);
   const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
   char* base = static_cast<char*>(a->workspace);
@@ -418,11 +434,13 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.part_ml = reinterpret_cast<float*>(base + w.ml);
   p.part_o = reinterpret_cast<float*>(base + w.o);
   DeviceGuard g(ctx->device);
-  void* args[1] = {&p};
-  ar_status st = launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
+  void* args[3] = {&p, &kmap, &vmap};
+  const bool ext = a->softcap > 0.0f || a->slopes || !(a->scale > 0.0f);
+  ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, ext), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
+                     : launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
-  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, (unsigned)(p.tile_rows / 8)), 128, 1, args, 0, stream);
-  if (st == AR_OK) ctx->last_variant = "paged_attention_mma";
+  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, 4), 256, 1, args, 0, stream);
+  if (st == AR_OK) ctx->last_variant = tma ? "paged_attention_tma" : "paged_attention_mma";
   return st;
 }
 
@@ -443,6 +461,9 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
     for (int d = 64; d <= 256; d *= 2)
       for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0)));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
+    for (int i = 0; i < 2; ++i)
+      for (int ext = 0; ext < 2; ++ext)
+        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, ext), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
     for (int i = 0; i < 3; ++i) {
       const int dp = 64 << i;
       const void* f = attn_mma_kernel(b, dp);
@@ -451,6 +472,9 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
       if (ctx->attn_mma_per_sm[b][i] < 1) ctx->attn_mma_per_sm[b][i] = 1;
     }
   }
+  cudaDriverEntryPointQueryResult found;
+  keep(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ctx->encode_tensor_map, 12000, cudaEnableDefault, &found));
+  if (e == cudaSuccess && found != cudaDriverEntryPointSuccess) e = cudaErrorSymbolNotFound;
   return e;
 }
 

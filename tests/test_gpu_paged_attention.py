@@ -299,6 +299,34 @@ def test_offsets_beyond_32_bits(ctx, form):
     assert ((out.cpu().double() - wo).abs() <= eo).all()
 
 
+def test_a_wait_that_runs_out_ends_the_call(ctx):
+    """The first copy of each CTA is held back: the call ends with code 1, and the next one is right."""
+    import tensor_all_reduce_gb300 as tar
+    x = make([40, 1], [500, 3000], 4, 2, 128, seed=17, garbage=0.0)
+    ctx.set_option(tar.AR_OPT_TEST_STALL, 1)
+    ctx.set_option(tar.AR_OPT_WAIT_CYCLES, 2000000)
+    try:
+        run(ctx, x)
+        assert ctx.last_variant == "paged_attention_tma"
+        assert ctx.device_status() == 1
+    finally:
+        ctx.set_option(tar.AR_OPT_TEST_STALL, 0)
+        ctx.set_option(tar.AR_OPT_WAIT_CYCLES, 0)
+    check(ctx, x)
+
+
+def test_forms(ctx):
+    """Which form serves which call."""
+    import tensor_all_reduce_gb300 as tar
+    for d, page, want in ((128, 16, "tma"), (64, 128, "tma"), (80, 24, "tma"), (128, 4, "mma"), (36, 16, "mma"), (256, 16, "mma")):
+        check(ctx, make([3], [50], 4, 2, d, page=page))
+        assert ctx.last_variant == "paged_attention_" + want
+    ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 4)
+    check(ctx, make([3], [50], 4, 2, 128))
+    assert ctx.last_variant == "paged_attention_mma"
+    ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 0)
+
+
 def test_binding_refuses(ctx):
     x = make([2], [20], 4, 2, 64)
     q, kc, vc, t, cu, lens = x["q"].cuda(), x["kc"].cuda(), x["vc"].cuda(), i32(x["table"]), i32(x["cu"]), i32(x["lens"])
