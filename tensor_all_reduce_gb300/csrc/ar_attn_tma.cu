@@ -108,6 +108,13 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -217,20 +224,24 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
   const int lane = threadIdx.x & 31;
   const int ksteps = (p.head_dim + 15) / 16;
   const uint32_t idesc_s = instr_desc<DT>(kKeys, false), idesc_o = instr_desc<DT>(ksteps * 16, true);
+  // descriptors differ in the address alone, in units of 16 bytes: constant offsets are added
+  const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(ring, 16), v_desc = matrix_desc(ring, S::kBlockBytes);
   auto scores = [&](int h, uint32_t slot) {  // queries of half h times the keys in `slot`
-    const uint32_t a = queries + h * S::kTileBytes, k = ring + slot * S::kTileBytes;
-    for (int i = 0; i < ksteps; ++i) {
-      const uint32_t off = (i >> 2) * S::kBlockBytes + (i & 3) * 32;
-      mma_ss(tmem + h * 128, matrix_desc(a + off, 16), matrix_desc(k + off, 16), idesc_s, i > 0);
+    const uint64_t a = q_desc + h * (S::kTileBytes >> 4), k = k_desc + slot * (S::kTileBytes >> 4);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const uint64_t off = ((i >> 2) * S::kBlockBytes + (i & 3) * 32) >> 4;
+      if (i < ksteps) mma_ss(tmem + h * 128, a + off, k + off, idesc_s, i > 0);
     }
     mma_commit(&b.s[h]);
   };
   auto weighted = [&](int h, uint32_t slot, bool more) {  // weights of half h times the values in `slot`
-    const uint32_t v = ring + slot * S::kTileBytes;
+    const uint64_t v = v_desc + slot * (S::kTileBytes >> 4);
 #pragma unroll
     for (int i = 0; i < kKeys / 16; ++i)
-      mma_ts(tmem + 256 + h * 128, tmem + h * 128 + i * 8, matrix_desc(v + i * 16 * 128, S::kBlockBytes), idesc_o, more || i > 0);
+      mma_ts(tmem + 256 + h * 128, tmem + h * 128 + i * 8, v + ((i * 16 * 128) >> 4), idesc_o, more || i > 0);
   };
+  const bool one = elect_one();
   Steps walk(p, span);
   Item it;
   uint32_t n = 0, items[2] = {0, 0}, tiles[2] = {0, 0};
@@ -246,10 +257,10 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
     if (!wait(&b.full[slot], (n / S::kSlots) & 1)) break;
     for (int h = 0; h < nh; ++h) {
       if (!wait(&b.q[h], items[h]++ & 1)) break;
-      if (lane == 0) scores(h, slot);
+      if (one) scores(h, slot);
     }
     if (!ok) break;
-    if (lane == 0) mma_commit(&b.empty[slot]);
+    if (one) mma_commit(&b.empty[slot]);
     ++n;
     for (int i = 0; ok && i < nt; ++i) {
       const uint32_t vs = n % S::kSlots, ks = (n + 1) % S::kSlots;
@@ -270,16 +281,16 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
       }
       for (int h = 0; h < nh; ++h) {
         if (!wait(&b.p[h], tiles[h]++ & 1)) break;
-        if (lane == 0) weighted(h, vs, i > 0);
+        if (one) weighted(h, vs, i > 0);
         if (more) {
           if (h == 0 && !wait(&b.full[ks], ((n + 1) / S::kSlots) & 1)) break;
-          if (lane == 0) scores(h, ks);
-        } else if (lane == 0) {
+          if (one) scores(h, ks);
+        } else if (one) {
           mma_commit(&b.o[h]);
         }
       }
       if (!ok) break;
-      if (lane == 0) {
+      if (one) {
         mma_commit(&b.empty[vs]);
         if (more) mma_commit(&b.empty[ks]);
       }
@@ -287,7 +298,7 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
     }
   }
   if (!ok) {  // matrix instructions in flight end before tensor memory is freed
-    if (lane == 0) mma_commit(&b.drain);
+    if (one) mma_commit(&b.drain);
     mbar_wait_bounded(&b.drain, 0, p.wait_cycles);
   }
 }
