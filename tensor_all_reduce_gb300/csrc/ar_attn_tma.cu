@@ -303,24 +303,43 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
   }
 }
 
-// Scores of a row in log2 units over the tile's 128 keys, masked.
-template <bool EXT>
-__device__ __forceinline__ void shape_scores(const AttnParams& p, const Item& it, const RowView& v, int key0, float (&s)[kKeys]) {
-  if constexpr (EXT) {
-#pragma unroll
-    for (int j = 0; j < kKeys; ++j) s[j] = visible(it, v, key0 + j) ? bend(p, v, s[j], key0 + j) : -INFINITY;
-  } else {
-    // the whole warp sees the whole tile: nothing to do
-    const bool all = (key0 + kKeys <= v.see_hi && key0 >= v.see_lo) || key0 + kKeys <= it.q.prefix;
-    if (__all_sync(0xffffffffu, all)) return;
-    const int hi = v.see_hi - key0, lo = v.see_lo - key0, pre = it.q.prefix - key0;
-#pragma unroll
-    for (int j = 0; j < kKeys; ++j)
-      if (!(j < pre || (j < hi && j >= lo))) s[j] = -INFINITY;
-  }
+// How scores are bent, a bit each: kCap (tanh), kBias (distance; also any scale that is not positive,
+// since the plain form scales after the maximum).
+enum { kCap = 1, kBias = 2 };
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <int DT, int DP, bool EXT>
+// A row's products over the tile's 128 keys to scores, masked: in log2 units where they are
+// bent, else as they are (the caller scales).
+template <int EXT>
+__device__ __forceinline__ void shape_scores(const AttnParams& p, const Item& it, const RowView& v, int key0, float (&s)[kKeys]) {
+  if constexpr (EXT & kCap) {
+    // c tanh(x) = c - 2 c / (1 + e^2x): one exponential and one reciprocal an element, absolute
+    // error 2^-22 c; an exponential that overflows gives c
+    const float twice = p.scale_log2 * 2.8853900817779268f, c = p.cap_log2;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
+  }
+  if constexpr (EXT & kBias) {
+    const float scale = EXT & kCap ? 1.0f : p.scale_log2;
+    const float far = (float)(v.pos - key0);
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) s[j] = fmaf(-v.slope, fabsf(far - (float)j), s[j] * scale);
+  }
+  // the whole warp sees the whole tile: nothing to mask
+  const bool all = (key0 + kKeys <= v.see_hi && key0 >= v.see_lo) || key0 + kKeys <= it.q.prefix;
+  if (__all_sync(0xffffffffu, all)) return;
+  const int hi = v.see_hi - key0, lo = v.see_lo - key0, pre = it.q.prefix - key0;
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j)
+    if (!(j < pre || (j < hi && j >= lo))) s[j] = -INFINITY;
+}
+
+template <int DT, int DP, int EXT>
 __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& b, uint8_t* queries, uint32_t tmem, bool (&wrote)[2]) {
   using S = Shape<DP>;
   const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5;
@@ -474,7 +493,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
   }
 }
 
-template <int DT, int DP, bool EXT>
+template <int DT, int DP, int EXT>
 __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                                                         const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<DP>;
@@ -532,15 +551,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+template <int DT, int DP>
+const void* tma_of(int ext) {
+  switch (ext) {
+    case 0: return reinterpret_cast<const void*>(&attn_tma<DT, DP, 0>);
+    case kCap: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kCap>);
+    case kBias: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kBias>);
+    default: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kCap | kBias>);
+  }
+}
+
 template <int DT>
-const void* tma_of(int dp, bool ext) {
-  if (dp == 64) return ext ? reinterpret_cast<const void*>(&attn_tma<DT, 64, true>) : reinterpret_cast<const void*>(&attn_tma<DT, 64, false>);
-  return ext ? reinterpret_cast<const void*>(&attn_tma<DT, 128, true>) : reinterpret_cast<const void*>(&attn_tma<DT, 128, false>);
+const void* tma_of(int dp, int ext) {
+  return dp == 64 ? tma_of<DT, 64>(ext) : tma_of<DT, 128>(ext);
 }
 
 }  // namespace
 
-const void* attn_tma_kernel(bool bf16, int padded_dim, bool ext) {
+const void* attn_tma_kernel(bool bf16, int padded_dim, bool cap, bool bias) {
+  const int ext = (cap ? kCap : 0) | (bias ? kBias : 0);
   return bf16 ? tma_of<kBF16>(padded_dim, ext) : tma_of<kF16>(padded_dim, ext);
 }
 

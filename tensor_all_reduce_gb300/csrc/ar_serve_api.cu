@@ -435,8 +435,8 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.part_o = reinterpret_cast<float*>(base + w.o);
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
-  const bool ext = a->softcap > 0.0f || a->slopes || !(a->scale > 0.0f);
-  ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, ext), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
+  const bool cap = a->softcap > 0.0f, bias = a->slopes || !(a->scale > 0.0f);
+  ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, cap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
   st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, 4), 256, 1, args, 0, stream);
@@ -462,8 +462,8 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
       for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0)));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int i = 0; i < 2; ++i)
-      for (int ext = 0; ext < 2; ++ext)
-        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, ext), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
+      for (int ext = 0; ext < 4; ++ext)
+        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, ext & 1, ext & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
     for (int i = 0; i < 3; ++i) {
       const int dp = 64 << i;
       const void* f = attn_mma_kernel(b, dp);
