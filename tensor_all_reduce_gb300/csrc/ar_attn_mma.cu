@@ -10,6 +10,7 @@ namespace ar {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+constexpr int kJoinRows = 4;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -221,8 +222,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
       if (!wrote[s]) write_header(p, s, 0, nullptr);
 }
 
-// Joins the parts of the items that more than one span holds: block (c, y) serves, a warp a row,
-// every gridDim.y-th group of 8 rows of the item that begins in span c and does not end there.
+// Joins the parts of the items that more than one span holds: the blocks (c, ...) serve the item
+// that begins in span c and does not end there.  A warp takes up to four rows, W apart for the W
+// warps of those blocks (few rows: one each), with the loads of all of them in flight.
 template <int DT>
 __global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ AttnParams p) {
   __shared__ int sh_end;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ Attn
   const int q0 = h[1], rows = h[2], qt = h[3], head0 = h[4] * p.group;
   const int row_base = qt * p.tile_rows;
   const int local_rows = min(rows - row_base, p.tile_rows);
-  if ((int)blockIdx.y * 8 >= local_rows) return;
+  if ((int)blockIdx.y * 8 >= local_rows) return;  // not one row for these warps
   if (threadIdx.x == 0) sh_end = p.spans;
   __syncthreads();
   for (int i = c + 1 + (int)threadIdx.x; i < p.spans; i += 256)
@@ -243,46 +245,70 @@ __global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ Attn
     }
   __syncthreads();
   const int end = min(sh_end, p.spans - 1);  // the chain: slot 1 of span c, slot 0 of spans c + 1 .. end
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warps = gridDim.y * 8, first = blockIdx.y * 8 + (threadIdx.x >> 5);
   auto place = [&](int i, int local) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.tile_rows + local; };
-  for (int local = blockIdx.y * 8 + warp; local < local_rows; local += gridDim.y * 8) {
-    const int row = row_base + local;
-    float top = -INFINITY;
-    for (int i = c + lane; i <= end; i += 32) top = fmaxf(top, p.part_ml[place(i, local) * 2]);
+  for (int local0 = first; local0 < local_rows; local0 += warps * kJoinRows) {
+    float top[kJoinRows], l[kJoinRows];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f;
-    for (int i = c + lane; i <= end; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + place(i, local) * 2);
-      l += ex2(ml.x - base) * ml.y;
+    for (int k = 0; k < kJoinRows; ++k) {
+      top[k] = -INFINITY;
+      l[k] = 0.0f;
     }
-    l = warp_sum(l);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int t = row / p.group, head = head0 + row - t * p.group;
-    uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+    for (int i = c + lane; i <= end; i += 32)
+#pragma unroll
+      for (int k = 0; k < kJoinRows; ++k)
+        if (local0 + k * warps < local_rows) top[k] = fmaxf(top[k], p.part_ml[place(i, local0 + k * warps) * 2]);
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+      if (top[k] == -INFINITY) top[k] = 0.0f;  // a row that sees nothing: every weight sum is 0
+    }
+    for (int i = c + lane; i <= end; i += 32)
+#pragma unroll
+      for (int k = 0; k < kJoinRows; ++k)
+        if (local0 + k * warps < local_rows) {
+          const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + place(i, local0 + k * warps) * 2);
+          l[k] += ex2(ml.x - top[k]) * ml.y;
+        }
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) l[k] = warp_sum(l[k]);
     for (int e = lane * 4; e < p.part_dim; e += 128) {
-      float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-      for (int i = c; i <= end; ++i) {
-        const int64_t at = place(i, local);
-        const float w = ex2(p.part_ml[at * 2] - base);
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * p.part_dim + e);
-        a[0] += w * v.x;
-        a[1] += w * v.y;
-        a[2] += w * v.z;
-        a[3] += w * v.w;
-      }
-      if (p.vec) {
-        if (e < p.head_dim) st_v2(dst + e, make_uint2(pack2<DT>(a[0] * inv, a[1] * inv), pack2<DT>(a[2] * inv, a[3] * inv)));
-      } else {
+      float4 a[kJoinRows];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (e + j < p.head_dim) st_u16(dst + e + j, round1<DT>(a[j] * inv));
+      for (int k = 0; k < kJoinRows; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+      for (int i = c; i <= end; ++i)
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k)
+          if (local0 + k * warps < local_rows) {
+            const int64_t at = place(i, local0 + k * warps);
+            const float w = ex2(p.part_ml[at * 2] - top[k]);
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * p.part_dim + e);
+            a[k].x += w * v.x;
+            a[k].y += w * v.y;
+            a[k].z += w * v.z;
+            a[k].w += w * v.w;
+          }
+#pragma unroll
+      for (int k = 0; k < kJoinRows; ++k) {
+        const int row = row_base + local0 + k * warps;
+        if (local0 + k * warps >= local_rows) continue;
+        const int t = row / p.group, head = head0 + row - t * p.group;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+        const float inv = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
+        const float f[4] = {a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv};
+        if (p.vec) {
+          if (e < p.head_dim) st_v2(dst + e, make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (e + j < p.head_dim) st_u16(dst + e + j, round1<DT>(f[j]));
+        }
+        if (p.lse && e == 0)
+          p.lse[(int64_t)(q0 + t) * p.q_heads + head] = l[k] > 0.0f ? (top[k] + log2f(l[k])) * 0.69314718055994531f : -INFINITY;
       }
     }
-    if (p.lse && lane == 0)
-      p.lse[(int64_t)(q0 + t) * p.q_heads + head] = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
 

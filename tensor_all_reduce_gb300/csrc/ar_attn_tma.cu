@@ -1,18 +1,19 @@
-// Paged attention on the fifth-generation tensor cores: heads of up to 128 elements, rows on
-// 16-byte boundaries, pages of a multiple of 8 tokens.
+// Paged attention on the fifth-generation tensor cores: rows on 16-byte boundaries, pages of a
+// multiple of 8 tokens.
 //
-// A CTA (one an SM, resident) takes items of 256 query rows, two halves of 128, against tiles of
-// 128 keys.  Of its twelve warps one loads keys and values by TMA, box by box through the block table,
-// into a ring of shared-memory slots; one issues the matrix instructions; a warpgroup for each half
-// turns scores into weights (the last two warps only complete the third warpgroup, which hands
-// registers to the others).  A thread of a warpgroup owns one query row, so row maxima and
-// sums need no exchange between threads.
+// A CTA (one an SM, resident) takes items of 256 query rows (128 for heads of more than 128
+// elements), in halves of 128, against tiles of 128 keys.  Of its twelve warps one loads keys and
+// values by TMA, box by box through the block table, into a ring of shared-memory slots; one
+// issues the matrix instructions; a warpgroup for each half turns scores into weights (the last
+// two warps only complete the third warpgroup, which hands registers to the others).  A thread
+// of a warpgroup owns one query row, so row maxima and sums need no exchange between threads.
 //
-// Tensor memory (512 columns of 128 lanes): scores of half h in columns [128 h, 128 h + 128), the
-// weighted sum of half h in [256 + 128 h, ...).  The weights, 16-bit, take the first 64 columns
-// of their half's scores and are the second product's A operand from there, so they never
-// touch shared memory.  Matrix instructions of one CTA run in the order in which they are issued:
-// while one half's softmax runs, the tensor core works on the other half's two products.
+// Tensor memory (512 columns of 128 lanes): two score buffers of 128 columns, and 256 columns for
+// the weighted sums, 128 a half or all for one half.  The weights, 16-bit, take the first 64
+// columns of their scores and are the second product's A operand from there, so they never touch
+// shared memory.  Matrix instructions of one CTA run in the order in which they are issued.  With
+// two halves, one half's softmax runs while the tensor core works on the other's products;
+// with one (single tokens, wide heads) the two buffers hold its present and next tile.
 //
 // The running maximum that the weights refer to moves only when a row's maximum has grown by more
 // than 2^8 (in weight), since the result does not depend on the reference: then the sum in
@@ -27,7 +28,7 @@
 namespace ar {
 namespace {
 
-constexpr int kRows = 256, kKeys = 128, kThreads = 384;
+constexpr int kKeys = 128, kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr uint32_t kTmemCols = 512;
 // 384 threads at 168 registers; the third warpgroup gives 96 a thread to the other two
@@ -36,19 +37,25 @@ static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168, "the split uses what the
 
 template <int DP>
 struct Shape {
-  static constexpr int kBlocks = DP / 64;               // 64-element (128-byte) column blocks of a row
+  static constexpr int kRows = DP == 256 ? 128 : 256;   // rows of an item
+  static constexpr int kUnits = DP == 256 ? 2 : 1;      // ring slots that a tile of keys or values takes
+  static constexpr int kBlocks = DP / 64 / kUnits;      // 64-element (128-byte) column blocks of a unit
   static constexpr int kBlockBytes = kKeys * 128;       // one column block of 128 rows
-  static constexpr int kTileBytes = kBlocks * kBlockBytes;
+  static constexpr int kUnitBytes = kBlocks * kBlockBytes;
+  static constexpr int kTileBytes = kUnits * kUnitBytes;
+  static constexpr int kQueryBytes = kRows / 128 * kTileBytes;
   static constexpr int kSlots = DP == 64 ? 10 : 5;
-  static constexpr int kBytes = (2 + kSlots) * kTileBytes;
+  static constexpr int kBytes = kQueryBytes + kSlots * kUnitBytes;
 };
 
+// Score buffers and their barriers: 0 and 1 for two halves, 2 and 3 (in the same columns) for the
+// turns of an item of one half.
 struct Bars {
   uint64_t full[10], empty[10];  // ring slots
   uint64_t q[2];                 // queries of a half stored
-  uint64_t s[2];                 // scores of a half ready
-  uint64_t p[2];                 // weights of a half stored
-  uint64_t o[2];                 // sum of a half complete
+  uint64_t s[4];                 // scores ready
+  uint64_t p[4], p2[4];          // weights of the first and second 64 keys stored
+  uint64_t o[4];                 // sum complete: of half 0, 1 (an item), of one half (a tile, by turns)
   uint64_t drain;
   uint32_t tmem;
   int stop;
@@ -178,9 +185,16 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars& b
 
 // ---- roles --------------------------------------------------------------------
 
-using Steps = Walk<kRows, kKeys>;
+// Every role walks the CTA's items for itself and counts barrier phases the same way:
+//   n: units loaded into the ring; items: items so far (phase of q[0], o[...] of paired halves);
+//   pairs: items of two halves; d: tiles of such items; g: tiles of items of one half.
+// An item of one half has two score buffers (S0, S1 by turns), so that the next tile's scores are
+// computed while the softmax works on the present one; one of two halves has one buffer each.
 
-__device__ __forceinline__ int halves(const Item& it) { return it.rows - it.qt * kRows > 128 ? 2 : 1; }
+template <int DP>
+__device__ __forceinline__ bool single_half(const Item& it) {
+  return Shape<DP>::kRows == 128 || it.rows - it.qt * Shape<DP>::kRows <= 128;
+}
 
 template <int DP>
 __device__ void load_role(const AttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, const SpanShared& span, Bars& b, uint32_t ring) {
@@ -189,25 +203,45 @@ __device__ void load_role(const AttnParams& p, const CUtensorMap* kmap, const CU
   const int boxes = kKeys / p.box_rows;
   const int box = lane / S::kBlocks, cb = lane - box * S::kBlocks;
   const bool issues = box < boxes;
-  Steps walk(p, span);
-  Item it;
+  Walk<S::kRows, kKeys> walk(p, span);
+  Item it = {};
   uint32_t n = 0;
   bool ok = true;
   while (ok && walk.next(p, it)) {
-    for (int ti = it.begin; ok && ti < it.end; ++ti) {
-      const int key = it.range.tile(ti) * kKeys + box * p.box_rows;
-      int block = -1, in_page = 0;
-      if (issues && key < it.q.len) block = (int)block_of(p, it.r, key, in_page);
-      const int w = block < 0 ? (int)p.num_blocks : block;  // outside the cache: the copy fills with zeros
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
+    const int nt = it.end - it.begin;
+    const bool one = single_half<DP>(it);
+    // block and place of this lane's box, of the tile after next, the last and the one before
+    int block_next = 0, page_next = 0, block_cur = 0, page_cur = 0, block_prev = 0, page_prev = 0;
+    auto look_up = [&](int t) {
+      const int key = it.range.tile(it.begin + t) * kKeys + box * p.box_rows;
+      int64_t w = -1;
+      page_next = 0;
+      if (issues && key < it.q.len) w = block_of(p, it.r, key, page_next);
+      block_next = w < 0 ? (int)p.num_blocks : (int)w;  // outside the cache: the copy fills with zeros
+    };
+    look_up(0);
+    // keys 0, then (values t, keys t + 1), or (keys t + 1, values t) where scores run ahead
+    for (int j = 0; ok && j < 2 * nt; ++j) {
+      const bool keys = one ? (j == 0 || ((j & 1) && j + 1 < 2 * nt)) : (j & 1) == 0;
+      if (keys) {
+        const int t = (j + 1) >> 1;
+        block_prev = block_cur;
+        page_prev = page_cur;
+        block_cur = block_next;
+        page_cur = page_next;
+        if (t + 1 < nt) look_up(t + 1);
+      }
+      const bool behind = one && !keys && j + 1 < 2 * nt;  // values of the tile before the last keys
+      const int w = behind ? block_prev : block_cur, y = behind ? page_prev : page_cur;
+      for (int u = 0; u < S::kUnits; ++u) {
         const uint32_t slot = n % S::kSlots, round = n / S::kSlots;
         ok = __all_sync(0xffffffffu, ok && wait_for(&b.empty[slot], (round & 1) ^ 1, b, p));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&b.full[slot], S::kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(&b.full[slot], S::kUnitBytes);
         __syncwarp();
         if (issues && !(p.stall && n == 0))
-          tma_4d(ring + slot * S::kTileBytes + cb * S::kBlockBytes + box * p.box_rows * 128, kv ? vmap : kmap, cb * 64, in_page, it.h, w, &b.full[slot]);
+          tma_4d(ring + slot * S::kUnitBytes + cb * S::kBlockBytes + box * p.box_rows * 128, keys ? kmap : vmap, u * 128 + cb * 64, y, it.h, w,
+                 &b.full[slot]);
         ++n;
       }
     }
@@ -223,79 +257,130 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
   using S = Shape<DP>;
   const int lane = threadIdx.x & 31;
   const int ksteps = (p.head_dim + 15) / 16;
-  const uint32_t idesc_s = instr_desc<DT>(kKeys, false), idesc_o = instr_desc<DT>(ksteps * 16, true);
+  const uint32_t idesc_s = instr_desc<DT>(kKeys, false);
   // descriptors differ in the address alone, in units of 16 bytes: constant offsets are added
   const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(ring, 16), v_desc = matrix_desc(ring, S::kBlockBytes);
-  auto scores = [&](int h, uint32_t slot) {  // queries of half h times the keys in `slot`
-    const uint64_t a = q_desc + h * (S::kTileBytes >> 4), k = k_desc + slot * (S::kTileBytes >> 4);
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i) {
-      const uint64_t off = ((i >> 2) * S::kBlockBytes + (i & 3) * 32) >> 4;
-      if (i < ksteps) mma_ss(tmem + h * 128, a + off, k + off, idesc_s, i > 0);
-    }
-    mma_commit(&b.s[h]);
-  };
-  auto weighted = [&](int h, uint32_t slot, bool more) {  // weights of half h times the values in `slot`
-    const uint64_t v = v_desc + slot * (S::kTileBytes >> 4);
-#pragma unroll
-    for (int i = 0; i < kKeys / 16; ++i)
-      mma_ts(tmem + 256 + h * 128, tmem + h * 128 + i * 8, v + ((i * 16 * 128) >> 4), idesc_o, more || i > 0);
-  };
   const bool one = elect_one();
-  Steps walk(p, span);
-  Item it;
-  uint32_t n = 0, items[2] = {0, 0}, tiles[2] = {0, 0};
+  Walk<S::kRows, kKeys> walk(p, span);
+  Item it = {};
+  uint32_t n = 0, items = 0, pairs = 0, d = 0, g = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
     fence_after();
     return ok;
   };
-  while (ok && walk.next(p, it)) {
-    const int nh = halves(it), nt = it.end - it.begin;
-    uint32_t slot = n % S::kSlots;
-    if (!wait(&b.full[slot], (n / S::kSlots) & 1)) break;
-    for (int h = 0; h < nh; ++h) {
-      if (!wait(&b.q[h], items[h]++ & 1)) break;
-      if (one) scores(h, slot);
-    }
-    if (!ok) break;
-    if (one) mma_commit(&b.empty[slot]);
-    ++n;
-    for (int i = 0; ok && i < nt; ++i) {
-      const uint32_t vs = n % S::kSlots, ks = (n + 1) % S::kSlots;
-      const bool more = i + 1 < nt;
-      if (!wait(&b.full[vs], (n / S::kSlots) & 1)) break;
-      const int key0 = it.range.tile(it.begin + i) * kKeys, left = it.q.len - key0;
-      if (left < kKeys) {
-        // values behind the request's end: whole boxes came as zeros, the rest of the last
-        // box holds whatever the cache does
-        const int lo = max(left, 0), hi = min((lo + p.box_rows - 1) / p.box_rows * p.box_rows, kKeys);
-        const uint32_t v = ring + vs * S::kTileBytes;
-        for (int x = lo * 8 + lane; x < hi * 8; x += 32)
+  auto wait_unit = [&](uint32_t i) { return wait(&b.full[i % S::kSlots], (i / S::kSlots) & 1); };
+  // queries of half h times the keys of unit i (column part u of the head) into score buffer `buf`
+  auto scores = [&](int buf, int h, uint32_t i, int u) {
+    const uint64_t a = q_desc + (h * S::kTileBytes + u * S::kUnitBytes) / 16, k = k_desc + (i % S::kSlots) * (S::kUnitBytes / 16);
 #pragma unroll
-          for (int cb = 0; cb < S::kBlocks; ++cb)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + cb * S::kBlockBytes + x * 16), "r"(0) : "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
+    for (int s = 0; s < S::kUnitBytes / kKeys / 32; ++s) {
+      const uint64_t off = ((s >> 2) * S::kBlockBytes + (s & 3) * 32) >> 4;
+      if (u * 8 + s < ksteps) mma_ss(tmem + buf * 128, a + off, k + off, idesc_s, u > 0 || s > 0);
+    }
+  };
+  // half `part` of the tile's weights in score buffer `buf` times the values of unit i, to columns `to`
+  auto weighted = [&](int buf, uint32_t i, int u, int part, uint32_t to, bool more) {
+    const uint64_t v = v_desc + (i % S::kSlots) * (S::kUnitBytes / 16);
+    const int cols = ksteps * 16 - u * 128;
+    if (cols <= 0) return;
+    const uint32_t idesc_o = instr_desc<DT>(cols < 128 ? cols : 128, true);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k = part * 4 + s;
+      mma_ts(tmem + to + u * 128, tmem + buf * 128 + k * 8, v + ((k * 16 * 128) >> 4), idesc_o, more || k > 0);
+    }
+  };
+  // Values behind the request's end: whole boxes came as zeros, the rest of the last box holds
+  // whatever the cache does.  Zeroed, because a weight of 0 does not cancel an infinity.
+  auto clear_tail = [&](int t, uint32_t i) {
+    const int left = it.q.len - it.range.tile(it.begin + t) * kKeys;
+    if (left >= kKeys) return;
+    const int lo = max(left, 0), hi = min((lo + p.box_rows - 1) / p.box_rows * p.box_rows, kKeys);
+    const uint32_t v = ring + (i % S::kSlots) * S::kUnitBytes;
+    for (int x = lo * 8 + lane; x < hi * 8; x += 32)
+#pragma unroll
+      for (int cb = 0; cb < S::kBlocks; ++cb)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + cb * S::kBlockBytes + x * 16), "r"(0) : "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  while (ok && walk.next(p, it)) {
+    const int nt = it.end - it.begin;
+    if (single_half<DP>(it)) {
+      if (!wait(&b.q[0], items & 1)) break;
+      for (int i = -1; ok && i < nt; ++i) {
+        if (i + 1 < nt) {
+          const uint32_t x = (g + i + 1) & 1;
+          for (int u = 0; u < S::kUnits; ++u, ++n) {
+            if (!wait_unit(n)) break;
+            if (one) {
+              scores(x, 0, n, u);
+              mma_commit(&b.empty[n % S::kSlots]);
+            }
+          }
+          if (!ok) break;
+          if (one) mma_commit(&b.s[2 + x]);
+        }
+        if (i < 0) continue;
+        const uint32_t x = (g + i) & 1, phase = ((g + i) >> 1) & 1;
+        for (int u = 0; u < S::kUnits; ++u, ++n) {
+          if (!wait_unit(n)) break;
+          clear_tail(i, n);
+          if (u == 0 && !wait(&b.p[2 + x], phase)) break;
+          if (one) weighted(x, n, u, 0, 256, i > 0);
+          if (u == 0 && !wait(&b.p2[2 + x], phase)) break;
+          if (one) {
+            weighted(x, n, u, 1, 256, true);
+            mma_commit(&b.empty[n % S::kSlots]);
+          }
+        }
+        if (!ok) break;
+        if (one) mma_commit(&b.o[2 + x]);
       }
-      for (int h = 0; h < nh; ++h) {
-        if (!wait(&b.p[h], tiles[h]++ & 1)) break;
-        if (one) weighted(h, vs, i > 0);
-        if (more) {
-          if (h == 0 && !wait(&b.full[ks], ((n + 1) / S::kSlots) & 1)) break;
-          if (one) scores(h, ks);
-        } else if (one) {
-          mma_commit(&b.o[h]);
+      g += nt;
+    } else {
+      if (!wait_unit(n)) break;
+      for (int h = 0; ok && h < 2; ++h) {
+        if (!wait(&b.q[h], (h ? pairs : items) & 1)) break;
+        if (one) {
+          scores(h, h, n, 0);
+          mma_commit(&b.s[h]);
         }
       }
       if (!ok) break;
-      if (one) {
-        mma_commit(&b.empty[vs]);
-        if (more) mma_commit(&b.empty[ks]);
+      if (one) mma_commit(&b.empty[n % S::kSlots]);
+      ++n;
+      for (int i = 0; ok && i < nt; ++i, ++d) {
+        const bool more = i + 1 < nt;
+        if (!wait_unit(n)) break;
+        clear_tail(i, n);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&b.p[h], d & 1)) break;
+          if (one) weighted(h, n, 0, 0, 256 + h * 128, i > 0);
+          if (!wait(&b.p2[h], d & 1)) break;
+          if (one) weighted(h, n, 0, 1, 256 + h * 128, true);
+          if (more) {
+            if (h == 0 && !wait_unit(n + 1)) break;
+            if (one) {
+              scores(h, h, n + 1, 0);
+              mma_commit(&b.s[h]);
+            }
+          } else if (one) {
+            mma_commit(&b.o[h]);
+          }
+        }
+        if (!ok) break;
+        if (one) {
+          mma_commit(&b.empty[n % S::kSlots]);
+          if (more) mma_commit(&b.empty[(n + 1) % S::kSlots]);
+        }
+        n += more ? 2 : 1;
       }
-      n += more ? 2 : 1;
+      ++pairs;
     }
+    ++items;
   }
   if (!ok) {  // matrix instructions in flight end before tensor memory is freed
     if (one) mma_commit(&b.drain);
@@ -342,34 +427,53 @@ __device__ __forceinline__ void shape_scores(const AttnParams& p, const Item& it
 template <int DT, int DP, int EXT>
 __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& b, uint8_t* queries, uint32_t tmem, bool (&wrote)[2]) {
   using S = Shape<DP>;
-  const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5;
+  const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-  const uint32_t ts = lanes + h * 128, to = lanes + 256 + h * 128;
   const float scale = EXT ? 1.0f : p.scale_log2;
-  Steps walk(p, span);
-  Item it;
-  uint32_t items = 0, tiles = 0;
+  Walk<S::kRows, kKeys> walk(p, span);
+  uint32_t pairs = 0, d = 0, g = 0;
   bool ok = true;
-  while (ok && walk.next(p, it)) {
-    if (h >= halves(it)) continue;
-    const int base_row = it.qt * kRows + h * 128;
-    // queries, 16 bytes a thread, neighbours along a row; rows and columns beyond are zero
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
+    fence_after();
+    return ok;
+  };
+  auto arrive = [&](uint64_t* bar) {  // a warp's stores are done
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto next_item = [&](Item& it) {  // the next one with rows in this half
+    while (walk.next(p, it))
+      if (h == 0 || !single_half<DP>(it)) return true;
+    return false;
+  };
+  // queries, 16 bytes a thread, neighbours along a row; rows and columns beyond are zero
+  auto load_queries = [&](const Item& it) {
     uint8_t* dst = queries + h * S::kTileBytes;
 #pragma unroll 4
     for (int x = tid; x < 128 * (DP / 8); x += 128) {
-      const int r = x / (DP / 8), c = x % (DP / 8), row = base_row + r;
+      const int r = x / (DP / 8), c = x % (DP / 8), row = it.qt * S::kRows + h * 128 + r;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (row < it.rows && c * 8 < p.head_dim) {
-        const int t = row / p.group, g = row - t * p.group;
-        v = ld_keep(static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * p.group + g) * p.q_hs + c * 8);
+        const int t = row / p.group, e = row - t * p.group;
+        v = ld_keep(static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * p.group + e) * p.q_hs + c * 8);
       }
       *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
-    mbar_arrive(&b.q[h]);
-
-    const int row = base_row + tid;
-    const bool busy = base_row + warp * 32 < it.rows;  // the warp has a row
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.q[h]);
+  };
+  Item it = {}, later = {};
+  bool have = next_item(it);
+  if (have) load_queries(it);
+  while (have) {
+    const int nt = it.end - it.begin;
+    const bool one = single_half<DP>(it);
+    const uint32_t to = lanes + 256 + (one ? 0 : h * 128);
+    const int row = it.qt * S::kRows + h * 128 + tid;
+    const bool busy = row - lane < it.rows;  // the warp has a row
     RowView view = row_view(p, it, row);
     if (row >= it.rows) {  // no row: sees all, so that the warp need not mask for it; nothing of it is stored
       view.see_lo = 0;
@@ -377,76 +481,88 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
     }
     float m = -INFINITY;
     uint64_t sum = two(0.0f, 0.0f);
-    for (int ti = it.begin; ti < it.end; ++ti) {
-      ok = wait_for(&b.s[h], tiles++ & 1, b, p);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+    for (int i = 0; i < nt; ++i) {
+      const uint32_t c = g + i, buf = one ? (c & 1) : h, x = one ? 2 + buf : h, phase = one ? (c >> 1) & 1 : (d + i) & 1;
+      const uint32_t ts = lanes + buf * 128;
+      if (!wait(&b.s[x], phase)) break;
+      if (!busy) {
+        arrive(&b.p[x]);
+        arrive(&b.p2[x]);
+        continue;
       }
-      fence_after();
-      if (busy) {
-        uint32_t raw[kKeys / 32][32];
+      uint32_t raw[kKeys / 32][32];
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(raw[c], ts + c * 32);
-        tmem_wait_ld();
-        float s[kKeys];
+      for (int k = 0; k < kKeys / 32; ++k) tmem_ld32(raw[k], ts + k * 32);
+      tmem_wait_ld();
+      float s[kKeys];
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          settle(raw[c]);
+      for (int k = 0; k < kKeys / 32; ++k) {
+        settle(raw[k]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[c * 32 + j] = __uint_as_float(raw[c][j]);
-        }
-        shape_scores<EXT>(p, it, view, it.range.tile(ti) * kKeys, s);
-        float top[4] = {s[0], s[1], s[2], s[3]};
+        for (int j = 0; j < 32; ++j) s[k * 32 + j] = __uint_as_float(raw[k][j]);
+      }
+      shape_scores<EXT>(p, it, view, it.range.tile(it.begin + i) * kKeys, s);
+      float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 4; j < kKeys; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
-        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-        const bool grown = high > m + 8.0f;  // m = -inf: any finite score
-        if (__any_sync(0xffffffffu, grown)) {
-          const float shrink = grown ? ex2(m - high) : 1.0f;  // m = -inf: 0
-          if (grown) m = high;
-          if (ti > it.begin) {
-            float lo, hi;
-            untwo(sum, lo, hi);
-            sum = two(lo * shrink, hi * shrink);
+      for (int j = 4; j < kKeys; j += 8)
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o, to + c * 32);
-              tmem_wait_ld();
-              settle(o);
+        for (int k = 0; k < 4; ++k) top[k] = j + 4 + k < kKeys ? fmaxf(fmaxf(top[k], s[j + k]), s[j + 4 + k]) : fmaxf(top[k], s[j + k]);
+      const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      const bool grown = high > m + 8.0f;  // m = -inf: any finite score
+      if (__any_sync(0xffffffffu, grown)) {
+        const float shrink = grown ? ex2(m - high) : 1.0f;  // m = -inf: 0
+        if (grown) m = high;
+        if (i > 0) {
+          // the sum holds the tiles so far: with two halves that is so once the scores are there,
+          // with scores that run ahead a barrier says so.  (Scores of tile c complete after the sum
+          // of tile c - 2, so this barrier is at most one phase behind.)
+          if (one && !wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) break;
+          float lo, hi;
+          untwo(sum, lo, hi);
+          sum = two(lo * shrink, hi * shrink);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
-              tmem_st32(to + c * 32, o);
-            }
+          for (int k = 0; k < DP / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32(o, to + k * 32);
+            tmem_wait_ld();
+            settle(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
+            tmem_st32(to + k * 32, o);
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
-        const uint64_t scale2 = two(scale, scale), base2 = two(-base, -base);
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      const uint64_t scale2 = two(scale, scale), base2 = two(-base, -base);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
+      for (int part = 0; part < 2; ++part) {
+        uint32_t w[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int e = c * 64 + j * 2;
-            float a, z;
-            untwo(fma2(two(s[e], s[e + 1]), scale2, base2), a, z);
-            a = ex2(a);
-            z = ex2(z);
-            sum = add2(sum, two(a, z));  // of the unrounded weights
-            w[j] = pack2<DT>(a, z);      // the second product's operand is 16-bit: half a step, relative, a weight
-          }
-          tmem_st32(ts + c * 32, w);
+        for (int j = 0; j < 32; ++j) {
+          const int e = part * 64 + j * 2;
+          float a, z;
+          untwo(fma2(two(s[e], s[e + 1]), scale2, base2), a, z);
+          a = ex2(a);
+          z = ex2(z);
+          sum = add2(sum, two(a, z));  // of the unrounded weights
+          w[j] = pack2<DT>(a, z);      // the second product's operand is 16-bit: half a step, relative, a weight
         }
+        tmem_st32(ts + part * 32, w);
         tmem_wait_st();
+        arrive(part ? &b.p2[x] : &b.p[x]);  // the second product starts on the first half of the keys
       }
-      fence_before();
-      mbar_arrive(&b.p[h]);
     }
     if (!ok) break;
-    ok = __all_sync(0xffffffffu, wait_for(&b.o[h], items++ & 1, b, p));
-    if (!ok) break;
-    fence_after();
+    // every score of the item is computed: its queries may go
+    const bool more = next_item(later);
+    if (more) load_queries(later);
+    if (one) {
+      g += nt;
+      if (!wait(&b.o[2 + ((g - 1) & 1)], ((g - 1) >> 1) & 1)) break;
+    } else {
+      d += nt;
+      if (!wait(&b.o[h], pairs++ & 1)) break;
+    }
     const bool whole = it.first && it.last;
     const int slot = it.first ? 1 : 0;
     if (busy) {
@@ -457,28 +573,28 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
       const int t = row / p.group, head = it.h * p.group + row - t * p.group;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
-      const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + h * 128 + tid;
+      const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * S::kRows + h * 128 + tid;
       float* part = p.part_o + at * p.part_dim;
 #pragma unroll
-      for (int c = 0; c < DP / 32; ++c) {
+      for (int k = 0; k < DP / 32; ++k) {
         uint32_t o[32];
-        tmem_ld32(o, to + c * 32);
+        tmem_ld32(o, to + k * 32);
         tmem_wait_ld();
         settle(o);
         if (!mine) continue;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
-          if (c * 32 + j >= p.head_dim) break;
+          if (k * 32 + j >= p.head_dim) break;
           float f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[j + e]);
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = l > 0.0f ? f[e] * inv : 0.0f;
-            st_v4(out + c * 32 + j, pack8<DT>(f));
+            st_v4(out + k * 32 + j, pack8<DT>(f));
           } else {
-            *reinterpret_cast<float4*>(part + c * 32 + j) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(part + c * 32 + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            *reinterpret_cast<float4*>(part + k * 32 + j) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(part + k * 32 + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
           }
         }
       }
@@ -489,7 +605,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
       wrote[slot] = true;
       if (threadIdx.x == 0) write_header(p, slot, kThere | (it.last ? kEnds : 0), &it);
     }
-    fence_before();
+    it = later;
+    have = more;
   }
 }
 
@@ -507,13 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
       mbar_init(&b.full[i], 1);
       mbar_init(&b.empty[i], 1);
     }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(&b.q[h], 128);
-      mbar_init(&b.s[h], 1);
-      mbar_init(&b.p[h], 128);
-      mbar_init(&b.o[h], 1);
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(&b.s[x], 1);
+      mbar_init(&b.o[x], 1);
+      mbar_init(&b.p[x], 4);  // one arrival a warp
+      mbar_init(&b.p2[x], 4);
     }
-    mbar_init(&b.drain, 1);
+    for (int h = 0; h < 2; ++h) mbar_init(&b.q[h], 4);
+        mbar_init(&b.drain, 1);
     b.stop = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
@@ -527,9 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
   fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&b.tmem);
   pdl_wait_and_release();
-  find_span<kRows, kKeys, kThreads>(p, span);
+  find_span<S::kRows, kKeys, kThreads>(p, span);
 
-  const uint32_t queries = smem_addr(smem), ring = queries + 2 * S::kTileBytes;
+  const uint32_t queries = smem_addr(smem), ring = queries + S::kQueryBytes;
   bool wrote[2] = {false, false};
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -563,7 +681,7 @@ const void* tma_of(int ext) {
 
 template <int DT>
 const void* tma_of(int dp, int ext) {
-  return dp == 64 ? tma_of<DT, 64>(ext) : tma_of<DT, 128>(ext);
+  return dp == 64 ? tma_of<DT, 64>(ext) : dp == 128 ? tma_of<DT, 128>(ext) : tma_of<DT, 256>(ext);
 }
 
 }  // namespace
@@ -573,7 +691,11 @@ const void* attn_tma_kernel(bool bf16, int padded_dim, bool cap, bool bias) {
   return bf16 ? tma_of<kBF16>(padded_dim, ext) : tma_of<kF16>(padded_dim, ext);
 }
 
-size_t attn_tma_smem(int padded_dim) { return (padded_dim == 64 ? Shape<64>::kBytes : Shape<128>::kBytes) + 1024; }
+size_t attn_tma_smem(int padded_dim) {
+  return (padded_dim == 64 ? Shape<64>::kBytes : padded_dim == 128 ? Shape<128>::kBytes : Shape<256>::kBytes) + 1024;
+}
+
+int attn_tma_rows(int padded_dim) { return padded_dim == 256 ? Shape<256>::kRows : Shape<128>::kRows; }
 
 bool attn_tensor_map(void* encode, CUtensorMap* map, const void* base, bool bf16, int64_t dim, int64_t page, int64_t heads, int64_t blocks,
                      int64_t page_stride, int64_t head_stride, int64_t block_stride, int box_rows) {

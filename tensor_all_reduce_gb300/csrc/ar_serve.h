@@ -108,8 +108,9 @@ const void* attn_combine_kernel(bool bf16);
 // padded by 16 bytes.
 inline size_t attn_mma_smem(int padded_dim) { return (size_t)3 * 64 * (padded_dim + 8) * 2; }
 
-const void* attn_tma_kernel(bool bf16, int padded_dim, bool cap, bool bias);  // padded_dim 64 or 128; bias: also a scale that is not positive
+const void* attn_tma_kernel(bool bf16, int padded_dim, bool cap, bool bias);  // bias: also a scale that is not positive
 size_t attn_tma_smem(int padded_dim);
+int attn_tma_rows(int padded_dim);  // query rows of an item
 
 // Tensor map of a cache [blocks, page, heads, dim] (strides in elements) with boxes of box_rows
 // tokens by 64 elements; `encode` is the driver's cuTensorMapEncodeTiled.

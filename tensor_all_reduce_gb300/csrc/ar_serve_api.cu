@@ -279,7 +279,7 @@ namespace {
 
 int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-constexpr int kMmaRows = 64, kTmaRows = 256;
+constexpr int kMmaRows = 64;
 
 struct Workspace {
   int64_t ml, o, bytes;  // offsets of the statistics and the sums behind the headers
@@ -302,8 +302,8 @@ int part_dim(int d) { return (d + 3) / 4 * 4; }
 
 int64_t workspace_need(const ar_ctx* ctx, bool bf16, int d) {
   const int64_t general = workspace_of(mma_spans(ctx, bf16, padded_dim(d)), kMmaRows, part_dim(d)).bytes;
-  const int64_t tma = workspace_of(ctx->sm_count, kTmaRows, part_dim(d)).bytes;
-  return d <= 128 && tma > general ? tma : general;
+  const int64_t tma = workspace_of(ctx->sm_count, ar::attn_tma_rows(padded_dim(d)), part_dim(d)).bytes;
+  return tma > general ? tma : general;
 }
 
 }  // namespace
@@ -410,12 +410,12 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.status = ctx->d_status;
   p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
 
-  // The tensor-core form takes aligned rows of up to 128 elements and pages that whole groups of
+  // The tensor-core form takes aligned rows and pages that whole groups of
   // 8 keys (the swizzle's period) fill; the general form the rest.
   const int dp = padded_dim(a->head_dim);
   int box = 1;
   while (box < 128 && pg % (box * 2) == 0) box *= 2;
-  bool tma = p.vec && dp <= 128 && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
+  bool tma = p.vec && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
   CUtensorMap kmap, vmap;
   if (tma) {
     p.box_rows = box;
@@ -426,7 +426,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
                               a->v_block_stride, box);
   }
   p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp);
-  p.tile_rows = tma ? kTmaRows : kMmaRows;
+  p.tile_rows = tma ? ar::attn_tma_rows(dp) : kMmaRows;
   p.part_dim = part_dim(a->head_dim);
   const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
   char* base = static_cast<char*>(a->workspace);
@@ -439,7 +439,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, cap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
-  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, 4), 256, 1, args, 0, stream);
+  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, (unsigned)(p.tile_rows + 31) / 32), 256, 1, args, 0, stream);
   if (st == AR_OK) ctx->last_variant = tma ? "paged_attention_tma" : "paged_attention_mma";
   return st;
 }
@@ -461,7 +461,7 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
     for (int d = 64; d <= 256; d *= 2)
       for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0)));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 3; ++i)
       for (int ext = 0; ext < 4; ++ext)
         keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, ext & 1, ext & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
     for (int i = 0; i < 3; ++i) {

@@ -171,6 +171,22 @@ def test_growing_maximum(ctx, form):
                 x["kc"][x["table"][r][j // 16], j % 16] = (sign * j / 60.0) / 8.0
         x["q"] = torch.ones_like(x["q"])
         check(ctx, x)
+    for d in (128, 256):  # in leaps of more than the 2^8 that the reference tolerates, up and down
+        x = make([5, 150], [1500, 1500], 2, 1, d, seed=d, garbage=0.0)
+        for r, length in enumerate(x["lens"]):
+            for j in range(length):
+                x["kc"][x["table"][r][j // 16], j % 16] = (((j // 100) * 7) % 11) * 16.0 / d
+        x["q"] = torch.ones_like(x["q"])
+        check(ctx, x, scale=1.0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_items_of_one_and_two_halves(ctx, form, d):
+    """Requests of few and of many rows in turn, one tile of keys and many, in one CTA's span and over several."""
+    new = [1, 90, 2, 60, 1, 1, 130, 43, 42, 1, 0, 200, 3]
+    lens = [5, 90, 900, 61, 300, 129, 140, 43, 2000, 128, 77, 1000, 3]
+    check(ctx, make(new * 2, lens * 2, 6, 2, d, seed=d))
+    check(ctx, make(new * 12, [min(x, 300) for x in lens] * 12, 12, 4, d, "fp16", seed=d + 1))
 
 
 @pytest.mark.parametrize("seed", range(6))
@@ -318,7 +334,7 @@ def test_a_wait_that_runs_out_ends_the_call(ctx):
 def test_forms(ctx):
     """Which form serves which call."""
     import tensor_all_reduce_gb300 as tar
-    for d, page, want in ((128, 16, "tma"), (64, 128, "tma"), (80, 24, "tma"), (128, 4, "mma"), (36, 16, "mma"), (256, 16, "mma")):
+    for d, page, want in ((128, 16, "tma"), (64, 128, "tma"), (80, 24, "tma"), (256, 16, "tma"), (128, 4, "mma"), (36, 16, "mma"), (256, 7, "mma")):
         check(ctx, make([3], [50], 4, 2, d, page=page))
         assert ctx.last_variant == "paged_attention_" + want
     ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 4)
