@@ -21,6 +21,8 @@ namespace ar {
 constexpr int kHeaderInts = 8;  // flags (1: there, 2: the item ends here), first row of the request, rows of the request, query tile, head
 constexpr int kThere = 1, kEnds = 2;
 
+__device__ __forceinline__ int operator/(int n, const FastDiv& f) { return (int)((__umulhi((uint32_t)n, f.m) + (uint32_t)n) >> f.s); }
+
 struct Request {
   int q0, n, len, prefix;  // first row of q, new tokens, keys, keys that every row sees
 };
@@ -47,9 +49,8 @@ struct TileRange {
 
 template <int ROWS, int KT>
 __device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Request& q, int qt) {
-  const int64_t row0 = (int64_t)qt * ROWS;
-  const int64_t rows = (int64_t)q.n * p.group;
-  const int t0 = (int)row0 / p.group, t1 = (int)(min(row0 + ROWS, rows) - 1) / p.group;
+  const int row0 = qt * ROWS, rows = q.n * (int)p.group.d;  // at most 2^30
+  const int t0 = row0 / p.group, t1 = (min(row0 + ROWS, rows) - 1) / p.group;
   const int p0 = q.len - q.n + t0, p1 = q.len - q.n + t1;  // may be negative: rows that see no key
   const int high = p.causal ? min(max(p1 + 1, 0), q.len) : q.len;
   const int low = p.window ? max(p0 - p.window + 1, 0) : 0;  // |p0| and window are at most 2^30
@@ -76,42 +77,46 @@ struct Item {
 
 struct SpanShared {
   long long warp_sum[32];
-  long long offset;
   Cursor at;
+  Request q;        // of request at.r
   long long tiles;  // tiles of this CTA's span
 };
 
-// The CTA's span: where it starts and how many tiles it has.  All threads take part.
+// The CTA's span: where it starts and how many tiles it has.  All threads take part, a thread a
+// request: the scan over the requests is redone by every CTA, which costs about a microsecond and
+// saves a launch that would do it once.
 template <int ROWS, int KT, int THREADS>
 __device__ void find_span(const AttnParams& p, SpanShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int WARPS = THREADS / 32;
-  auto request_tiles = [&](int r, bool there) -> long long {  // key tiles of each thread's request, over its query tiles and heads
-    Request q = {0, 0, 0, 0};
-    if (there) q = load_request(p, r);
-    const int nqt = (int)(((int64_t)q.n * p.group + ROWS - 1) / ROWS);
-    long long mine = 0;
-    if (nqt == 1) mine = tile_range<ROWS, KT>(p, q, 0).count();
+  Request q = {0, 0, 0, 0};
+  long long before = 0, mine = 0, excl = 0;
+  auto query_tiles = [&](int n) { return (int)((n * p.group.d + ROWS - 1) / ROWS); };
+  auto share = [&](int src) {  // a lane's request, to its warp
+    Request o;
+    o.q0 = 0;
+    o.n = __shfl_sync(0xffffffffu, q.n, src);
+    o.len = __shfl_sync(0xffffffffu, q.len, src);
+    o.prefix = __shfl_sync(0xffffffffu, q.prefix, src);
+    return o;
+  };
+  auto scan = [&](int base) {  // `mine`: tiles of the thread's request; `excl`: of those before it; `before`: of all so far
+    const int r = base + (int)threadIdx.x;
+    q.n = 0;
+    if (r < p.requests) q = load_request(p, r);
+    const int nqt = query_tiles(q.n);
+    mine = nqt == 1 ? tile_range<ROWS, KT>(p, q, 0).count() : 0;
     for (unsigned many = __ballot_sync(0xffffffffu, nqt > 1); many; many &= many - 1) {  // the warp together
       const int src = __ffs(many) - 1;
-      Request o;
-      o.q0 = 0;
-      o.n = __shfl_sync(0xffffffffu, q.n, src);
-      o.len = __shfl_sync(0xffffffffu, q.len, src);
-      o.prefix = __shfl_sync(0xffffffffu, q.prefix, src);
-      const int m = __shfl_sync(0xffffffffu, nqt, src);
+      const Request o = share(src);
+      const int m = query_tiles(o.n);
       long long s = 0;
       for (int t = lane; t < m; t += 32) s += tile_range<ROWS, KT>(p, o, t).count();
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
       if (lane == src) mine = s;
     }
-    return mine * p.kv_heads;
-  };
-  long long before = 0, mine = 0, excl = 0;
-  auto scan = [&](int base) {  // `mine` and its exclusive prefix over all requests; adds the chunk to `before`
-    const int r = base + (int)threadIdx.x;
-    mine = request_tiles(r, r < p.requests);
+    mine *= p.kv_heads;
     long long s = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -121,54 +126,59 @@ __device__ void find_span(const AttnParams& p, SpanShared& sh) {
     if (lane == 31) sh.warp_sum[warp] = s;
     __syncthreads();
     excl = before + s - mine;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) excl += sh.warp_sum[w];
-      before += sh.warp_sum[w];
+      const long long u = sh.warp_sum[w];
+      if (w < warp) excl += u;
+      before += u;
     }
-    __syncthreads();
   };
-  for (int base = 0; base < p.requests; base += THREADS) scan(base);
-  const long long total = before;
-  // spans with tiles stand side by side: with fewer tiles than CTAs the first ones take one each
-  auto start = [&](long long b) { return total >= gridDim.x ? total * b / gridDim.x : min(b, total); };
-  const long long s0 = start(blockIdx.x), s1 = start(blockIdx.x + 1);
-  if (threadIdx.x == 0) {
-    sh.tiles = s1 - s0;
-    sh.at = {0, 0, 0, 0};
-    sh.offset = 0;
-  }
-  __syncthreads();
   const bool one = p.requests <= THREADS;
+  for (int base = 0; base < p.requests; base += THREADS) {
+    if (base) __syncthreads();
+    scan(base);
+  }
+  // equal spans, the first ones a tile longer; with fewer tiles than CTAs the first ones have
+  // one each, so that spans with tiles stand side by side
+  const long long total = before;
+  const unsigned grid = gridDim.x, b = blockIdx.x;
+  const long long each = total < 0x7fffffffLL ? (unsigned)total / grid : total / grid;
+  const long long more = total - each * grid;
+  const long long s0 = each * b + (b < more ? b : more), tiles = each + (b < more ? 1 : 0);
+  if (threadIdx.x == 0) sh.tiles = tiles;
   before = 0;
   for (int base = 0; base < p.requests; base += THREADS) {
-    if (!one) scan(base);
-    if (s1 > s0 && mine > 0 && excl <= s0 && s0 < excl + mine) {
-      sh.at.r = base + (int)threadIdx.x;
-      sh.offset = s0 - excl;
+    if (!one) {
+      __syncthreads();
+      scan(base);
     }
-  }
-  __syncthreads();
-  if (s1 > s0 && warp == 0) {  // the query tile within the request
-    const Request q = load_request(p, sh.at.r);
-    const int nqt = (int)(((int64_t)q.n * p.group + ROWS - 1) / ROWS);
-    long long left = sh.offset;
-    for (int base = 0; base < nqt; base += 32) {
-      const int t = base + lane;
-      const int c = t < nqt ? tile_range<ROWS, KT>(p, q, t).count() : 0;
-      const long long own = (long long)c * p.kv_heads;
+    const unsigned owner = __ballot_sync(0xffffffffu, tiles > 0 && mine > 0 && excl <= s0 && s0 < excl + mine);
+    if (!owner) continue;
+    const int src = __ffs(owner) - 1;  // this warp has the span's first request: find the query tile, head and key tile
+    if (lane == src) {
+      sh.at.r = base + (int)threadIdx.x;
+      sh.q = q;
+    }
+    const Request o = share(src);
+    long long left = s0 - __shfl_sync(0xffffffffu, excl, src);
+    const int m = query_tiles(o.n);
+    for (int first = 0; first < m; first += 32) {
+      const int t = first + lane;
+      const int n = t < m ? tile_range<ROWS, KT>(p, o, t).count() : 0;
+      const long long own = (long long)n * p.kv_heads;
       long long s = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
+      for (int k = 1; k < 32; k <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, s, k);
+        if (lane >= k) s += u;
       }
       const unsigned over = __ballot_sync(0xffffffffu, s > left);
       if (over) {
         if (lane == __ffs(over) - 1) {
-          const long long in = left - (s - own);
+          const long long in = left - (s - own);  // below 2^31: heads times tiles of one query tile
           sh.at.qt = t;
-          sh.at.h = (int)(in / c);
-          sh.at.tile = (int)(in - (long long)sh.at.h * c);
+          sh.at.h = (int)((unsigned)in / (unsigned)n);
+          sh.at.tile = (int)in - sh.at.h * n;
         }
         break;
       }
@@ -185,13 +195,15 @@ struct Walk {
   long long left;
   Request q;
 
-  __device__ __forceinline__ Walk(const AttnParams& p, const SpanShared& sh) : at(sh.at), left(sh.tiles) {
-    if (left > 0) q = load_request(p, at.r);
+  __device__ __forceinline__ void start(const SpanShared& sh) {
+    at = sh.at;
+    left = sh.tiles;
+    q = sh.q;
   }
 
   __device__ __forceinline__ bool next(const AttnParams& p, Item& it) {
     if (left <= 0) return false;
-    const int rows = q.n * p.group;
+    const int rows = q.n * (int)p.group.d;
     it.q = q;
     it.rows = rows;
     it.r = at.r;
@@ -207,7 +219,7 @@ struct Walk {
     at.tile = 0;
     if (++at.h == p.kv_heads) {
       at.h = 0;
-      if ((int64_t)++at.qt * ROWS >= rows) {
+      if (++at.qt * ROWS >= rows) {
         at.qt = 0;
         if (left > 0) {  // a request with rows follows
           q.n = 0;
@@ -230,11 +242,11 @@ struct RowView {
 
 __device__ __forceinline__ RowView row_view(const AttnParams& p, const Item& it, int row) {
   RowView v;
-  const int t = row / p.group, g = row - t * p.group;
+  const int t = row / p.group, g = row - t * (int)p.group.d;
   v.pos = it.q.len - it.q.n + t;
   v.see_hi = p.causal ? min(v.pos + 1, it.q.len) : it.q.len;
   v.see_lo = p.window ? v.pos - p.window + 1 : 0;
-  v.slope = p.slopes && row < it.rows ? p.slopes[it.h * p.group + g] * 1.4426950408889634f : 0.0f;
+  v.slope = p.slopes && row < it.rows ? p.slopes[it.h * (int)p.group.d + g] * 1.4426950408889634f : 0.0f;
   if (row >= it.rows) v.see_hi = 0;
   return v;
 }
@@ -261,7 +273,7 @@ __device__ __forceinline__ float ex2(float x) {
 // Block and place in it of a key; -1 for a block number outside the cache.
 __device__ __forceinline__ int64_t block_of(const AttnParams& p, int r, int key, int& in_page) {
   const int j = key / p.page;
-  in_page = key - j * p.page;
+  in_page = key - j * (int)p.page.d;
   const int b = p.table[(int64_t)r * p.table_stride + j];
   if (b < 0 || b >= p.num_blocks) {
     *p.status = kStatusBadIndex;

@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
   find_span<kRows, kKeys, kThreads>(p, span);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool wrote[2] = {false, false};
-  Walk<kRows, kKeys> walk(p, span);
+  Walk<kRows, kKeys> walk;
+  walk.start(span);
   Item it;
   while (walk.next(p, it)) {
     __syncthreads();
@@ -80,8 +81,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
       const int row = it.qt * kRows + r;
       const uint16_t* src = nullptr;
       if (row < it.rows) {
-        const int t = row / p.group, g = row - t * p.group;
-        src = static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * p.group + g) * p.q_hs;
+        const int t = row / p.group, g = row - t * (int)p.group.d;
+        src = static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * (int)p.group.d + g) * p.q_hs;
       }
       fill_row<DP>(p, sq + r * LD, src, threadIdx.x & 3, 4);
     }
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
       const int local = warp * 16 + (lane >> 2) + i * 8, row = it.qt * kRows + local;
       if (row >= it.rows) continue;
       if (whole) {
-        const int t = row / p.group, head = it.h * p.group + row - t * p.group;
+        const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
         const float inv = l[i] > 0.0f ? 1.0f / l[i] : 0.0f;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
 #pragma unroll
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ Attn
   const int c = blockIdx.x;
   const int* h = p.headers + ((int64_t)c * 2 + 1) * kHeaderInts;
   if (!(h[0] & kThere)) return;
-  const int q0 = h[1], rows = h[2], qt = h[3], head0 = h[4] * p.group;
+  const int q0 = h[1], rows = h[2], qt = h[3], head0 = h[4] * (int)p.group.d;
   const int row_base = qt * p.tile_rows;
   const int local_rows = min(rows - row_base, p.tile_rows);
   if ((int)blockIdx.y * 8 >= local_rows) return;  // not one row for these warps
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ Attn
       for (int k = 0; k < kJoinRows; ++k) {
         const int row = row_base + local0 + k * warps;
         if (local0 + k * warps >= local_rows) continue;
-        const int t = row / p.group, head = head0 + row - t * p.group;
+        const int t = row / p.group, head = head0 + row - t * (int)p.group.d;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
         const float inv = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
         const float f[4] = {a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv};

@@ -2,11 +2,11 @@
 // multiple of 8 tokens.
 //
 // A CTA (one an SM, resident) takes items of 256 query rows (128 for heads of more than 128
-// elements), in halves of 128, against tiles of 128 keys.  Of its twelve warps one loads keys and
+// elements), in halves of 128, against tiles of 128 keys.  Of its twelve warps two load keys and
 // values by TMA, box by box through the block table, into a ring of shared-memory slots; one
 // issues the matrix instructions; a warpgroup for each half turns scores into weights (the last
-// two warps only complete the third warpgroup, which hands registers to the others).  A thread
-// of a warpgroup owns one query row, so row maxima and sums need no exchange between threads.
+// warp only completes the third warpgroup, which hands registers to the others).  A thread of a
+// warpgroup owns one query row, so row maxima and sums need no exchange between threads.
 //
 // Tensor memory (512 columns of 128 lanes): two score buffers of 128 columns, and 256 columns for
 // the weighted sums, 128 a half or all for one half.  The weights, 16-bit, take the first 64
@@ -29,10 +29,10 @@ namespace ar {
 namespace {
 
 constexpr int kKeys = 128, kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;  // and kLoadWarp + 1
 constexpr uint32_t kTmemCols = 512;
-// 384 threads at 168 registers; the third warpgroup gives 96 a thread to the other two
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// 384 threads at 168 registers; the third warpgroup gives 80 a thread to the other two
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168, "the split uses what the launch has");
 
 template <int DP>
@@ -57,6 +57,7 @@ struct Bars {
   uint64_t p[4], p2[4];          // weights of the first and second 64 keys stored
   uint64_t o[4];                 // sum complete: of half 0, 1 (an item), of one half (a tile, by turns)
   uint64_t drain;
+  uint32_t issued[10];           // rounds whose copies were issued, a slot
   uint32_t tmem;
   int stop;
 };
@@ -196,59 +197,69 @@ __device__ __forceinline__ bool single_half(const Item& it) {
   return Shape<DP>::kRows == 128 || it.rows - it.qt * Shape<DP>::kRows <= 128;
 }
 
+// Two warps load, one the keys and one the values: with small pages a tile is up to 32 copies, and
+// issuing them is what takes the time.  The lanes look the blocks up, one elected lane issues.
 template <int DP>
-__device__ void load_role(const AttnParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, const SpanShared& span, Bars& b, uint32_t ring) {
+__device__ void load_role(const AttnParams& p, bool keys, const CUtensorMap* map, const SpanShared& span, Bars& b, uint32_t ring) {
   using S = Shape<DP>;
   const int lane = threadIdx.x & 31;
   const int boxes = kKeys / p.box_rows;
-  const int box = lane / S::kBlocks, cb = lane - box * S::kBlocks;
-  const bool issues = box < boxes;
-  Walk<S::kRows, kKeys> walk(p, span);
+  const bool one = elect_one();
+  Walk<S::kRows, kKeys> walk;
+  walk.start(span);
   Item it = {};
   uint32_t n = 0;
   bool ok = true;
   while (ok && walk.next(p, it)) {
     const int nt = it.end - it.begin;
-    const bool one = single_half<DP>(it);
-    // block and place of this lane's box, of the tile after next, the last and the one before
-    int block_next = 0, page_next = 0, block_cur = 0, page_cur = 0, block_prev = 0, page_prev = 0;
+    const bool ahead = single_half<DP>(it);  // scores run a tile ahead
+    // block of this lane's box, and its place in the block
+    int block = 0, place = 0;
     auto look_up = [&](int t) {
-      const int key = it.range.tile(it.begin + t) * kKeys + box * p.box_rows;
-      int64_t w = -1;
-      page_next = 0;
-      if (issues && key < it.q.len) w = block_of(p, it.r, key, page_next);
-      block_next = w < 0 ? (int)p.num_blocks : (int)w;  // outside the cache: the copy fills with zeros
+      const int key = it.range.tile(it.begin + t) * kKeys + lane * p.box_rows;
+      block = -1;
+      place = 0;
+      if (lane < boxes && key < it.q.len) {
+        const int j = key / p.page;
+        place = key - j * (int)p.page.d;
+        block = p.table[(int64_t)it.r * p.table_stride + j];
+      }
     };
     look_up(0);
-    // keys 0, then (values t, keys t + 1), or (keys t + 1, values t) where scores run ahead
-    for (int j = 0; ok && j < 2 * nt; ++j) {
-      const bool keys = one ? (j == 0 || ((j & 1) && j + 1 < 2 * nt)) : (j & 1) == 0;
-      if (keys) {
-        const int t = (j + 1) >> 1;
-        block_prev = block_cur;
-        page_prev = page_cur;
-        block_cur = block_next;
-        page_cur = page_next;
-        if (t + 1 < nt) look_up(t + 1);
+    for (int t = 0; ok && t < nt; ++t) {
+      // ring units of the item: keys 0, then (values t, keys t + 1), or (keys t + 1, values t) where scores run ahead
+      uint32_t i;
+      if (keys)
+        i = t == 0 ? 0 : (ahead ? 2 * t - 1 : 2 * t);
+      else
+        i = ahead && t + 1 < nt ? 2 * t + 2 : 2 * t + 1;
+      i = n + i * S::kUnits;
+      // outside the cache: the copy fills with zeros
+      int w = block, y = place;
+      if (w < 0 || w >= p.num_blocks) {
+        if (lane < boxes && it.range.tile(it.begin + t) * kKeys + lane * p.box_rows < it.q.len) *p.status = kStatusBadIndex;
+        w = (int)p.num_blocks;
       }
-      const bool behind = one && !keys && j + 1 < 2 * nt;  // values of the tile before the last keys
-      const int w = behind ? block_prev : block_cur, y = behind ? page_prev : page_cur;
-      for (int u = 0; u < S::kUnits; ++u) {
-        const uint32_t slot = n % S::kSlots, round = n / S::kSlots;
+      if (t + 1 < nt) look_up(t + 1);
+      for (int u = 0; u < S::kUnits; ++u, ++i) {
+        const uint32_t slot = i % S::kSlots, round = i / S::kSlots;
         ok = __all_sync(0xffffffffu, ok && wait_for(&b.empty[slot], (round & 1) ^ 1, b, p));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&b.full[slot], S::kUnitBytes);
-        __syncwarp();
-        if (issues && !(p.stall && n == 0))
-          tma_4d(ring + slot * S::kUnitBytes + cb * S::kBlockBytes + box * p.box_rows * 128, keys ? kmap : vmap, u * 128 + cb * 64, y, it.h, w,
-                 &b.full[slot]);
-        ++n;
+        if (one) {
+          mbar_arrive_expect_tx(&b.full[slot], S::kUnitBytes);
+          b.issued[slot] = round + 1;
+        }
+        const uint32_t dst = ring + slot * S::kUnitBytes;
+        for (int x = 0; x < boxes; ++x) {
+          const int wx = __shfl_sync(0xffffffffu, w, x), yx = __shfl_sync(0xffffffffu, y, x);
+          if (one && !(p.stall && i == 0))
+#pragma unroll
+            for (int cb = 0; cb < S::kBlocks; ++cb)
+              tma_4d(dst + cb * S::kBlockBytes + x * p.box_rows * 128, map, u * 128 + cb * 64, yx, it.h, wx, &b.full[slot]);
+        }
       }
     }
-  }
-  if (!ok) {  // copies in flight end before the CTA does
-    for (uint32_t i = n > S::kSlots ? n - S::kSlots : 0; i < n; ++i)
-      if (!(p.stall && i == 0)) mbar_wait_bounded(&b.full[i % S::kSlots], (i / S::kSlots) & 1, p.wait_cycles);
+    n += 2 * nt * S::kUnits;
   }
 }
 
@@ -261,7 +272,8 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
   // descriptors differ in the address alone, in units of 16 bytes: constant offsets are added
   const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(ring, 16), v_desc = matrix_desc(ring, S::kBlockBytes);
   const bool one = elect_one();
-  Walk<S::kRows, kKeys> walk(p, span);
+  Walk<S::kRows, kKeys> walk;
+  walk.start(span);
   Item it = {};
   uint32_t n = 0, items = 0, pairs = 0, d = 0, g = 0;
   bool ok = true;
@@ -360,7 +372,10 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
           if (!wait(&b.p[h], d & 1)) break;
           if (one) weighted(h, n, 0, 0, 256 + h * 128, i > 0);
           if (!wait(&b.p2[h], d & 1)) break;
-          if (one) weighted(h, n, 0, 1, 256 + h * 128, true);
+          if (one) {
+            weighted(h, n, 0, 1, 256 + h * 128, true);
+            if (h == 1) mma_commit(&b.empty[n % S::kSlots]);
+          }
           if (more) {
             if (h == 0 && !wait_unit(n + 1)) break;
             if (one) {
@@ -372,10 +387,7 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
           }
         }
         if (!ok) break;
-        if (one) {
-          mma_commit(&b.empty[n % S::kSlots]);
-          if (more) mma_commit(&b.empty[(n + 1) % S::kSlots]);
-        }
+        if (one && more) mma_commit(&b.empty[(n + 1) % S::kSlots]);
         n += more ? 2 : 1;
       }
       ++pairs;
@@ -424,13 +436,24 @@ __device__ __forceinline__ void shape_scores(const AttnParams& p, const Item& it
     if (!(j < pre || (j < hi && j >= lo))) s[j] = -INFINITY;
 }
 
+template <int DP>
+struct SoftmaxState {  // of a warp
+  Walk<Shape<DP>::kRows, kKeys> walk;
+  Item it, later;
+  int wrote;  // headers, a bit a slot
+};
+
 template <int DT, int DP, int EXT>
-__device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& b, uint8_t* queries, uint32_t tmem, bool (&wrote)[2]) {
+__device__ void softmax_role(const AttnParams& p, const SpanShared& span, SoftmaxState<DP>& state, Bars& b, uint8_t* queries, uint32_t tmem) {
   using S = Shape<DP>;
   const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
   const float scale = EXT ? 1.0f : p.scale_log2;
-  Walk<S::kRows, kKeys> walk(p, span);
+  // A thread's scores take most of its registers: what is the same for a warp stays in shared
+  // memory (every lane writes the same values).
+  auto& walk = state.walk;
+  Item &it = state.it, &later = state.later;
+  walk.start(span);
   uint32_t pairs = 0, d = 0, g = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -443,10 +466,11 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  auto next_item = [&](Item& it) {  // the next one with rows in this half
-    while (walk.next(p, it))
-      if (h == 0 || !single_half<DP>(it)) return true;
-    return false;
+  auto next_item = [&](Item& to) {  // the next one with rows in this half
+    bool found = false;
+    while (!found && walk.next(p, to)) found = h == 0 || !single_half<DP>(to);
+    __syncwarp();
+    return found;
   };
   // queries, 16 bytes a thread, neighbours along a row; rows and columns beyond are zero
   auto load_queries = [&](const Item& it) {
@@ -456,8 +480,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
       const int r = x / (DP / 8), c = x % (DP / 8), row = it.qt * S::kRows + h * 128 + r;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (row < it.rows && c * 8 < p.head_dim) {
-        const int t = row / p.group, e = row - t * p.group;
-        v = ld_keep(static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * p.group + e) * p.q_hs + c * 8);
+        const int t = row / p.group, e = row - t * (int)p.group.d;
+        v = ld_keep(static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * (int)p.group.d + e) * p.q_hs + c * 8);
       }
       *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
     }
@@ -465,7 +489,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.q[h]);
   };
-  Item it = {}, later = {};
+  state.wrote = 0;
   bool have = next_item(it);
   if (have) load_queries(it);
   while (have) {
@@ -570,7 +594,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
       untwo(sum, lo, hi);
       const float l = lo + hi;
       const bool mine = row < it.rows;
-      const int t = row / p.group, head = it.h * p.group + row - t * p.group;
+      const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
       const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * S::kRows + h * 128 + tid;
@@ -602,12 +626,16 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Bars& 
       if (mine && !whole) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
     }
     if (!whole) {
-      wrote[slot] = true;
+      state.wrote |= 1 << slot;
       if (threadIdx.x == 0) write_header(p, slot, kThere | (it.last ? kEnds : 0), &it);
     }
     it = later;
+    __syncwarp();
     have = more;
   }
+  if (threadIdx.x == 0)
+    for (int x = 0; x < 2; ++x)
+      if (!(state.wrote >> x & 1)) write_header(p, x, 0, nullptr);
 }
 
 template <int DT, int DP, int EXT>
@@ -617,12 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
   extern __shared__ uint8_t raw[];
   __shared__ SpanShared span;
   __shared__ Bars b;
+  __shared__ SoftmaxState<DP> states[8];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // swizzled tiles start on 1024 bytes
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&b.full[i], 1);
       mbar_init(&b.empty[i], 1);
+      b.issued[i] = 0;
     }
     for (int x = 0; x < 4; ++x) {
       mbar_init(&b.s[x], 1);
@@ -648,23 +678,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
   find_span<S::kRows, kKeys, kThreads>(p, span);
 
   const uint32_t queries = smem_addr(smem), ring = queries + S::kQueryBytes;
-  bool wrote[2] = {false, false};
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp)
-      load_role<DP>(p, &kmap, &vmap, span, b, ring);
+      load_role<DP>(p, true, &kmap, span, b, ring);
+    else if (warp == kLoadWarp + 1)
+      load_role<DP>(p, false, &vmap, span, b, ring);
     else if (warp == kMmaWarp)
       mma_role<DT, DP>(p, span, b, queries, ring, tmem);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<DT, DP, EXT>(p, span, b, smem, tmem, wrote);
+    softmax_role<DT, DP, EXT>(p, span, states[warp], b, smem, tmem);
   }
-  if (threadIdx.x == 0)
-    for (int s = 0; s < 2; ++s)
-      if (!wrote[s]) write_header(p, s, 0, nullptr);
   fence_before();
   __syncthreads();
   fence_after();
+  if (b.stop && warp == kLoadWarp)  // copies in flight end before the CTA does
+    for (int i = 0; i < S::kSlots; ++i)
+      if (b.issued[i] > (p.stall && i == 0 ? 1u : 0u)) mbar_wait_bounded(&b.full[i], (b.issued[i] - 1) & 1, p.wait_cycles);
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }

@@ -12,6 +12,22 @@ namespace ar {
 
 constexpr int kStatusBadIndex = 2;  // status word: an index in device memory was out of range
 
+// Division by an invariant d of numerators below 2^31 (T. Granlund and P. Montgomery, "Division by
+// invariant integers using multiplication", PLDI 1994): n / d = (hi(n m) + n) >> s.
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  f.s = 0;
+  while (((uint64_t)1 << f.s) < d) ++f.s;
+  f.m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.s) - d)) / d + 1);
+  return f;
+}
+
 struct PlanParams {
   int requests, page;
   int64_t max_tokens, free_capacity, table_cols, table_stride;
@@ -59,7 +75,8 @@ struct RopeParams {
 
 struct AttnParams {
   int64_t tokens;
-  int requests, q_heads, kv_heads, group, head_dim;
+  int requests, q_heads, kv_heads, head_dim;
+  FastDiv group;  // q heads of a key head
   const void* q;
   void* out;
   int64_t q_ts, q_hs, o_ts, o_hs;
@@ -68,7 +85,7 @@ struct AttnParams {
   const void* v;
   int64_t k_bs, k_ps, k_hs, v_bs, v_ps, v_hs;
   int64_t num_blocks;
-  int page;
+  FastDiv page;
   const int32_t* table;
   int64_t table_stride;
   int max_len;  // keys that a table row can name, at most 2^30

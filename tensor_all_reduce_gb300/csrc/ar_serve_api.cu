@@ -370,7 +370,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.requests = a->requests;
   p.q_heads = a->q_heads;
   p.kv_heads = a->kv_heads;
-  p.group = a->q_heads / a->kv_heads;
+  p.group = ar::fast_div((uint32_t)(a->q_heads / a->kv_heads));
   p.head_dim = a->head_dim;
   p.q = a->q;
   p.out = a->out;
@@ -388,7 +388,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.v_ps = a->v_page_stride;
   p.v_hs = a->v_head_stride;
   p.num_blocks = a->num_blocks;
-  p.page = a->page_size;
+  p.page = ar::fast_div((uint32_t)pg);
   p.table = a->block_table;
   p.table_stride = ts;
   const int64_t room = a->table_cols * pg;
