@@ -10,7 +10,7 @@ namespace ar {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 128;
-constexpr int kJoinRows = 4;
+constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
   pdl_wait_and_release();
   find_span<kRows, kKeys, kThreads>(p, span);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  bool wrote[2] = {false, false};
+  bool goes_on = false;
   Walk<kRows, kKeys> walk;
   walk.start(span);
   Item it;
@@ -213,102 +213,93 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
         if ((lane & 3) == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[i], l[i]);
       }
     }
-    if (!whole) {
-      wrote[slot] = true;
-      if (threadIdx.x == 0) write_header(p, slot, kThere | (it.last ? kEnds : 0), &it);
+    if (it.first && !it.last) {
+      goes_on = true;
+      if (threadIdx.x == 0) write_header(p, span, &it);
     }
   }
-  if (threadIdx.x == 0)
-    for (int s = 0; s < 2; ++s)
-      if (!wrote[s]) write_header(p, s, 0, nullptr);
+  if (threadIdx.x == 0 && !goes_on) write_header(p, span, nullptr);
+}
+
+// A partial softmax: sum and weight sum relative to the maximum m (log2 units).
+struct Part {
+  float m, l;
+  float4 o;
+};
+
+__device__ __forceinline__ void join(Part& a, float m, float l, const float4& o) {
+  const float top = fmaxf(a.m, m), base = top == -INFINITY ? 0.0f : top;
+  const float x = ex2(a.m - base), y = ex2(m - base);
+  a.m = top;
+  a.l = a.l * x + l * y;
+  a.o = make_float4(a.o.x * x + o.x * y, a.o.y * x + o.y * y, a.o.z * x + o.z * y, a.o.w * x + o.w * y);
 }
 
 // Joins the parts of the items that more than one span holds: the blocks (c, ...) serve the item
-// that begins in span c and does not end there.  A warp takes up to four rows, W apart for the W
-// warps of those blocks (few rows: one each), with the loads of all of them in flight.
+// that begins in span c and goes on; its parts are slot 1 of span c and slot 0 of the spans behind
+// it.  Many rows with few parts (chunks): a warp takes whole rows.  Few rows with many parts
+// (single tokens): a block takes a row, its warps share the parts.
 template <int DT>
-__global__ void __launch_bounds__(256) attn_combine(const __grid_constant__ AttnParams p) {
-  __shared__ int sh_end;
+__global__ void __launch_bounds__(kJoinThreads) attn_combine(const __grid_constant__ AttnParams p) {
+  constexpr int WARPS = kJoinThreads / 32, AHEAD = 8;
+  __shared__ Part sh[WARPS][32];
   pdl_wait_and_release();
   const int c = blockIdx.x;
-  const int* h = p.headers + ((int64_t)c * 2 + 1) * kHeaderInts;
-  if (!(h[0] & kThere)) return;
-  const int q0 = h[1], rows = h[2], qt = h[3], head0 = h[4] * (int)p.group.d;
-  const int row_base = qt * p.tile_rows;
-  const int local_rows = min(rows - row_base, p.tile_rows);
-  if ((int)blockIdx.y * 8 >= local_rows) return;  // not one row for these warps
-  if (threadIdx.x == 0) sh_end = p.spans;
-  __syncthreads();
-  for (int i = c + 1 + (int)threadIdx.x; i < p.spans; i += 256)
-    if (p.headers[(int64_t)i * 2 * kHeaderInts] & kEnds) {
-      atomicMin(&sh_end, i);
-      break;
-    }
-  __syncthreads();
-  const int end = min(sh_end, p.spans - 1);  // the chain: slot 1 of span c, slot 0 of spans c + 1 .. end
-  const int lane = threadIdx.x & 31, warps = gridDim.y * 8, first = blockIdx.y * 8 + (threadIdx.x >> 5);
-  auto place = [&](int i, int local) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.tile_rows + local; };
-  for (int local0 = first; local0 < local_rows; local0 += warps * kJoinRows) {
-    float top[kJoinRows], l[kJoinRows];
+  const int* h = p.headers + (int64_t)c * kHeaderInts;
+  const int end = h[0];
+  if (end == 0) return;
+  const int q0 = h[1], rows = h[2], row_base = h[3] * p.tile_rows, head0 = h[4] * (int)p.group.d;
+  const int local_rows = min(rows - row_base, p.tile_rows), parts = end - c + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // rounds of loads one after another in either way
+  const int by_rows = (local_rows + WARPS * (int)gridDim.y - 1) / (WARPS * (int)gridDim.y) * ((parts + AHEAD - 1) / AHEAD);
+  const int by_parts = (local_rows + (int)gridDim.y - 1) / (int)gridDim.y * ((parts + WARPS * AHEAD - 1) / (WARPS * AHEAD));
+  const bool share = by_parts < by_rows;  // the warps share a row's parts
+  const int step = share ? gridDim.y : gridDim.y * WARPS;
+  for (int local = share ? blockIdx.y : blockIdx.y * WARPS + warp; local < local_rows; local += step) {
+    const int row = row_base + local;
+    const int t = row / p.group, head = head0 + row - t * (int)p.group.d;
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+    for (int e0 = 0; e0 < p.part_dim; e0 += 128) {
+      const int e = e0 + lane * 4;
+      Part a = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+      const int stride = share ? WARPS : 1;
+      for (int i0 = c + (share ? warp : 0); i0 <= end; i0 += stride * AHEAD) {
+        float2 ml[AHEAD];
+        float4 o[AHEAD];
 #pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) {
-      top[k] = -INFINITY;
-      l[k] = 0.0f;
-    }
-    for (int i = c + lane; i <= end; i += 32)
-#pragma unroll
-      for (int k = 0; k < kJoinRows; ++k)
-        if (local0 + k * warps < local_rows) top[k] = fmaxf(top[k], p.part_ml[place(i, local0 + k * warps) * 2]);
-#pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-      if (top[k] == -INFINITY) top[k] = 0.0f;  // a row that sees nothing: every weight sum is 0
-    }
-    for (int i = c + lane; i <= end; i += 32)
-#pragma unroll
-      for (int k = 0; k < kJoinRows; ++k)
-        if (local0 + k * warps < local_rows) {
-          const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + place(i, local0 + k * warps) * 2);
-          l[k] += ex2(ml.x - top[k]) * ml.y;
-        }
-#pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) l[k] = warp_sum(l[k]);
-    for (int e = lane * 4; e < p.part_dim; e += 128) {
-      float4 a[kJoinRows];
-#pragma unroll
-      for (int k = 0; k < kJoinRows; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-      for (int i = c; i <= end; ++i)
-#pragma unroll
-        for (int k = 0; k < kJoinRows; ++k)
-          if (local0 + k * warps < local_rows) {
-            const int64_t at = place(i, local0 + k * warps);
-            const float w = ex2(p.part_ml[at * 2] - top[k]);
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * p.part_dim + e);
-            a[k].x += w * v.x;
-            a[k].y += w * v.y;
-            a[k].z += w * v.z;
-            a[k].w += w * v.w;
+        for (int k = 0; k < AHEAD; ++k) {
+          const int i = i0 + k * stride;
+          ml[k] = make_float2(-INFINITY, 0.0f);
+          o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (i <= end) {
+            const int64_t at = ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.tile_rows + local;
+            ml[k] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+            if (e < p.part_dim) o[k] = *reinterpret_cast<const float4*>(p.part_o + at * p.part_dim + e);
           }
-#pragma unroll
-      for (int k = 0; k < kJoinRows; ++k) {
-        const int row = row_base + local0 + k * warps;
-        if (local0 + k * warps >= local_rows) continue;
-        const int t = row / p.group, head = head0 + row - t * (int)p.group.d;
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
-        const float inv = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
-        const float f[4] = {a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv};
-        if (p.vec) {
-          if (e < p.head_dim) st_v2(dst + e, make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (e + j < p.head_dim) st_u16(dst + e + j, round1<DT>(f[j]));
         }
-        if (p.lse && e == 0)
-          p.lse[(int64_t)(q0 + t) * p.q_heads + head] = l[k] > 0.0f ? (top[k] + log2f(l[k])) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) join(a, ml[k].x, ml[k].y, o[k]);
       }
+      if (share) {
+        __syncthreads();
+        sh[warp][lane] = a;
+        __syncthreads();
+        if (warp != 0) continue;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) join(a, sh[w][lane].m, sh[w][lane].l, sh[w][lane].o);
+      }
+      const float inv = a.l > 0.0f ? 1.0f / a.l : 0.0f;
+      const float f[4] = {a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv};
+      if (p.vec) {
+        if (e < p.head_dim) st_v2(dst + e, make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e + j < p.head_dim) st_u16(dst + e + j, round1<DT>(f[j]));
+      }
+      if (p.lse && e == 0)
+        p.lse[(int64_t)(q0 + t) * p.q_heads + head] = a.l > 0.0f ? (a.m + log2f(a.l)) * 0.69314718055994531f : -INFINITY;
     }
   }
 }

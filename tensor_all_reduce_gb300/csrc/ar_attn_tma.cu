@@ -440,7 +440,6 @@ template <int DP>
 struct SoftmaxState {  // of a warp
   Walk<Shape<DP>::kRows, kKeys> walk;
   Item it, later;
-  int wrote;  // headers, a bit a slot
 };
 
 template <int DT, int DP, int EXT>
@@ -489,7 +488,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.q[h]);
   };
-  state.wrote = 0;
+  bool goes_on = false;
   bool have = next_item(it);
   if (have) load_queries(it);
   while (have) {
@@ -625,17 +624,15 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       if (mine && whole && p.lse) p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       if (mine && !whole) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
     }
-    if (!whole) {
-      state.wrote |= 1 << slot;
-      if (threadIdx.x == 0) write_header(p, slot, kThere | (it.last ? kEnds : 0), &it);
+    if (it.first && !it.last) {
+      goes_on = true;
+      if (threadIdx.x == 0) write_header(p, span, &it);
     }
     it = later;
     __syncwarp();
     have = more;
   }
-  if (threadIdx.x == 0)
-    for (int x = 0; x < 2; ++x)
-      if (!(state.wrote >> x & 1)) write_header(p, x, 0, nullptr);
+  if (threadIdx.x == 0 && !goes_on) write_header(p, span, nullptr);
 }
 
 template <int DT, int DP, int EXT>

@@ -288,7 +288,7 @@ struct Workspace {
 Workspace workspace_of(int64_t spans, int64_t rows, int64_t part_dim) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   Workspace w;
-  w.ml = up(spans * 2 * 8 * 4);
+  w.ml = up(spans * 8 * 4);
   w.o = w.ml + up(spans * 2 * rows * 8);
   w.bytes = w.o + up(spans * 2 * rows * part_dim * 4);
   return w;
@@ -439,7 +439,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, cap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
-  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, (unsigned)(p.tile_rows + 31) / 32), 256, 1, args, 0, stream);
+  st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, 8), 256, 1, args, 0, stream);
   if (st == AR_OK) ctx->last_variant = tma ? "paged_attention_tma" : "paged_attention_mma";
   return st;
 }
