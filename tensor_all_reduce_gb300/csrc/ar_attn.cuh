@@ -21,6 +21,7 @@
 #pragma once
 
 #include "ar_common.cuh"
+#include "ar_fastdiv.cuh"
 #include "ar_serve.h"
 
 namespace ar {
@@ -31,8 +32,6 @@ constexpr int kHeaderInts = 8;
 
 constexpr int kSplitCost = 12, kWholeMost = 24;
 constexpr int kFewRows = 64;  // items of so few rows are split at any length: their parts are small
-
-__device__ __forceinline__ int operator/(int n, const FastDiv& f) { return (int)((__umulhi((uint32_t)n, f.m) + (uint32_t)n) >> f.s); }
 
 struct Request {
   int q0, n, len, prefix;  // first row of q, new tokens, keys, keys that every row sees

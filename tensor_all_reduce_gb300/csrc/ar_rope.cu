@@ -10,6 +10,7 @@
 // 2^-64, so at position 2^20 and one radian a position the angle is off by less than 2^-35 turns,
 // under the 2^-33 of the cut to 32 bits.
 #include "ar_common.cuh"
+#include "ar_fastdiv.cuh"
 #include "ar_serve.h"
 
 namespace ar {
@@ -124,57 +125,85 @@ __device__ __forceinline__ uint4 ld_row(const void* p) {
   return v;
 }
 
-constexpr int kMaxTokensPerStep = 4;
+constexpr int kMaxTokensPerStep = 8;
 constexpr int kHeadsInFlight = 4;
 enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 
-// Rows on 16-byte boundaries and heads of a multiple of 8 elements: L lanes hold a head, 8
-// elements each (L the power of two at or above head_dim / 8), so a warp serves 32 / L heads at
-// a time.  A CTA takes `step` tokens: it computes their angles once, for all heads, into shared
-// memory (a sincos a head would cost more than the memory traffic does), and each lane keeps
-// the eight that its elements need in registers over the heads of a token.  Four heads a
-// lane are loaded before the first is worked on, so that an SM has about 48 KB in flight.  The
-// partner of an element is in the lane itself (pairs), in one other lane at the same place
-// (halves that are a multiple of 8: a shuffle), or anywhere (kHalvesAny: through shared
-// memory, rows of 8 skewed by one float so that lanes fall into different banks).
-// With few tokens the heads are shared out over `split` CTAs a token.
-template <int DT, int L, int MODE>
+// a * b, a * b + c on two floats at a time
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// Rows on 16-byte boundaries and heads of a multiple of 8 elements: n = head_dim / 8 lanes hold a
+// head, 8 elements each, and a warp as many heads as fit (three of 80 elements, for instance).
+// A CTA takes `step` tokens: it computes their angles once, for all heads, into shared memory (a
+// sincos a head would cost more than the memory traffic does), then works through the tokens' q
+// heads, k heads and v heads, four a lane loaded before the first is worked on, so that an SM
+// has about 48 KB in flight.  The partner of an element is in the lane itself (pairs), in
+// one other lane at the same place (halves that are a multiple of 8: a shuffle), or anywhere
+// (kHalvesAny: through shared memory, rows of 8 skewed by one float so that lanes fall into
+// different banks).  With few tokens the heads are shared out over `split` CTAs a token.
+template <int DT, int MODE>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_vec(const __grid_constant__ RopeParams p, int step, int split) {
-  constexpr int GROUPS = kRopeThreads / L;
   __shared__ unsigned long long turn[AR_MAX_HEAD_DIM / 2];
   __shared__ int axis[AR_MAX_HEAD_DIM / 2];
   __shared__ __align__(16) float cosv[kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];
   __shared__ __align__(16) float sinv[kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];
   __shared__ int64_t k_at[kMaxTokensPerStep], v_at[kMaxTokensPerStep];  // cache offsets of a token, -1: none
   __shared__ float skew[MODE == kHalvesAny ? kRopeThreads * 9 : 1];
-  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const int n = p.head_dim / 8, per_warp = 32 / n, groups = per_warp * (kRopeThreads / 32);
+  const int wl = threadIdx.x & 31, in_warp = wl / n;
+  const int lane = wl - in_warp * n, first = in_warp * n;  // place in the head; the head's first lane
+  const bool there = in_warp < per_warp;
+  const int group = (int)(threadIdx.x >> 5) * per_warp + in_warp;
   const int e0 = lane * 8;
-  const bool there = e0 < p.head_dim;
   pdl_wait_and_release();
   for (int i = threadIdx.x; i < p.half; i += kRopeThreads) {
     turn[i] = turn_of(p.inv_freq[i]);
     axis[i] = axis_of(p, i);
   }
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (there && p.q.weight) wq = ld_keep(static_cast<const uint16_t*>(p.q.weight) + e0);
-  if (there && p.k.weight) wk = ld_keep(static_cast<const uint16_t*>(p.k.weight) + e0);
-  const float one = p.gemma ? 1.0f : 0.0f;
-  // the place of this lane's first frequency, and whether its elements turn
-  const int f0 = MODE == kPairs ? lane * 4 : (e0 < p.half ? e0 : e0 - p.half);
+  // Sum over a head's lanes, to all of them: windows of 1, 2, 4, .. lanes by doubling, and the
+  // head as the windows that the bits of n name, low bits first.
+  auto rotated = [&](int by) {
+    const int x = lane + by;
+    return first + (x >= n ? x - n : x);
+  };
+  auto head_sum = [&](float s) {
+    float sum = 0.0f;
+    int off = 0;
+#pragma unroll
+    for (int k = 1; k <= 32; k <<= 1) {
+      if (n & k) {
+        sum = off ? sum + __shfl_sync(0xffffffffu, s, rotated(off)) : s;
+        off += k;
+      }
+      if (2 * k <= n) s += __shfl_sync(0xffffffffu, s, rotated(k));
+    }
+    return sum;
+  };
 
-  const int heads = p.q.heads + p.k.heads * (p.k_cache ? 2 : 1);
-  const int per = (heads + split - 1) / split;
   const int64_t units = (p.tokens + step - 1) / step * split;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t t0 = u / split * step;
-    const int h_lo = (int)(u % split) * per, h_hi = min(h_lo + per, heads);
-    const int n = (int)min((int64_t)step, p.tokens - t0);
+    const int mine = (int)(u % split) * groups + group, stride = groups * split;
+    const int tokens = (int)min((int64_t)step, p.tokens - t0);
     __syncthreads();
-    for (int x = threadIdx.x; x < n * p.half; x += kRopeThreads) {
-      const int t = x / p.half, i = x - t * p.half;
+    for (int x = threadIdx.x; x < tokens * p.half; x += kRopeThreads) {
+      const int t = x / p.half_div, i = x - t * p.half;
       angle(turn[i], p.positions[axis[i] * p.pos_stride + t0 + t], &sinv[t][i], &cosv[t][i]);
     }
-    if (p.k_cache && threadIdx.x >= kRopeThreads - 32 && (int)threadIdx.x - (kRopeThreads - 32) < n) {
+    if (p.k_cache && threadIdx.x >= kRopeThreads - 32 && (int)threadIdx.x - (kRopeThreads - 32) < tokens) {
       const int t = threadIdx.x - (kRopeThreads - 32);
       const int64_t slot = p.slots[t0 + t];
       k_at[t] = v_at[t] = -1;
@@ -187,110 +216,129 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_vec(const __grid_constan
       }
     }
     __syncthreads();
-    for (int t = 0; t < n; ++t) {
-      float c[8], s[8];
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {  // q heads, k heads
+      const HeadRows& r = kind ? p.k : p.q;
+      const int total = tokens * r.heads;
+      float2 w[4];
+      if (r.weight && there) {
+        float f[8];
+        unpack8<DT>(ld_keep(static_cast<const uint16_t*>(r.weight) + e0), f);
+        const float one = p.gemma ? 1.0f : 0.0f;
 #pragma unroll
-      for (int i = 0; i < (MODE == kPairs ? 4 : 8); ++i) {
-        const int f = MODE == kHalvesAny ? (e0 + i < p.half ? e0 + i : e0 + i - p.half) : f0 + i;
-        const bool turns = MODE == kHalvesAny ? e0 + i < 2 * p.half : f < p.half;
-        c[i] = turns ? cosv[t][f] : 0.0f;
-        s[i] = turns ? sinv[t][f] : 0.0f;
-        if (MODE != kPairs && e0 + i < p.half) s[i] = -s[i];  // a' = a cos - b sin, b' = b cos + a sin
+        for (int i = 0; i < 4; ++i) w[i] = make_float2(f[2 * i] + one, f[2 * i + 1] + one);
       }
-      for (int hb = h_lo + group; hb - group < h_hi; hb += GROUPS * kHeadsInFlight) {
+      for (int base = 0; base < total; base += stride * kHeadsInFlight) {
         uint4 raw[kHeadsInFlight];
 #pragma unroll
         for (int j = 0; j < kHeadsInFlight; ++j) {
-          const int h = hb + j * GROUPS;
+          const int x = base + j * stride + mine;
           raw[j] = make_uint4(0, 0, 0, 0);
-          if (h < h_hi && there) {
-            const uint16_t* src;
-            if (h < p.q.heads)
-              src = static_cast<const uint16_t*>(p.q.in) + (t0 + t) * p.q.in_ts + h * p.q.in_hs;
-            else if (h < p.q.heads + p.k.heads)
-              src = static_cast<const uint16_t*>(p.k.in) + (t0 + t) * p.k.in_ts + (h - p.q.heads) * p.k.in_hs;
-            else
-              src = static_cast<const uint16_t*>(p.v) + (t0 + t) * p.v_ts + (h - p.q.heads - p.k.heads) * p.v_hs;
-            raw[j] = ld_row(src + e0);
+          if (x < total && there) {
+            const int t = x / r.div, h = x - t * r.heads;
+            raw[j] = ld_row(static_cast<const uint16_t*>(r.in) + (t0 + t) * r.in_ts + h * r.in_hs + e0);
           }
         }
 #pragma unroll
         for (int j = 0; j < kHeadsInFlight; ++j) {
-          if (hb - group + j * GROUPS >= h_hi) break;  // the same for the whole CTA
-          const int h = hb + j * GROUPS;
-          const bool is_q = h < p.q.heads, is_v = h >= p.q.heads + p.k.heads;
-          float x[8], y[8];
-          unpack8<DT>(raw[j], x);
-          if (p.q.weight || p.k.weight) {  // the whole warp takes part: its heads may be of different kinds
-            float ss = 0.0f;
+          if (base + j * stride >= total) break;  // the same for the whole grid
+          const int x = base + j * stride + mine;
+          const int t = min(x, total - 1) / r.div, h = x - t * r.heads;
+          float f[8];
+          float2 a[4], y[4];
+          unpack8<DT>(raw[j], f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+          for (int i = 0; i < 4; ++i) a[i] = make_float2(f[2 * i], f[2 * i + 1]);
+          if (r.weight) {
+            float2 ss = mul2(a[0], a[0]);
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (is_q ? p.q.weight != nullptr : p.k.weight != nullptr) {
-              const float rs = rsqrtf(ss * p.inv_dim + p.eps);
-              float w[8];
-              unpack8<DT>(is_q ? wq : wk, w);
+            for (int i = 1; i < 4; ++i) ss = fma2(a[i], a[i], ss);
+            const float rs = rsqrtf(head_sum(ss.x + ss.y) * p.inv_dim + p.eps);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * (w[i] + one);
-            }
+            for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], make_float2(rs, rs)), w[i]);
           }
+          // an element that does not turn keeps its value, infinities included
           if constexpr (MODE == kPairs) {
+            const float4 c = *reinterpret_cast<const float4*>(&cosv[t][lane * 4]), s = *reinterpret_cast<const float4*>(&sinv[t][lane * 4]);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const bool turns = f0 + i < p.half;  // an element that does not turn keeps its value, infinities included
-              y[2 * i] = turns ? x[2 * i] * c[i] - x[2 * i + 1] * s[i] : x[2 * i];
-              y[2 * i + 1] = turns ? x[2 * i + 1] * c[i] + x[2 * i] * s[i] : x[2 * i + 1];
+              const float2 turned = fma2(make_float2(a[i].y, a[i].x), make_float2(-sc[i], sc[i]), mul2(a[i], make_float2(cc[i], cc[i])));
+              y[i] = lane * 4 + i < p.half ? turned : a[i];
             }
           } else if constexpr (MODE == kHalves8) {
-            const int src = e0 < p.half ? lane + p.half / 8 : (e0 < 2 * p.half ? lane - p.half / 8 : lane);
+            const bool low = e0 < p.half, turns = e0 < 2 * p.half;
+            const int f0 = turns ? (low ? e0 : e0 - p.half) : 0;
+            const int src = first + (turns ? (low ? lane + p.half / 8 : lane - p.half / 8) : lane);
+            const float sign = low ? -1.0f : 1.0f;  // a' = a cos - b sin, b' = b cos + a sin
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float other = __shfl_sync(0xffffffffu, x[i], src, L);
-              y[i] = e0 < 2 * p.half ? x[i] * c[i] + other * s[i] : x[i];
+            for (int i = 0; i < 4; ++i) {
+              const float2 other = make_float2(__shfl_sync(0xffffffffu, a[i].x, src & 31), __shfl_sync(0xffffffffu, a[i].y, src & 31));
+              const float2 c = *reinterpret_cast<const float2*>(&cosv[t][f0 + 2 * i]), s = *reinterpret_cast<const float2*>(&sinv[t][f0 + 2 * i]);
+              const float2 turned = fma2(other, make_float2(sign * s.x, sign * s.y), mul2(a[i], c));
+              y[i] = turns ? turned : a[i];
             }
           } else {
-            float* row = skew + group * L * 9;  // element e at e + e / 8
+            float* row = skew + (threadIdx.x - lane) * 9;  // element e at e + e / 8
 #pragma unroll
-            for (int i = 0; i < 8; ++i) row[lane * 9 + i] = x[i];
+            for (int i = 0; i < 8; ++i) row[lane * 9 + i] = i & 1 ? a[i / 2].y : a[i / 2].x;
             __syncwarp();
+            float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int e = e0 + i, q = e < p.half ? e + p.half : (e < 2 * p.half ? e - p.half : e);
-              y[i] = e < 2 * p.half ? x[i] * c[i] + row[q + (q >> 3)] * s[i] : x[i];
+              const int e = e0 + i;
+              const bool low = e < p.half;
+              const float own = i & 1 ? a[i / 2].y : a[i / 2].x;
+              v[i] = own;
+              if (there && e < 2 * p.half) {  // (lanes behind the warp's last head would read behind the array)
+                const int q = low ? e + p.half : e - p.half, k = low ? e : q;
+                const float other = row[q + (q >> 3)];
+                v[i] = low ? own * cosv[t][k] - other * sinv[t][k] : own * cosv[t][k] + other * sinv[t][k];
+              }
             }
             __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = make_float2(v[2 * i], v[2 * i + 1]);
           }
-          if (h < h_hi && there) {
-            if (is_v) {
-              if (v_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + v_at[t] + (h - p.q.heads - p.k.heads) * p.vc_hs + e0, raw[j]);
-            } else {
-              const uint4 out = pack8<DT>(y);
-              const HeadRows& r = is_q ? p.q : p.k;
-              const int hh = is_q ? h : h - p.q.heads;
-              if (r.out) st_v4(static_cast<uint16_t*>(r.out) + (t0 + t) * r.out_ts + hh * r.out_hs + e0, out);
-              if (!is_q && p.k_cache && k_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + k_at[t] + hh * p.kc_hs + e0, out);
-            }
+          if (x < total && there) {
+            const uint4 out = make_uint4(pack2<DT>(y[0].x, y[0].y), pack2<DT>(y[1].x, y[1].y), pack2<DT>(y[2].x, y[2].y), pack2<DT>(y[3].x, y[3].y));
+            if (r.out) st_v4(static_cast<uint16_t*>(r.out) + (t0 + t) * r.out_ts + h * r.out_hs + e0, out);
+            if (kind && p.k_cache && k_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + k_at[t] + h * p.kc_hs + e0, out);
           }
+        }
+      }
+    }
+    if (!p.k_cache) continue;
+    const int total = tokens * p.k.heads;
+    for (int base = 0; base < total; base += stride * kHeadsInFlight) {  // v heads: copied
+      uint4 raw[kHeadsInFlight];
+#pragma unroll
+      for (int j = 0; j < kHeadsInFlight; ++j) {
+        const int x = base + j * stride + mine;
+        if (x < total && there) {
+          const int t = x / p.k.div, h = x - t * p.k.heads;
+          raw[j] = ld_stream(static_cast<const uint16_t*>(p.v) + (t0 + t) * p.v_ts + h * p.v_hs + e0);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kHeadsInFlight; ++j) {
+        const int x = base + j * stride + mine;
+        if (x < total && there) {
+          const int t = x / p.k.div, h = x - t * p.k.heads;
+          if (v_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + v_at[t] + h * p.vc_hs + e0, raw[j]);
         }
       }
     }
   }
 }
 
-template <int DT, int L>
+template <int DT>
 const void* vec_of(int mode) {
   switch (mode) {
-    case kPairs: return reinterpret_cast<const void*>(&rope_vec<DT, L, kPairs>);
-    case kHalves8: return reinterpret_cast<const void*>(&rope_vec<DT, L, kHalves8>);
-    default: return reinterpret_cast<const void*>(&rope_vec<DT, L, kHalvesAny>);
+    case kPairs: return reinterpret_cast<const void*>(&rope_vec<DT, kPairs>);
+    case kHalves8: return reinterpret_cast<const void*>(&rope_vec<DT, kHalves8>);
+    default: return reinterpret_cast<const void*>(&rope_vec<DT, kHalvesAny>);
   }
-}
-
-template <int DT>
-const void* vec_of(int dim, int mode) {
-  if (dim <= 64) return vec_of<DT, 8>(mode);
-  return dim <= 128 ? vec_of<DT, 16>(mode) : vec_of<DT, 32>(mode);
 }
 
 }  // namespace
@@ -299,19 +347,19 @@ const void* rope_scalar_kernel(bool bf16) {
   return bf16 ? reinterpret_cast<const void*>(&rope_scalar<kBF16>) : reinterpret_cast<const void*>(&rope_scalar<kF16>);
 }
 
-const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs) {
+const void* rope_vec_kernel(bool bf16, int half, bool pairs) {
   const int mode = pairs ? kPairs : (half % 8 == 0 ? kHalves8 : kHalvesAny);
-  return bf16 ? vec_of<kBF16>(head_dim, mode) : vec_of<kF16>(head_dim, mode);
+  return bf16 ? vec_of<kBF16>(mode) : vec_of<kF16>(mode);
 }
 
 RopeGrid rope_vec_grid(const RopeParams& p, int sm_count) {
-  // kMaxTokensPerStep tokens a CTA once every resident CTA has one such step, else single
-  // tokens; below one token an SM the heads of a token go to several CTAs, as long as each has
-  // a round of heads
-  const int lanes = p.head_dim <= 64 ? 8 : (p.head_dim <= 128 ? 16 : 32);
-  const int heads = p.q.heads + p.k.heads * (p.k_cache ? 2 : 1), groups = kRopeThreads / lanes;
+  // several tokens a CTA once every resident CTA has such a step, else single tokens; below one
+  // token an SM the heads of a token go to several CTAs, as long as each has a round of heads
+  const int groups = 32 / (p.head_dim / 8) * (kRopeThreads / 32);
+  const int heads = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;
   RopeGrid g;
-  g.step = p.tokens >= (int64_t)kMaxTokensPerStep * 3 * sm_count ? kMaxTokensPerStep : 1;
+  g.step = kMaxTokensPerStep;
+  while (g.step > 1 && p.tokens < (int64_t)g.step * 3 * sm_count) g.step /= 2;
   g.split = 1;
   while (g.step == 1 && p.tokens * g.split < sm_count && heads > groups * g.split) g.split *= 2;
   const int64_t units = (p.tokens + g.step - 1) / g.step * g.split;

@@ -50,6 +50,7 @@ struct HeadRows {  // [tokens, heads, head_dim] with unit last stride
   int64_t in_ts, in_hs, out_ts, out_hs;
   const void* weight;  // NULL: no norm
   int heads;
+  FastDiv div;  // by heads
 };
 
 struct RopeParams {
@@ -60,6 +61,7 @@ struct RopeParams {
   int64_t v_ts, v_hs;
   float eps, inv_dim;
   int gemma, half, pairs, axes, dealt;  // half: frequencies, rot_dim / 2
+  FastDiv half_div;
   int sections[AR_MAX_ROPE_AXES];
   const int32_t* positions;
   int64_t pos_stride;
@@ -116,7 +118,7 @@ struct RopeGrid {  // of the vector form: tokens a CTA takes at a time, CTAs a t
 };
 
 const void* rope_scalar_kernel(bool bf16);
-const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs);
+const void* rope_vec_kernel(bool bf16, int half, bool pairs);
 RopeGrid rope_vec_grid(const RopeParams& p, int sm_count);
 const void* attn_mma_kernel(bool bf16, int padded_dim);
 const void* attn_combine_kernel(bool bf16);

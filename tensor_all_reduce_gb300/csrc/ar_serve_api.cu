@@ -218,8 +218,8 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   memset(&p, 0, sizeof(p));
   p.tokens = n;
   p.head_dim = a->head_dim;
-  p.q = {a->q, hq ? a->q_out : nullptr, a->q_token_stride, a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride, a->q_weight, a->q_heads};
-  p.k = {a->k, k_out ? a->k_out : nullptr, a->k_token_stride, a->k_head_stride, a->k_out_token_stride, a->k_out_head_stride, a->k_weight, a->kv_heads};
+  p.q = {a->q, hq ? a->q_out : nullptr, a->q_token_stride, a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride, a->q_weight, a->q_heads, ar::fast_div(hq ? (uint32_t)hq : 1)};
+  p.k = {a->k, k_out ? a->k_out : nullptr, a->k_token_stride, a->k_head_stride, a->k_out_token_stride, a->k_out_head_stride, a->k_weight, a->kv_heads, ar::fast_div(hk ? (uint32_t)hk : 1)};
   p.v = a->v;
   p.v_ts = a->v_token_stride;
   p.v_hs = a->v_head_stride;
@@ -227,6 +227,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   p.inv_dim = (float)(1.0 / (double)d);
   p.gemma = a->gemma != 0;
   p.half = half;
+  p.half_div = ar::fast_div(half ? (uint32_t)half : 1);
   p.pairs = a->pairs != 0;
   p.axes = half ? a->axes : 1;
   p.dealt = a->dealt != 0;
@@ -261,7 +262,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   if (vec) {
     ar::RopeGrid rg = ar::rope_vec_grid(p, ctx->sm_count);
     void* args[3] = {&p, &rg.step, &rg.split};
-    st = launch(ctx, ar::rope_vec_kernel(bf16, p.head_dim, half, p.pairs), rg.ctas, 256, 1, args, 0, stream);
+    st = launch(ctx, ar::rope_vec_kernel(bf16, half, p.pairs), rg.ctas, 256, 1, args, 0, stream);
   } else {
     const int64_t warps = n * (hq + hk * (cache ? 2 : 1));
     int64_t grid = (warps + 7) / 8;
@@ -458,8 +459,7 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
   keep(cudaFuncSetAttribute(plan_kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, AR_MAX_REQUESTS * 8));
   for (int b = 0; b < 2; ++b) {
     keep(cudaFuncGetAttributes(&fa, rope_scalar_kernel(b)));
-    for (int d = 64; d <= 256; d *= 2)
-      for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0)));
+    for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, mode == 1 ? 8 : 4, mode == 0)));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int i = 0; i < 3; ++i)
       for (int ext = 0; ext < 4; ++ext)
