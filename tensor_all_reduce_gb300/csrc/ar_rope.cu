@@ -146,7 +146,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 // Rows on 16-byte boundaries and heads of a multiple of 8 elements: n = head_dim / 8 lanes hold a
-// head, 8 elements each, and a warp as many heads as fit (three of 80 elements, for instance).
+// head, 8 elements each, and a warp as many heads as fit (three of 80 elements, for instance;
+// LANES = 8, 16 or 32 for the powers of two, where a head's sum is a butterfly, 0 for others).
 // A CTA takes `step` tokens: it computes their angles once, for all heads, into shared memory (a
 // sincos a head would cost more than the memory traffic does), then works through the tokens' q
 // heads, k heads and v heads, four a lane loaded before the first is worked on, so that an SM
@@ -154,170 +155,178 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // one other lane at the same place (halves that are a multiple of 8: a shuffle), or anywhere
 // (kHalvesAny: through shared memory, rows of 8 skewed by one float so that lanes fall into
 // different banks).  With few tokens the heads are shared out over `split` CTAs a token.
-template <int DT, int MODE>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_vec(const __grid_constant__ RopeParams p, int step, int split) {
-  __shared__ unsigned long long turn[AR_MAX_HEAD_DIM / 2];
-  __shared__ int axis[AR_MAX_HEAD_DIM / 2];
-  __shared__ __align__(16) float cosv[kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];
-  __shared__ __align__(16) float sinv[kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];
-  __shared__ int64_t k_at[kMaxTokensPerStep], v_at[kMaxTokensPerStep];  // cache offsets of a token, -1: none
-  __shared__ float skew[MODE == kHalvesAny ? kRopeThreads * 9 : 1];
-  const int n = p.head_dim / 8, per_warp = 32 / n, groups = per_warp * (kRopeThreads / 32);
-  const int wl = threadIdx.x & 31, in_warp = wl / n;
-  const int lane = wl - in_warp * n, first = in_warp * n;  // place in the head; the head's first lane
-  const bool there = in_warp < per_warp;
-  const int group = (int)(threadIdx.x >> 5) * per_warp + in_warp;
-  const int e0 = lane * 8;
-  pdl_wait_and_release();
-  for (int i = threadIdx.x; i < p.half; i += kRopeThreads) {
-    turn[i] = turn_of(p.inv_freq[i]);
-    axis[i] = axis_of(p, i);
-  }
-  // Sum over a head's lanes, to all of them: windows of 1, 2, 4, .. lanes by doubling, and the
-  // head as the windows that the bits of n name, low bits first.
-  auto rotated = [&](int by) {
-    const int x = lane + by;
-    return first + (x >= n ? x - n : x);
-  };
-  auto head_sum = [&](float s) {
-    float sum = 0.0f;
-    int off = 0;
-#pragma unroll
-    for (int k = 1; k <= 32; k <<= 1) {
-      if (n & k) {
-        sum = off ? sum + __shfl_sync(0xffffffffu, s, rotated(off)) : s;
-        off += k;
-      }
-      if (2 * k <= n) s += __shfl_sync(0xffffffffu, s, rotated(k));
-    }
-    return sum;
+// Instructions are what bounds it next to memory: offsets within a step are 32-bit, and the
+// sine is kept with either sign.
+template <int DT, int MODE, int LANES>
+struct RopeVec {
+  struct Shared {
+    unsigned long long turn[AR_MAX_HEAD_DIM / 2];
+    int axis[AR_MAX_HEAD_DIM / 2];
+    __align__(16) float cosv[kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];
+    __align__(16) float sinv[2][kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];  // -sin, sin
+    int64_t k_at[kMaxTokensPerStep], v_at[kMaxTokensPerStep];               // cache offsets of a token, -1: none
+    float skew[MODE == kHalvesAny ? kRopeThreads * 9 : 1];
   };
 
-  const int64_t units = (p.tokens + step - 1) / step * split;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t t0 = u / split * step;
-    const int mine = (int)(u % split) * groups + group, stride = groups * split;
-    const int tokens = (int)min((int64_t)step, p.tokens - t0);
-    __syncthreads();
-    for (int x = threadIdx.x; x < tokens * p.half; x += kRopeThreads) {
-      const int t = x / p.half_div, i = x - t * p.half;
-      angle(turn[i], p.positions[axis[i] * p.pos_stride + t0 + t], &sinv[t][i], &cosv[t][i]);
-    }
-    if (p.k_cache && threadIdx.x >= kRopeThreads - 32 && (int)threadIdx.x - (kRopeThreads - 32) < tokens) {
-      const int t = threadIdx.x - (kRopeThreads - 32);
-      const int64_t slot = p.slots[t0 + t];
-      k_at[t] = v_at[t] = -1;
-      if (slot >= 0 && slot < p.num_slots) {
-        const int64_t b = slot / p.page, off = slot - b * p.page;
-        k_at[t] = b * p.kc_bs + off * p.kc_ps;
-        v_at[t] = b * p.vc_bs + off * p.vc_ps;
-      } else if (slot != -1) {
-        *p.status = kStatusBadIndex;
+  const RopeParams& p;
+  Shared& sh;
+  int n, lane, first, group, groups, e0;  // lanes of a head; place in the head; the head's first lane; heads at a time
+  bool there;
+
+  __device__ __forceinline__ RopeVec(const RopeParams& params, Shared& shared) : p(params), sh(shared) {
+    n = LANES ? LANES : p.head_dim / 8;
+    const int per_warp = 32 / n, wl = threadIdx.x & 31, in_warp = wl / n;
+    lane = wl - in_warp * n;
+    first = in_warp * n;
+    there = LANES ? true : in_warp < per_warp;
+    groups = per_warp * (kRopeThreads / 32);
+    group = (int)(threadIdx.x >> 5) * per_warp + in_warp;
+    e0 = lane * 8;
+  }
+
+  // Sum over a head's lanes, to all of them.
+  __device__ __forceinline__ float head_sum(float s) const {
+    if constexpr (LANES != 0) {
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      return s;
+    } else {
+      // windows of 1, 2, 4, .. lanes by doubling, and the head as the windows that the bits of n
+      // name, low bits first
+      auto rotated = [&](int by) {
+        const int x = lane + by;
+        return first + (x >= n ? x - n : x);
+      };
+      float sum = 0.0f;
+      int off = 0;
+#pragma unroll
+      for (int k = 1; k <= 16; k <<= 1) {
+        if (n & k) {
+          sum = off ? sum + __shfl_sync(0xffffffffu, s, rotated(off)) : s;
+          off += k;
+        }
+        if (2 * k <= n) s += __shfl_sync(0xffffffffu, s, rotated(k));
       }
+      return sum;
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind) {  // q heads, k heads
-      const HeadRows& r = kind ? p.k : p.q;
-      const int total = tokens * r.heads;
-      float2 w[4];
-      if (r.weight && there) {
+  }
+
+  // The q (or k) heads of tokens t0 .. t0 + tokens.
+  template <bool KEYS>
+  __device__ __forceinline__ void heads(int64_t t0, int tokens, int mine, int stride) {
+    const HeadRows& r = KEYS ? p.k : p.q;
+    const int total = tokens * r.heads;
+    float2 w[4];
+    if (r.weight && there) {
+      float f[8];
+      unpack8<DT>(ld_keep(static_cast<const uint16_t*>(r.weight) + e0), f);
+      const float one = p.gemma ? 1.0f : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = make_float2(f[2 * i] + one, f[2 * i + 1] + one);
+    }
+    const uint16_t* in = static_cast<const uint16_t*>(r.in) + t0 * r.in_ts + e0;
+    uint16_t* out = r.out ? static_cast<uint16_t*>(r.out) + t0 * r.out_ts + e0 : nullptr;
+    const int in_ts = (int)r.in_ts, in_hs = (int)r.in_hs, out_ts = (int)r.out_ts, out_hs = (int)r.out_hs;
+    const bool low = e0 < p.half, turns = e0 < 2 * p.half;  // of kHalves8
+    const int f0 = turns ? (low ? e0 : e0 - p.half) : 0;
+    const int partner = (first + (turns ? (low ? lane + p.half / 8 : lane - p.half / 8) : lane)) & 31;
+    for (int base = 0; base < total; base += stride * kHeadsInFlight) {
+      uint4 raw[kHeadsInFlight];
+#pragma unroll
+      for (int j = 0; j < kHeadsInFlight; ++j) {
+        const int x = base + j * stride + mine;
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (x < total && there) {
+          const int t = x / r.div, h = x - t * r.heads;
+          raw[j] = ld_row(in + (t * in_ts + h * in_hs));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kHeadsInFlight; ++j) {
+        if (base + j * stride >= total) break;  // the same for the whole CTA
+        const int x = base + j * stride + mine;
+        const int t = min(x, total - 1) / r.div, h = x - t * r.heads;
         float f[8];
-        unpack8<DT>(ld_keep(static_cast<const uint16_t*>(r.weight) + e0), f);
-        const float one = p.gemma ? 1.0f : 0.0f;
+        float2 a[4], y[4];
+        unpack8<DT>(raw[j], f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_float2(f[2 * i] + one, f[2 * i + 1] + one);
-      }
-      for (int base = 0; base < total; base += stride * kHeadsInFlight) {
-        uint4 raw[kHeadsInFlight];
+        for (int i = 0; i < 4; ++i) a[i] = make_float2(f[2 * i], f[2 * i + 1]);
+        if (r.weight) {
+          float2 ss = mul2(a[0], a[0]);
 #pragma unroll
-        for (int j = 0; j < kHeadsInFlight; ++j) {
-          const int x = base + j * stride + mine;
-          raw[j] = make_uint4(0, 0, 0, 0);
-          if (x < total && there) {
-            const int t = x / r.div, h = x - t * r.heads;
-            raw[j] = ld_row(static_cast<const uint16_t*>(r.in) + (t0 + t) * r.in_ts + h * r.in_hs + e0);
-          }
+          for (int i = 1; i < 4; ++i) ss = fma2(a[i], a[i], ss);
+          const float rs = rsqrtf(head_sum(ss.x + ss.y) * p.inv_dim + p.eps);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], make_float2(rs, rs)), w[i]);
         }
+        // an element that does not turn keeps its value, infinities included
+        if constexpr (MODE == kPairs) {
+          const float4 c = *reinterpret_cast<const float4*>(&sh.cosv[t][lane * 4]), s = *reinterpret_cast<const float4*>(&sh.sinv[1][t][lane * 4]);
+          const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-        for (int j = 0; j < kHeadsInFlight; ++j) {
-          if (base + j * stride >= total) break;  // the same for the whole grid
-          const int x = base + j * stride + mine;
-          const int t = min(x, total - 1) / r.div, h = x - t * r.heads;
-          float f[8];
-          float2 a[4], y[4];
-          unpack8<DT>(raw[j], f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = make_float2(f[2 * i], f[2 * i + 1]);
-          if (r.weight) {
-            float2 ss = mul2(a[0], a[0]);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) ss = fma2(a[i], a[i], ss);
-            const float rs = rsqrtf(head_sum(ss.x + ss.y) * p.inv_dim + p.eps);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], make_float2(rs, rs)), w[i]);
+          for (int i = 0; i < 4; ++i) {
+            y[i] = a[i];
+            if (lane * 4 + i < p.half) y[i] = make_float2(a[i].x * cc[i] - a[i].y * sc[i], a[i].y * cc[i] + a[i].x * sc[i]);
           }
-          // an element that does not turn keeps its value, infinities included
-          if constexpr (MODE == kPairs) {
-            const float4 c = *reinterpret_cast<const float4*>(&cosv[t][lane * 4]), s = *reinterpret_cast<const float4*>(&sinv[t][lane * 4]);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
+        } else if constexpr (MODE == kHalves8) {
+          float2 other[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 turned = fma2(make_float2(a[i].y, a[i].x), make_float2(-sc[i], sc[i]), mul2(a[i], make_float2(cc[i], cc[i])));
-              y[i] = lane * 4 + i < p.half ? turned : a[i];
+          for (int i = 0; i < 4; ++i) other[i] = make_float2(__shfl_sync(0xffffffffu, a[i].x, partner), __shfl_sync(0xffffffffu, a[i].y, partner));
+          const float* c = &sh.cosv[t][f0];
+          const float* s = &sh.sinv[low ? 0 : 1][t][f0];  // a' = a cos - b sin, b' = b cos + a sin
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const float4 c4 = *reinterpret_cast<const float4*>(c + 2 * i), s4 = *reinterpret_cast<const float4*>(s + 2 * i);
+            y[i] = a[i];
+            y[i + 1] = a[i + 1];
+            if (turns) {
+              y[i] = fma2(other[i], make_float2(s4.x, s4.y), mul2(a[i], make_float2(c4.x, c4.y)));
+              y[i + 1] = fma2(other[i + 1], make_float2(s4.z, s4.w), mul2(a[i + 1], make_float2(c4.z, c4.w)));
             }
-          } else if constexpr (MODE == kHalves8) {
-            const bool low = e0 < p.half, turns = e0 < 2 * p.half;
-            const int f0 = turns ? (low ? e0 : e0 - p.half) : 0;
-            const int src = first + (turns ? (low ? lane + p.half / 8 : lane - p.half / 8) : lane);
-            const float sign = low ? -1.0f : 1.0f;  // a' = a cos - b sin, b' = b cos + a sin
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 other = make_float2(__shfl_sync(0xffffffffu, a[i].x, src & 31), __shfl_sync(0xffffffffu, a[i].y, src & 31));
-              const float2 c = *reinterpret_cast<const float2*>(&cosv[t][f0 + 2 * i]), s = *reinterpret_cast<const float2*>(&sinv[t][f0 + 2 * i]);
-              const float2 turned = fma2(other, make_float2(sign * s.x, sign * s.y), mul2(a[i], c));
-              y[i] = turns ? turned : a[i];
-            }
-          } else {
-            float* row = skew + (threadIdx.x - lane) * 9;  // element e at e + e / 8
-#pragma unroll
-            for (int i = 0; i < 8; ++i) row[lane * 9 + i] = i & 1 ? a[i / 2].y : a[i / 2].x;
-            __syncwarp();
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int e = e0 + i;
-              const bool low = e < p.half;
-              const float own = i & 1 ? a[i / 2].y : a[i / 2].x;
-              v[i] = own;
-              if (there && e < 2 * p.half) {  // (lanes behind the warp's last head would read behind the array)
-                const int q = low ? e + p.half : e - p.half, k = low ? e : q;
-                const float other = row[q + (q >> 3)];
-                v[i] = low ? own * cosv[t][k] - other * sinv[t][k] : own * cosv[t][k] + other * sinv[t][k];
-              }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = make_float2(v[2 * i], v[2 * i + 1]);
           }
-          if (x < total && there) {
-            const uint4 out = make_uint4(pack2<DT>(y[0].x, y[0].y), pack2<DT>(y[1].x, y[1].y), pack2<DT>(y[2].x, y[2].y), pack2<DT>(y[3].x, y[3].y));
-            if (r.out) st_v4(static_cast<uint16_t*>(r.out) + (t0 + t) * r.out_ts + h * r.out_hs + e0, out);
-            if (kind && p.k_cache && k_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + k_at[t] + h * p.kc_hs + e0, out);
+        } else {
+          float* row = sh.skew + (threadIdx.x - lane) * 9;  // element e at e + e / 8
+#pragma unroll
+          for (int i = 0; i < 8; ++i) row[lane * 9 + i] = i & 1 ? a[i / 2].y : a[i / 2].x;
+          __syncwarp();
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i;
+            v[i] = i & 1 ? a[i / 2].y : a[i / 2].x;
+            if (there && e < 2 * p.half) {  // (lanes behind the warp's last head would read behind the array)
+              const bool lo = e < p.half;
+              const int q = lo ? e + p.half : e - p.half, k = lo ? e : q;
+              v[i] = v[i] * sh.cosv[t][k] + row[q + (q >> 3)] * sh.sinv[lo ? 0 : 1][t][k];
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = make_float2(v[2 * i], v[2 * i + 1]);
+        }
+        if (x < total && there) {
+          const uint4 z = make_uint4(pack2<DT>(y[0].x, y[0].y), pack2<DT>(y[1].x, y[1].y), pack2<DT>(y[2].x, y[2].y), pack2<DT>(y[3].x, y[3].y));
+          if (out) st_v4(out + (t * out_ts + h * out_hs), z);
+          if constexpr (KEYS) {
+            if (p.k_cache && sh.k_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + sh.k_at[t] + h * p.kc_hs + e0, z);
           }
         }
       }
     }
-    if (!p.k_cache) continue;
+  }
+
+  __device__ __forceinline__ void values(int64_t t0, int tokens, int mine, int stride) {  // copied
     const int total = tokens * p.k.heads;
-    for (int base = 0; base < total; base += stride * kHeadsInFlight) {  // v heads: copied
+    const uint16_t* in = static_cast<const uint16_t*>(p.v) + t0 * p.v_ts + e0;
+    const int in_ts = (int)p.v_ts, in_hs = (int)p.v_hs;
+    for (int base = 0; base < total; base += stride * kHeadsInFlight) {
       uint4 raw[kHeadsInFlight];
 #pragma unroll
       for (int j = 0; j < kHeadsInFlight; ++j) {
         const int x = base + j * stride + mine;
         if (x < total && there) {
           const int t = x / p.k.div, h = x - t * p.k.heads;
-          raw[j] = ld_stream(static_cast<const uint16_t*>(p.v) + (t0 + t) * p.v_ts + h * p.v_hs + e0);
+          raw[j] = ld_stream(in + (t * in_ts + h * in_hs));
         }
       }
 #pragma unroll
@@ -325,20 +334,71 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_vec(const __grid_constan
         const int x = base + j * stride + mine;
         if (x < total && there) {
           const int t = x / p.k.div, h = x - t * p.k.heads;
-          if (v_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + v_at[t] + h * p.vc_hs + e0, raw[j]);
+          if (sh.v_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + sh.v_at[t] + h * p.vc_hs + e0, raw[j]);
         }
       }
     }
   }
+
+  __device__ __forceinline__ void run(int step, int split) {
+    for (int i = threadIdx.x; i < p.half; i += kRopeThreads) {
+      sh.turn[i] = turn_of(p.inv_freq[i]);
+      sh.axis[i] = axis_of(p, i);
+    }
+    const int64_t units = (p.tokens + step - 1) / step * split;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+      const int64_t t0 = (split == 1 ? u : u / split) * step;
+      const int mine = (split == 1 ? 0 : (int)(u % split) * groups) + group, stride = groups * split;
+      const int tokens = (int)min((int64_t)step, p.tokens - t0);
+      __syncthreads();
+      for (int x = threadIdx.x; x < tokens * p.half; x += kRopeThreads) {
+        const int t = x / p.half_div, i = x - t * p.half;
+        float s, c;
+        angle(sh.turn[i], p.positions[sh.axis[i] * p.pos_stride + t0 + t], &s, &c);
+        sh.cosv[t][i] = c;
+        sh.sinv[0][t][i] = -s;
+        sh.sinv[1][t][i] = s;
+      }
+      if (p.k_cache && threadIdx.x >= kRopeThreads - 32 && (int)threadIdx.x - (kRopeThreads - 32) < tokens) {
+        const int t = threadIdx.x - (kRopeThreads - 32);
+        const int64_t slot = p.slots[t0 + t];
+        sh.k_at[t] = sh.v_at[t] = -1;
+        if (slot >= 0 && slot < p.num_slots) {
+          const int64_t b = slot / p.page, off = slot - b * p.page;
+          sh.k_at[t] = b * p.kc_bs + off * p.kc_ps;
+          sh.v_at[t] = b * p.vc_bs + off * p.vc_ps;
+        } else if (slot != -1) {
+          *p.status = kStatusBadIndex;
+        }
+      }
+      __syncthreads();
+      heads<false>(t0, tokens, mine, stride);
+      heads<true>(t0, tokens, mine, stride);
+      if (p.k_cache) values(t0, tokens, mine, stride);
+    }
+  }
+};
+
+template <int DT, int MODE, int LANES>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_vec(const __grid_constant__ RopeParams p, int step, int split) {
+  __shared__ typename RopeVec<DT, MODE, LANES>::Shared sh;
+  pdl_wait_and_release();
+  RopeVec<DT, MODE, LANES>(p, sh).run(step, split);
+}
+
+template <int DT, int MODE>
+const void* vec_of(int dim) {
+  switch (dim) {
+    case 64: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 8>);
+    case 128: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 16>);
+    case 256: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 32>);
+    default: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 0>);
+  }
 }
 
 template <int DT>
-const void* vec_of(int mode) {
-  switch (mode) {
-    case kPairs: return reinterpret_cast<const void*>(&rope_vec<DT, kPairs>);
-    case kHalves8: return reinterpret_cast<const void*>(&rope_vec<DT, kHalves8>);
-    default: return reinterpret_cast<const void*>(&rope_vec<DT, kHalvesAny>);
-  }
+const void* vec_of(int mode, int dim) {
+  return mode == kPairs ? vec_of<DT, kPairs>(dim) : mode == kHalves8 ? vec_of<DT, kHalves8>(dim) : vec_of<DT, kHalvesAny>(dim);
 }
 
 }  // namespace
@@ -347,9 +407,9 @@ const void* rope_scalar_kernel(bool bf16) {
   return bf16 ? reinterpret_cast<const void*>(&rope_scalar<kBF16>) : reinterpret_cast<const void*>(&rope_scalar<kF16>);
 }
 
-const void* rope_vec_kernel(bool bf16, int half, bool pairs) {
+const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs) {
   const int mode = pairs ? kPairs : (half % 8 == 0 ? kHalves8 : kHalvesAny);
-  return bf16 ? vec_of<kBF16>(mode) : vec_of<kF16>(mode);
+  return bf16 ? vec_of<kBF16>(mode, head_dim) : vec_of<kF16>(mode, head_dim);
 }
 
 RopeGrid rope_vec_grid(const RopeParams& p, int sm_count) {

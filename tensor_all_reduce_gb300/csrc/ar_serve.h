@@ -118,7 +118,7 @@ struct RopeGrid {  // of the vector form: tokens a CTA takes at a time, CTAs a t
 };
 
 const void* rope_scalar_kernel(bool bf16);
-const void* rope_vec_kernel(bool bf16, int half, bool pairs);
+const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs);
 RopeGrid rope_vec_grid(const RopeParams& p, int sm_count);
 const void* attn_mma_kernel(bool bf16, int padded_dim);
 const void* attn_combine_kernel(bool bf16);
