@@ -12,11 +12,15 @@
 #include "ar_common.cuh"
 #include "ar_fastdiv.cuh"
 #include "ar_serve.h"
+#include "ar_staged.cuh"
 
 namespace ar {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;   // of the general form
+constexpr int kRopeWorkers = 256;   // working threads of the vector form
+constexpr int kRopeMaxStep = 8;     // tokens of a unit
+constexpr int kRopeRowBytes = 16384;  // rows of a unit, unless one head is longer
 
 // Fraction of a turn a position, in units of 2^-64 turns (modulo 1).
 __device__ __forceinline__ unsigned long long turn_of(float inv_freq) {
@@ -115,20 +119,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar(const __grid_constan
   }
 }
 
-// 16-byte load that an in-place store may follow: coherent, and not moved across it.
-__device__ __forceinline__ uint4 ld_row(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
-constexpr int kMaxTokensPerStep = 8;
-constexpr int kHeadsInFlight = 4;
-enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
-
 // a * b, a * b + c on two floats at a time
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
@@ -145,141 +135,233 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return r;
 }
 
-// Rows on 16-byte boundaries and heads of a multiple of 8 elements: n = head_dim / 8 lanes hold a
-// head, 8 elements each, and a warp as many heads as fit (three of 80 elements, for instance;
-// LANES = 8, 16 or 32 for the powers of two, where a head's sum is a butterfly, 0 for others).
-// A CTA takes `step` tokens: it computes their angles once, for all heads, into shared memory (a
-// sincos a head would cost more than the memory traffic does), then works through the tokens' q
-// heads, k heads and v heads, four a lane loaded before the first is worked on, so that an SM
-// has about 48 KB in flight.  The partner of an element is in the lane itself (pairs), in
-// one other lane at the same place (halves that are a multiple of 8: a shuffle), or anywhere
-// (kHalvesAny: through shared memory, rows of 8 skewed by one float so that lanes fall into
-// different banks).  With few tokens the heads are shared out over `split` CTAs a token.
-// Instructions are what bounds it next to memory: offsets within a step are 32-bit, and the
-// sine is kept with either sign.
+constexpr int kStages = 4;
+enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
+
+// Rows on 16-byte boundaries and heads of a multiple of 8 elements.  A CTA works through units of
+// `step` tokens by `per` heads (q heads, k heads, v heads counted on), staged through a ring in
+// shared memory.  One warp brings them in by bulk copies, computes the unit's angles, once for
+// all heads (a sincos a head would cost more than the memory traffic does), and finds the
+// tokens' places in the cache.  Eight warps work: n = head_dim / 8 lanes hold a head, 8
+// elements each, and a warp as many heads as fit (three of 80 elements; LANES = 8, 16 or 32 for
+// the powers of two, where a head's sum is a butterfly, 0 for others).  The partner of an element
+// is in the lane itself (pairs), in one other lane at the same place (halves that are a multiple
+// of 8: a shuffle), or anywhere (kHalvesAny: through shared memory, rows of 8 skewed by one float
+// so that lanes fall into different banks).
+//
+// The ring is what reaches the memory's bandwidth: with rows loaded straight into registers, four
+// a lane in flight, loads alone ran at 3 TB/s and the arithmetic came on top of them.
 template <int DT, int MODE, int LANES>
 struct RopeVec {
   struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    int64_t k_at[kStages][kRopeMaxStep], v_at[kStages][kRopeMaxStep];  // cache offsets of a token, -1: none
     unsigned long long turn[AR_MAX_HEAD_DIM / 2];
     int axis[AR_MAX_HEAD_DIM / 2];
-    __align__(16) float cosv[kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];
-    __align__(16) float sinv[2][kMaxTokensPerStep][AR_MAX_HEAD_DIM / 2 + 8];  // -sin, sin
-    int64_t k_at[kMaxTokensPerStep], v_at[kMaxTokensPerStep];               // cache offsets of a token, -1: none
-    float skew[MODE == kHalvesAny ? kRopeThreads * 9 : 1];
+    __align__(16) float weight[2][AR_MAX_HEAD_DIM];  // w or 1 + w of q and k
+    float skew[MODE == kHalvesAny ? kRopeWorkers * 9 : 1];
+    int stop;
   };
 
   const RopeParams& p;
+  const RopePlan& plan;
   Shared& sh;
-  int n, lane, first, group, groups, e0;  // lanes of a head; place in the head; the head's first lane; heads at a time
-  bool there;
+  uint8_t* stage;  // kStages stages: rows, then cosines, sines negated, sines
 
-  __device__ __forceinline__ RopeVec(const RopeParams& params, Shared& shared) : p(params), sh(shared) {
-    n = LANES ? LANES : p.head_dim / 8;
-    const int per_warp = 32 / n, wl = threadIdx.x & 31, in_warp = wl / n;
-    lane = wl - in_warp * n;
-    first = in_warp * n;
-    there = LANES ? true : in_warp < per_warp;
-    groups = per_warp * (kRopeThreads / 32);
-    group = (int)(threadIdx.x >> 5) * per_warp + in_warp;
-    e0 = lane * 8;
+  struct Unit {
+    int64_t t0;
+    int tokens, lo, hi;  // heads [lo, hi)
+  };
+  __device__ __forceinline__ Unit unit(int64_t u) const {
+    Unit x;
+    const int64_t group = plan.split == 1 ? u : u / plan.split;
+    x.t0 = group * plan.step;
+    x.tokens = (int)min((int64_t)plan.step, p.tokens - x.t0);
+    x.lo = (int)(u - group * plan.split) * plan.per;
+    x.hi = min(x.lo + plan.per, plan.heads);
+    return x;
+  }
+  __device__ __forceinline__ uint8_t* rows_of(int s) const { return stage + (size_t)s * plan.stage_bytes; }
+  __device__ __forceinline__ float* angles_of(int s) const { return reinterpret_cast<float*>(rows_of(s) + plan.row_bytes); }
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+      if (*reinterpret_cast<volatile int*>(&sh.stop)) return false;
+      if (clock64() - t0 > p.wait_cycles) {
+        *reinterpret_cast<volatile int*>(&sh.stop) = 1;
+        *p.status = 1;
+        return false;
+      }
+    }
+    return true;
   }
 
-  // Sum over a head's lanes, to all of them.
-  __device__ __forceinline__ float head_sum(float s) const {
-    if constexpr (LANES != 0) {
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      return s;
+  // Copies the heads [a, b) of one kind that lie in the unit, of token t.
+  __device__ __forceinline__ void copy(const Unit& x, int t, int a, int b, const void* in, int64_t ts, int64_t hs, int s) {
+    const int lo = max(a, x.lo), hi = min(b, x.hi);
+    if (lo >= hi) return;
+    const uint32_t head = p.head_dim * 2;
+    const uint16_t* src = static_cast<const uint16_t*>(in) + (x.t0 + t) * ts + (lo - a) * hs;
+    uint8_t* dst = rows_of(s) + (t * plan.per + lo - x.lo) * head;
+    if (hs == p.head_dim) {
+      bulk_g2s(dst, src, (hi - lo) * head, &sh.full[s]);
     } else {
-      // windows of 1, 2, 4, .. lanes by doubling, and the head as the windows that the bits of n
-      // name, low bits first
-      auto rotated = [&](int by) {
-        const int x = lane + by;
-        return first + (x >= n ? x - n : x);
-      };
-      float sum = 0.0f;
-      int off = 0;
-#pragma unroll
-      for (int k = 1; k <= 16; k <<= 1) {
-        if (n & k) {
-          sum = off ? sum + __shfl_sync(0xffffffffu, s, rotated(off)) : s;
-          off += k;
-        }
-        if (2 * k <= n) s += __shfl_sync(0xffffffffu, s, rotated(k));
-      }
-      return sum;
+      for (int h = lo; h < hi; ++h, src += hs, dst += head) bulk_g2s(dst, src, head, &sh.full[s]);
     }
   }
 
-  // The q (or k) heads of tokens t0 .. t0 + tokens.
-  template <bool KEYS>
-  __device__ __forceinline__ void heads(int64_t t0, int tokens, int mine, int stride) {
-    const HeadRows& r = KEYS ? p.k : p.q;
-    const int total = tokens * r.heads;
-    float2 w[4];
-    if (r.weight && there) {
-      float f[8];
-      unpack8<DT>(ld_keep(static_cast<const uint16_t*>(r.weight) + e0), f);
-      const float one = p.gemma ? 1.0f : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = make_float2(f[2 * i] + one, f[2 * i + 1] + one);
-    }
-    const uint16_t* in = static_cast<const uint16_t*>(r.in) + t0 * r.in_ts + e0;
-    uint16_t* out = r.out ? static_cast<uint16_t*>(r.out) + t0 * r.out_ts + e0 : nullptr;
-    const int in_ts = (int)r.in_ts, in_hs = (int)r.in_hs, out_ts = (int)r.out_ts, out_hs = (int)r.out_hs;
-    const bool low = e0 < p.half, turns = e0 < 2 * p.half;  // of kHalves8
-    const int f0 = turns ? (low ? e0 : e0 - p.half) : 0;
-    const int partner = (first + (turns ? (low ? lane + p.half / 8 : lane - p.half / 8) : lane)) & 31;
-    for (int base = 0; base < total; base += stride * kHeadsInFlight) {
-      uint4 raw[kHeadsInFlight];
-#pragma unroll
-      for (int j = 0; j < kHeadsInFlight; ++j) {
-        const int x = base + j * stride + mine;
-        raw[j] = make_uint4(0, 0, 0, 0);
-        if (x < total && there) {
-          const int t = x / r.div, h = x - t * r.heads;
-          raw[j] = ld_row(in + (t * in_ts + h * in_hs));
-        }
+  __device__ __forceinline__ void load() {
+    const int lane = threadIdx.x & 31;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++n) {
+      const int s = n % kStages;
+      const Unit x = unit(u);
+      ok = __all_sync(0xffffffffu, wait(&sh.empty[s], ((n / kStages) & 1) ^ 1));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], x.tokens * (x.hi - x.lo) * p.head_dim * 2);
+      __syncwarp();
+      if (lane < x.tokens * 3 && !(p.stall && n == 0)) {  // a lane a token and kind
+        const int t = lane / 3, kind = lane - t * 3;
+        if (kind == 0) copy(x, t, 0, p.q.heads, p.q.in, p.q.in_ts, p.q.in_hs, s);
+        if (kind == 1) copy(x, t, p.q.heads, p.q.heads + p.k.heads, p.k.in, p.k.in_ts, p.k.in_hs, s);
+        if (kind == 2) copy(x, t, p.q.heads + p.k.heads, plan.heads, p.v, p.v_ts, p.v_hs, s);
       }
+      float* c = angles_of(s);
+      const int size = plan.step * plan.pitch;
+      for (int i = lane; i < x.tokens * p.half; i += 32) {
+        const int t = i / p.half_div, f = i - t * p.half;
+        float sn, cs;
+        angle(sh.turn[f], p.positions[sh.axis[f] * p.pos_stride + x.t0 + t], &sn, &cs);
+        const int at = t * plan.pitch + f;
+        c[at] = cs;
+        c[size + at] = -sn;
+        c[2 * size + at] = sn;
+      }
+      if (p.k_cache && lane < x.tokens) {
+        const int64_t slot = p.slots[x.t0 + lane];
+        int64_t k = -1, v = -1;
+        if (slot >= 0 && slot < p.num_slots) {
+          const int64_t b = slot / p.page, off = slot - b * p.page;
+          k = b * p.kc_bs + off * p.kc_ps;
+          v = b * p.vc_bs + off * p.vc_ps;
+        } else if (slot != -1) {
+          *p.status = kStatusBadIndex;
+        }
+        sh.k_at[s][lane] = k;
+        sh.v_at[s][lane] = v;
+      }
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&sh.full[s])) : "memory");
+    }
+    if (!ok)  // copies in flight end before the CTA does
+      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+        if (!(p.stall && i == 0)) mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, p.wait_cycles);
+  }
+
+  __device__ __forceinline__ void work() {
+    const int n = LANES ? LANES : p.head_dim / 8;  // lanes of a head
+    const int per_warp = 32 / n, wl = threadIdx.x & 31, in_warp = wl / n;
+    const int lane = wl - in_warp * n, first = in_warp * n;  // place in the head; its first lane
+    const bool there = LANES ? true : in_warp < per_warp;
+    const int e0 = lane * 8, warp = threadIdx.x >> 5;
+    // Sum over a head's lanes, to all of them.
+    auto head_sum = [&](float s) {
+      if constexpr (LANES != 0) {
 #pragma unroll
-      for (int j = 0; j < kHeadsInFlight; ++j) {
-        if (base + j * stride >= total) break;  // the same for the whole CTA
-        const int x = base + j * stride + mine;
-        const int t = min(x, total - 1) / r.div, h = x - t * r.heads;
+        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+      } else {
+        // windows of 1, 2, 4, .. lanes by doubling, and the head as the windows that the bits of n
+        // name, low bits first
+        auto rotated = [&](int by) {
+          const int x = lane + by;
+          return first + (x >= n ? x - n : x);
+        };
+        float sum = 0.0f;
+        int off = 0;
+#pragma unroll
+        for (int k = 1; k <= 16; k <<= 1) {
+          if (n & k) {
+            sum = off ? sum + __shfl_sync(0xffffffffu, s, rotated(off)) : s;
+            off += k;
+          }
+          if (2 * k <= n) s += __shfl_sync(0xffffffffu, s, rotated(k));
+        }
+        return sum;
+      }
+    };
+    const bool low = e0 < p.half, turns = e0 < 2 * p.half;  // of kHalves8
+    const int f0 = MODE == kPairs ? lane * 4 : (turns ? (low ? e0 : e0 - p.half) : 0);
+    const int partner = (first + (turns ? (low ? lane + p.half / 8 : lane - p.half / 8) : lane)) & 31;
+    const int size = plan.step * plan.pitch;
+    uint32_t k = 0;
+    for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++k) {
+      const int s = k % kStages;
+      const Unit x = unit(u);
+      const bool ok = wait(&sh.full[s], (k / kStages) & 1);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const uint8_t* rows = rows_of(s);
+      const float* cosv = angles_of(s);
+      const int heads = x.hi - x.lo, total = x.tokens * heads;
+      for (int base = warp * per_warp; base < total; base += (kRopeWorkers / 32) * per_warp) {
+        const int at = base + in_warp;
+        const bool mine = there && at < total;
+        const int i0 = min(at, total - 1);
+        const int t = plan.split == 1 ? i0 / plan.heads_div : 0, hh = i0 - t * heads;
+        int h = x.lo + hh;
+        const bool is_q = h < p.q.heads, is_v = h >= p.q.heads + p.k.heads;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (mine) raw = lds_v4(rows + ((size_t)(t * plan.per + hh) * p.head_dim + e0) * 2);
+        if (__all_sync(0xffffffffu, is_v || !mine)) {  // v is copied
+          if (mine && sh.v_at[s][t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + sh.v_at[s][t] + (h - p.q.heads - p.k.heads) * p.vc_hs + e0, raw);
+          continue;
+        }
         float f[8];
         float2 a[4], y[4];
-        unpack8<DT>(raw[j], f);
+        unpack8<DT>(raw, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = make_float2(f[2 * i], f[2 * i + 1]);
-        if (r.weight) {
+        if (p.q.weight || p.k.weight) {
           float2 ss = mul2(a[0], a[0]);
 #pragma unroll
           for (int i = 1; i < 4; ++i) ss = fma2(a[i], a[i], ss);
           const float rs = rsqrtf(head_sum(ss.x + ss.y) * p.inv_dim + p.eps);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], make_float2(rs, rs)), w[i]);
+          if (is_q ? p.q.weight != nullptr : p.k.weight != nullptr) {
+            const float* w = sh.weight[is_q ? 0 : 1] + e0;
+            const float4 w0 = *reinterpret_cast<const float4*>(w), w1 = *reinterpret_cast<const float4*>(w + 4);
+            const float2 r2 = make_float2(rs, rs);
+            a[0] = mul2(mul2(a[0], r2), make_float2(w0.x, w0.y));
+            a[1] = mul2(mul2(a[1], r2), make_float2(w0.z, w0.w));
+            a[2] = mul2(mul2(a[2], r2), make_float2(w1.x, w1.y));
+            a[3] = mul2(mul2(a[3], r2), make_float2(w1.z, w1.w));
+          }
         }
         // an element that does not turn keeps its value, infinities included
+        const float* c = cosv + t * plan.pitch;
         if constexpr (MODE == kPairs) {
-          const float4 c = *reinterpret_cast<const float4*>(&sh.cosv[t][lane * 4]), s = *reinterpret_cast<const float4*>(&sh.sinv[1][t][lane * 4]);
-          const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[i] = a[i];
-            if (lane * 4 + i < p.half) y[i] = make_float2(a[i].x * cc[i] - a[i].y * sc[i], a[i].y * cc[i] + a[i].x * sc[i]);
+          for (int i = 0; i < 4; ++i) y[i] = a[i];
+          if (f0 < p.half) {
+            const float4 c4 = *reinterpret_cast<const float4*>(c + f0), s4 = *reinterpret_cast<const float4*>(c + 2 * size + f0);
+            const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, sc[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (f0 + i < p.half) y[i] = make_float2(a[i].x * cc[i] - a[i].y * sc[i], a[i].y * cc[i] + a[i].x * sc[i]);
           }
         } else if constexpr (MODE == kHalves8) {
           float2 other[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) other[i] = make_float2(__shfl_sync(0xffffffffu, a[i].x, partner), __shfl_sync(0xffffffffu, a[i].y, partner));
-          const float* c = &sh.cosv[t][f0];
-          const float* s = &sh.sinv[low ? 0 : 1][t][f0];  // a' = a cos - b sin, b' = b cos + a sin
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const float4 c4 = *reinterpret_cast<const float4*>(c + 2 * i), s4 = *reinterpret_cast<const float4*>(s + 2 * i);
+          for (int i = 0; i < 4; ++i) {
+            other[i] = make_float2(__shfl_sync(0xffffffffu, a[i].x, partner), __shfl_sync(0xffffffffu, a[i].y, partner));
             y[i] = a[i];
-            y[i + 1] = a[i + 1];
-            if (turns) {
+          }
+          if (turns) {  // a' = a cos - b sin, b' = b cos + a sin
+            const float* sn = c + (low ? size : 2 * size);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float4 c4 = *reinterpret_cast<const float4*>(c + f0 + 2 * i), s4 = *reinterpret_cast<const float4*>(sn + f0 + 2 * i);
               y[i] = fma2(other[i], make_float2(s4.x, s4.y), mul2(a[i], make_float2(c4.x, c4.y)));
               y[i + 1] = fma2(other[i + 1], make_float2(s4.z, s4.w), mul2(a[i + 1], make_float2(c4.z, c4.w)));
             }
@@ -296,94 +378,66 @@ struct RopeVec {
             v[i] = i & 1 ? a[i / 2].y : a[i / 2].x;
             if (there && e < 2 * p.half) {  // (lanes behind the warp's last head would read behind the array)
               const bool lo = e < p.half;
-              const int q = lo ? e + p.half : e - p.half, k = lo ? e : q;
-              v[i] = v[i] * sh.cosv[t][k] + row[q + (q >> 3)] * sh.sinv[lo ? 0 : 1][t][k];
+              const int q = lo ? e + p.half : e - p.half, g = lo ? e : q;
+              v[i] = v[i] * c[g] + row[q + (q >> 3)] * c[(lo ? size : 2 * size) + g];
             }
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[i] = make_float2(v[2 * i], v[2 * i + 1]);
         }
-        if (x < total && there) {
-          const uint4 z = make_uint4(pack2<DT>(y[0].x, y[0].y), pack2<DT>(y[1].x, y[1].y), pack2<DT>(y[2].x, y[2].y), pack2<DT>(y[3].x, y[3].y));
-          if (out) st_v4(out + (t * out_ts + h * out_hs), z);
-          if constexpr (KEYS) {
-            if (p.k_cache && sh.k_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + sh.k_at[t] + h * p.kc_hs + e0, z);
-          }
+        if (!mine) continue;
+        if (is_v) {
+          if (sh.v_at[s][t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + sh.v_at[s][t] + (h - p.q.heads - p.k.heads) * p.vc_hs + e0, raw);
+          continue;
+        }
+        const uint4 z = make_uint4(pack2<DT>(y[0].x, y[0].y), pack2<DT>(y[1].x, y[1].y), pack2<DT>(y[2].x, y[2].y), pack2<DT>(y[3].x, y[3].y));
+        if (is_q) {
+          st_v4(static_cast<uint16_t*>(p.q.out) + (x.t0 + t) * p.q.out_ts + h * p.q.out_hs + e0, z);
+        } else {
+          h -= p.q.heads;
+          if (p.k.out) st_v4(static_cast<uint16_t*>(p.k.out) + (x.t0 + t) * p.k.out_ts + h * p.k.out_hs + e0, z);
+          if (p.k_cache && sh.k_at[s][t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + sh.k_at[s][t] + h * p.kc_hs + e0, z);
         }
       }
+      __syncwarp();
+      if (wl == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&sh.empty[s])) : "memory");
     }
   }
 
-  __device__ __forceinline__ void values(int64_t t0, int tokens, int mine, int stride) {  // copied
-    const int total = tokens * p.k.heads;
-    const uint16_t* in = static_cast<const uint16_t*>(p.v) + t0 * p.v_ts + e0;
-    const int in_ts = (int)p.v_ts, in_hs = (int)p.v_hs;
-    for (int base = 0; base < total; base += stride * kHeadsInFlight) {
-      uint4 raw[kHeadsInFlight];
-#pragma unroll
-      for (int j = 0; j < kHeadsInFlight; ++j) {
-        const int x = base + j * stride + mine;
-        if (x < total && there) {
-          const int t = x / p.k.div, h = x - t * p.k.heads;
-          raw[j] = ld_stream(in + (t * in_ts + h * in_hs));
-        }
+  __device__ __forceinline__ void run() {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < kStages; ++s) {
+        mbar_init(&sh.full[s], 33);  // the copies' bytes, and each lane of the loading warp
+        mbar_init(&sh.empty[s], kRopeWorkers / 32);
       }
-#pragma unroll
-      for (int j = 0; j < kHeadsInFlight; ++j) {
-        const int x = base + j * stride + mine;
-        if (x < total && there) {
-          const int t = x / p.k.div, h = x - t * p.k.heads;
-          if (sh.v_at[t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + sh.v_at[t] + h * p.vc_hs + e0, raw[j]);
-        }
-      }
+      sh.stop = 0;
+      mbar_fence_init();
+      fence_proxy_async_smem();
     }
-  }
-
-  __device__ __forceinline__ void run(int step, int split) {
-    for (int i = threadIdx.x; i < p.half; i += kRopeThreads) {
+    pdl_wait_and_release();
+    for (int i = threadIdx.x; i < p.half; i += kRopeWorkers + 32) {
       sh.turn[i] = turn_of(p.inv_freq[i]);
       sh.axis[i] = axis_of(p, i);
     }
-    const int64_t units = (p.tokens + step - 1) / step * split;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-      const int64_t t0 = (split == 1 ? u : u / split) * step;
-      const int mine = (split == 1 ? 0 : (int)(u % split) * groups) + group, stride = groups * split;
-      const int tokens = (int)min((int64_t)step, p.tokens - t0);
-      __syncthreads();
-      for (int x = threadIdx.x; x < tokens * p.half; x += kRopeThreads) {
-        const int t = x / p.half_div, i = x - t * p.half;
-        float s, c;
-        angle(sh.turn[i], p.positions[sh.axis[i] * p.pos_stride + t0 + t], &s, &c);
-        sh.cosv[t][i] = c;
-        sh.sinv[0][t][i] = -s;
-        sh.sinv[1][t][i] = s;
-      }
-      if (p.k_cache && threadIdx.x >= kRopeThreads - 32 && (int)threadIdx.x - (kRopeThreads - 32) < tokens) {
-        const int t = threadIdx.x - (kRopeThreads - 32);
-        const int64_t slot = p.slots[t0 + t];
-        sh.k_at[t] = sh.v_at[t] = -1;
-        if (slot >= 0 && slot < p.num_slots) {
-          const int64_t b = slot / p.page, off = slot - b * p.page;
-          sh.k_at[t] = b * p.kc_bs + off * p.kc_ps;
-          sh.v_at[t] = b * p.vc_bs + off * p.vc_ps;
-        } else if (slot != -1) {
-          *p.status = kStatusBadIndex;
-        }
-      }
-      __syncthreads();
-      heads<false>(t0, tokens, mine, stride);
-      heads<true>(t0, tokens, mine, stride);
-      if (p.k_cache) values(t0, tokens, mine, stride);
+    const float one = p.gemma ? 1.0f : 0.0f;
+    for (int i = threadIdx.x; i < p.head_dim; i += kRopeWorkers + 32) {
+      if (p.q.weight) sh.weight[0][i] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.q.weight) + i)) + one;
+      if (p.k.weight) sh.weight[1][i] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.k.weight) + i)) + one;
     }
+    __syncthreads();
+    if (threadIdx.x >= kRopeWorkers)
+      load();
+    else
+      work();
   }
 };
 
 template <int DT, int MODE, int LANES>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_vec(const __grid_constant__ RopeParams p, int step, int split) {
+__global__ void __launch_bounds__(kRopeWorkers + 32, 3) rope_vec(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
+  extern __shared__ __align__(128) uint8_t raw[];
   __shared__ typename RopeVec<DT, MODE, LANES>::Shared sh;
-  pdl_wait_and_release();
-  RopeVec<DT, MODE, LANES>(p, sh).run(step, split);
+  RopeVec<DT, MODE, LANES>{p, plan, sh, raw}.run();
 }
 
 template <int DT, int MODE>
@@ -412,19 +466,33 @@ const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs) {
   return bf16 ? vec_of<kBF16>(mode, head_dim) : vec_of<kF16>(mode, head_dim);
 }
 
-RopeGrid rope_vec_grid(const RopeParams& p, int sm_count) {
-  // several tokens a CTA once every resident CTA has such a step, else single tokens; below one
-  // token an SM the heads of a token go to several CTAs, as long as each has a round of heads
-  const int groups = 32 / (p.head_dim / 8) * (kRopeThreads / 32);
-  const int heads = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;
-  RopeGrid g;
-  g.step = kMaxTokensPerStep;
-  while (g.step > 1 && p.tokens < (int64_t)g.step * 3 * sm_count) g.step /= 2;
-  g.split = 1;
-  while (g.step == 1 && p.tokens * g.split < sm_count && heads > groups * g.split) g.split *= 2;
-  const int64_t units = (p.tokens + g.step - 1) / g.step * g.split;
-  g.ctas = units < (int64_t)3 * sm_count ? (unsigned)units : 3u * sm_count;
-  return g;
+RopePlan rope_plan(const RopeParams& p, int sm_count) {
+  RopePlan r;
+  r.heads = p.q.heads + p.k.heads * (p.k_cache ? 2 : 1);
+  const int head = p.head_dim * 2, round = 32 / (p.head_dim / 8) * (kRopeWorkers / 32);  // heads at a time
+  // heads of a unit: all, or what fits a stage
+  r.split = 1;
+  while ((r.heads + r.split - 1) / r.split * head > kRopeRowBytes && r.split < r.heads) r.split *= 2;
+  // few tokens: their heads are shared out over the SMs, as long as each unit has a round of them
+  while (p.tokens * r.split < sm_count && r.heads > round * r.split) r.split *= 2;
+  r.per = (r.heads + r.split - 1) / r.split;
+  r.split = (r.heads + r.per - 1) / r.per;
+  // several tokens a unit where rows are short and there are enough of them for every CTA
+  r.step = 1;
+  while (r.split == 1 && r.step < kRopeMaxStep && 2 * r.step * r.per * head <= kRopeRowBytes && p.tokens >= (int64_t)r.step * 2 * 3 * sm_count) r.step *= 2;
+  r.heads_div = fast_div((uint32_t)r.per);
+  r.pitch = (p.half + 3) / 4 * 4;
+  r.row_bytes = (r.step * r.per * head + 127) / 128 * 128;
+  r.stage_bytes = (r.row_bytes + r.step * r.pitch * 12 + 127) / 128 * 128;
+  r.units = (p.tokens + r.step - 1) / r.step * r.split;
+  r.ctas = r.units < (int64_t)3 * sm_count ? (unsigned)r.units : 3u * sm_count;
+  return r;
 }
+
+size_t rope_smem(const RopePlan& r) { return (size_t)kStages * r.stage_bytes; }
+
+// The largest that rope_plan asks for: a stage of rows and the angles of the most tokens that
+// fit beside them.
+size_t rope_smem_most() { return (size_t)kStages * (kRopeRowBytes + 128 + kRopeMaxStep * (AR_MAX_HEAD_DIM / 2) * 12 + 128); }
 
 }  // namespace ar

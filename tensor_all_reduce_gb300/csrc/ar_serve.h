@@ -73,6 +73,8 @@ struct RopeParams {
   int page;
   const int64_t* slots;
   int* status;
+  int stall;  // test hook: the first copy of the vector form is not issued, so that its wait runs out
+  long long wait_cycles;
 };
 
 struct AttnParams {
@@ -112,14 +114,20 @@ struct AttnParams {
 };
 
 const void* plan_kernel();
-struct RopeGrid {  // of the vector form: tokens a CTA takes at a time, CTAs a token's heads are shared by
-  int step, split;
+struct RopePlan {  // how the vector form divides its work
+  int step, split, per, heads;  // tokens of a unit; units that share a token's heads; heads of a unit, in all
+  int pitch;                    // floats between the tokens of a unit's cosines and sines
+  int row_bytes, stage_bytes;   // a unit's rows; with its angles
+  FastDiv heads_div;            // by `per`
+  int64_t units;
   unsigned ctas;
 };
 
 const void* rope_scalar_kernel(bool bf16);
 const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs);
-RopeGrid rope_vec_grid(const RopeParams& p, int sm_count);
+RopePlan rope_plan(const RopeParams& p, int sm_count);
+size_t rope_smem(const RopePlan& plan);
+size_t rope_smem_most();
 const void* attn_mma_kernel(bool bf16, int padded_dim);
 const void* attn_combine_kernel(bool bf16);
 

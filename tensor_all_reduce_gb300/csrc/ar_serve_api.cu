@@ -247,11 +247,10 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   p.num_slots = cache ? a->num_blocks * a->page_size : 0;
   p.slots = a->slots;
   p.status = ctx->d_status;
-  // the vector form: every row on a 16-byte boundary; offsets of 8 tokens and of all heads in 32 bits
-  const int64_t most = 1 << 27, wide = hq > hk ? hq : hk;
-  auto row = [&](const void* q, int64_t ts, int64_t hs) {
-    return aligned(q, 16) && ts % 8 == 0 && hs % 8 == 0 && ts < most && hs * wide < most;
-  };
+  p.stall = ctx->test_stall;
+  p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
+  // the vector form: every row on a 16-byte boundary
+  auto row = [](const void* q, int64_t ts, int64_t hs) { return aligned(q, 16) && ts % 8 == 0 && hs % 8 == 0; };
   bool vec = d % 8 == 0 && ctx->force_variant != 4;
   if (hq) vec = vec && row(a->q, a->q_token_stride, a->q_head_stride) && row(a->q_out, a->q_out_token_stride, a->q_out_head_stride) && aligned(a->q_weight, 16);
   if (hk) vec = vec && row(a->k, a->k_token_stride, a->k_head_stride) && aligned(a->k_weight, 16);
@@ -263,9 +262,9 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   DeviceGuard g(ctx->device);
   ar_status st;
   if (vec) {
-    ar::RopeGrid rg = ar::rope_vec_grid(p, ctx->sm_count);
-    void* args[3] = {&p, &rg.step, &rg.split};
-    st = launch(ctx, ar::rope_vec_kernel(bf16, p.head_dim, half, p.pairs), rg.ctas, 256, 1, args, 0, stream);
+    ar::RopePlan plan = ar::rope_plan(p, ctx->sm_count);
+    void* args[2] = {&p, &plan};
+    st = launch(ctx, ar::rope_vec_kernel(bf16, p.head_dim, half, p.pairs), plan.ctas, 288, 1, args, ar::rope_smem(plan), stream);
   } else {
     const int64_t warps = n * (hq + hk * (cache ? 2 : 1));
     int64_t grid = (warps + 7) / 8;
@@ -463,7 +462,8 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
   for (int b = 0; b < 2; ++b) {
     keep(cudaFuncGetAttributes(&fa, rope_scalar_kernel(b)));
     for (int d : {64, 128, 256, 80})
-      for (int mode = 0; mode < 3; ++mode) keep(cudaFuncGetAttributes(&fa, rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0)));
+      for (int mode = 0; mode < 3; ++mode)
+        keep(cudaFuncSetAttribute(rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rope_smem_most()));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int i = 0; i < 3; ++i)
       for (int ext = 0; ext < 4; ++ext)
