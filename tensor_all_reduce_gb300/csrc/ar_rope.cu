@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;   // of the general form
 constexpr int kRopeWorkers = 256;   // working threads of the vector form
+constexpr int kRopeLoaders = 64;    // and those that run ahead
 constexpr int kRopeMaxStep = 8;     // tokens of a unit
 constexpr int kRopeRowBytes = 16384;  // rows of a unit, unless one head is longer
 
@@ -140,9 +141,10 @@ enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 
 // Rows on 16-byte boundaries and heads of a multiple of 8 elements.  A CTA works through units of
 // `step` tokens by `per` heads (q heads, k heads, v heads counted on), staged through a ring in
-// shared memory.  One warp brings them in by bulk copies, computes the unit's angles, once for
-// all heads (a sincos a head would cost more than the memory traffic does), and finds the
-// tokens' places in the cache.  Eight warps work: n = head_dim / 8 lanes hold a head, 8
+// shared memory.  Two warps run ahead: one brings the rows in by bulk copies, the other finds the
+// tokens' places in the cache, and both compute the units' angles, once for all heads (a sincos
+// a head would cost more than the memory traffic does; one warp alone was the bound where rows
+// are short).  Eight warps work: n = head_dim / 8 lanes hold a head, 8
 // elements each, and a warp as many heads as fit (three of 80 elements; LANES = 8, 16 or 32 for
 // the powers of two, where a head's sum is a butterfly, 0 for others).  The partner of an element
 // is in the lane itself (pairs), in one other lane at the same place (halves that are a multiple
@@ -213,7 +215,7 @@ struct RopeVec {
   }
 
   __device__ __forceinline__ void load() {
-    const int lane = threadIdx.x & 31;
+    const int tid = threadIdx.x - kRopeWorkers, lane = tid & 31;
     uint32_t n = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++n) {
@@ -221,26 +223,16 @@ struct RopeVec {
       const Unit x = unit(u);
       ok = __all_sync(0xffffffffu, wait(&sh.empty[s], ((n / kStages) & 1) ^ 1));
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], x.tokens * (x.hi - x.lo) * p.head_dim * 2);
-      __syncwarp();
-      if (lane < x.tokens * 3 && !(p.stall && n == 0)) {  // a lane a token and kind
-        const int t = lane / 3, kind = lane - t * 3;
-        if (kind == 0) copy(x, t, 0, p.q.heads, p.q.in, p.q.in_ts, p.q.in_hs, s);
-        if (kind == 1) copy(x, t, p.q.heads, p.q.heads + p.k.heads, p.k.in, p.k.in_ts, p.k.in_hs, s);
-        if (kind == 2) copy(x, t, p.q.heads + p.k.heads, plan.heads, p.v, p.v_ts, p.v_hs, s);
-      }
-      float* c = angles_of(s);
-      const int size = plan.step * plan.pitch;
-      for (int i = lane; i < x.tokens * p.half; i += 32) {
-        const int t = i / p.half_div, f = i - t * p.half;
-        float sn, cs;
-        angle(sh.turn[f], p.positions[sh.axis[f] * p.pos_stride + x.t0 + t], &sn, &cs);
-        const int at = t * plan.pitch + f;
-        c[at] = cs;
-        c[size + at] = -sn;
-        c[2 * size + at] = sn;
-      }
-      if (p.k_cache && lane < x.tokens) {
+      if (tid < 32) {
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], x.tokens * (x.hi - x.lo) * p.head_dim * 2);
+        __syncwarp();
+        if (lane < x.tokens * 3 && !(p.stall && n == 0)) {  // a lane a token and kind
+          const int t = lane / 3, kind = lane - t * 3;
+          if (kind == 0) copy(x, t, 0, p.q.heads, p.q.in, p.q.in_ts, p.q.in_hs, s);
+          if (kind == 1) copy(x, t, p.q.heads, p.q.heads + p.k.heads, p.k.in, p.k.in_ts, p.k.in_hs, s);
+          if (kind == 2) copy(x, t, p.q.heads + p.k.heads, plan.heads, p.v, p.v_ts, p.v_hs, s);
+        }
+      } else if (p.k_cache && lane < x.tokens) {
         const int64_t slot = p.slots[x.t0 + lane];
         int64_t k = -1, v = -1;
         if (slot >= 0 && slot < p.num_slots) {
@@ -253,9 +245,21 @@ struct RopeVec {
         sh.k_at[s][lane] = k;
         sh.v_at[s][lane] = v;
       }
+      float* c = angles_of(s);
+      const int size = plan.step * plan.pitch;
+#pragma unroll 4
+      for (int i = tid; i < x.tokens * p.half; i += kRopeLoaders) {
+        const int t = i / p.half_div, f = i - t * p.half;
+        float sn, cs;
+        angle(sh.turn[f], p.positions[sh.axis[f] * p.pos_stride + x.t0 + t], &sn, &cs);
+        const int at = t * plan.pitch + f;
+        c[at] = cs;
+        c[size + at] = -sn;
+        c[2 * size + at] = sn;
+      }
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&sh.full[s])) : "memory");
     }
-    if (!ok)  // copies in flight end before the CTA does
+    if (!ok && tid < 32)  // copies in flight end before the CTA does
       for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
         if (!(p.stall && i == 0)) mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, p.wait_cycles);
   }
@@ -408,7 +412,7 @@ struct RopeVec {
   __device__ __forceinline__ void run() {
     if (threadIdx.x == 0) {
       for (int s = 0; s < kStages; ++s) {
-        mbar_init(&sh.full[s], 33);  // the copies' bytes, and each lane of the loading warp
+        mbar_init(&sh.full[s], 1 + kRopeLoaders);  // the copies' bytes, and each loading thread
         mbar_init(&sh.empty[s], kRopeWorkers / 32);
       }
       sh.stop = 0;
@@ -416,12 +420,12 @@ struct RopeVec {
       fence_proxy_async_smem();
     }
     pdl_wait_and_release();
-    for (int i = threadIdx.x; i < p.half; i += kRopeWorkers + 32) {
+    for (int i = threadIdx.x; i < p.half; i += kRopeWorkers + kRopeLoaders) {
       sh.turn[i] = turn_of(p.inv_freq[i]);
       sh.axis[i] = axis_of(p, i);
     }
     const float one = p.gemma ? 1.0f : 0.0f;
-    for (int i = threadIdx.x; i < p.head_dim; i += kRopeWorkers + 32) {
+    for (int i = threadIdx.x; i < p.head_dim; i += kRopeWorkers + kRopeLoaders) {
       if (p.q.weight) sh.weight[0][i] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.q.weight) + i)) + one;
       if (p.k.weight) sh.weight[1][i] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.k.weight) + i)) + one;
     }
@@ -434,7 +438,7 @@ struct RopeVec {
 };
 
 template <int DT, int MODE, int LANES>
-__global__ void __launch_bounds__(kRopeWorkers + 32, 3) rope_vec(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
+__global__ void __launch_bounds__(kRopeWorkers + kRopeLoaders, 3) rope_vec(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
   extern __shared__ __align__(128) uint8_t raw[];
   __shared__ typename RopeVec<DT, MODE, LANES>::Shared sh;
   RopeVec<DT, MODE, LANES>{p, plan, sh, raw}.run();

@@ -264,7 +264,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   if (vec) {
     ar::RopePlan plan = ar::rope_plan(p, ctx->sm_count);
     void* args[2] = {&p, &plan};
-    st = launch(ctx, ar::rope_vec_kernel(bf16, p.head_dim, half, p.pairs), plan.ctas, 288, 1, args, ar::rope_smem(plan), stream);
+    st = launch(ctx, ar::rope_vec_kernel(bf16, p.head_dim, half, p.pairs), plan.ctas, 320, 1, args, ar::rope_smem(plan), stream);
   } else {
     const int64_t warps = n * (hq + hk * (cache ? 2 : 1));
     int64_t grid = (warps + 7) / 8;
