@@ -120,22 +120,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar(const __grid_constan
   }
 }
 
-// a * b, a * b + c on two floats at a time
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
 constexpr int kStages = 4;
 enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 
@@ -144,12 +128,14 @@ enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 // shared memory.  Two warps run ahead: one brings the rows in by bulk copies, the other finds the
 // tokens' places in the cache, and both compute the units' angles, once for all heads (a sincos
 // a head would cost more than the memory traffic does; one warp alone was the bound where rows
-// are short).  Eight warps work: n = head_dim / 8 lanes hold a head, 8
-// elements each, and a warp as many heads as fit (three of 80 elements; LANES = 8, 16 or 32 for
-// the powers of two, where a head's sum is a butterfly, 0 for others).  The partner of an element
-// is in the lane itself (pairs), in one other lane at the same place (halves that are a multiple
-// of 8: a shuffle), or anywhere (kHalvesAny: through shared memory, rows of 8 skewed by one float
-// so that lanes fall into different banks).
+// are short).  Eight warps work: n = head_dim / 16 lanes hold a head (rounded up), two chunks of 8
+// elements each, and a warp as many heads as fit (six of 80 elements; LANES = 4, 8 or 16 for
+// the powers of two, where a head's sum is a butterfly, 0 for others).  The chunks of a lane are
+// chosen so that it has both elements of each pair: adjacent pairs anyway, halves of a multiple
+// of 8 as chunk c and the one half a rotation on.  Other halves go through shared memory
+// (kHalvesAny; rows of 8 skewed by one float so that lanes fall into different banks).  With one
+// chunk a lane and shuffles between partners it took twice the instructions an element, and
+// they, not the memory, were the bound.
 //
 // The ring is what reaches the memory's bandwidth: with rows loaded straight into registers, four
 // a lane in flight, loads alone ran at 3 TB/s and the arithmetic came on top of them.
@@ -160,15 +146,21 @@ struct RopeVec {
     int64_t k_at[kStages][kRopeMaxStep], v_at[kStages][kRopeMaxStep];  // cache offsets of a token, -1: none
     unsigned long long turn[AR_MAX_HEAD_DIM / 2];
     int axis[AR_MAX_HEAD_DIM / 2];
-    __align__(16) float weight[2][AR_MAX_HEAD_DIM];  // w or 1 + w of q and k
-    float skew[MODE == kHalvesAny ? kRopeWorkers * 9 : 1];
+    __align__(16) float weight[2][AR_MAX_HEAD_DIM];  // w or 1 + w of q and k, in planes
+    float skew[MODE == kHalvesAny ? kRopeWorkers * 18 : 1];
     int stop;
   };
 
   const RopeParams& p;
   const RopePlan& plan;
   Shared& sh;
-  uint8_t* stage;  // kStages stages: rows, then cosines, sines negated, sines
+  uint8_t* stage;  // kStages stages: rows, then cosines and sines
+
+  // Eight floats a lane are read as two times 16 bytes.  Neighbouring lanes' 16 bytes stand side by
+  // side, so that they fall into different banks: element e of `count` in two planes of four
+  // each out of eight.
+  __device__ __forceinline__ static int in_planes(int e, int count) { return ((e >> 2) & 1) * (count / 2) + (e >> 3) * 4 + (e & 3); }
+  __device__ __forceinline__ int angle_at(int f) const { return MODE == kHalves8 ? in_planes(f, p.half) : f; }
 
   struct Unit {
     int64_t t0;
@@ -252,10 +244,9 @@ struct RopeVec {
         const int t = i / p.half_div, f = i - t * p.half;
         float sn, cs;
         angle(sh.turn[f], p.positions[sh.axis[f] * p.pos_stride + x.t0 + t], &sn, &cs);
-        const int at = t * plan.pitch + f;
+        const int at = t * plan.pitch + angle_at(f);
         c[at] = cs;
-        c[size + at] = -sn;
-        c[2 * size + at] = sn;
+        c[size + at] = sn;
       }
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&sh.full[s])) : "memory");
     }
@@ -264,12 +255,25 @@ struct RopeVec {
         if (!(p.stall && i == 0)) mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, p.wait_cycles);
   }
 
+  // Eight floats of chunk c out of two planes.
+  __device__ __forceinline__ static void planes(const float* p, int plane, int c, float (&f)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p + c * 4), b = *reinterpret_cast<const float4*>(p + plane + c * 4);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+
   __device__ __forceinline__ void work() {
-    const int n = LANES ? LANES : p.head_dim / 8;  // lanes of a head
+    const int chunks = p.head_dim / 8, n = LANES ? LANES : (chunks + 1) / 2;  // lanes of a head
     const int per_warp = 32 / n, wl = threadIdx.x & 31, in_warp = wl / n;
     const int lane = wl - in_warp * n, first = in_warp * n;  // place in the head; its first lane
     const bool there = LANES ? true : in_warp < per_warp;
-    const int e0 = lane * 8, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
+    // this lane's chunks; `two`: it has the second
+    const int hb = p.half / 8;
+    const bool turns = MODE != kHalves8 || lane < hb;
+    const int c0 = MODE != kHalves8 || turns ? lane : 2 * lane;
+    const int c1_raw = MODE != kHalves8 ? lane + n : (turns ? lane + hb : c0 + 1);
+    const bool two = c1_raw < chunks;
+    const int c1 = two ? c1_raw : c0;
     // Sum over a head's lanes, to all of them.
     auto head_sum = [&](float s) {
       if constexpr (LANES != 0) {
@@ -296,10 +300,12 @@ struct RopeVec {
         return sum;
       }
     };
-    const bool low = e0 < p.half, turns = e0 < 2 * p.half;  // of kHalves8
-    const int f0 = MODE == kPairs ? lane * 4 : (turns ? (low ? e0 : e0 - p.half) : 0);
-    const int partner = (first + (turns ? (low ? lane + p.half / 8 : lane - p.half / 8) : lane)) & 31;
-    const int size = plan.step * plan.pitch;
+    const int size = plan.step * plan.pitch, head = p.head_dim * 2, v0 = p.q.heads + p.k.heads;
+    const int per_round = (kRopeWorkers / 32) * per_warp;
+    auto store2 = [&](uint16_t* dst, const uint4& a, const uint4& b) {
+      st_v4(dst + c0 * 8, a);
+      if (two) st_v4(dst + c1 * 8, b);
+    };
     uint32_t k = 0;
     for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++k) {
       const int s = k % kStages;
@@ -307,101 +313,112 @@ struct RopeVec {
       const bool ok = wait(&sh.full[s], (k / kStages) & 1);
       if (!__all_sync(0xffffffffu, ok)) return;
       const uint8_t* rows = rows_of(s);
-      const float* cosv = angles_of(s);
-      const int heads = x.hi - x.lo, total = x.tokens * heads;
-      for (int base = warp * per_warp; base < total; base += (kRopeWorkers / 32) * per_warp) {
-        const int at = base + in_warp;
+      const float* angles = angles_of(s);
+      uint16_t* q_out = static_cast<uint16_t*>(p.q.out) + x.t0 * p.q.out_ts;
+      uint16_t* k_out = p.k.out ? static_cast<uint16_t*>(p.k.out) + x.t0 * p.k.out_ts : nullptr;
+      const int total = x.tokens * (x.hi - x.lo);
+      for (int at = warp * per_warp + in_warp; at - in_warp < total; at += per_round) {
         const bool mine = there && at < total;
         const int i0 = min(at, total - 1);
-        const int t = plan.split == 1 ? i0 / plan.heads_div : 0, hh = i0 - t * heads;
-        int h = x.lo + hh;
-        const bool is_q = h < p.q.heads, is_v = h >= p.q.heads + p.k.heads;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (mine) raw = lds_v4(rows + ((size_t)(t * plan.per + hh) * p.head_dim + e0) * 2);
-        if (__all_sync(0xffffffffu, is_v || !mine)) {  // v is copied
-          if (mine && sh.v_at[s][t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + sh.v_at[s][t] + (h - p.q.heads - p.k.heads) * p.vc_hs + e0, raw);
+        const int t = plan.step > 1 ? i0 / plan.heads_div : 0;
+        const int h = x.lo + i0 - t * plan.per;
+        const uint8_t* row = rows + i0 * head;
+        const uint4 raw0 = lds_v4(row + c0 * 16), raw1 = two ? lds_v4(row + c1 * 16) : make_uint4(0, 0, 0, 0);
+        const bool is_q = h < p.q.heads, is_v = h >= v0;
+        uint16_t* v_dst = static_cast<uint16_t*>(p.v_cache) + sh.v_at[s][t] + (h - v0) * p.vc_hs;
+        if (__all_sync(0xffffffffu, is_v)) {  // v is copied
+          if (mine && sh.v_at[s][t] >= 0) store2(v_dst, raw0, raw1);
           continue;
         }
-        float f[8];
-        float2 a[4], y[4];
-        unpack8<DT>(raw, f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = make_float2(f[2 * i], f[2 * i + 1]);
+        float a[8], b[8], y[8], z[8];
+        unpack8<DT>(raw0, a);
+        unpack8<DT>(raw1, b);
         if (p.q.weight || p.k.weight) {
-          float2 ss = mul2(a[0], a[0]);
+          float sa = a[0] * a[0], sb = b[0] * b[0];
 #pragma unroll
-          for (int i = 1; i < 4; ++i) ss = fma2(a[i], a[i], ss);
-          const float rs = rsqrtf(head_sum(ss.x + ss.y) * p.inv_dim + p.eps);
+          for (int i = 1; i < 8; ++i) {
+            sa = fmaf(a[i], a[i], sa);
+            sb = fmaf(b[i], b[i], sb);
+          }
+          const float rs = rsqrtf(head_sum(sa + sb) * p.inv_dim + p.eps);
           if (is_q ? p.q.weight != nullptr : p.k.weight != nullptr) {
-            const float* w = sh.weight[is_q ? 0 : 1] + e0;
-            const float4 w0 = *reinterpret_cast<const float4*>(w), w1 = *reinterpret_cast<const float4*>(w + 4);
-            const float2 r2 = make_float2(rs, rs);
-            a[0] = mul2(mul2(a[0], r2), make_float2(w0.x, w0.y));
-            a[1] = mul2(mul2(a[1], r2), make_float2(w0.z, w0.w));
-            a[2] = mul2(mul2(a[2], r2), make_float2(w1.x, w1.y));
-            a[3] = mul2(mul2(a[3], r2), make_float2(w1.z, w1.w));
+            const float* w = sh.weight[is_q ? 0 : 1];
+            float wa[8], wb[8];
+            planes(w, p.head_dim / 2, c0, wa);
+            planes(w, p.head_dim / 2, c1, wb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              a[i] *= rs * wa[i];
+              b[i] *= rs * wb[i];
+            }
           }
         }
         // an element that does not turn keeps its value, infinities included
-        const float* c = cosv + t * plan.pitch;
-        if constexpr (MODE == kPairs) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = a[i];
-          if (f0 < p.half) {
-            const float4 c4 = *reinterpret_cast<const float4*>(c + f0), s4 = *reinterpret_cast<const float4*>(c + 2 * size + f0);
+        for (int i = 0; i < 8; ++i) {
+          y[i] = a[i];
+          z[i] = b[i];
+        }
+        const float* c = angles + t * plan.pitch;
+        if constexpr (MODE == kPairs) {
+          auto turn = [&](int chunk, const float (&from)[8], float (&to)[8]) {
+            if (chunk * 4 >= p.half) return;
+            const float4 c4 = *reinterpret_cast<const float4*>(c + chunk * 4), s4 = *reinterpret_cast<const float4*>(c + size + chunk * 4);
             const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, sc[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (f0 + i < p.half) y[i] = make_float2(a[i].x * cc[i] - a[i].y * sc[i], a[i].y * cc[i] + a[i].x * sc[i]);
-          }
+              if (chunk * 4 + i < p.half) {
+                to[2 * i] = from[2 * i] * cc[i] - from[2 * i + 1] * sc[i];
+                to[2 * i + 1] = from[2 * i + 1] * cc[i] + from[2 * i] * sc[i];
+              }
+          };
+          turn(c0, a, y);
+          turn(c1, b, z);
         } else if constexpr (MODE == kHalves8) {
-          float2 other[4];
+          if (turns) {
+            float cc[8], sc[8];
+            planes(c, p.half / 2, lane, cc);
+            planes(c + size, p.half / 2, lane, sc);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            other[i] = make_float2(__shfl_sync(0xffffffffu, a[i].x, partner), __shfl_sync(0xffffffffu, a[i].y, partner));
-            y[i] = a[i];
-          }
-          if (turns) {  // a' = a cos - b sin, b' = b cos + a sin
-            const float* sn = c + (low ? size : 2 * size);
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float4 c4 = *reinterpret_cast<const float4*>(c + f0 + 2 * i), s4 = *reinterpret_cast<const float4*>(sn + f0 + 2 * i);
-              y[i] = fma2(other[i], make_float2(s4.x, s4.y), mul2(a[i], make_float2(c4.x, c4.y)));
-              y[i + 1] = fma2(other[i + 1], make_float2(s4.z, s4.w), mul2(a[i + 1], make_float2(c4.z, c4.w)));
+            for (int i = 0; i < 8; ++i) {
+              y[i] = a[i] * cc[i] - b[i] * sc[i];
+              z[i] = b[i] * cc[i] + a[i] * sc[i];
             }
           }
         } else {
-          float* row = sh.skew + (threadIdx.x - lane) * 9;  // element e at e + e / 8
-#pragma unroll
-          for (int i = 0; i < 8; ++i) row[lane * 9 + i] = i & 1 ? a[i / 2].y : a[i / 2].x;
-          __syncwarp();
-          float v[8];
+          float* skew = sh.skew + (threadIdx.x - lane) * 18;  // element e at e + e / 8
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            v[i] = i & 1 ? a[i / 2].y : a[i / 2].x;
-            if (there && e < 2 * p.half) {  // (lanes behind the warp's last head would read behind the array)
-              const bool lo = e < p.half;
-              const int q = lo ? e + p.half : e - p.half, g = lo ? e : q;
-              v[i] = v[i] * c[g] + row[q + (q >> 3)] * c[(lo ? size : 2 * size) + g];
-            }
+            if (there) skew[c0 * 9 + i] = a[i];  // (lanes behind the warp's last head have no place)
+            if (there && two) skew[c1 * 9 + i] = b[i];
           }
           __syncwarp();
+          auto turn = [&](int chunk, const float (&from)[8], float (&to)[8]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = make_float2(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) {
+              const int e = chunk * 8 + i;
+              if (there && e < 2 * p.half) {
+                const bool lo = e < p.half;
+                const int q = lo ? e + p.half : e - p.half, g = lo ? e : q;
+                const float other = skew[q + (q >> 3)] * c[size + g];
+                to[i] = from[i] * c[g] + (lo ? -other : other);
+              }
+            }
+          };
+          turn(c0, a, y);
+          turn(c1, b, z);
+          __syncwarp();
         }
         if (!mine) continue;
-        if (is_v) {
-          if (sh.v_at[s][t] >= 0) st_v4(static_cast<uint16_t*>(p.v_cache) + sh.v_at[s][t] + (h - p.q.heads - p.k.heads) * p.vc_hs + e0, raw);
-          continue;
-        }
-        const uint4 z = make_uint4(pack2<DT>(y[0].x, y[0].y), pack2<DT>(y[1].x, y[1].y), pack2<DT>(y[2].x, y[2].y), pack2<DT>(y[3].x, y[3].y));
+        const uint4 out0 = pack8<DT>(y), out1 = pack8<DT>(z);
         if (is_q) {
-          st_v4(static_cast<uint16_t*>(p.q.out) + (x.t0 + t) * p.q.out_ts + h * p.q.out_hs + e0, z);
+          store2(q_out + t * p.q.out_ts + h * p.q.out_hs, out0, out1);
+        } else if (is_v) {
+          if (sh.v_at[s][t] >= 0) store2(v_dst, raw0, raw1);
         } else {
-          h -= p.q.heads;
-          if (p.k.out) st_v4(static_cast<uint16_t*>(p.k.out) + (x.t0 + t) * p.k.out_ts + h * p.k.out_hs + e0, z);
-          if (p.k_cache && sh.k_at[s][t] >= 0) st_v4(static_cast<uint16_t*>(p.k_cache) + sh.k_at[s][t] + h * p.kc_hs + e0, z);
+          const int kh = h - p.q.heads;
+          if (k_out) store2(k_out + t * p.k.out_ts + kh * p.k.out_hs, out0, out1);
+          if (p.k_cache && sh.k_at[s][t] >= 0) store2(static_cast<uint16_t*>(p.k_cache) + sh.k_at[s][t] + kh * p.kc_hs, out0, out1);
         }
       }
       __syncwarp();
@@ -426,8 +443,8 @@ struct RopeVec {
     }
     const float one = p.gemma ? 1.0f : 0.0f;
     for (int i = threadIdx.x; i < p.head_dim; i += kRopeWorkers + kRopeLoaders) {
-      if (p.q.weight) sh.weight[0][i] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.q.weight) + i)) + one;
-      if (p.k.weight) sh.weight[1][i] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.k.weight) + i)) + one;
+      if (p.q.weight) sh.weight[0][in_planes(i, p.head_dim)] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.q.weight) + i)) + one;
+      if (p.k.weight) sh.weight[1][in_planes(i, p.head_dim)] = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.k.weight) + i)) + one;
     }
     __syncthreads();
     if (threadIdx.x >= kRopeWorkers)
@@ -447,9 +464,9 @@ __global__ void __launch_bounds__(kRopeWorkers + kRopeLoaders, 3) rope_vec(const
 template <int DT, int MODE>
 const void* vec_of(int dim) {
   switch (dim) {
-    case 64: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 8>);
-    case 128: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 16>);
-    case 256: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 32>);
+    case 64: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 4>);
+    case 128: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 8>);
+    case 256: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 16>);
     default: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 0>);
   }
 }
@@ -473,7 +490,7 @@ const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs) {
 RopePlan rope_plan(const RopeParams& p, int sm_count) {
   RopePlan r;
   r.heads = p.q.heads + p.k.heads * (p.k_cache ? 2 : 1);
-  const int head = p.head_dim * 2, round = 32 / (p.head_dim / 8) * (kRopeWorkers / 32);  // heads at a time
+  const int head = p.head_dim * 2, round = 32 / ((p.head_dim / 8 + 1) / 2) * (kRopeWorkers / 32);  // heads at a time
   // heads of a unit: all, or what fits a stage
   r.split = 1;
   while ((r.heads + r.split - 1) / r.split * head > kRopeRowBytes && r.split < r.heads) r.split *= 2;
@@ -487,7 +504,7 @@ RopePlan rope_plan(const RopeParams& p, int sm_count) {
   r.heads_div = fast_div((uint32_t)r.per);
   r.pitch = (p.half + 3) / 4 * 4;
   r.row_bytes = (r.step * r.per * head + 127) / 128 * 128;
-  r.stage_bytes = (r.row_bytes + r.step * r.pitch * 12 + 127) / 128 * 128;
+  r.stage_bytes = (r.row_bytes + r.step * r.pitch * 8 + 127) / 128 * 128;
   r.units = (p.tokens + r.step - 1) / r.step * r.split;
   r.ctas = r.units < (int64_t)3 * sm_count ? (unsigned)r.units : 3u * sm_count;
   return r;
@@ -497,6 +514,6 @@ size_t rope_smem(const RopePlan& r) { return (size_t)kStages * r.stage_bytes; }
 
 // The largest that rope_plan asks for: a stage of rows and the angles of the most tokens that
 // fit beside them.
-size_t rope_smem_most() { return (size_t)kStages * (kRopeRowBytes + 128 + kRopeMaxStep * (AR_MAX_HEAD_DIM / 2) * 12 + 128); }
+size_t rope_smem_most() { return (size_t)kStages * (kRopeRowBytes + 128 + kRopeMaxStep * (AR_MAX_HEAD_DIM / 2) * 8 + 128); }
 
 }  // namespace ar
