@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar(const __grid_constan
   }
 }
 
-constexpr int kStages = 4;
+constexpr int kStages = 3;  // with four, three CTAs do not fit an SM where angles are many (52618 x 10 heads of 96: 59 us, 92 with four)
 enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 
 // Rows on 16-byte boundaries and heads of a multiple of 8 elements.  A CTA works through units of
