@@ -144,6 +144,11 @@ class ArPagedAttentionArgs(ctypes.Structure):
     """)
 
 
+_Sections = ctypes.c_int * AR_MAX_ROPE_AXES
+_NO_SECTIONS = _Sections()
+_NO_CACHES = (None, None, 0, 0, 0, 0, 0, 0, 0, 1)
+
+
 class PagedPlan(NamedTuple):
     """One step's plan (see ar_paged_plan): device tensors."""
     block_table: object
@@ -313,23 +318,23 @@ def ar_fused_reduce_rmsnorm_batch(ctx: int, calls: Sequence[ArFusedArgs], stream
 
 
 def ar_paged_plan(ctx: int, args: ArPagedPlanArgs, stream: Optional[int] = None, raise_on_error: bool = True) -> int:
-    st = load_library().ar_paged_plan(ctx, ctypes.byref(args), stream)
-    if raise_on_error:
+    st = (_lib or load_library()).ar_paged_plan(ctx, ctypes.byref(args), stream)
+    if st != AR_OK and raise_on_error:
         _check(ctx, st, "ar_paged_plan")
     return st
 
 
 def ar_qk_norm_rope(ctx: int, args: ArQkNormRopeArgs, stream: Optional[int] = None, raise_on_error: bool = True) -> int:
-    st = load_library().ar_qk_norm_rope(ctx, ctypes.byref(args), stream)
-    if raise_on_error:
+    st = (_lib or load_library()).ar_qk_norm_rope(ctx, ctypes.byref(args), stream)
+    if st != AR_OK and raise_on_error:
         _check(ctx, st, "ar_qk_norm_rope")
     return st
 
 
 def ar_paged_attention(ctx: int, args: ArPagedAttentionArgs, stream: Optional[int] = None,
                        raise_on_error: bool = True) -> int:
-    st = load_library().ar_paged_attention(ctx, ctypes.byref(args), stream)
-    if raise_on_error:
+    st = (_lib or load_library()).ar_paged_attention(ctx, ctypes.byref(args), stream)
+    if st != AR_OK and raise_on_error:
         _check(ctx, st, "ar_paged_attention")
     return st
 
@@ -409,44 +414,70 @@ def _row_stride(tensors, m, h, dtype, what, host: bool = False) -> int:
     return h if ld is None else ld
 
 
+# What the attention block's methods need of torch, bound at the first use (importing this
+# package does not import torch).
+class _Torch:
+    def __init__(self):
+        import torch
+        self.i32, self.i64, self.f32, self.u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+        self.codes = {torch.bfloat16: AR_DTYPE_BF16, torch.float16: AR_DTYPE_F16}
+        self.empty, self.device, self.use_stream = torch.empty, torch.device, torch.cuda.stream
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_torch: Optional[_Torch] = None
+
+
+def _bind_torch() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
 def _flat(t, dtype, n, device, what) -> Optional[int]:
     """Address of a contiguous CUDA tensor of `n` elements (None: any number) on `device`."""
     if t is None:
         return None
-    if t.dtype != dtype or t.get_device() != device or not t.is_contiguous() or (n is not None and t.numel() != n):
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor on cuda:{device}"
                          + ("" if n is None else f" with {n} elements"))
     return t.data_ptr()
 
 
-def _heads(t, tokens, heads, dim, dtype, device, what):
+def _heads(t, shape, dtype, device, what):
     """(address, token stride, head stride) of a [tokens, heads, dim] tensor with unit last stride."""
-    if t.shape != (tokens, heads, dim) or t.dtype != dtype or t.get_device() != device:
-        raise ValueError(f"{what} must be a [{tokens}, {heads}, {dim}] {dtype} tensor on cuda:{device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what} must be a {list(shape)} {dtype} tensor on cuda:{device}")
     ts, hs, one = t.stride()
-    if one != 1 and dim > 1:
+    if one != 1 and shape[2] > 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
     return t.data_ptr(), ts, hs
 
 
-def _cache(t, heads, dim, dtype, device, what):
-    """(address, block, token, head stride, blocks, page) of a [blocks, page, heads, dim] cache."""
-    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim or t.dtype != dtype or t.get_device() != device:
-        raise ValueError(f"{what} must be a [blocks, page, {heads}, {dim}] {dtype} tensor on cuda:{device}")
-    bs, ps, hs, one = t.stride()
-    if one != 1 and dim > 1:
-        raise ValueError(f"{what} must have unit stride in its last dimension")
-    return t.data_ptr(), bs, ps, hs, t.shape[0], t.shape[1]
+def _caches(k, v, heads, dim, dtype, device):
+    """(k address, v address, k's block, token and head strides, v's, blocks, page) of two
+    [blocks, page, heads, dim] caches."""
+    shape = k.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != dim or v.shape != shape or k.dtype is not dtype or \
+            v.dtype is not dtype or k.get_device() != device or v.get_device() != device:
+        raise ValueError(f"k_cache and v_cache must be [blocks, page, {heads}, {dim}] {dtype} tensors on cuda:{device}")
+    kb, kp, kh, one = k.stride()
+    vb, vp, vh, one_v = v.stride()
+    if (one != 1 or one_v != 1) and dim > 1:
+        raise ValueError("k_cache and v_cache must have unit stride in their last dimension")
+    return k.data_ptr(), v.data_ptr(), kb, kp, kh, vb, vp, vh, shape[0], shape[1]
 
 
 def _table(t, requests, device):
     """(address, columns, row stride) of a [requests, columns] int32 block table."""
-    import torch
-    if t.dim() != 2 or t.shape[0] != requests or t.dtype != torch.int32 or t.get_device() != device or \
-            (t.shape[1] > 1 and t.stride(1) != 1) or (requests > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"block_table must be a [{requests}, columns] int32 tensor on cuda:{device}, "
-                         "unit stride in its rows")
-    return t.data_ptr(), t.shape[1], t.stride(0) if requests > 1 else 0
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != requests or t.dtype is not _torch.i32 or t.get_device() != device:
+        raise ValueError(f"block_table must be a [{requests}, columns] int32 tensor on cuda:{device}")
+    rows, one = t.stride()
+    if (shape[1] > 1 and one != 1) or (requests > 1 and rows < shape[1]):
+        raise ValueError("block_table must have unit stride in its rows, and rows that do not overlap")
+    return t.data_ptr(), shape[1], rows if requests > 1 else 0
 
 
 class Context:
@@ -456,6 +487,7 @@ class Context:
         self.device = device
         self.handle = ar_init(device)
         self._workspace_bytes = {}
+        self._torch_device = None
 
     def close(self):
         if self.handle:
@@ -593,20 +625,23 @@ class Context:
     # ---- the attention block ------------------------------------------------
 
     def _raw_stream(self, stream) -> int:
-        import torch
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _torch.raw_stream(self.device)
         if stream.device.index != self.device:
             raise ValueError(f"the stream belongs to another device than cuda:{self.device}")
         return stream.cuda_stream
 
     def _empty(self, shape, dtype, stream):
         """An output on this device that belongs to `stream` (None: the current one)."""
-        import torch
+        t = _bind_torch()
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.device))
+            return t.empty(shape, dtype=dtype, device=self._torch_device or self._make_torch_device())
+        with t.use_stream(stream):
+            return t.empty(shape, dtype=dtype, device=self._torch_device or self._make_torch_device())
+
+    def _make_torch_device(self):
+        self._torch_device = _torch.device("cuda", self.device)
+        return self._torch_device
 
     def paged_plan(self, cached_lens, new_lens, free_blocks, free_count, block_table, page_size: int,
                    max_tokens: Optional[int] = None, cu_q=None, seq_lens=None, slots=None, positions=None,
@@ -615,8 +650,8 @@ class Context:
         `block_table` [requests, columns] is updated in place; the others are returned, allocated
         where not given.  `max_tokens` is the length of slots and positions (needed unless one of
         them is given); free_count_out must not be free_count itself."""
-        import torch
-        dev, i32, r = self.device, torch.int32, cached_lens.numel()
+        t = _torch or _bind_torch()
+        dev, i32, r = self.device, t.i32, cached_lens.numel()
         if max_tokens is None:
             given = slots if slots is not None else positions
             if given is None:
@@ -627,7 +662,7 @@ class Context:
         if seq_lens is None:
             seq_lens = self._empty((r,), i32, stream)
         if slots is None:
-            slots = self._empty((max_tokens,), torch.int64, stream)
+            slots = self._empty((max_tokens,), t.i64, stream)
         if positions is None:
             positions = self._empty((max_tokens,), i32, stream)
         if free_count_out is None:
@@ -640,7 +675,7 @@ class Context:
             _flat(cached_lens, i32, r, dev, "cached_lens"), _flat(new_lens, i32, r, dev, "new_lens"),
             _flat(free_blocks, i32, None, dev, "free_blocks"), _flat(free_count, i32, 1, dev, "free_count"),
             table, _flat(cu_q, i32, r + 1, dev, "cu_q"), _flat(seq_lens, i32, r, dev, "seq_lens"),
-            _flat(slots, torch.int64, max_tokens, dev, "slots"), _flat(positions, i32, max_tokens, dev, "positions"),
+            _flat(slots, t.i64, max_tokens, dev, "slots"), _flat(positions, i32, max_tokens, dev, "positions"),
             _flat(free_count_out, i32, 1, dev, "free_count_out"), _flat(info, i32, 4, dev, "info"))
         ar_paged_plan(self.handle, args, self._raw_stream(stream))
         return PagedPlan(block_table, cu_q, seq_lens, slots, positions, free_count_out, info)
@@ -654,59 +689,68 @@ class Context:
         the write of k and v to the paged cache at `slots` (see ar_qk_norm_rope).  q, k, v are
         [tokens, heads, head_dim] and may be views of one packed projection; q or k may be None.
         Returns (q_out, k_out); with a cache, want_k_out=False leaves k_out out (None)."""
-        import torch
+        t = _torch or _bind_torch()
         dev = self.device
         x0 = q if q is not None else k
         if x0 is None:
             raise ValueError("q or k must be given")
-        n, _, d = x0.shape
+        n, heads, d = x0.shape
         dt = x0.dtype
-        if dt not in (torch.bfloat16, torch.float16):
+        code = t.codes.get(dt)
+        if code is None:
             raise ValueError("q, k and v must be bfloat16 or float16")
-        hq, hk = (0 if q is None else q.shape[1]), (0 if k is None else k.shape[1])
-        none = (None, 0, 0)
-        qa = _heads(q, n, hq, d, dt, dev, "q") if hq else none
-        ka = _heads(k, n, hk, d, dt, dev, "k") if hk else none
-        if hq and q_out is None:
-            q_out = self._empty((n, hq, d), dt, stream)
-        if hk and k_out is None and (want_k_out or k_cache is None):
-            k_out = self._empty((n, hk, d), dt, stream)
-        qo = _heads(q_out, n, hq, d, dt, dev, "q_out") if hq else none
-        ko = _heads(k_out, n, hk, d, dt, dev, "k_out") if hk and k_out is not None else none
-        half = 0 if inv_freq is None else inv_freq.numel()
-        axes, pos, pos_stride = 1, None, 0
-        if half:
-            if positions.dtype != torch.int32 or positions.get_device() != dev or positions.dim() not in (1, 2) or \
-                    positions.shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
-                raise ValueError(f"positions must be a [{n}] or [axes, {n}] int32 tensor on cuda:{dev}, unit stride")
-            pos = positions.data_ptr()
-            if positions.dim() == 2:
-                axes = positions.shape[0]
-                pos_stride = positions.stride(0) if axes > 1 else 0
-            if not 1 <= axes <= AR_MAX_ROPE_AXES:
-                raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
-            if axes > 1 and (sections is None or len(sections) != axes):
-                raise ValueError("sections must name the frequencies of each position axis")
-        sec = (ctypes.c_int * AR_MAX_ROPE_AXES)(*(sections if axes > 1 else ()))
-        kc = vc = (None, 0, 0, 0, 0, 1)
-        va, slot = none, None
+        hq, hk = (0 if q is None else heads), (0 if k is None else k.shape[1])
+        qp = kp = vp = qop = kop = slot = None
+        qt = qh = kt = kh = vt = vh = qot = qoh = kot = koh = 0
+        if hq:
+            shape = (n, hq, d)
+            qp, qt, qh = _heads(q, shape, dt, dev, "q")
+            if q_out is None:
+                q_out = self._empty(shape, dt, stream)
+            qop, qot, qoh = _heads(q_out, shape, dt, dev, "q_out")
+        caches = _NO_CACHES
         if (k_cache is None) != (v_cache is None):
             raise ValueError("k_cache and v_cache are given together")
+        if hk:
+            shape = (n, hk, d)
+            kp, kt, kh = _heads(k, shape, dt, dev, "k")
+            if k_out is None and (want_k_out or k_cache is None):
+                k_out = self._empty(shape, dt, stream)
+            if k_out is not None:
+                kop, kot, koh = _heads(k_out, shape, dt, dev, "k_out")
         if k_cache is not None:
-            if v is None or slots is None:
-                raise ValueError("a cache needs v and slots")
-            va = _heads(v, n, hk, d, dt, dev, "v")
-            kc = _cache(k_cache, hk, d, dt, dev, "k_cache")
-            vc = _cache(v_cache, hk, d, dt, dev, "v_cache")
-            if kc[4:] != vc[4:]:
-                raise ValueError("k_cache and v_cache must have the same blocks and page size")
-            slot = _flat(slots, torch.int64, n, dev, "slots")
+            if not hk or v is None or slots is None:
+                raise ValueError("a cache needs k, v and slots")
+            vp, vt, vh = _heads(v, shape, dt, dev, "v")
+            caches = _caches(k_cache, v_cache, hk, d, dt, dev)
+            slot = _flat(slots, t.i64, n, dev, "slots")
+        half, axes, pos, pos_stride, freq = 0, 1, None, 0, None
+        sec = _NO_SECTIONS
+        if inv_freq is not None:
+            half = inv_freq.numel()
+            freq = _flat(inv_freq, t.f32, half, dev, "inv_freq")
+        if half:
+            shape = positions.shape
+            if positions.dtype is not t.i32 or positions.get_device() != dev or len(shape) not in (1, 2) or \
+                    shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
+                raise ValueError(f"positions must be a [{n}] or [axes, {n}] int32 tensor on cuda:{dev}, unit stride")
+            pos = positions.data_ptr()
+            if len(shape) == 2:
+                axes = shape[0]
+                if axes > 1:
+                    pos_stride = positions.stride(0)
+                    if axes > AR_MAX_ROPE_AXES:
+                        raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
+                    if sections is None or len(sections) != axes:
+                        raise ValueError("sections must name the frequencies of each position axis")
+                    sec = _Sections(*sections)
+                elif axes < 1:
+                    raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
         args = ArQkNormRopeArgs(
-            n, hq, hk, d, AR_DTYPE_BF16 if dt == torch.bfloat16 else AR_DTYPE_F16, qa[0], ka[0], va[0],
-            qa[1], qa[2], ka[1], ka[2], va[1], va[2], qo[0], ko[0], qo[1], qo[2], ko[1], ko[2],
-            _flat(q_weight, dt, d, dev, "q_weight"), _flat(k_weight, dt, d, dev, "k_weight"), eps, gemma, 2 * half,
-            pairs, axes, sec, dealt, pos, pos_stride, _flat(inv_freq, torch.float32, half, dev, "inv_freq"),
-            kc[0], vc[0], kc[1], kc[2], kc[3], vc[1], vc[2], vc[3], kc[4], kc[5], slot)
+            n, hq, hk, d, code, qp, kp, vp, qt, qh, kt, kh, vt, vh, qop, kop, qot, qoh, kot, koh,
+            None if q_weight is None else _flat(q_weight, dt, d, dev, "q_weight"),
+            None if k_weight is None else _flat(k_weight, dt, d, dev, "k_weight"),
+            eps, gemma, 2 * half, pairs, axes, sec, dealt, pos, pos_stride, freq, *caches, slot)
         ar_qk_norm_rope(self.handle, args, self._raw_stream(stream))
         return q_out, k_out
 
@@ -719,50 +763,49 @@ class Context:
         wanted.  Rows of no request are not written.  `workspace` (uint8, from
         paged_attention_workspace) is allocated where not given; calls that may run at the
         same time need one each."""
-        import torch
+        t = _torch or _bind_torch()
         dev = self.device
-        n, hq, d = q.shape
+        shape = q.shape
+        n, hq, d = shape
         dt = q.dtype
-        if dt not in (torch.bfloat16, torch.float16):
+        code = t.codes.get(dt)
+        if code is None:
             raise ValueError("q must be bfloat16 or float16")
-        code = AR_DTYPE_BF16 if dt == torch.bfloat16 else AR_DTYPE_F16
         r, hk = seq_lens.numel(), k_cache.shape[2]
         if hk < 1 or hq % hk:
             raise ValueError("q_heads must be a multiple of kv_heads")
         if out is None:
-            out = self._empty((n, hq, d), dt, stream)
+            out = self._empty(shape, dt, stream)
         if lse is None and want_lse:
-            lse = self._empty((n, hq), torch.float32, stream)
+            lse = self._empty((n, hq), t.f32, stream)
         if workspace is None:
-            workspace = self._empty((self._attention_workspace(d, code),), torch.uint8, stream)
-        qa = _heads(q, n, hq, d, dt, dev, "q")
-        oa = _heads(out, n, hq, d, dt, dev, "out")
-        kc = _cache(k_cache, hk, d, dt, dev, "k_cache")
-        vc = _cache(v_cache, hk, d, dt, dev, "v_cache")
-        if kc[4:] != vc[4:]:
-            raise ValueError("k_cache and v_cache must have the same blocks and page size")
+            size = self._attention_workspace(d, code)
+            workspace = self._empty(size, t.u8, stream)
+            work = workspace.data_ptr()
+        else:
+            work, size = _flat(workspace, t.u8, None, dev, "workspace"), workspace.numel()
+        qp, qt, qh = _heads(q, shape, dt, dev, "q")
+        op, ot, oh = _heads(out, shape, dt, dev, "out")
+        kp, vp, kb, kt, kh, vb, vt, vh, blocks, page = _caches(k_cache, v_cache, hk, d, dt, dev)
         table, cols, stride = _table(block_table, r, dev)
         args = ArPagedAttentionArgs(
-            n, r, hq, hk, d, code, qa[0], oa[0], qa[1], qa[2], oa[1], oa[2],
-            _flat(lse, torch.float32, n * hq, dev, "lse"), kc[0], vc[0], kc[1], kc[2], kc[3], vc[1], vc[2], vc[3],
-            kc[4], kc[5], table, cols, stride, _flat(cu_q, torch.int32, r + 1, dev, "cu_q"),
-            _flat(seq_lens, torch.int32, r, dev, "seq_lens"), d ** -0.5 if scale is None else scale, causal, window,
-            softcap, _flat(slopes, torch.float32, hq, dev, "slopes"),
-            _flat(prefix_lens, torch.int32, r, dev, "prefix_lens"),
-            _flat(workspace, torch.uint8, None, dev, "workspace"), workspace.numel())
+            n, r, hq, hk, d, code, qp, op, qt, qh, ot, oh,
+            None if lse is None else _flat(lse, t.f32, n * hq, dev, "lse"), kp, vp, kb, kt, kh, vb, vt, vh, blocks, page,
+            table, cols, stride, _flat(cu_q, t.i32, r + 1, dev, "cu_q"), _flat(seq_lens, t.i32, r, dev, "seq_lens"),
+            d ** -0.5 if scale is None else scale, causal, window, softcap,
+            None if slopes is None else _flat(slopes, t.f32, hq, dev, "slopes"),
+            None if prefix_lens is None else _flat(prefix_lens, t.i32, r, dev, "prefix_lens"), work, size)
         ar_paged_attention(self.handle, args, self._raw_stream(stream))
         return out, lse
 
     def _attention_workspace(self, head_dim: int, code: int) -> int:
-        key = (head_dim, code)
-        n = self._workspace_bytes.get(key)
+        n = self._workspace_bytes.get((head_dim, code))
         if n is None:
-            n = self._workspace_bytes[key] = ar_paged_attention_workspace(
+            n = self._workspace_bytes[head_dim, code] = ar_paged_attention_workspace(
                 self.handle, ArPagedAttentionArgs(head_dim=head_dim, dtype=code))
         return n
 
     def paged_attention_workspace(self, head_dim: int, dtype):
         """A workspace for paged_attention calls with this head size and element type, of any lengths."""
-        import torch
-        code = {torch.bfloat16: AR_DTYPE_BF16, torch.float16: AR_DTYPE_F16}[dtype]
-        return self._empty((self._attention_workspace(head_dim, code),), torch.uint8, None)
+        t = _bind_torch()
+        return self._empty(self._attention_workspace(head_dim, t.codes[dtype]), t.u8, None)
