@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -144,9 +145,17 @@ class ArPagedAttentionArgs(ctypes.Structure):
     """)
 
 
-_Sections = ctypes.c_int * AR_MAX_ROPE_AXES
-_NO_SECTIONS = _Sections()
-_NO_CACHES = (None, None, 0, 0, 0, 0, 0, 0, 0, 1)
+def _packer(args):
+    """pack(*values) of an argument structure's fields, as bytes that the C functions take for it
+    (a third of the time of building the ctypes structure)."""
+    codes = {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_size_t: "N", ctypes.c_void_p: "P",
+             ctypes.c_int * AR_MAX_ROPE_AXES: f"{AR_MAX_ROPE_AXES}i"}
+    return struct.Struct("@" + "".join(codes[kind] for _, kind in args._fields_)).pack
+
+
+_pack_plan, _pack_rope, _pack_attention = map(_packer, (ArPagedPlanArgs, ArQkNormRopeArgs, ArPagedAttentionArgs))
+_NO_SECTIONS = (0,) * AR_MAX_ROPE_AXES
+_NO_CACHES = (0, 0, 0, 0, 0, 0, 0, 0, 0, 1)
 
 
 class PagedPlan(NamedTuple):
@@ -170,6 +179,7 @@ class ArError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+_packed = {}  # C functions that take their arguments as packed bytes
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -207,6 +217,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
               "ar_get_info", "ar_device_status", "ar_fused_reduce_rmsnorm_batch", "ar_fused_reduce_rmsnorm_host",
               "ar_fused_reduce_rmsnorm_noalloc"):
         getattr(lib, f).restype = c_int
+    for f in ("ar_paged_plan", "ar_qk_norm_rope", "ar_paged_attention"):
+        _packed[f] = fn = lib[f]  # a function object of its own
+        fn.argtypes, fn.restype = [vp, ctypes.c_char_p, vp], c_int
     _lib = lib
     return lib
 
@@ -435,10 +448,10 @@ def _bind_torch() -> _Torch:
     return _torch
 
 
-def _flat(t, dtype, n, device, what) -> Optional[int]:
-    """Address of a contiguous CUDA tensor of `n` elements (None: any number) on `device`."""
+def _flat(t, dtype, n, device, what) -> int:
+    """Address (0 for None) of a contiguous CUDA tensor of `n` elements (None: any number) on `device`."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor on cuda:{device}"
                          + ("" if n is None else f" with {n} elements"))
@@ -639,6 +652,11 @@ class Context:
         with t.use_stream(stream):
             return t.empty(shape, dtype=dtype, device=self._torch_device or self._make_torch_device())
 
+    def _call(self, name, packed, stream):
+        st = _packed[name](self.handle, packed, self._raw_stream(stream))
+        if st != AR_OK:
+            _check(self.handle, st, name)
+
     def _make_torch_device(self):
         self._torch_device = _torch.device("cuda", self.device)
         return self._torch_device
@@ -670,14 +688,14 @@ class Context:
         if info is None:
             info = self._empty((4,), i32, stream)
         table, cols, stride = _table(block_table, r, dev)
-        args = ArPagedPlanArgs(
+        args = _pack_plan(
             r, page_size, max_tokens, free_blocks.numel(), cols, stride,
             _flat(cached_lens, i32, r, dev, "cached_lens"), _flat(new_lens, i32, r, dev, "new_lens"),
             _flat(free_blocks, i32, None, dev, "free_blocks"), _flat(free_count, i32, 1, dev, "free_count"),
             table, _flat(cu_q, i32, r + 1, dev, "cu_q"), _flat(seq_lens, i32, r, dev, "seq_lens"),
             _flat(slots, t.i64, max_tokens, dev, "slots"), _flat(positions, i32, max_tokens, dev, "positions"),
             _flat(free_count_out, i32, 1, dev, "free_count_out"), _flat(info, i32, 4, dev, "info"))
-        ar_paged_plan(self.handle, args, self._raw_stream(stream))
+        self._call("ar_paged_plan", args, stream)
         return PagedPlan(block_table, cu_q, seq_lens, slots, positions, free_count_out, info)
 
     def qk_norm_rope(self, q, k, v, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -700,7 +718,7 @@ class Context:
         if code is None:
             raise ValueError("q, k and v must be bfloat16 or float16")
         hq, hk = (0 if q is None else heads), (0 if k is None else k.shape[1])
-        qp = kp = vp = qop = kop = slot = None
+        qp = kp = vp = qop = kop = slot = 0
         qt = qh = kt = kh = vt = vh = qot = qoh = kot = koh = 0
         if hq:
             shape = (n, hq, d)
@@ -724,7 +742,7 @@ class Context:
             vp, vt, vh = _heads(v, shape, dt, dev, "v")
             caches = _caches(k_cache, v_cache, hk, d, dt, dev)
             slot = _flat(slots, t.i64, n, dev, "slots")
-        half, axes, pos, pos_stride, freq = 0, 1, None, 0, None
+        half, axes, pos, pos_stride, freq = 0, 1, 0, 0, 0
         sec = _NO_SECTIONS
         if inv_freq is not None:
             half = inv_freq.numel()
@@ -743,15 +761,15 @@ class Context:
                         raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
                     if sections is None or len(sections) != axes:
                         raise ValueError("sections must name the frequencies of each position axis")
-                    sec = _Sections(*sections)
+                    sec = (*sections, *_NO_SECTIONS[axes:])
                 elif axes < 1:
                     raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
-        args = ArQkNormRopeArgs(
+        args = _pack_rope(
             n, hq, hk, d, code, qp, kp, vp, qt, qh, kt, kh, vt, vh, qop, kop, qot, qoh, kot, koh,
-            None if q_weight is None else _flat(q_weight, dt, d, dev, "q_weight"),
-            None if k_weight is None else _flat(k_weight, dt, d, dev, "k_weight"),
-            eps, gemma, 2 * half, pairs, axes, sec, dealt, pos, pos_stride, freq, *caches, slot)
-        ar_qk_norm_rope(self.handle, args, self._raw_stream(stream))
+            0 if q_weight is None else _flat(q_weight, dt, d, dev, "q_weight"),
+            0 if k_weight is None else _flat(k_weight, dt, d, dev, "k_weight"),
+            eps, gemma, 2 * half, pairs, axes, *sec, dealt, pos, pos_stride, freq, *caches, slot)
+        self._call("ar_qk_norm_rope", args, stream)
         return q_out, k_out
 
     def paged_attention(self, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: Optional[float] = None,
@@ -788,14 +806,14 @@ class Context:
         op, ot, oh = _heads(out, shape, dt, dev, "out")
         kp, vp, kb, kt, kh, vb, vt, vh, blocks, page = _caches(k_cache, v_cache, hk, d, dt, dev)
         table, cols, stride = _table(block_table, r, dev)
-        args = ArPagedAttentionArgs(
+        args = _pack_attention(
             n, r, hq, hk, d, code, qp, op, qt, qh, ot, oh,
-            None if lse is None else _flat(lse, t.f32, n * hq, dev, "lse"), kp, vp, kb, kt, kh, vb, vt, vh, blocks, page,
+            0 if lse is None else _flat(lse, t.f32, n * hq, dev, "lse"), kp, vp, kb, kt, kh, vb, vt, vh, blocks, page,
             table, cols, stride, _flat(cu_q, t.i32, r + 1, dev, "cu_q"), _flat(seq_lens, t.i32, r, dev, "seq_lens"),
             d ** -0.5 if scale is None else scale, causal, window, softcap,
-            None if slopes is None else _flat(slopes, t.f32, hq, dev, "slopes"),
-            None if prefix_lens is None else _flat(prefix_lens, t.i32, r, dev, "prefix_lens"), work, size)
-        ar_paged_attention(self.handle, args, self._raw_stream(stream))
+            0 if slopes is None else _flat(slopes, t.f32, hq, dev, "slopes"),
+            0 if prefix_lens is None else _flat(prefix_lens, t.i32, r, dev, "prefix_lens"), work, size)
+        self._call("ar_paged_attention", args, stream)
         return out, lse
 
     def _attention_workspace(self, head_dim: int, code: int) -> int:

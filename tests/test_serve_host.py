@@ -150,3 +150,20 @@ def test_argument_blocks_match_the_header(tmp_path):
     subprocess.run(["gcc", "-std=c11", "-I", include, str(src), "-o", str(tmp_path / "layout")], check=True)
     got = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True, timeout=60).stdout.split()
     assert [int(x) for x in got] == want
+
+
+def test_packed_arguments_are_the_structures():
+    """The bytes that the methods pass hold the fields where the structures do."""
+    for args, pack in ((tar.ArPagedPlanArgs, tar._pack_plan), (tar.ArQkNormRopeArgs, tar._pack_rope),
+                       (tar.ArPagedAttentionArgs, tar._pack_attention)):
+        values, n = [], 0
+        for _, kind in args._fields_:
+            count = getattr(kind, "_length_", 1)
+            values.append(tuple(range(n + 1, n + 1 + count)) if hasattr(kind, "_length_") else n + 1)
+            n += count
+        flat = [x for v in values for x in (v if isinstance(v, tuple) else (v,))]
+        blob = pack(*flat)
+        a = args.from_buffer_copy(blob + bytes(ctypes.sizeof(args) - len(blob)))
+        for (name, kind), v in zip(args._fields_, values):
+            got = getattr(a, name)
+            assert (tuple(got) if isinstance(v, tuple) else got) == v, name
