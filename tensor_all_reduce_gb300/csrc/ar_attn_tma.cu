@@ -161,6 +161,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -410,30 +415,43 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// A row's products over the tile's 128 keys to scores, masked: in log2 units where they are
-// bent, else as they are (the caller scales).
+// A row's products with the 64 keys from key0 on to scores: in log2 units where they are bent, else
+// as they are (the caller scales); masked where `edge` says that some row of the warp does not see all.
 template <int EXT>
-__device__ __forceinline__ void shape_scores(const AttnParams& p, const Item& it, const RowView& v, int key0, float (&s)[kKeys]) {
+__device__ __forceinline__ void shape_scores(const AttnParams& p, int prefix, const RowView& v, int key0, bool edge, float (&s)[64]) {
   if constexpr (EXT & kCap) {
     // c tanh(x) = c - 2 c / (1 + e^2x): one exponential and one reciprocal an element, absolute
     // error 2^-22 c; an exponential that overflows gives c
     const float twice = p.scale_log2 * 2.8853900817779268f, c = p.cap_log2;
 #pragma unroll
-    for (int j = 0; j < kKeys; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
+    for (int j = 0; j < 64; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
   }
   if constexpr (EXT & kBias) {
     const float scale = EXT & kCap ? 1.0f : p.scale_log2;
     const float far = (float)(v.pos - key0);
 #pragma unroll
-    for (int j = 0; j < kKeys; ++j) s[j] = fmaf(-v.slope, fabsf(far - (float)j), s[j] * scale);
+    for (int j = 0; j < 64; ++j) s[j] = fmaf(-v.slope, fabsf(far - (float)j), s[j] * scale);
   }
-  // the whole warp sees the whole tile: nothing to mask
-  const bool all = (key0 + kKeys <= v.see_hi && key0 >= v.see_lo) || key0 + kKeys <= it.q.prefix;
-  if (__all_sync(0xffffffffu, all)) return;
-  const int hi = v.see_hi - key0, lo = v.see_lo - key0, pre = it.q.prefix - key0;
+  if (!edge) return;
+  const int hi = v.see_hi - key0, lo = v.see_lo - key0, pre = prefix - key0;
 #pragma unroll
-  for (int j = 0; j < kKeys; ++j)
+  for (int j = 0; j < 64; ++j)
     if (!(j < pre || (j < hi && j >= lo))) s[j] = -INFINITY;
+}
+
+// 64 columns of scores.
+__device__ __forceinline__ void load_scores(uint32_t addr, float (&s)[64]) {
+  uint32_t a[32], b[32];
+  tmem_ld32(a, addr);
+  tmem_ld32(b, addr + 32);
+  tmem_wait_ld();
+  settle(a);
+  settle(b);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    s[j] = __uint_as_float(a[j]);
+    s[32 + j] = __uint_as_float(b[j]);
+  }
 }
 
 template <int DP>
@@ -471,15 +489,17 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     __syncwarp();
     return found;
   };
-  // queries, 16 bytes a thread, neighbours along a row; rows and columns beyond are zero
+  // Queries, 16 bytes a thread, neighbours along a row; columns beyond the head are zero.  Rows
+  // beyond the item's keep what was there: they meet no other row, and nothing of them is stored.
   auto load_queries = [&](const Item& it) {
     uint8_t* dst = queries + h * S::kTileBytes;
+    const int base = it.qt * S::kRows + h * 128, rows = min(it.rows - base, 128);
 #pragma unroll 4
-    for (int x = tid; x < 128 * (DP / 8); x += 128) {
-      const int r = x / (DP / 8), c = x % (DP / 8), row = it.qt * S::kRows + h * 128 + r;
+    for (int x = tid; x < rows * (DP / 8); x += 128) {
+      const int r = x / (DP / 8), c = x % (DP / 8);
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < it.rows && c * 8 < p.head_dim) {
-        const int t = row / p.group, e = row - t * (int)p.group.d;
+      if (c * 8 < p.head_dim) {
+        const int t = (base + r) / p.group, e = base + r - t * (int)p.group.d;
         v = ld_keep(static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * (int)p.group.d + e) * p.q_hs + c * 8);
       }
       *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
@@ -503,7 +523,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       view.see_hi = 0x7fffffff;
     }
     float m = -INFINITY;
-    uint64_t sum = two(0.0f, 0.0f);
+    uint64_t sum[4] = {0, 0, 0, 0};  // of the weights, eight floats: one chain of additions would take longer than the exponentials
     for (int i = 0; i < nt; ++i) {
       const uint32_t c = g + i, buf = one ? (c & 1) : h, x = one ? 2 + buf : h, phase = one ? (c >> 1) & 1 : (d + i) & 1;
       const uint32_t ts = lanes + buf * 128;
@@ -513,24 +533,44 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
         arrive(&b.p2[x]);
         continue;
       }
-      uint32_t raw[kKeys / 32][32];
+      // Twice over the scores: for the maximum (bent and masked scores go back to tensor memory) and
+      // for the weights, 64 at a time.  Kept in registers from one to the other they spilled
+      // (decode of 64 requests 220 us so, 217 us read twice; prefix with bias 60 and 59 us).
+      const int key0 = it.range.tile(it.begin + i) * kKeys, prefix = it.q.prefix;
+      const bool edge = !__all_sync(0xffffffffu, (key0 + kKeys <= view.see_hi && key0 >= view.see_lo) || key0 + kKeys <= prefix);
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (!EXT && !edge) {
+        uint32_t s[4][32];
 #pragma unroll
-      for (int k = 0; k < kKeys / 32; ++k) tmem_ld32(raw[k], ts + k * 32);
-      tmem_wait_ld();
-      float s[kKeys];
+        for (int k = 0; k < 4; ++k) tmem_ld32(s[k], ts + k * 32);
+        tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < kKeys / 32; ++k) {
-        settle(raw[k]);
+        for (int k = 0; k < 4; ++k) {
+          settle(s[k]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[k * 32 + j] = __uint_as_float(raw[k][j]);
+          for (int j = 0; j < 32; j += 2) top[k] = max3(top[k], __uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1]));
+        }
+      } else {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          float s[64];
+          load_scores(ts + part * 64, s);
+          shape_scores<EXT>(p, prefix, view, key0 + part * 64, edge, s);
+          uint32_t back[32];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) back[j] = __float_as_uint(s[k * 32 + j]);
+            tmem_st32(ts + part * 64 + k * 32, back);
+          }
+#pragma unroll
+          for (int j = 0; j < 64; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[k] = max3(top[k], s[j + k], s[j + 4 + k]);
+        }
+        tmem_wait_st();
       }
-      shape_scores<EXT>(p, it, view, it.range.tile(it.begin + i) * kKeys, s);
-      float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int j = 4; j < kKeys; j += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = j + 4 + k < kKeys ? fmaxf(fmaxf(top[k], s[j + k]), s[j + 4 + k]) : fmaxf(top[k], s[j + k]);
-      const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+      const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
       const bool grown = high > m + 8.0f;  // m = -inf: any finite score
       if (__any_sync(0xffffffffu, grown)) {
         const float shrink = grown ? ex2(m - high) : 1.0f;  // m = -inf: 0
@@ -540,9 +580,12 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
           // with scores that run ahead a barrier says so.  (Scores of tile c complete after the sum
           // of tile c - 2, so this barrier is at most one phase behind.)
           if (one && !wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) break;
-          float lo, hi;
-          untwo(sum, lo, hi);
-          sum = two(lo * shrink, hi * shrink);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            untwo(sum[k], lo, hi);
+            sum[k] = two(lo * shrink, hi * shrink);
+          }
 #pragma unroll
           for (int k = 0; k < DP / 32; ++k) {
             uint32_t o[32];
@@ -559,15 +602,16 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       const uint64_t scale2 = two(scale, scale), base2 = two(-base, -base);
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
+        float s[64];
+        load_scores(ts + part * 64, s);
         uint32_t w[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const int e = part * 64 + j * 2;
           float a, z;
-          untwo(fma2(two(s[e], s[e + 1]), scale2, base2), a, z);
+          untwo(fma2(two(s[2 * j], s[2 * j + 1]), scale2, base2), a, z);
           a = ex2(a);
           z = ex2(z);
-          sum = add2(sum, two(a, z));  // of the unrounded weights
+          sum[j & 3] = add2(sum[j & 3], two(a, z));  // of the unrounded weights
           w[j] = pack2<DT>(a, z);      // the second product's operand is 16-bit: half a step, relative, a weight
         }
         tmem_st32(ts + part * 32, w);
@@ -590,7 +634,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     const int slot = it.first ? 1 : 0;
     if (busy) {
       float lo, hi;
-      untwo(sum, lo, hi);
+      untwo(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
       const float l = lo + hi;
       const bool mine = row < it.rows;
       const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
