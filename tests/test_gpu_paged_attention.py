@@ -200,6 +200,24 @@ def test_mixed_batches(ctx, form, seed):
 
 def test_many_requests(ctx, form):
     check(ctx, make([1] * 700, [1 + i % 37 for i in range(700)], 2, 1, 64, page=8, seed=8))
+    new = [(1, 0, 2, 0, 0, 30)[i % 6] if i % 50 else 70 for i in range(3000)]  # several rounds of requests a CTA's threads
+    check(ctx, make(new, [n + i % 41 for i, n in enumerate(new)], 2, 1, 64, page=8, seed=9))
+
+
+def test_rows_that_begin_behind_the_first(ctx, form):
+    """cu_q need not start at 0: the rows in front belong to nobody."""
+    x = make([3, 0, 50], [40, 5, 300], 4, 2, 64, seed=18)
+    x["q"] = torch.cat([x["q"][:7], x["q"]])
+    x["cu"] = [c + 7 for c in x["cu"]]
+    check(ctx, x)
+
+
+def test_requests_that_share_blocks(ctx, form):
+    """A common prefix kept once: two tables name the same blocks, also twice in one table."""
+    x = make([2, 5], [200, 90], 4, 2, 64, seed=19, garbage=0.0)
+    x["table"][1][:4] = x["table"][0][:4]
+    x["table"][0][7] = x["table"][0][6]
+    check(ctx, x)
 
 
 def test_long_cache_is_split(ctx, form):

@@ -263,6 +263,47 @@ def test_streams_and_graph(ctx):
     assert torch.equal(qo, fresh) and not torch.equal(qo, want)
 
 
+def test_a_wait_that_runs_out_ends_the_call(ctx):
+    """The first copy of each CTA is held back: the call ends with code 1, and the next one is right."""
+    import tensor_all_reduce_gb300 as tar
+    x = make(3000, 8, 2, 128, "bf16", 128)
+    g = on_gpu(x)
+    ctx.set_option(tar.AR_OPT_TEST_STALL, 1)
+    ctx.set_option(tar.AR_OPT_WAIT_CYCLES, 2000000)
+    try:
+        ctx.qk_norm_rope(g["q"], g["k"], None, g["pos"][0], g["freq"], q_weight=g["wq"])
+        assert ctx.last_variant == "qk_norm_rope_vec" and ctx.device_status() == 1
+    finally:
+        ctx.set_option(tar.AR_OPT_TEST_STALL, 0)
+        ctx.set_option(tar.AR_OPT_WAIT_CYCLES, 0)
+    check(ctx, x)
+
+
+def test_more_heads_than_a_stage_holds(ctx):
+    """A token's heads are split over units: 300 q heads of 256, and 100 of 80 with few tokens."""
+    check(ctx, make(5, 300, 3, 256, "bf16", 256))
+    check(ctx, make(700, 90, 40, 128, "bf16", 64))
+    check(ctx, make(2, 100, 7, 80, "fp16", 80), pairs=True)
+
+
+def test_heads_apart_in_memory(ctx):
+    """q of shape [tokens, heads, dim] with a gap between heads, and transposed: each head is fetched by itself."""
+    x = make(60, 6, 2, 128, "bf16", 128)
+    g = on_gpu(x)
+    want = ctx.qk_norm_rope(g["q"], g["k"], None, g["pos"][0], g["freq"], q_weight=g["wq"], k_weight=g["wk"])
+    gap = torch.zeros(60, 6, 160, dtype=torch.bfloat16, device="cuda")[..., :128]
+    gap.copy_(g["q"])
+    turned = g["k"].transpose(0, 1).contiguous().transpose(0, 1)
+    got = ctx.qk_norm_rope(gap, g["k"], None, g["pos"][0], g["freq"], q_weight=g["wq"], k_weight=g["wk"])
+    assert ctx.last_variant == "qk_norm_rope_vec"
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    import tensor_all_reduce_gb300 as tar
+    with pytest.raises(tar.ArError):  # tokens closer than a head: not rows that stand apart
+        ctx.qk_norm_rope(None, turned[:, :, :].as_strided((60, 2, 128), (64, 128 * 60, 1)), None, g["pos"][0], g["freq"], k_weight=g["wk"])
+    again = ctx.qk_norm_rope(None, turned, None, g["pos"][0], g["freq"], k_weight=g["wk"])[1]
+    assert torch.equal(again, want[1])
+
+
 def test_binding_refuses(ctx):
     x = on_gpu(make(8, 4, 2, 64, "bf16", 64, axes=3))
     with pytest.raises(ValueError):
