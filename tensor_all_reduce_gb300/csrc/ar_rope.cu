@@ -13,6 +13,7 @@
 #include "ar_fastdiv.cuh"
 #include "ar_serve.h"
 #include "ar_staged.cuh"
+#include "ar_two.cuh"
 
 namespace ar {
 namespace {
@@ -129,16 +130,19 @@ enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 // tokens' places in the cache, and both compute the units' angles, once for all heads (a sincos
 // a head would cost more than the memory traffic does; one warp alone was the bound where rows
 // are short).  Eight warps work: n = head_dim / 16 lanes hold a head (rounded up), two chunks of 8
-// elements each, and a warp as many heads as fit (six of 80 elements; LANES = 4, 8 or 16 for
-// the powers of two, where a head's sum is a butterfly, 0 for others).  The chunks of a lane are
-// chosen so that it has both elements of each pair: adjacent pairs anyway, halves of a multiple
-// of 8 as chunk c and the one half a rotation on.  Other halves go through shared memory
-// (kHalvesAny; rows of 8 skewed by one float so that lanes fall into different banks).  With one
-// chunk a lane and shuffles between partners it took twice the instructions an element, and
-// they, not the memory, were the bound.
+// elements each, and a warp as many heads as fit (six of 80 elements; LANES: n of the usual
+// sizes, 0 for others).  The chunks of a lane are chosen so that it has both elements of each
+// pair: adjacent pairs anyway, halves of a multiple of 8 as chunk c and the one half a rotation
+// on.  Other halves go through shared memory (kHalvesAny; rows of 8 skewed by one float so that
+// lanes fall into different banks).
 //
-// The ring is what reaches the memory's bandwidth: with rows loaded straight into registers, four
-// a lane in flight, loads alone ran at 3 TB/s and the arithmetic came on top of them.
+// The bound is memory, with the arithmetic not far behind.  Measured on GB300 (CUDA graph, cold
+// inputs): 2800 tokens x 64 heads of 128, half rotated, 92 MB: 24.0 us, 3.8 TB/s with the launch;
+// the same without norm and rotation 18.3 us, without the stores too 13.0 us.  16384 tokens x 48
+// heads of 80, adjacent pairs, three axes, 252 MB: 61.9 us, 4.1 TB/s.  What it took to get there,
+// 2800 and 16384 tokens: rows loaded straight into registers 32 and 89 us; staged 25 and 78 us; two
+// chunks a lane instead of shuffles between partners 23 and 70 us; two floats an instruction and
+// sums unrolled for n = 5 and 6 24 and 62 us.
 template <int DT, int MODE, int LANES>
 struct RopeVec {
   struct Shared {
@@ -255,28 +259,44 @@ struct RopeVec {
         if (!(p.stall && i == 0)) mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, p.wait_cycles);
   }
 
-  // Eight floats of chunk c out of two planes.
-  __device__ __forceinline__ static void planes(const float* p, int plane, int c, float (&f)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p + c * 4), b = *reinterpret_cast<const float4*>(p + plane + c * 4);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  // Eight floats of chunk c out of two planes, in pairs.
+  __device__ __forceinline__ static void planes(const float* p, int plane, int c, uint64_t (&f)[4]) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p + c * 4), b = *reinterpret_cast<const ulonglong2*>(p + plane + c * 4);
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+  }
+  __device__ __forceinline__ static void unpack(const uint4& v, uint64_t (&f)[4]) {
+    float a[8];
+    unpack8<DT>(v, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = two(a[2 * i], a[2 * i + 1]);
+  }
+  __device__ __forceinline__ static uint4 pack(const uint64_t (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      untwo(f[i], a, b);
+      w[i] = pack2<DT>(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 
   __device__ __forceinline__ void work() {
     const int chunks = p.head_dim / 8, n = LANES ? LANES : (chunks + 1) / 2;  // lanes of a head
     const int per_warp = 32 / n, wl = threadIdx.x & 31, in_warp = wl / n;
     const int lane = wl - in_warp * n, first = in_warp * n;  // place in the head; its first lane
-    const bool there = LANES ? true : in_warp < per_warp;
+    const bool there = 32 % (LANES ? LANES : 32) == 0 && LANES ? true : in_warp < per_warp;
     const int warp = threadIdx.x >> 5;
-    // this lane's chunks; `two`: it has the second
+    // this lane's chunks; `two_chunks`: it has the second
     const int hb = p.half / 8;
     const bool turns = MODE != kHalves8 || lane < hb;
     const int c0 = MODE != kHalves8 || turns ? lane : 2 * lane;
     const int c1_raw = MODE != kHalves8 ? lane + n : (turns ? lane + hb : c0 + 1);
-    const bool two = c1_raw < chunks;
-    const int c1 = two ? c1_raw : c0;
+    const bool two_chunks = c1_raw < chunks;
+    const int c1 = two_chunks ? c1_raw : c0;
     // Sum over a head's lanes, to all of them.
     auto head_sum = [&](float s) {
-      if constexpr (LANES != 0) {
+      if constexpr (LANES != 0 && (LANES & (LANES - 1)) == 0) {
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;
@@ -304,7 +324,7 @@ struct RopeVec {
     const int per_round = (kRopeWorkers / 32) * per_warp;
     auto store2 = [&](uint16_t* dst, const uint4& a, const uint4& b) {
       st_v4(dst + c0 * 8, a);
-      if (two) st_v4(dst + c1 * 8, b);
+      if (two_chunks) st_v4(dst + c1 * 8, b);
     };
     uint32_t k = 0;
     for (int64_t u = blockIdx.x; u < plan.units; u += gridDim.x, ++k) {
@@ -323,86 +343,98 @@ struct RopeVec {
         const int t = plan.step > 1 ? i0 / plan.heads_div : 0;
         const int h = x.lo + i0 - t * plan.per;
         const uint8_t* row = rows + i0 * head;
-        const uint4 raw0 = lds_v4(row + c0 * 16), raw1 = two ? lds_v4(row + c1 * 16) : make_uint4(0, 0, 0, 0);
+        const uint4 raw0 = lds_v4(row + c0 * 16), raw1 = two_chunks ? lds_v4(row + c1 * 16) : make_uint4(0, 0, 0, 0);
         const bool is_q = h < p.q.heads, is_v = h >= v0;
         uint16_t* v_dst = static_cast<uint16_t*>(p.v_cache) + sh.v_at[s][t] + (h - v0) * p.vc_hs;
         if (__all_sync(0xffffffffu, is_v)) {  // v is copied
           if (mine && sh.v_at[s][t] >= 0) store2(v_dst, raw0, raw1);
           continue;
         }
-        float a[8], b[8], y[8], z[8];
-        unpack8<DT>(raw0, a);
-        unpack8<DT>(raw1, b);
+        uint64_t a[4], b[4], y[4], z[4];
+        unpack(raw0, a);
+        unpack(raw1, b);
         if (p.q.weight || p.k.weight) {
-          float sa = a[0] * a[0], sb = b[0] * b[0];
+          uint64_t ss = mul2(a[0], a[0]), sb = mul2(b[0], b[0]);
 #pragma unroll
-          for (int i = 1; i < 8; ++i) {
-            sa = fmaf(a[i], a[i], sa);
-            sb = fmaf(b[i], b[i], sb);
+          for (int i = 1; i < 4; ++i) {
+            ss = fma2(a[i], a[i], ss);
+            sb = fma2(b[i], b[i], sb);
           }
-          const float rs = rsqrtf(head_sum(sa + sb) * p.inv_dim + p.eps);
+          float lo, hi;
+          untwo(add2(ss, sb), lo, hi);
+          const float rs = rsqrtf(head_sum(lo + hi) * p.inv_dim + p.eps);
           if (is_q ? p.q.weight != nullptr : p.k.weight != nullptr) {
             const float* w = sh.weight[is_q ? 0 : 1];
-            float wa[8], wb[8];
+            uint64_t wa[4], wb[4];
             planes(w, p.head_dim / 2, c0, wa);
             planes(w, p.head_dim / 2, c1, wb);
+            const uint64_t r2 = two(rs, rs);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              a[i] *= rs * wa[i];
-              b[i] *= rs * wb[i];
+            for (int i = 0; i < 4; ++i) {
+              a[i] = mul2(a[i], mul2(r2, wa[i]));
+              b[i] = mul2(b[i], mul2(r2, wb[i]));
             }
           }
         }
         // an element that does not turn keeps its value, infinities included
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           y[i] = a[i];
           z[i] = b[i];
         }
         const float* c = angles + t * plan.pitch;
         if constexpr (MODE == kPairs) {
-          auto turn = [&](int chunk, const float (&from)[8], float (&to)[8]) {
+          auto turn = [&](int chunk, const uint64_t (&from)[4], uint64_t (&to)[4]) {
             if (chunk * 4 >= p.half) return;
             const float4 c4 = *reinterpret_cast<const float4*>(c + chunk * 4), s4 = *reinterpret_cast<const float4*>(c + size + chunk * 4);
             const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, sc[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (chunk * 4 + i < p.half) {
-                to[2 * i] = from[2 * i] * cc[i] - from[2 * i + 1] * sc[i];
-                to[2 * i + 1] = from[2 * i + 1] * cc[i] + from[2 * i] * sc[i];
+                float u, v;
+                untwo(from[i], u, v);
+                to[i] = two(u * cc[i] - v * sc[i], v * cc[i] + u * sc[i]);
               }
           };
           turn(c0, a, y);
           turn(c1, b, z);
         } else if constexpr (MODE == kHalves8) {
           if (turns) {
-            float cc[8], sc[8];
+            uint64_t cc[4], sc[4];
             planes(c, p.half / 2, lane, cc);
             planes(c + size, p.half / 2, lane, sc);
+            const uint64_t minus = two(-1.0f, -1.0f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              y[i] = a[i] * cc[i] - b[i] * sc[i];
-              z[i] = b[i] * cc[i] + a[i] * sc[i];
+            for (int i = 0; i < 4; ++i) {
+              y[i] = fma2(b[i], mul2(sc[i], minus), mul2(a[i], cc[i]));
+              z[i] = fma2(a[i], sc[i], mul2(b[i], cc[i]));
             }
           }
         } else {
           float* skew = sh.skew + (threadIdx.x - lane) * 18;  // element e at e + e / 8
+          auto write = [&](int chunk, const uint64_t (&from)[4]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (there) skew[c0 * 9 + i] = a[i];  // (lanes behind the warp's last head have no place)
-            if (there && two) skew[c1 * 9 + i] = b[i];
-          }
+            for (int i = 0; i < 4; ++i) untwo(from[i], skew[chunk * 9 + 2 * i], skew[chunk * 9 + 2 * i + 1]);
+          };
+          if (there) write(c0, a);  // (lanes behind the warp's last head have no place)
+          if (there && two_chunks) write(c1, b);
           __syncwarp();
-          auto turn = [&](int chunk, const float (&from)[8], float (&to)[8]) {
+          auto turn = [&](int chunk, const uint64_t (&from)[4], uint64_t (&to)[4]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int e = chunk * 8 + i;
-              if (there && e < 2 * p.half) {
-                const bool lo = e < p.half;
-                const int q = lo ? e + p.half : e - p.half, g = lo ? e : q;
-                const float other = skew[q + (q >> 3)] * c[size + g];
-                to[i] = from[i] * c[g] + (lo ? -other : other);
+            for (int i = 0; i < 4; ++i) {
+              float v[2];
+              untwo(from[i], v[0], v[1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int e = chunk * 8 + 2 * i + j;
+                if (there && e < 2 * p.half) {
+                  const bool low = e < p.half;
+                  const int q = low ? e + p.half : e - p.half, g = low ? e : q;
+                  const float other = skew[q + (q >> 3)] * c[size + g];
+                  v[j] = v[j] * c[g] + (low ? -other : other);
+                }
               }
+              to[i] = two(v[0], v[1]);
             }
           };
           turn(c0, a, y);
@@ -410,7 +442,7 @@ struct RopeVec {
           __syncwarp();
         }
         if (!mine) continue;
-        const uint4 out0 = pack8<DT>(y), out1 = pack8<DT>(z);
+        const uint4 out0 = pack(y), out1 = pack(z);
         if (is_q) {
           store2(q_out + t * p.q.out_ts + h * p.q.out_hs, out0, out1);
         } else if (is_v) {
@@ -465,6 +497,8 @@ template <int DT, int MODE>
 const void* vec_of(int dim) {
   switch (dim) {
     case 64: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 4>);
+    case 80: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 5>);
+    case 96: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 6>);
     case 128: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 8>);
     case 256: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 16>);
     default: return reinterpret_cast<const void*>(&rope_vec<DT, MODE, 0>);

@@ -464,7 +464,7 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
   keep(cudaFuncSetAttribute(plan_kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, AR_MAX_REQUESTS * 8));
   for (int b = 0; b < 2; ++b) {
     keep(cudaFuncGetAttributes(&fa, rope_scalar_kernel(b)));
-    for (int d : {64, 128, 256, 80})
+    for (int d : {64, 80, 96, 128, 256, 72})
       for (int mode = 0; mode < 3; ++mode)
         keep(cudaFuncSetAttribute(rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rope_smem_most()));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
