@@ -436,6 +436,7 @@ class _Torch:
         self.codes = {torch.bfloat16: AR_DTYPE_BF16, torch.float16: AR_DTYPE_F16}
         self.empty, self.device, self.use_stream = torch.empty, torch.device, torch.cuda.stream
         self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.capturing = torch.cuda.is_current_stream_capturing
 
 
 _torch: Optional[_Torch] = None
@@ -501,11 +502,13 @@ class Context:
         self.handle = ar_init(device)
         self._workspace_bytes = {}
         self._torch_device = None
+        self._workspaces = {}
 
     def close(self):
         if self.handle:
             ar_destroy(self.handle)
             self.handle = None
+            self._workspaces = {}
 
     def __enter__(self):
         return self
@@ -778,9 +781,9 @@ class Context:
         """Attention of the requests' new tokens q [tokens, q_heads, head_dim] over the paged
         cache [blocks, page, kv_heads, head_dim] (see ar_paged_attention); scale defaults to
         head_dim ** -0.5.  Returns (out, lse); lse [tokens, q_heads] fp32 is None unless given or
-        wanted.  Rows of no request are not written.  `workspace` (uint8, from
-        paged_attention_workspace) is allocated where not given; calls that may run at the
-        same time need one each."""
+        wanted.  Rows of no request are not written.  `workspace` is a uint8 tensor from
+        paged_attention_workspace; calls that may run at the same time need one each.  Where it is not
+        given the context keeps one for each stream, and a captured call allocates its own."""
         t = _torch or _bind_torch()
         dev = self.device
         shape = q.shape
@@ -798,7 +801,7 @@ class Context:
             lse = self._empty((n, hq), t.f32, stream)
         if workspace is None:
             size = self._attention_workspace(d, code)
-            workspace = self._empty(size, t.u8, stream)
+            workspace = self._own_workspace(size, stream)
             work = workspace.data_ptr()
         else:
             work, size = _flat(workspace, t.u8, None, dev, "workspace"), workspace.numel()
@@ -815,6 +818,20 @@ class Context:
             0 if prefix_lens is None else _flat(prefix_lens, t.i32, r, dev, "prefix_lens"), work, size)
         self._call("ar_paged_attention", args, stream)
         return out, lse
+
+    def _own_workspace(self, size: int, stream):
+        """`size` bytes for one call on `stream`: kept for the calls behind it on that stream, which
+        cannot overlap it; a captured call gets its own, which belongs to its graph."""
+        if stream is not None:
+            with _torch.use_stream(stream):
+                return self._own_workspace(size, None)
+        if _torch.capturing():
+            return self._empty(size, _torch.u8, None)
+        key = _torch.raw_stream(self.device)
+        kept = self._workspaces.get(key)
+        if kept is None or kept.numel() < size:
+            kept = self._workspaces[key] = self._empty(size, _torch.u8, None)
+        return kept
 
     def _attention_workspace(self, head_dim: int, code: int) -> int:
         n = self._workspace_bytes.get((head_dim, code))

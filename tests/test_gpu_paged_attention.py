@@ -318,6 +318,28 @@ def test_captured_call_follows_the_lengths(ctx, form):
             assert ((out.cpu().double() - wo).abs() <= eo).all()
 
 
+def test_own_workspaces(ctx):
+    """Without a workspace: calls on two streams at once, and a captured call replayed beside eager ones, each
+    have their own."""
+    xs = [make([1, 1], [3000 + 500 * i, 700], 6, 2, 128, seed=30 + i, garbage=0.0) for i in range(3)]
+    args = [(x["q"].cuda(), x["kc"].cuda(), x["vc"].cuda(), i32(x["table"]), i32(x["cu"]), i32(x["lens"])) for x in xs]
+    want = [ctx.paged_attention(*a)[0].clone() for a in args]
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    out = torch.zeros_like(args[2][0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ctx.paged_attention(*args[2], out=out)
+    for _ in range(20):
+        a = ctx.paged_attention(*args[0], stream=s)[0]
+        with torch.cuda.stream(t):
+            b = ctx.paged_attention(*args[1])[0]
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(out, want[2])
+        out.zero_()
+
+
 def test_offsets_beyond_32_bits(ctx, form):
     """A cache of more than 2^32 elements: the last blocks are read at their own place."""
     page, hk, d = 64, 8, 128
