@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
       if (row >= it.rows) continue;
       if (whole) {
         const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
-        const float inv = l[i] > 0.0f ? 1.0f / l[i] : 0.0f;
+        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
         uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
 #pragma unroll
         for (int j = 0; j < DP / 8; ++j) {
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
           }
         }
         if (p.lse && (lane & 3) == 0)
-          p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l[i] > 0.0f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+          p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
       } else {
         const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + local;
 #pragma unroll
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine(const __grid_consta
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) join(a, sh[w][lane].m, sh[w][lane].l, sh[w][lane].o);
       }
-      const float inv = a.l > 0.0f ? 1.0f / a.l : 0.0f;
+      const float inv = a.l == 0.0f ? 0.0f : 1.0f / a.l;
       const float f[4] = {a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv};
       if (p.vec) {
         if (e < p.head_dim) st_v2(dst + e, make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])));
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine(const __grid_consta
           if (e + j < p.head_dim) st_u16(dst + e + j, round1<DT>(f[j]));
       }
       if (p.lse && e == 0)
-        p.lse[(int64_t)(q0 + t) * p.q_heads + head] = a.l > 0.0f ? (a.m + log2f(a.l)) * 0.69314718055994531f : -INFINITY;
+        p.lse[(int64_t)(q0 + t) * p.q_heads + head] = a.l == 0.0f ? -INFINITY : (a.m + log2f(a.l)) * 0.69314718055994531f;
     }
   }
 }

@@ -12,8 +12,11 @@
 // the weighted sums, 128 a half or all for one half.  The weights, 16-bit, take the first 64
 // columns of their scores and are the second product's A operand from there, so they never touch
 // shared memory.  Matrix instructions of one CTA run in the order in which they are issued.  With
-// two halves, one half's softmax runs while the tensor core works on the other's products;
-// with one (single tokens, wide heads) the two buffers hold its present and next tile.
+// two halves, one half's softmax runs while the tensor core works on the other's products; with
+// one (few rows, wide heads) the two buffers hold its present and next tile, and the warpgroups
+// take tiles by turns, each with a maximum and a sum of its own, joined at the item's end (17
+// requests, one of them 700 tokens, window and cap: 56 us with one warpgroup, 53 us with both;
+// heads of more than 128 have no columns for a second sum).
 //
 // The running maximum that the weights refer to moves only when a row's maximum has grown by more
 // than 2^8 (in weight), since the result does not depend on the reference: then the sum in
@@ -39,6 +42,7 @@ static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168, "the split uses what the
 template <int DP>
 struct Shape {
   static constexpr int kRows = DP == 256 ? 128 : 256;   // rows of an item
+  static constexpr bool kTurns = DP <= 128;             // the warpgroups take an item of one half by turns, tile by tile
   static constexpr int kUnits = DP == 256 ? 2 : 1;      // ring slots that a tile of keys or values takes
   static constexpr int kBlocks = DP / 64 / kUnits;      // 64-element (128-byte) column blocks of a unit
   static constexpr int kBlockBytes = kKeys * 128;       // one column block of 128 rows
@@ -57,6 +61,7 @@ struct Bars {
   uint64_t s[4];                 // scores ready
   uint64_t p[4], p2[4];          // weights of the first and second 64 keys stored
   uint64_t o[4];                 // sum complete: of half 0, 1 (an item), of one half (a tile, by turns)
+  uint64_t join[2];              // sums of an item taken by turns: both there, both read
   uint64_t drain;
   uint32_t issued[10];           // rounds whose copies were issued, a slot
   uint32_t tmem;
@@ -177,8 +182,10 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Bars& b
 // Every role walks the CTA's items for itself and counts barrier phases the same way:
 //   n: units loaded into the ring; items: items so far (phase of q[0], o[...] of paired halves);
 //   pairs: items of two halves; d: tiles of such items; g: tiles of items of one half.
-// An item of one half has two score buffers (S0, S1 by turns), so that the next tile's scores are
-// computed while the softmax works on the present one; one of two halves has one buffer each.
+// An item of one half has two score buffers (by turns), so that the next tile's scores are computed
+// while the softmax works on the present one; one of two halves has one buffer each.  For heads of
+// up to 128 the turns are the warpgroups' too: each keeps a maximum and a sum of its own over every
+// other tile, and the two are joined at the item's end.
 
 template <int DP>
 __device__ __forceinline__ bool single_half(const Item& it) {
@@ -324,15 +331,15 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
           if (one) mma_commit(&b.s[2 + x]);
         }
         if (i < 0) continue;
-        const uint32_t x = (g + i) & 1, phase = ((g + i) >> 1) & 1;
+        const uint32_t x = (g + i) & 1, phase = ((g + i) >> 1) & 1, sum_at = 256 + (S::kTurns ? x * 128 : 0);
         for (int u = 0; u < S::kUnits; ++u, ++n) {
           if (!wait_unit(n)) break;
           clear_tail(i, n);
           if (u == 0 && !wait(&b.p[2 + x], phase)) break;
-          if (one) weighted(x, n, u, 0, 256, i > 0);
+          if (one) weighted(x, n, u, 0, sum_at, S::kTurns ? i > 1 : i > 0);
           if (u == 0 && !wait(&b.p2[2 + x], phase)) break;
           if (one) {
-            weighted(x, n, u, 1, 256, true);
+            weighted(x, n, u, 1, sum_at, true);
             mma_commit(&b.empty[n % S::kSlots]);
           }
         }
@@ -454,7 +461,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   auto& walk = state.walk;
   Item &it = state.it, &later = state.later;
   walk.start(span);
-  uint32_t pairs = 0, d = 0, g = 0;
+  uint32_t pairs = 0, d = 0, g = 0, joined = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
@@ -466,15 +473,15 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  auto next_item = [&](Item& to) {  // the next one with rows in this half
-    bool found = false;
-    while (!found && walk.next(p, to)) found = h == 0 || !single_half<DP>(to);
+  auto next_item = [&](Item& to) {  // the next one that this warpgroup has a part in
+    const bool found = (S::kTurns || h == 0) && walk.next(p, to);
     __syncwarp();
     return found;
   };
   // Queries, 16 bytes a thread, neighbours along a row; columns beyond the head are zero.  Rows
   // beyond the item's keep what was there: they meet no other row, and nothing of them is stored.
   auto load_queries = [&](const Item& it) {
+    if (h == 1 && single_half<DP>(it)) return;
     uint8_t* dst = queries + h * S::kTileBytes;
     const int base = it.qt * S::kRows + h * 128, rows = min(it.rows - base, 128);
 #pragma unroll 4
@@ -497,8 +504,9 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   while (have) {
     const int nt = it.end - it.begin;
     const bool one = single_half<DP>(it);
-    const uint32_t to = lanes + 256 + (one ? 0 : h * 128);
-    const int row = it.qt * S::kRows + h * 128 + tid;
+    const bool turns = S::kTurns && one;
+    const uint32_t to = lanes + 256 + (one && !S::kTurns ? 0 : h * 128);
+    const int half_row = (one ? 0 : h * 128) + tid, row = it.qt * S::kRows + half_row;
     const bool busy = row - lane < it.rows;  // the warp has a row
     RowView view = row_view(p, it, row);
     if (row >= it.rows) {  // no row: sees all, so that the warp need not mask for it; nothing of it is stored
@@ -507,7 +515,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     }
     float m = -INFINITY;
     uint64_t sum[4] = {0, 0, 0, 0};  // of the weights, eight floats: one chain of additions would take longer than the exponentials
-    for (int i = 0; i < nt; ++i) {
+    const int first = turns ? (g ^ h) & 1 : 0, step = turns ? 2 : 1;
+    for (int i = first; i < nt; i += step) {
       const uint32_t c = g + i, buf = one ? (c & 1) : h, x = one ? 2 + buf : h, phase = one ? (c >> 1) & 1 : (d + i) & 1;
       const uint32_t ts = lanes + buf * 128;
       if (!wait(&b.s[x], phase)) break;
@@ -558,11 +567,11 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       if (__any_sync(0xffffffffu, grown)) {
         const float shrink = grown ? ex2(m - high) : 1.0f;  // m = -inf: 0
         if (grown) m = high;
-        if (i > 0) {
-          // the sum holds the tiles so far: with two halves that is so once the scores are there,
-          // with scores that run ahead a barrier says so.  (Scores of tile c complete after the sum
-          // of tile c - 2, so this barrier is at most one phase behind.)
-          if (one && !wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) break;
+        if (i > first) {
+          // the sum holds this warpgroup's tiles so far: that is so once the scores are there, but for
+          // one warpgroup with scores that run ahead, where a barrier says so.  (Scores of tile c
+          // complete after the sum of tile c - 2, so this barrier is at most one phase behind.)
+          if (!S::kTurns && !wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) break;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float lo, hi;
@@ -603,53 +612,93 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       }
     }
     if (!ok) break;
+    const uint32_t end = g + nt - 1;  // the last tile
+    const bool other_ends = turns && (end & 1) != h;
+    if (other_ends && (h == 0 || nt > 1) && !wait(&b.s[2 + (end & 1)], (end >> 1) & 1)) break;
     // every score of the item is computed: its queries may go
-    const bool more = next_item(later);
-    if (more) load_queries(later);
-    if (one) {
-      g += nt;
-      if (!wait(&b.o[2 + ((g - 1) & 1)], ((g - 1) >> 1) & 1)) break;
-    } else {
+    const bool more = next_item(later), shared = turns && nt > 1;
+    if (more && !(shared && h == 1)) load_queries(later);
+    if (!one) {
       d += nt;
       if (!wait(&b.o[h], pairs++ & 1)) break;
+    } else {
+      g += nt;
+      // (scores of the last tile are there, so the sum's barrier is at most one phase behind)
+      if ((shared || !other_ends) && !wait(&b.o[2 + (end & 1)], (end >> 1) & 1)) break;
     }
     const bool whole = it.first && it.last;
     const int slot = it.first ? 1 : 0;
-    if (busy) {
-      float lo, hi;
-      untwo(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
-      const float l = lo + hi;
+    float lo, hi;
+    untwo(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
+    float l = lo + hi, scale0 = 1.0f, scale1 = 1.0f;
+    if (shared) {  // the second half's queries have no use for an item of one half: their room takes m and l
+      float2* ml = reinterpret_cast<float2*>(queries + S::kTileBytes);
+      ml[threadIdx.x] = make_float2(m, l);
+      arrive(&b.join[0]);
+      if (!wait(&b.join[0], joined & 1)) break;
+      const float2 mine = make_float2(m, l), theirs = ml[threadIdx.x ^ 128];
+      m = fmaxf(m, theirs.x);
+      const float a = m == -INFINITY ? 0.0f : ex2(mine.x - m), z = m == -INFINITY ? 0.0f : ex2(theirs.x - m);
+      // in one order for both, so that they agree
+      scale0 = h ? z : a;
+      scale1 = h ? a : z;
+      l = (h ? theirs.y : mine.y) * scale0 + (h ? mine.y : theirs.y) * scale1;
+    }
+    if (busy && (shared || !other_ends)) {
       const bool mine = row < it.rows;
       const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw nothing gives 0
       uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
-      const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * S::kRows + h * 128 + tid;
+      const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * S::kRows + half_row;
       float* part = p.part_o + at * p.part_dim;
-#pragma unroll
-      for (int k = 0; k < DP / 32; ++k) {
+      // 32 columns at a time, one copy of the code: unrolled, calls of few tokens took up to 0.7 us longer.
+      // Of a shared item each warpgroup joins half of the columns.
+      const int col0 = shared ? h * (DP / 2) : 0, cols = min(p.head_dim, shared ? col0 + DP / 2 : DP);
+#pragma unroll 1
+      for (int col = col0; col < cols; col += 32) {
         uint32_t o[32];
-        tmem_ld32(o, to + k * 32);
+        float f[32];
+        tmem_ld32(o, (shared ? lanes + 256 : to) + col);
         tmem_wait_ld();
         settle(o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
+        if (shared) {
+          tmem_ld32(o, lanes + 384 + col);
+          tmem_wait_ld();
+          settle(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = f[j] * scale0 + __uint_as_float(o[j]) * scale1;
+        }
         if (!mine) continue;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
-          if (k * 32 + j >= p.head_dim) break;
-          float f[8];
+          if (col + j >= p.head_dim) break;
+          float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[j + e]);
+          for (int e = 0; e < 8; ++e) v[e] = f[j + e];
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = l > 0.0f ? f[e] * inv : 0.0f;
-            st_v4(out + k * 32 + j, pack8<DT>(f));
+            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            st_v4(out + col + j, pack8<DT>(v));
           } else {
-            *reinterpret_cast<float4*>(part + k * 32 + j) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(part + k * 32 + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            *reinterpret_cast<float4*>(part + col + j) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(part + col + j + 4) = make_float4(v[4], v[5], v[6], v[7]);
           }
         }
       }
-      if (mine && whole && p.lse) p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-      if (mine && !whole) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+      if (mine && !(shared && h == 1)) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+        else if (p.lse)
+          p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      }
+    }
+    // neither sum nor the room of m and l is written again until both warpgroups have read them
+    if (shared) {
+      arrive(&b.join[1]);
+      if (!wait(&b.join[1], joined++ & 1)) break;
+      if (more && h == 1) load_queries(later);
     }
     if (it.first && !it.last) {
       goes_on = true;
@@ -685,7 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
       mbar_init(&b.p2[x], 4);
     }
     for (int h = 0; h < 2; ++h) mbar_init(&b.q[h], 4);
-        mbar_init(&b.drain, 1);
+    for (int x = 0; x < 2; ++x) mbar_init(&b.join[x], 8);
+    mbar_init(&b.drain, 1);
     b.stop = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
@@ -759,11 +809,16 @@ bool attn_tensor_map(void* encode, CUtensorMap* map, const void* base, bool bf16
   const cuuint64_t strides[3] = {(cuuint64_t)(page > 1 ? page_stride * 2 : 16), (cuuint64_t)(heads > 1 ? head_stride * 2 : 16),
                                  (cuuint64_t)(blocks > 1 ? block_stride * 2 : 16)};
   const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, steps[4] = {1, 1, 1, 1};
+  // L2 fetches 256 bytes at a time only where they belong to the tile: rows of whole 256 bytes, or one
+  // row right behind the other.  (64 requests' tokens over 350 MB, heads of 64 that lie between a token's
+  // other heads: 141 us; with 256 bytes throughout 182 us.)
+  const CUtensorMapL2promotion promotion =
+      dim % 128 == 0 || page_stride == dim ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   return reinterpret_cast<Encode>(encode)(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                                           const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                          CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -103,7 +103,7 @@ def test_page_sizes(ctx, form, page):
     check(ctx, make([1, 33, 130], [700, 400, 130], 4, 2, 64, page=page, seed=page))
 
 
-@pytest.mark.parametrize("hq, hk", [(1, 1), (12, 2), (6, 1), (8, 8), (7, 1), (48, 8), (20, 4), (64, 1), (300, 1)])
+@pytest.mark.parametrize("hq, hk", [(1, 1), (12, 2), (6, 1), (8, 8), (7, 1), (40, 8), (20, 4), (64, 1), (300, 1)])
 def test_head_groups(ctx, form, hq, hk):
     check(ctx, make([3, 1, 40], [3, 260, 100], hq, hk, 64, seed=hq))
 
@@ -186,7 +186,7 @@ def test_items_of_one_and_two_halves(ctx, form, d):
     new = [1, 90, 2, 60, 1, 1, 130, 43, 42, 1, 0, 200, 3]
     lens = [5, 90, 900, 61, 300, 129, 140, 43, 2000, 128, 77, 1000, 3]
     check(ctx, make(new * 2, lens * 2, 6, 2, d, seed=d))
-    check(ctx, make(new * 12, [min(x, 300) for x in lens] * 12, 12, 4, d, "fp16", seed=d + 1))
+    check(ctx, make(new * 12, [min(x, 300) for x in lens] * 12, 15, 5, d, "fp16", seed=d + 1))
 
 
 @pytest.mark.parametrize("seed", range(6))
@@ -231,6 +231,25 @@ def test_long_cache_is_split(ctx, form):
 def test_infinities_where_nothing_is_seen(ctx, form):
     for bad in (float("inf"), float("-inf"), float("nan")):
         check(ctx, make([20, 1], [100, 77], 4, 2, 64, seed=10, garbage=bad, page=32))
+
+
+def test_nan_reaches_the_rows_that_see_it(ctx, form):
+    """A NaN in a query or a visible key: its rows are NaN, every other row keeps its bits."""
+    for d, ctx_len in ((64, 40), (64, 5000), (256, 700)):
+        x = make([70], [ctx_len + 70], 4, 2, d, seed=20)
+        want, wl = run(ctx, x, scale=d ** -0.5)
+        assert torch.isfinite(want).all()
+        x["q"][3, 1, d - 1] = float("nan")  # token 3, head 1
+        at = ctx_len + 60  # its place; seen by rows 60 to 69, key head 1 (heads 2 and 3)
+        page = x["kc"].shape[1]
+        x["kc"][x["table"][0][at // page], at % page, 1, 0] = float("nan")
+        out, lse = run(ctx, x, scale=d ** -0.5)
+        bad = torch.zeros(70, 4, dtype=torch.bool)
+        bad[3, 1] = True
+        bad[60:, 2:] = True
+        bad = bad.to(out.device)
+        assert out[bad].isnan().all() and lse[bad].isnan().all()
+        assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
 
 
 def test_keys_outside_the_window_may_be_gone(ctx, form):
