@@ -12,12 +12,17 @@
 // item that began before it (slot 0) and one that ends after it (slot 1).  A second small
 // kernel joins the parts in a fixed order, so results do not depend on timing.
 //
-// Storing and joining the parts of an item of many rows takes as long as about kSplitCost tiles.  So
-// one of no more tiles than that and a span together is not split, as long as it is short (up to
-// kWholeMost tiles; long ones would leave SMs idle): a span that would begin or end inside it is
-// moved to its nearer end (both neighbours decide alike).  Measured on GB300 with 12 q heads, 2
-// key heads of 128, us without the rule and with it: 512 tokens over 1000: 43.6, 34.1; 1024 over
-// none: 36.2, 28.7; 128 over 3000, where every rule splits: 40.4 (unsplit 69.2).
+// An item of many rows costs more than its tiles: its queries arrive, its first scores and its last
+// sum stand alone, its rows are written.  So it counts kItemCost tiles more, in front of its own.
+// (Measured on GB300 with 20 q heads, 4 key heads of 128, causal, us with 0, 2, 4, 6 tiles: 5 requests
+// of 983 tokens 94, 61, 58, 61; 12 q heads, 300 tokens over 10000: 43, 41, 38, 38.)
+//
+// Storing and joining its parts takes as long as about kSplitCost tiles.  So one of no more tiles
+// than that and a span together is not split, as long as it is short (up to kWholeMost tiles; long
+// ones would leave SMs idle): a span that would begin or end inside it is moved to its nearer end
+// (both neighbours decide alike).  (12 q heads, 2 key heads of 128, us with 12, 8, 6, 4: 512 tokens
+// over 1000 32.1, 34.2, 26.9, 26.9; 1024 over none 25.9, 25.9, 26.0, 27.3; without the rule, on an
+// earlier form that took 34 and 29 us with it, 44 and 36.)
 #pragma once
 
 #include "ar_common.cuh"
@@ -30,8 +35,8 @@ namespace ar {
 // ends (0: there is no such item), first row of the request, rows of the request, query tile, head.
 constexpr int kHeaderInts = 8;
 
-constexpr int kSplitCost = 12, kWholeMost = 24;
-constexpr int kFewRows = 64;  // items of so few rows are split at any length: their parts are small
+constexpr int kItemCost = 4, kSplitCost = 6, kWholeMost = 24;
+constexpr int kFewRows = 64;  // items of no more rows are split at any length, and count their tiles alone: their parts are small
 
 struct Request {
   int q0, n, len, prefix;  // first row of q, new tokens, keys, keys that every row sees
@@ -71,8 +76,14 @@ __device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Reque
   return t;
 }
 
+// Tiles that an item of so many rows counts besides its own, in front of them.
+template <int ROWS>
+__device__ __forceinline__ int extra_tiles(const AttnParams& p, const Request& q, int qt) {
+  return q.n * (int)p.group.d - qt * ROWS > kFewRows ? kItemCost : 0;
+}
+
 struct Cursor {  // a place in the sequence
-  int r, qt, h, tile;
+  int r, qt, h, tile;  // tile: extra ones first
 };
 
 // One item as a CTA walks over it.
@@ -103,6 +114,7 @@ __device__ void find_span(const AttnParams& p, SpanShared& sh) {
   Request q = {0, 0, 0, 0};
   long long before = 0, mine = 0, excl = 0;
   auto query_tiles = [&](int n) { return (int)((n * p.group.d + ROWS - 1) / ROWS); };
+  auto weight_of = [&](const Request& o, int qt) { return tile_range<ROWS, KT>(p, o, qt).count() + extra_tiles<ROWS>(p, o, qt); };
   auto share = [&](int src) {  // a lane's request, to its warp
     Request o;
     o.q0 = 0;
@@ -116,13 +128,13 @@ __device__ void find_span(const AttnParams& p, SpanShared& sh) {
     q.n = 0;
     if (r < p.requests) q = load_request(p, r);
     const int nqt = query_tiles(q.n);
-    mine = nqt == 1 ? tile_range<ROWS, KT>(p, q, 0).count() : 0;
+    mine = nqt == 1 ? weight_of(q, 0) : 0;
     for (unsigned many = __ballot_sync(0xffffffffu, nqt > 1); many; many &= many - 1) {  // the warp together
       const int src = __ffs(many) - 1;
       const Request o = share(src);
       const int m = query_tiles(o.n);
       long long s = 0;
-      for (int t = lane; t < m; t += 32) s += tile_range<ROWS, KT>(p, o, t).count();
+      for (int t = lane; t < m; t += 32) s += weight_of(o, t);
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
       if (lane == src) mine = s;
@@ -180,7 +192,7 @@ __device__ void find_span(const AttnParams& p, SpanShared& sh) {
     const int m = query_tiles(o.n);
     for (int first = 0; first < m; first += 32) {
       const int t = first + lane;
-      const int n = t < m ? tile_range<ROWS, KT>(p, o, t).count() : 0;
+      const int n = t < m ? weight_of(o, t) : 0;
       const long long own = (long long)n * p.kv_heads;
       long long s = own;
 #pragma unroll
@@ -228,12 +240,15 @@ struct Walk {
       it.qt = at.qt;
       it.h = at.h;
       it.range = tile_range<ROWS, KT>(p, q, at.qt);
-      const int n = it.range.count();
-      int begin = at.tile, end = (int)min((long long)n, at.tile + left);
+      const int n = it.range.count(), extra = extra_tiles<ROWS>(p, q, at.qt);
+      int begin = at.tile, end = (int)min((long long)(n + extra), at.tile + left);
       left -= end - begin;
       if (n <= whole && rows - it.qt * ROWS > kFewRows) {  // whole or not at all
-        begin = begin * 2 < n ? 0 : n;
-        end = end * 2 < n ? 0 : n;
+        begin = begin * 2 < n + extra ? 0 : n;
+        end = end * 2 < n + extra ? 0 : n;
+      } else {
+        begin = max(begin - extra, 0);
+        end = max(end - extra, 0);
       }
       it.begin = begin;
       it.end = end;

@@ -154,6 +154,18 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
+__device__ __forceinline__ void st_v8(void* dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 16 bytes to shared memory, the last 16 - bytes of them zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -478,22 +490,28 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     __syncwarp();
     return found;
   };
-  // Queries, 16 bytes a thread, neighbours along a row; columns beyond the head are zero.  Rows
-  // beyond the item's keep what was there: they meet no other row, and nothing of them is stored.
+  // Queries, 16 bytes a thread, neighbours along a row, by asynchronous copies: all are in flight
+  // at once and hold no registers.  Columns beyond the head are zero.  Rows beyond the item's keep
+  // what was there: they meet no other row, and nothing of them is stored.
+  bool loading = false;
   auto load_queries = [&](const Item& it) {
     if (h == 1 && single_half<DP>(it)) return;
-    uint8_t* dst = queries + h * S::kTileBytes;
+    loading = true;
+    const uint32_t dst = smem_addr(queries + h * S::kTileBytes);
     const int base = it.qt * S::kRows + h * 128, rows = min(it.rows - base, 128);
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)it.q.q0 * p.q_ts + (int64_t)it.h * (int)p.group.d * p.q_hs;
 #pragma unroll 4
     for (int x = tid; x < rows * (DP / 8); x += 128) {
       const int r = x / (DP / 8), c = x % (DP / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c * 8 < p.head_dim) {
-        const int t = (base + r) / p.group, e = base + r - t * (int)p.group.d;
-        v = ld_keep(static_cast<const uint16_t*>(p.q) + (int64_t)(it.q.q0 + t) * p.q_ts + (int64_t)(it.h * (int)p.group.d + e) * p.q_hs + c * 8);
-      }
-      *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      const int t = (base + r) / p.group, e = base + r - t * (int)p.group.d;
+      const uint16_t* src = q + t * p.q_ts + e * p.q_hs + c * 8;
+      cp_async16(dst + (c >> 3) * S::kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), c * 8 < p.head_dim ? src : q, c * 8 < p.head_dim ? 16 : 0);
     }
+  };
+  auto queries_loaded = [&] {
+    if (!loading) return;
+    loading = false;
+    cp_async_wait();
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.q[h]);
@@ -501,6 +519,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   bool goes_on = false;
   bool have = next_item(it);
   if (have) load_queries(it);
+  queries_loaded();
   while (have) {
     const int nt = it.end - it.begin;
     const bool one = single_half<DP>(it);
@@ -626,6 +645,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       // (scores of the last tile are there, so the sum's barrier is at most one phase behind)
       if ((shared || !other_ends) && !wait(&b.o[2 + (end & 1)], (end >> 1) & 1)) break;
     }
+    queries_loaded();
     const bool whole = it.first && it.last;
     const int slot = it.first ? 1 : 0;
     float lo, hi;
@@ -671,6 +691,26 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
           for (int j = 0; j < 32; ++j) f[j] = f[j] * scale0 + __uint_as_float(o[j]) * scale1;
         }
         if (!mine) continue;
+        if (p.wide) {  // whole sectors
+#pragma unroll
+          for (int j = 0; j < 32; j += 16) {
+            if (col + j >= p.head_dim) break;
+            uint32_t v[8];
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = pack2<DT>(f[j + 2 * e] * inv, f[j + 2 * e + 1] * inv);
+              st_v8(out + col + j, v);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 16; x += 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(f[j + x + e]);
+                st_v8(part + col + j + x, v);
+              }
+            }
+          }
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           if (col + j >= p.head_dim) break;
@@ -699,6 +739,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       arrive(&b.join[1]);
       if (!wait(&b.join[1], joined++ & 1)) break;
       if (more && h == 1) load_queries(later);
+      queries_loaded();
     }
     if (it.first && !it.last) {
       goes_on = true;
@@ -708,6 +749,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     __syncwarp();
     have = more;
   }
+  cp_async_wait();  // of queries, after a wait that ran out
   if (threadIdx.x == 0 && !goes_on) write_header(p, span, nullptr);
 }
 

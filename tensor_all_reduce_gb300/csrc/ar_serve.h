@@ -101,6 +101,7 @@ struct AttnParams {
   const float* slopes;
   const int32_t* prefix;
   int vec;  // 16-byte loads of q and the cache, 16-byte stores of out
+  int wide;  // 32-byte stores of out and of partial rows (the tensor-core form)
   // workspace: the partial results of the spans that begin or end inside an item
   int spans, tile_rows, part_dim;  // CTAs, rows of an item, floats of a partial row
   int* headers;

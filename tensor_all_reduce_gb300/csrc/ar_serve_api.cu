@@ -436,6 +436,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.headers = reinterpret_cast<int*>(base);
   p.part_ml = reinterpret_cast<float*>(base + w.ml);
   p.part_o = reinterpret_cast<float*>(base + w.o);
+  p.wide = d % 16 == 0 && a->out_token_stride % 16 == 0 && a->out_head_stride % 16 == 0 && aligned(a->out, 32) && aligned(base, 32);
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
   const bool cap = a->softcap > 0.0f, bias = a->slopes || !(a->scale > 0.0f);
