@@ -651,7 +651,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       // (scores of the last tile are there, so the sum's barrier is at most one phase behind)
       if ((shared || !other_ends) && !wait(&b.o[2 + (end & 1)], (end >> 1) & 1)) break;
     }
-    queries_loaded();
+    if (!shared) queries_loaded();
     const bool whole = it.first && it.last;
     const int slot = it.first ? 1 : 0;
     float lo, hi;
@@ -662,6 +662,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       ml[threadIdx.x] = make_float2(m, l);
       arrive(&b.join[0]);
       if (!wait(&b.join[0], joined & 1)) break;
+      // Not before: the next item's scores would complete phases that the other warpgroup still waits for.
+      queries_loaded();
       const float2 mine = make_float2(m, l), theirs = ml[threadIdx.x ^ 128];
       m = fmaxf(m, theirs.x);
       const float a = m == -INFINITY ? 0.0f : ex2(mine.x - m), z = m == -INFINITY ? 0.0f : ex2(theirs.x - m);

@@ -233,6 +233,24 @@ def test_infinities_where_nothing_is_seen(ctx, form):
         check(ctx, make([20, 1], [100, 77], 4, 2, 64, seed=10, garbage=bad, page=32))
 
 
+@pytest.mark.parametrize("shift", [0, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_on_16_and_32_byte_boundaries(ctx, d, shift):
+    """Outputs and workspace that begin 16 bytes behind a 32-byte boundary, rows of an odd number of 16 bytes: the same bits."""
+    x = make([1, 90, 300, 2], [4000, 2100, 300, 64], 6, 2, d, seed=21)
+    want, _ = run(ctx, x, scale=d ** -0.5)
+    n = x["q"].shape[0]
+    room = torch.full((n, 6 * d + 8 + shift), 7.0, dtype=x["q"].dtype, device="cuda")
+    out = torch.as_strided(room, (n, 6, d), (6 * d + 8 + shift, d, 1), shift)
+    work = ctx.paged_attention_workspace(d, x["q"].dtype)
+    room_w = torch.empty(work.numel() + 16, dtype=torch.uint8, device="cuda")
+    ctx.paged_attention(x["q"].cuda(), x["kc"].cuda(), x["vc"].cuda(), i32(x["table"]), i32(x["cu"]), i32(x["lens"]), scale=d ** -0.5,
+                        out=out, workspace=room_w[2 * shift:][:work.numel()])
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want)
+    assert (room[:, :shift] == 7.0).all() and (room[:, shift + 6 * d:] == 7.0).all()
+
+
 def test_nan_reaches_the_rows_that_see_it(ctx, form):
     """A NaN in a query or a visible key: its rows are NaN, every other row keeps its bits."""
     for d, ctx_len in ((64, 40), (64, 5000), (256, 700)):

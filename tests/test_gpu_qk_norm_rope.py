@@ -88,6 +88,15 @@ def test_tokens_and_heads(ctx, tokens, hq, hk):
     check(ctx, make(tokens, hq, hk, 128, "bf16", 128, seed=tokens))
 
 
+@pytest.mark.parametrize("tokens", [460, 1001, 1501, 2203, 2705, 3101, 3501])
+@pytest.mark.parametrize("hq, hk, d, rot, pairs", [(4, 2, 64, 64, False), (4, 2, 80, 80, True), (2, 1, 96, 24, False), (3, 1, 256, 72, False)])
+def test_units_of_several_tokens(ctx, tokens, hq, hk, d, rot, pairs):
+    """Short rows: two to eight tokens are staged together, the last unit is not full, some have no slot."""
+    x = make(tokens, hq, hk, d, "bf16", rot, axes=2, seed=tokens)
+    x["slots"][::7] = -1
+    check(ctx, x, sections=[rot // 2 - 3, 3], dealt=pairs, pairs=pairs)
+
+
 @pytest.mark.parametrize("axes", [2, 3, 4])
 @pytest.mark.parametrize("dealt", [False, True])
 @pytest.mark.parametrize("d, pairs", [(128, False), (80, True)])
