@@ -37,7 +37,7 @@ bool overlap(const Extent& a, const Extent& b) {
   return !(d >= a.span && d + b.span <= s);
 }
 
-struct Checker {
+struct Operands {
   Extent in[24], out[8];
   int ni = 0, no = 0;
   void read(const Extent& e) { if (!e.empty()) in[ni++] = e; }
@@ -88,7 +88,7 @@ ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* a, void* stream) 
       !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) || !aligned(a->seq_lens, 4) || !aligned(a->slots, 8) ||
       !aligned(a->positions, 4) || !aligned(a->free_count_out, 4) || !aligned(a->info, 4))
     return AR_ERR_ALIGNMENT;
-  Checker c;
+  Operands c;
   c.read(flat(a->cached_lens, r * 4));
   c.read(flat(a->new_lens, r * 4));
   c.read(flat(a->free_blocks, a->free_capacity * 4));
@@ -182,7 +182,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
     if (!aligned(x, 2)) return AR_ERR_ALIGNMENT;
   if ((half && (!aligned(a->positions, 4) || !aligned(a->inv_freq, 4))) || (cache && !aligned(a->slots, 8))) return AR_ERR_ALIGNMENT;
 
-  Checker c;
+  Operands c;
   int alias[4] = {0, 0, 0, 0};
   auto heads = [&](const void* p, int64_t ts, int64_t h, int64_t hs) { return Extent{p, ((h - 1) * hs + d) * 2, ts * 2, n}; };
   if (hq) c.read(heads(a->q, a->q_token_stride, hq, a->q_head_stride));
@@ -350,7 +350,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
       !aligned(a->prefix_lens, 4) || !aligned(a->workspace, 16))
     return AR_ERR_ALIGNMENT;
   const int64_t ts = a->table_stride ? a->table_stride : a->table_cols;
-  Checker c;
+  Operands c;
   c.read({a->q, ((hq - 1) * a->q_head_stride + d) * 2, a->q_token_stride * 2, n});
   c.read({a->k_cache, span3(pg, a->k_page_stride, hk, a->k_head_stride, d) * 2, a->k_block_stride * 2, a->num_blocks});
   c.read({a->v_cache, span3(pg, a->v_page_stride, hk, a->v_head_stride, d) * 2, a->v_block_stride * 2, a->num_blocks});
