@@ -388,8 +388,11 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* args, void* s
  * Scores, softmax statistics and sums are fp32; the weights are rounded to dtype for the
  * second product, which is summed in fp32.
  *
- * workspace: ar_paged_attention_workspace(args) bytes of device memory, 16-byte aligned, for
- * the parts of rows whose keys were split over SMs.  Its contents need no preparation; calls
+ * How a row's keys are split over the SMs follows from the whole batch: equal calls give equal
+ * bits, the same row in another batch may differ in its last ones.
+ *
+ * workspace: ar_paged_attention_workspace(args) bytes of device memory (fewer: AR_ERR_INVALID_ARG),
+ * 16-byte aligned, for the parts of rows whose keys were split over SMs.  Its contents need no preparation; calls
  * that may run at the same time need one each.
  */
 typedef struct {
