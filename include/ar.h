@@ -355,7 +355,8 @@ typedef struct {
   int sections[AR_MAX_ROPE_AXES];       /* frequencies of each axis (axes = 1: ignored) */
   int dealt;
   const int32_t* positions;             /* device [axes, tokens] */
-  int64_t position_stride;              /* elements between the axes' rows (0: tokens) */
+  int64_t position_stride;              /* elements between the axes' rows (0: tokens; one row that all
+                                           axes share is axes = 1) */
   const float* inv_freq;                /* device fp32 [rot_dim / 2], radians a position */
   void* k_cache;                        /* both or neither */
   void* v_cache;

@@ -709,6 +709,7 @@ class Context:
         ([tokens] or [axes, tokens] int32) with the fp32 frequencies `inv_freq` (None: none), and
         the write of k and v to the paged cache at `slots` (see ar_qk_norm_rope).  q, k, v are
         [tokens, heads, head_dim] and may be views of one packed projection; q or k may be None.
+        Positions that all axes share may be an expanded row.
         Returns (q_out, k_out); with a cache, want_k_out=False leaves k_out out (None)."""
         t = _torch or _bind_torch()
         dev = self.device
@@ -764,7 +765,12 @@ class Context:
                         raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
                     if sections is None or len(sections) != axes:
                         raise ValueError("sections must name the frequencies of each position axis")
-                    sec = (*sections, *_NO_SECTIONS[axes:])
+                    if pos_stride:
+                        sec = (*sections, *_NO_SECTIONS[axes:])
+                    else:  # one row for all axes (an expanded view) is the rotation by one axis; the C call takes 0 for `tokens`
+                        if sum(sections) != half or min(sections) < 0:
+                            raise ArError(AR_ERR_INVALID_ARG, "ar_qk_norm_rope", "sections must add up to the frequencies")
+                        axes = 1
                 elif axes < 1:
                     raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
         args = _pack_rope(

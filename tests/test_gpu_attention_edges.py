@@ -1,0 +1,40 @@
+"""Calls of the attention block that its documentation allows at the edges: shared position rows, pages
+released behind a window, wide caps, bad block numbers, orders in memory, many streams."""
+import pytest
+import torch
+
+import serve_ref as ref
+import test_gpu_paged_attention as pa
+import test_gpu_qk_norm_rope as nr
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    import tensor_all_reduce_gb300 as tar
+    with tar.Context(0) as c:
+        yield c
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 700])
+@pytest.mark.parametrize("dealt", [False, True])
+@pytest.mark.parametrize("d, pairs", [(128, False), (80, True), (33, False)])
+def test_positions_that_all_axes_share(ctx, tokens, dealt, d, pairs):
+    """Text tokens on several axes: one row expanded, against the 64-bit form and the rows written out."""
+    rot = d // 2 * 2
+    x = nr.make(tokens, 4, 2, d, "bf16", rot, far=1 << 20, seed=tokens)
+    sections = nr.cut(rot // 2, 3)
+    g = nr.on_gpu(x)
+    row = g["pos"][0].clone()
+    call = lambda pos: ctx.qk_norm_rope(g["q"], g["k"], None, pos, g["freq"], q_weight=g["wq"], k_weight=g["wk"], pairs=pairs,  # noqa: E731
+                                        sections=sections, dealt=dealt)
+    got, whole = call(row.expand(3, tokens)), call(row.repeat(3, 1))
+    apart = torch.full((3, tokens + 5), -1, dtype=torch.int32, device="cuda")[:, 2:2 + tokens]
+    apart.copy_(row.expand(3, tokens))
+    strided = call(apart)
+    axis = [0] * (rot // 2)
+    for i, (n, w) in enumerate((("q", "wq"), ("k", "wk"))):
+        nr.near(got[i], *ref.rope(x[n], x[w], 1e-6, False, x["pos"], x["freq"], pairs, axis))
+        assert torch.equal(got[i], whole[i]) and torch.equal(got[i], strided[i])
+    assert ctx.device_status() == 0
