@@ -475,10 +475,10 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
   const float scale = EXT ? 1.0f : p.scale_log2;
   // A thread's scores take most of its registers: what is the same for a warp stays in shared
-  // memory (every lane writes the same values).
+  // memory.  Lane 0 alone steps the walk (a step reads and writes it), between two barriers of the warp.
   auto& walk = state.walk;
   Item &it = state.it, &later = state.later;
-  walk.start(span);
+  if (lane == 0) walk.start(span);
   uint32_t pairs = 0, d = 0, g = 0, joined = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -490,11 +490,14 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
+    __syncwarp();  // tensor memory is read and written by whole warps
   };
   auto next_item = [&](Item& to) {  // the next one that this warpgroup has a part in
-    const bool found = (S::kTurns || h == 0) && walk.next(p, to);
     __syncwarp();
-    return found;
+    bool found = false;
+    if (lane == 0) found = (S::kTurns || h == 0) && walk.next(p, to);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, found, 0) != 0;
   };
   // Queries, 16 bytes a thread, neighbours along a row, by asynchronous copies: all are in flight
   // at once and hold no registers.  Columns beyond the head are zero.  Rows beyond the item's keep
@@ -685,6 +688,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
 #pragma unroll 1
       for (int col = col0; col < cols; col += 32) {
         uint32_t o[32];
+        __syncwarp();  // lanes without a row come from the last round early
         float f[32];
         tmem_ld32(o, (shared ? lanes + 256 : to) + col);
         tmem_wait_ld();
@@ -753,7 +757,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       goes_on = true;
       if (threadIdx.x == 0) write_header(p, span, &it);
     }
-    it = later;
+    __syncwarp();  // every lane is done with the item
+    if (lane == 0) it = later;
     __syncwarp();
     have = more;
   }

@@ -38,3 +38,16 @@ def test_positions_that_all_axes_share(ctx, tokens, dealt, d, pairs):
         nr.near(got[i], *ref.rope(x[n], x[w], 1e-6, False, x["pos"], x["freq"], pairs, axis))
         assert torch.equal(got[i], whole[i]) and torch.equal(got[i], strided[i])
     assert ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_items_a_span(ctx, d):
+    """Each CTA walks over many items, of one and two halves in turn, with rows of a warp missing: every role keeps
+    the same place in the sequence, so repeated calls give equal bits, and each row is its own request's."""
+    new = [1, 45, 3, 128, 0, 7, 33, 2] * 40
+    lens = [(37 * i) % 290 + n for i, n in enumerate(new)]
+    x = pa.make(new, lens, 6, 2, d, seed=d)
+    want = pa.check(ctx, x)
+    for _ in range(10):
+        out, lse = pa.run(ctx, x, scale=d ** -0.5)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
