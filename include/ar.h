@@ -384,8 +384,9 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* args, void* s
  * request's length is never used, NaN and infinities included; k may hold them wherever it is
  * not visible; v must be finite at the tokens of a request (a token that one row does not see
  * shares matrix products with rows that do).
- * A block number outside the cache reads as zeros and leaves code 2; lengths are cut to what
- * the table's columns hold, and row ranges to the tokens, likewise with code 2.
+ * A block number outside the cache reads as zeros, and leaves code 2 where a row sees one of the
+ * block's keys (the blocks that have left every row's window may be gone); lengths are cut to
+ * what the table's columns hold, and row ranges to the tokens, likewise with code 2.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to dtype for the
  * second product, which is summed in fp32.
  *

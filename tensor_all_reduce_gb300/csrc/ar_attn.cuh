@@ -55,6 +55,19 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int r) {
   return q;
 }
 
+// Keys [low, high) that some of a request's new tokens [t0, t1) sees besides the prefix: their windows, of
+// neighbouring positions, leave no gap.
+struct KeyRange {
+  int low, high;
+  __device__ __forceinline__ bool sees(const Request& q, int key) const { return key < q.prefix || (key < high && key >= low); }
+};
+
+__device__ __forceinline__ KeyRange key_range(const AttnParams& p, const Request& q, int t0, int t1) {
+  const int p0 = q.len - q.n + t0, p1 = q.len - q.n + t1;  // positions; may be negative: rows that see no key
+  // |p0| and window are at most 2^30
+  return {p.window ? max(p0 - p.window + 1, 0) : 0, p.causal ? min(max(p1, 0), q.len) : q.len};
+}
+
 // Key tiles of a query tile: [0, pre), then [lo, hi).
 struct TileRange {
   int pre, lo, hi;
@@ -65,14 +78,11 @@ struct TileRange {
 template <int ROWS, int KT>
 __device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Request& q, int qt) {
   const int row0 = qt * ROWS, rows = q.n * (int)p.group.d;  // at most 2^30
-  const int t0 = row0 / p.group, t1 = (min(row0 + ROWS, rows) - 1) / p.group;
-  const int p0 = q.len - q.n + t0, p1 = q.len - q.n + t1;  // may be negative: rows that see no key
-  const int high = p.causal ? min(max(p1 + 1, 0), q.len) : q.len;
-  const int low = p.window ? max(p0 - p.window + 1, 0) : 0;  // |p0| and window are at most 2^30
+  const KeyRange k = key_range(p, q, row0 / p.group, (min(row0 + ROWS, rows) - 1) / p.group + 1);
   TileRange t;
   t.pre = (q.prefix + KT - 1) / KT;
-  t.lo = max(low / KT, t.pre);
-  t.hi = (high + KT - 1) / KT;
+  t.lo = max(k.low / KT, t.pre);
+  t.hi = (k.high + KT - 1) / KT;
   return t;
 }
 
@@ -310,13 +320,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Block and place in it of a key; -1 for a block number outside the cache.
-__device__ __forceinline__ int64_t block_of(const AttnParams& p, int r, int key, int& in_page) {
+// Block and place in it of a key; -1 for a block number outside the cache, which is an error only
+// where a row of the request sees the key (blocks behind a window may be gone).
+__device__ __forceinline__ int64_t block_of(const AttnParams& p, const Item& it, int key, int& in_page) {
   const int j = key / p.page;
   in_page = key - j * (int)p.page.d;
-  const int b = p.table[(int64_t)r * p.table_stride + j];
+  const int b = p.table[(int64_t)it.r * p.table_stride + j];
   if (b < 0 || b >= p.num_blocks) {
-    *p.status = kStatusBadIndex;
+    if (key_range(p, it.q, 0, it.q.n).sees(it.q, key)) *p.status = kStatusBadIndex;
     return -1;
   }
   return b;

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
         const uint16_t *k = nullptr, *v = nullptr;
         if (key < it.q.len) {
           int off;
-          const int64_t b = block_of(p, it.r, key, off);
+          const int64_t b = block_of(p, it, key, off);
           if (b >= 0) {
             k = static_cast<const uint16_t*>(p.k) + b * p.k_bs + off * p.k_ps + it.h * p.k_hs;
             v = static_cast<const uint16_t*>(p.v) + b * p.v_bs + off * p.v_ps + it.h * p.v_hs;

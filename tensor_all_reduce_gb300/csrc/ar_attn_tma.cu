@@ -29,6 +29,7 @@
 // leave twice the reads of keys and values a product; short prompts by an item's start and end.
 //
 // Every wait is bounded; one that runs out leaves code 1 in the status word, and all roles stop.
+// Shared memory is full to 64 bytes: 225 KB of tiles for heads of 65 to 128, and about 2 KB static.
 #include <cuda.h>
 
 #include "ar_attn.cuh"
@@ -248,11 +249,7 @@ __device__ void load_role(const AttnParams& p, bool keys, const CUtensorMap* map
         i = ahead && t + 1 < nt ? 2 * t + 2 : 2 * t + 1;
       i = n + i * S::kUnits;
       // outside the cache: the copy fills with zeros
-      int w = block, y = place;
-      if (w < 0 || w >= p.num_blocks) {
-        if (lane < boxes && it.range.tile(it.begin + t) * kKeys + lane * p.box_rows < it.q.len) *p.status = kStatusBadIndex;
-        w = (int)p.num_blocks;
-      }
+      const int w = (unsigned)block < (unsigned)p.num_blocks ? block : (int)p.num_blocks, y = place;
       if (t + 1 < nt) look_up(t + 1);
       for (int u = 0; u < S::kUnits; ++u, ++i) {
         const uint32_t slot = i % S::kSlots, round = i / S::kSlots;
@@ -273,6 +270,24 @@ __device__ void load_role(const AttnParams& p, bool keys, const CUtensorMap* map
       }
     }
     n += 2 * nt * S::kUnits;
+  }
+}
+
+// Block numbers outside the cache are an error where a row of the request sees one of the block's keys
+// (those behind a window may be gone).  A warp whose copies are issued looks for them, request by request,
+// many CTAs a request where there are few: between the copies, which wide heads wait for, the test cost
+// 2 x 1024 tokens over 8000 (heads of 256) 4 to 10 us of 162.
+__device__ void check_blocks(const AttnParams& p) {
+  const int lane = threadIdx.x & 31, grid = (int)gridDim.x;
+  const int parts = max(grid / p.requests, 1), part = (int)blockIdx.x % parts;
+  for (int r = (int)blockIdx.x / parts; r < p.requests; r += grid / parts) {
+    const Request q = load_request(p, r);
+    const KeyRange range = key_range(p, q, 0, q.n);
+    const int32_t* row = p.table + (int64_t)r * p.table_stride;
+    const int pre = (q.prefix + (int)p.page.d - 1) / p.page, end = (range.high + (int)p.page.d - 1) / p.page;
+    const int first = max(range.low / p.page, pre), blocks = q.n ? pre + max(end - first, 0) : 0;
+    for (int i = part * 32 + lane; i < blocks; i += parts * 32)
+      if ((unsigned)row[i < pre ? i : first + (i - pre)] >= (unsigned)p.num_blocks) *p.status = kStatusBadIndex;
   }
 }
 
@@ -809,12 +824,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tma(const __grid_constant__ 
   const uint32_t queries = smem_addr(smem), ring = queries + S::kQueryBytes;
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp)
+    if (warp == kLoadWarp) {
       load_role<DP>(p, true, &kmap, span, b, ring);
-    else if (warp == kLoadWarp + 1)
+    } else if (warp == kLoadWarp + 1) {
       load_role<DP>(p, false, &vmap, span, b, ring);
-    else if (warp == kMmaWarp)
+      check_blocks(p);
+    } else if (warp == kMmaWarp) {
       mma_role<DT, DP>(p, span, b, queries, ring, tmem);
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     softmax_role<DT, DP, EXT>(p, span, states[warp], b, smem, tmem);

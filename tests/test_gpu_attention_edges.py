@@ -51,3 +51,37 @@ def test_many_items_a_span(ctx, d):
     for _ in range(10):
         out, lse = pa.run(ctx, x, scale=d ** -0.5)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.fixture(params=[0, 4], ids=["auto", "general"])
+def form(ctx, request):
+    import tensor_all_reduce_gb300 as tar
+    ctx.set_option(tar.AR_OPT_FORCE_VARIANT, request.param)
+    yield request.param
+    ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 0)
+
+
+@pytest.mark.parametrize("page", [1, 8, 16, 24, 384])
+@pytest.mark.parametrize("prefix", [0, 70])
+@pytest.mark.parametrize("causal", [True, False])
+def test_blocks_released_behind_the_window(ctx, form, page, prefix, causal):
+    """A server gives a block back as soon as no row sees a key of it (-1 in the table), inside a tile too: the
+    call is right and leaves no code.  One block more is missed."""
+    window, new, lens = 100, [1, 4, 300, 1], [1900, 700, 1300, 90]
+    x = pa.make(new, lens, 4, 2, 64, page=page, seed=page, garbage=0.0)
+    kw = dict(window=window, causal=causal)
+    if prefix:
+        kw["prefix_lens"] = torch.full((4,), prefix, dtype=torch.int32)
+    edges = []
+    for row, n, length in zip(x["table"], new, lens):
+        low = max(length - n - window + 1, 0)  # the first key of the first row's window
+        first, last = -(-prefix // page), low // page
+        for j in range(first, last):
+            row[j] = -1 if j % 2 else x["kc"].shape[0] + j
+        edges.append(last)
+    pa.check(ctx, x, **kw)
+    for r in range(3):
+        y = dict(x, table=[list(t) for t in x["table"]])
+        y["table"][r][edges[r]] = -1
+        pa.run(ctx, y, **kw)
+        assert ctx.device_status() == 2
