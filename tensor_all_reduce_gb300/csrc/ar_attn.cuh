@@ -309,7 +309,10 @@ __device__ __forceinline__ bool visible(const Item& it, const RowView& v, int ke
 // Score in log2 units from the raw product.
 __device__ __forceinline__ float bend(const AttnParams& p, const RowView& v, float dot, int key) {
   float s = dot * p.scale_log2;
-  if (p.cap_log2 > 0.0f) s = p.cap_log2 * tanhf(s);
+  if (p.cap_log2 > 0.0f) {
+    const float x = s * p.cap_inv;
+    if (!(fabsf(x) < 0x1p-13f)) s = p.cap_log2 * tanhf(x);  // below, tanh(x) is x to 2^-27, and x may be subnormal
+  }
   if (p.slopes) s -= v.slope * (float)abs(v.pos - key);
   return s;
 }

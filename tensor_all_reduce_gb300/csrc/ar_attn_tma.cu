@@ -429,8 +429,9 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
 }
 
 // How scores are bent, a bit each: kCap (tanh), kBias (distance; also any scale that is not positive,
-// since the plain form scales after the maximum).
-enum { kCap = 1, kBias = 2 };
+// since the plain form scales after the maximum), kWide (a wide cap, always with the other two: a kernel of its
+// own, since a branch in the others cost a mixed batch with a cap of 30 6 %).
+enum { kCap = 1, kBias = 2, kWide = 4 };
 
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -443,11 +444,24 @@ __device__ __forceinline__ float rcp(float x) {
 template <int EXT>
 __device__ __forceinline__ void shape_scores(const AttnParams& p, int prefix, const RowView& v, int key0, bool edge, float (&s)[64]) {
   if constexpr (EXT & kCap) {
-    // c tanh(x) = c - 2 c / (1 + e^2x): one exponential and one reciprocal an element, absolute
-    // error 2^-22 c; an exponential that overflows gives c
-    const float twice = p.scale_log2 * 2.8853900817779268f, c = p.cap_log2;
+    // c tanh(x) = c - 2 c / (1 + e^2x): one exponential and one reciprocal an element; an exponential that
+    // overflows gives c.  The difference leaves an absolute error of 2^-22 c, whatever the score: 2^-16 at
+    // most for caps of up to 64, far below the weights' rounding.  With wider caps, where usual scores are a
+    // small part of c, |x| < 1/2 takes the score times tanh(x) / x, a polynomial in x^2 (interpolation at the
+    // Chebyshev points of [0, 1/4], relative error 2^-24): the error is then 2^-21 of the score itself.
+    const float twice = p.cap_twice, c = p.cap_log2;
+    if constexpr (EXT & kWide) {
 #pragma unroll
-    for (int j = 0; j < 64; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
+      for (int j = 0; j < 64; ++j) {
+        const float t = s[j] * p.scale_log2, x = t * p.cap_inv, u = x * x;
+        const float far = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
+        const float near = t * fmaf(fmaf(fmaf(fmaf(0.0171313444f, u, -0.0529842388f), u, 0.133247505f), u, -0.333330679f), u, 1.0f);
+        s[j] = u < 0.25f ? near : far;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 64; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
+    }
   }
   if constexpr (EXT & kBias) {
     const float scale = EXT & kCap ? 1.0f : p.scale_log2;
@@ -852,6 +866,7 @@ const void* tma_of(int ext) {
     case 0: return reinterpret_cast<const void*>(&attn_tma<DT, DP, 0>);
     case kCap: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kCap>);
     case kBias: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kBias>);
+    case kCap | kBias | kWide: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kCap | kBias | kWide>);
     default: return reinterpret_cast<const void*>(&attn_tma<DT, DP, kCap | kBias>);
   }
 }
@@ -863,8 +878,8 @@ const void* tma_of(int dp, int ext) {
 
 }  // namespace
 
-const void* attn_tma_kernel(bool bf16, int padded_dim, bool cap, bool bias) {
-  const int ext = (cap ? kCap : 0) | (bias ? kBias : 0);
+const void* attn_tma_kernel(bool bf16, int padded_dim, float cap, bool bias) {
+  const int ext = cap > 64.0f ? kCap | kBias | kWide : (cap > 0.0f ? kCap : 0) | (bias ? kBias : 0);
   return bf16 ? tma_of<kBF16>(padded_dim, ext) : tma_of<kF16>(padded_dim, ext);
 }
 

@@ -95,8 +95,10 @@ struct AttnParams {
   int max_len;  // keys that a table row can name, at most 2^30
   const int32_t* cu_q;
   const int32_t* seq_lens;
-  float scale_log2;  // scale * log2(e); with a cap, scale / cap
+  float scale_log2;  // scale * log2(e)
   float cap_log2;    // cap * log2(e), 0: no cap
+  float cap_inv;     // 1 / cap_log2
+  float cap_twice;   // exponent (to the base 2) of e^2x, x = scale q.k / cap, a unit of q.k
   int causal, window;
   const float* slopes;
   const int32_t* prefix;
@@ -136,7 +138,7 @@ const void* attn_combine_kernel(bool bf16);
 // padded by 16 bytes.
 inline size_t attn_mma_smem(int padded_dim) { return (size_t)3 * 64 * (padded_dim + 8) * 2; }
 
-const void* attn_tma_kernel(bool bf16, int padded_dim, bool cap, bool bias);  // bias: also a scale that is not positive
+const void* attn_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  // cap 0: none; bias: also a scale that is not positive
 size_t attn_tma_smem(int padded_dim);
 int attn_tma_rows(int padded_dim);  // query rows of an item
 

@@ -401,8 +401,16 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.causal = a->causal != 0;
   p.window = a->window >= kMaxRows ? 0 : a->window;  // no length reaches it
   const double log2e = 1.4426950408889634;
-  p.cap_log2 = (float)(a->softcap * log2e);
-  p.scale_log2 = (float)(a->softcap > 0.0f ? (double)a->scale / a->softcap : a->scale * log2e);
+  // Factors that a type of 32 bits does not hold are cut to its largest (half of it for the cap, which is
+  // doubled), so that a product of 0 stays 0.
+  auto cut = [](double x, double most) { return (float)(x > most ? most : x < -most ? -most : x); };
+  constexpr double most = 3.4028234663852886e38;
+  p.scale_log2 = cut(a->scale * log2e, most);
+  if (a->softcap > 0.0f) {
+    p.cap_log2 = cut(a->softcap * log2e, most / 2);
+    p.cap_inv = cut(1.0 / (a->softcap * log2e), most);
+    p.cap_twice = cut(2.0 * log2e * a->scale / a->softcap, most);
+  }
   p.slopes = a->slopes;
   p.prefix = a->prefix_lens;
   auto eight = [](int64_t x) { return x % 8 == 0; };
@@ -439,8 +447,8 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.wide = d % 16 == 0 && a->out_token_stride % 16 == 0 && a->out_head_stride % 16 == 0 && aligned(a->out, 32) && aligned(base, 32);
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
-  const bool cap = a->softcap > 0.0f, bias = a->slopes || !(a->scale > 0.0f);
-  ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, cap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
+  const bool bias = a->slopes || !(a->scale > 0.0f);
+  ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
   // Blocks that may join the rows of one item: 4 where a request has few rows, else 16 (us with
@@ -470,8 +478,8 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
         keep(cudaFuncSetAttribute(rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rope_smem_most()));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int i = 0; i < 3; ++i)
-      for (int ext = 0; ext < 4; ++ext)
-        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, ext & 1, ext & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
+      for (int ext = 0; ext < 6; ++ext)  // no cap, a cap, a wide one
+        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, (float)(ext >> 1) * 50.0f, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
     for (int i = 0; i < 3; ++i) {
       const int dp = 64 << i;
       const void* f = attn_mma_kernel(b, dp);

@@ -85,3 +85,44 @@ def test_blocks_released_behind_the_window(ctx, form, page, prefix, causal):
         y["table"][r][edges[r]] = -1
         pa.run(ctx, y, **kw)
         assert ctx.device_status() == 2
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cap", [64.0, 65.0, 200.0, 1e3, 1e4, 1e6, 1e20, 1e30, 3e38, 1.0, 1e-3, 1e-30, 1e-38, 1e-42])
+def test_caps_of_any_size(ctx, form, cap, d):
+    """A cap costs a score no more than its own precision: with a wide one the call is the call without.
+    The bound is the one of serve_ref with the cap left out: a score's error is relative to min(sum |q k| scale, cap),
+    plus 2^-21 cap for caps of up to 64 (of the difference that gives the tanh; 2^-22 and its half again for log2 units)."""
+    import math
+    for peak in (1.0, 20.0):
+        x = pa.make([1, 40], [300, 700], 2, 1, d, seed=d, garbage=0.0, peak=peak)
+        scale, u = d ** -0.5, ref.half_step(torch.bfloat16)
+        out, lse = pa.run(ctx, x, scale=scale, softcap=cap)
+        assert ctx.device_status() == 0
+        for r, (lo, hi, length) in enumerate(((0, 1, 300), (1, 41, 700))):
+            blocks = torch.tensor(x["table"][r][: -(-length // 16)])
+            k, v = (c[blocks].flatten(0, 1)[:length, 0].double() for c in (x["kc"], x["vc"]))
+            pos, j = torch.arange(length - (hi - lo), length)[:, None], torch.arange(length)
+            for h in range(2):
+                q = x["q"][lo:hi, h].double()
+                s = cap * torch.tanh(q @ k.t() * scale / cap)
+                size = (q.abs() @ k.t().abs() * scale).clamp(max=2 * cap)
+                s = s.masked_fill(j > pos, -math.inf)
+                p = torch.softmax(s, -1)
+                ds = (2 * d + 16) * 2.0 ** -24 * size.amax(-1, keepdim=True) + (2.0 ** -21 * cap if cap <= 64 else 0.0)
+                rel = 4 * ds + 2.0 ** -20 + length * 2.0 ** -22
+                want = p @ v
+                eo = u * want.abs() + (1 + u) * (u + rel) * (p @ v.abs()) + ref.smallest(torch.bfloat16) * (1 + v.abs().sum(0))
+                wl = torch.logsumexp(s, -1)
+                el = 2 * ds[:, 0] + 2.0 ** -20 + length * 2.0 ** -22 + 2.0 ** -22 * wl.abs()
+                assert ((out[lo:hi, h].double() - want).abs() <= eo).all(), (cap, peak, ((out[lo:hi, h].double() - want).abs() - eo).max())
+                assert ((lse[lo:hi, h].double() - wl).abs() <= el).all(), (cap, peak, ((lse[lo:hi, h].double() - wl).abs() - el).max())
+
+
+@pytest.mark.parametrize("cap", [0.0, 5.0, 1e6])
+@pytest.mark.parametrize("scale", [1e38, -3e38, 1e-38])
+def test_scales_of_any_size(ctx, form, scale, cap):
+    """Products of 0 stay 0 whatever they are scaled by: equal weights."""
+    x = pa.make([3, 30], [50, 300], 2, 1, 64, seed=3, garbage=0.0)
+    x["q"].zero_()
+    pa.check(ctx, x, scale=scale, softcap=cap)
