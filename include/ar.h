@@ -282,6 +282,7 @@ enum { AR_PLAN_OK = 0, AR_PLAN_NO_BLOCKS = 1, AR_PLAN_TABLE_FULL = 2, AR_PLAN_TO
  *   seq_lens[r]  cached_lens[r] + new_lens[r]
  *   positions[t] place of token t in its request;  0 for t >= cu_q[requests]
  *   slots[t]     its cache slot;                  -1 for t >= cu_q[requests]
+ *                (-2, with code 2, where its block's number is negative: the cache write drops it)
  *   *free_count_out  the free blocks left (free_blocks itself is not changed)
  *   info[0..3]   tokens, blocks taken, refusal (AR_PLAN_*, the largest that applies), blocks needed
  *

@@ -145,6 +145,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan(const __grid_constant__ Pla
       const int block = j < have ? p.table[(int64_t)r * p.table_stride + j]
                                  : p.free_blocks[count - 1 - first_block[r] - (j - have)];
       slot = (int64_t)block * p.page + (pos - j * p.page);
+      if (block < 0) {  // no block: not a slot, and not the -1 of a row without a token
+        slot = -2;
+        *p.status = kStatusBadIndex;
+      }
     }
     p.slots[t] = slot;
     p.positions[t] = pos;

@@ -42,6 +42,7 @@ struct PlanParams {
   int32_t* positions;
   int32_t* free_count_out;
   int32_t* info;
+  int* status;
 };
 
 struct HeadRows {  // [tokens, heads, head_dim] with unit last stride

@@ -121,6 +121,7 @@ ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* a, void* stream) 
   p.positions = a->positions;
   p.free_count_out = a->free_count_out;
   p.info = a->info;
+  p.status = ctx->d_status;
   // a CTA for every 512 tokens, one an SM at most
   int64_t grid = (a->max_tokens + 511) / 512;
   if (grid > ctx->sm_count) grid = ctx->sm_count;

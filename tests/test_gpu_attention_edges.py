@@ -126,3 +126,33 @@ def test_scales_of_any_size(ctx, form, scale, cap):
     x = pa.make([3, 30], [50, 300], 2, 1, 64, seed=3, garbage=0.0)
     x["q"].zero_()
     pa.check(ctx, x, scale=scale, softcap=cap)
+
+
+@pytest.mark.parametrize("page", [1, 8])
+def test_negative_block_numbers_are_no_padding(ctx, page):
+    """A block number of -1 in the part of the table that is in use, or in the free list, times the page and with the
+    last place of a page, is the -1 of a row without a token: the plan says -2, and both calls leave code 2."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cached, new = [page - 1, 0, 2 * page - 1], [1, 2 * page, 1]
+    # the plan takes blocks off the end of the free list: request 0 needs one where the page is 1
+    table = i32([[-1, -9, -9], [-9, -9, -9], [0, 1, -9]])
+    free = i32([2, 3, -1, 4])
+    p = ctx.paged_plan(i32(cached), i32(new), free, i32([4]), table, page, max_tokens=sum(new) + 2)
+    assert ctx.device_status() == 2
+    if page == 1:  # taken: 4 (request 0), -1 and 3 (request 1), 2 (request 2)
+        want, bad = [4, -2, 3, 2], [1]
+    else:          # request 0 writes the last place of its block -1; request 1 takes 4 and -1
+        want, bad = [-2] + list(range(32, 40)) + [-2] * 8 + [15], [0] + list(range(9, 17))
+    assert p.slots.tolist() == want + [-1, -1]
+    n = len(want) + 2
+    g = nr.on_gpu(nr.make(n, 4, 2, 64, "bf16", 64, page=page))
+    kc = torch.full((8, page, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    ctx.qk_norm_rope(g["q"], g["k"], g["v"], p.positions, g["freq"], k_cache=kc, v_cache=vc, slots=p.slots)
+    assert ctx.device_status() == 2
+    flat = vc.flatten(0, 1)
+    for t, s in enumerate(want):
+        if t not in bad:
+            assert torch.equal(flat[s], g["v"][t])
+            flat[s] = 3.0
+    assert (flat == 3.0).all()
