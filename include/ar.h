@@ -262,7 +262,8 @@ ar_status ar_fused_reduce_rmsnorm_noalloc(const ar_fused_args* args, void* strea
  *
  * A paged cache is [num_blocks, page_size, kv_heads, head_dim] with unit stride in head_dim
  * and any strides (in elements) otherwise, so other orders of the first three dimensions are
- * the same call.  Slot s is token s % page_size of block s / page_size.
+ * the same call; the two caches may lie between each other in one tensor.  Slot s is token
+ * s % page_size of block s / page_size.
  * ------------------------------------------------------------------------------------- */
 
 #define AR_MAX_REQUESTS 8192

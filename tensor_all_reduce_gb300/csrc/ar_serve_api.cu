@@ -15,26 +15,40 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 
-// A strided array as the bytes it spans: `rows` rows of `span` bytes, `stride` bytes apart.
+// A strided array: runs of `run` bytes in up to three dimensions, `stride` bytes apart.
 struct Extent {
   const void* p;
-  int64_t span, stride, rows;
-  bool empty() const { return !p || span <= 0 || rows <= 0; }
-  int64_t bytes() const { return (rows - 1) * stride + span; }
+  int64_t run;
+  int64_t stride[3], count[3];
+  bool empty() const { return !p || run <= 0 || count[0] <= 0 || count[1] <= 0 || count[2] <= 0; }
+  // Bytes from the first to the last one of the dimensions that are not whole multiples of s apart (s 0: of all).
+  int64_t bytes(int64_t s = 0) const {
+    int64_t n = run;
+    for (int i = 0; i < 3; ++i)
+      if (count[i] > 1 && (s == 0 || stride[i] % s)) n += (count[i] - 1) * stride[i];
+    return n;
+  }
 };
 
-Extent flat(const void* p, int64_t bytes) { return {p, bytes, bytes, 1}; }
+Extent flat(const void* p, int64_t bytes) { return {p, bytes, {0, 0, 0}, {1, 1, 1}}; }
 
-// Whether two arrays share a byte.  Arrays of one row stride may lie side by side in each row
-// (q, k and v of a packed projection, k and v of one cache tensor).
+Extent table(const void* p, int64_t run, int64_t stride, int64_t rows) { return {p, run, {0, 0, stride}, {1, 1, rows}}; }
+
+// Whether two arrays share a byte.  They may lie between each other's runs (q, k and v of a packed projection,
+// side by side in a token or in a head; k and v of one cache tensor, side by side in a block, a token or a
+// head): that is so where, modulo one of the strides, the two keep to parts that do not meet.
 bool overlap(const Extent& a, const Extent& b) {
   if (a.empty() || b.empty()) return false;
   if (!overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
-  if (a.stride != b.stride || a.rows < 2 || b.rows < 2) return true;
-  const int64_t s = a.stride;
-  int64_t d = (int64_t)(addr(b.p) - addr(a.p)) % s;  // b's row start within a's row
-  if (d < 0) d += s;
-  return !(d >= a.span && d + b.span <= s);
+  for (int i = 0; i < 6; ++i) {
+    const Extent& e = i < 3 ? a : b;
+    const int64_t s = e.stride[i % 3];
+    if (e.count[i % 3] < 2 || s <= 0) continue;
+    int64_t d = (int64_t)(addr(b.p) - addr(a.p)) % s;  // b's start after a's
+    if (d < 0) d += s;
+    if (d >= a.bytes(s) && d + b.bytes(s) <= s) return false;
+  }
+  return true;
 }
 
 struct Operands {
@@ -63,8 +77,8 @@ bool strides_ok(int64_t outer, int64_t os, int64_t inner, int64_t is, int64_t di
   return true;
 }
 
-int64_t span3(int64_t b, int64_t bs, int64_t c, int64_t cs, int64_t d) {
-  return (b - 1) * bs + (c - 1) * cs + d;
+Extent cache_extent(const void* p, int64_t d, int64_t heads, int64_t hs, int64_t page, int64_t ps, int64_t blocks, int64_t bs) {
+  return {p, d * 2, {hs * 2, ps * 2, bs * 2}, {heads, page, blocks}};
 }
 
 }  // namespace
@@ -93,7 +107,7 @@ ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* a, void* stream) 
   c.read(flat(a->new_lens, r * 4));
   c.read(flat(a->free_blocks, a->free_capacity * 4));
   c.read(flat(a->free_count, 4));
-  c.write({a->block_table, a->table_cols * 4, ts * 4, r});
+  c.write(table(a->block_table, a->table_cols * 4, ts * 4, r));
   c.write(flat(a->cu_q, (r + 1) * 4));
   c.write(flat(a->seq_lens, r * 4));
   c.write(flat(a->slots, a->max_tokens * 8));
@@ -185,7 +199,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
 
   Operands c;
   int alias[4] = {0, 0, 0, 0};
-  auto heads = [&](const void* p, int64_t ts, int64_t h, int64_t hs) { return Extent{p, ((h - 1) * hs + d) * 2, ts * 2, n}; };
+  auto heads = [&](const void* p, int64_t ts, int64_t h, int64_t hs) { return Extent{p, d * 2, {hs * 2, 0, ts * 2}, {h, 1, n}}; };
   if (hq) c.read(heads(a->q, a->q_token_stride, hq, a->q_head_stride));
   const int qi = c.ni;
   if (hk) c.read(heads(a->k, a->k_token_stride, hk, a->k_head_stride));
@@ -195,7 +209,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   if (hk) c.read(flat(a->k_weight, d * 2));
   if (half) {
     const int64_t ps = a->position_stride ? a->position_stride : n;
-    c.read({a->positions, n * 4, ps * 4, a->axes});
+    c.read(table(a->positions, n * 4, ps * 4, a->axes));
     c.read(flat(a->inv_freq, half * 4));
   }
   if (cache) c.read(flat(a->slots, n * 8));
@@ -209,8 +223,8 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   }
   if (cache && a->num_blocks) {
     const int64_t pg = a->page_size;
-    c.write({a->k_cache, span3(pg, a->k_page_stride, hk, a->k_cache_head_stride, d) * 2, a->k_block_stride * 2, a->num_blocks});
-    c.write({a->v_cache, span3(pg, a->v_page_stride, hk, a->v_cache_head_stride, d) * 2, a->v_block_stride * 2, a->num_blocks});
+    c.write(cache_extent(a->k_cache, d, hk, a->k_cache_head_stride, pg, a->k_page_stride, a->num_blocks, a->k_block_stride));
+    c.write(cache_extent(a->v_cache, d, hk, a->v_cache_head_stride, pg, a->v_page_stride, a->num_blocks, a->v_block_stride));
   }
   if (!c.ok(alias)) return AR_ERR_OVERLAP;
   if (!ctx) return AR_ERR_NOT_INITIALIZED;
@@ -352,15 +366,15 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
     return AR_ERR_ALIGNMENT;
   const int64_t ts = a->table_stride ? a->table_stride : a->table_cols;
   Operands c;
-  c.read({a->q, ((hq - 1) * a->q_head_stride + d) * 2, a->q_token_stride * 2, n});
-  c.read({a->k_cache, span3(pg, a->k_page_stride, hk, a->k_head_stride, d) * 2, a->k_block_stride * 2, a->num_blocks});
-  c.read({a->v_cache, span3(pg, a->v_page_stride, hk, a->v_head_stride, d) * 2, a->v_block_stride * 2, a->num_blocks});
-  c.read({a->block_table, a->table_cols * 4, ts * 4, r});
+  c.read({a->q, d * 2, {a->q_head_stride * 2, 0, a->q_token_stride * 2}, {hq, 1, n}});
+  c.read(cache_extent(a->k_cache, d, hk, a->k_head_stride, pg, a->k_page_stride, a->num_blocks, a->k_block_stride));
+  c.read(cache_extent(a->v_cache, d, hk, a->v_head_stride, pg, a->v_page_stride, a->num_blocks, a->v_block_stride));
+  c.read(table(a->block_table, a->table_cols * 4, ts * 4, r));
   c.read(flat(a->cu_q, (r + 1) * 4));
   c.read(flat(a->seq_lens, r * 4));
   c.read(flat(a->slopes, hq * 4));
   c.read(flat(a->prefix_lens, r * 4));
-  c.write({a->out, ((hq - 1) * a->out_head_stride + d) * 2, a->out_token_stride * 2, n});
+  c.write({a->out, d * 2, {a->out_head_stride * 2, 0, a->out_token_stride * 2}, {hq, 1, n}});
   c.write(flat(a->lse, n * hq * 4));
   c.write(flat(a->workspace, (int64_t)a->workspace_bytes));
   if (!c.ok()) return AR_ERR_OVERLAP;

@@ -156,3 +156,44 @@ def test_negative_block_numbers_are_no_padding(ctx, page):
             assert torch.equal(flat[s], g["v"][t])
             flat[s] = 3.0
     assert (flat == 3.0).all()
+
+
+@pytest.mark.parametrize("order", ["block, token, which, head", "block, token, head, which", "block, head, token, which", "block, head, which, token"])
+def test_keys_and_values_of_one_cache_tensor(ctx, form, order):
+    """Both calls on a cache tensor whose keys and values lie between each other: as on two tensors."""
+    x = pa.make([5, 1, 70], [300, 129, 70], 4, 2, 64, seed=14, garbage=0.0)
+    blocks, page, hk, d = x["kc"].shape
+    size = dict(block=blocks, token=page, head=hk, which=2)
+    names = order.split(", ")
+    one = torch.zeros([size[n] for n in names] + [d], dtype=torch.bfloat16, device="cuda")
+    turned = one.permute(*[names.index(n) for n in ("which", "block", "token", "head")], 4)
+    kc, vc = turned[0], turned[1]
+    kc.copy_(x["kc"].cuda())
+    vc.copy_(x["vc"].cuda())
+    g = nr.on_gpu(nr.make(90, 4, 2, 64, "bf16", 64, page=page, seed=2))
+    used = {b for t, n in zip(x["table"], x["lens"]) for b in t[: -(-n // page)]}
+    slots = torch.full((90,), -1, dtype=torch.int64, device="cuda")
+    rest = torch.tensor([b for b in range(blocks) if b not in used][:3], device="cuda")
+    slots[: 3 * page] = (rest[:, None] * page + torch.arange(page, device="cuda")).flatten()
+    two = x["kc"].cuda(), x["vc"].cuda()
+    for k, v in ((kc, vc), two):
+        ctx.qk_norm_rope(g["q"], g["k"], g["v"], g["pos"][0], g["freq"], q_weight=g["wq"], k_weight=g["wk"], k_cache=k, v_cache=v, slots=slots)
+    assert torch.equal(kc, two[0]) and torch.equal(vc, two[1])
+    a = (pa.i32(x["table"]), pa.i32(x["cu"]), pa.i32(x["lens"]))
+    got, _ = ctx.paged_attention(x["q"].cuda(), kc, vc, *a)
+    want, _ = ctx.paged_attention(x["q"].cuda(), *two, *a)
+    assert torch.equal(got, want) and ctx.device_status() == 0
+
+
+@pytest.mark.parametrize("tokens", [1, 50, 900])
+def test_in_place_on_heads_of_three_parts(ctx, form, tokens):
+    """q, k and v side by side in each head of the projection, q and k in place."""
+    g = torch.Generator().manual_seed(tokens)
+    qkv = torch.randn(tokens, 8, 3, 80, generator=g).to(torch.float16).cuda()
+    y = nr.on_gpu(nr.make(tokens, 8, 8, 80, "fp16", 80, seed=1))
+    q, k, v = (qkv[:, :, i] for i in range(3))
+    args = dict(q_weight=y["wq"], k_weight=y["wk"], pairs=True)
+    want = ctx.qk_norm_rope(q.contiguous(), k.contiguous(), None, y["pos"][0], y["freq"], **args)
+    before = v.clone()
+    ctx.qk_norm_rope(q, k, v, y["pos"][0], y["freq"], q_out=q, k_out=k, **args)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, before)
