@@ -74,7 +74,8 @@ enum { AR_QUANT_NONE = 0, AR_QUANT_FP8_E4M3_PER_TOKEN = 1, AR_QUANT_FP8_E4M3_PER
 /*
  * Create a context for CUDA device `device` (flags: must be 0).  Queries the SM count,
  * L2 size and cluster limits once and prepares the kernels (function attributes), so that
- * later calls can be captured in a CUDA graph.  Counterpart of constructing the
+ * later calls can be captured in a CUDA graph.  Where the attention block's kernels cannot be prepared,
+ * its calls return AR_ERR_CUDA (ar_last_error says why) and the others work.  Counterpart of constructing the
  * communicator, CustomAllreduce(group, device, max_size) ([P3] bench_allreduce_tail.py
  * listing).  Returns AR_ERR_UNSUPPORTED on a device other than compute capability 10.3.
  * The calling thread's current device is left unchanged.

@@ -172,10 +172,10 @@ ar_status ar_init(ar_ctx** out, int device, unsigned flags) {
         return AR_ERR_CUDA;
       }
     }
-    if (ar::serve_prepare(ctx) != cudaSuccess) {
-      free(ctx);
-      return AR_ERR_CUDA;
-    }
+    // The attention block's kernels (17 ms of the first context of a process).  A failure stays with its
+    // calls: the others do not need them.
+    ctx->serve_error = ar::serve_prepare(ctx);
+    cudaGetLastError();
     if (cudaMalloc(&ctx->d_status, 256) != cudaSuccess || cudaMemset(ctx->d_status, 0, 256) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
       if (ctx->d_status) cudaFree(ctx->d_status);

@@ -116,6 +116,7 @@ ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* a, void* stream) 
   c.write(flat(a->info, 16));
   if (!c.ok()) return AR_ERR_OVERLAP;
   if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  if (ctx->serve_error) return fail_cuda(ctx, ctx->serve_error, "the attention block's kernels");
 
   ar::PlanParams p;
   p.requests = a->requests;
@@ -228,6 +229,7 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   }
   if (!c.ok(alias)) return AR_ERR_OVERLAP;
   if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  if (ctx->serve_error) return fail_cuda(ctx, ctx->serve_error, "the attention block's kernels");
 
   ar::RopeParams p;
   memset(&p, 0, sizeof(p));
@@ -332,6 +334,7 @@ ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_arg
   if (!a || !bytes || a->head_dim < 1 || a->head_dim > AR_MAX_HEAD_DIM || (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
     return AR_ERR_INVALID_ARG;
   if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  if (ctx->serve_error) return fail_cuda(ctx, ctx->serve_error, "the attention block's kernels");
   *bytes = (size_t)workspace_need(ctx, a->dtype == AR_DTYPE_BF16, a->head_dim);
   return AR_OK;
 }
@@ -379,6 +382,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   c.write(flat(a->workspace, (int64_t)a->workspace_bytes));
   if (!c.ok()) return AR_ERR_OVERLAP;
   if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  if (ctx->serve_error) return fail_cuda(ctx, ctx->serve_error, "the attention block's kernels");
   const bool bf16 = a->dtype == AR_DTYPE_BF16;
   if ((int64_t)a->workspace_bytes < workspace_need(ctx, bf16, a->head_dim)) return AR_ERR_INVALID_ARG;
 
@@ -503,9 +507,10 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
       if (ctx->attn_mma_per_sm[b][i] < 1) ctx->attn_mma_per_sm[b][i] = 1;
     }
   }
-  cudaDriverEntryPointQueryResult found;
-  keep(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ctx->encode_tensor_map, 12000, cudaEnableDefault, &found));
-  if (e == cudaSuccess && found != cudaDriverEntryPointSuccess) e = cudaErrorSymbolNotFound;
+  cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ctx->encode_tensor_map, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    ctx->encode_tensor_map = nullptr;
   return e;
 }
 
