@@ -156,6 +156,7 @@ def _packer(args):
 _pack_plan, _pack_rope, _pack_attention = map(_packer, (ArPagedPlanArgs, ArQkNormRopeArgs, ArPagedAttentionArgs))
 _NO_SECTIONS = (0,) * AR_MAX_ROPE_AXES
 _NO_CACHES = (0, 0, 0, 0, 0, 0, 0, 0, 0, 1)
+_KEPT_WORKSPACES = 8  # streams that a context keeps a workspace for
 
 
 class PagedPlan(NamedTuple):
@@ -789,7 +790,8 @@ class Context:
         head_dim ** -0.5.  Returns (out, lse); lse [tokens, q_heads] fp32 is None unless given or
         wanted.  Rows of no request are not written.  `workspace` is a uint8 tensor from
         paged_attention_workspace; calls that may run at the same time need one each.  Where it is not
-        given the context keeps one for each stream, and a captured call allocates its own."""
+        given the context keeps one (up to 40 MB) for each of the last eight streams that called, until
+        release_workspaces or close, and a captured call allocates its own."""
         t = _torch or _bind_torch()
         dev = self.device
         shape = q.shape
@@ -834,10 +836,18 @@ class Context:
         if _torch.capturing():
             return self._empty(size, _torch.u8, None)
         key = _torch.raw_stream(self.device)
-        kept = self._workspaces.get(key)
+        kept = self._workspaces.pop(key, None)
         if kept is None or kept.numel() < size:
-            kept = self._workspaces[key] = self._empty(size, _torch.u8, None)
+            kept = self._empty(size, _torch.u8, None)
+        self._workspaces[key] = kept  # the last used one stands last
+        if len(self._workspaces) > _KEPT_WORKSPACES:
+            # back to torch's allocator, which hands it out on its own stream only, behind the calls that use it
+            del self._workspaces[next(iter(self._workspaces))]
         return kept
+
+    def release_workspaces(self):
+        """Gives the workspaces kept for paged_attention back to torch's allocator."""
+        self._workspaces.clear()
 
     def _attention_workspace(self, head_dim: int, code: int) -> int:
         n = self._workspace_bytes.get((head_dim, code))

@@ -197,3 +197,27 @@ def test_in_place_on_heads_of_three_parts(ctx, form, tokens):
     before = v.clone()
     ctx.qk_norm_rope(q, k, v, y["pos"][0], y["freq"], q_out=q, k_out=k, **args)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, before)
+
+
+def test_workspaces_of_many_streams(ctx):
+    """Calls on more streams than workspaces are kept for, in turn and all at once: each result as alone, and the
+    memory held stays bounded."""
+    ctx.release_workspaces()
+    streams = [torch.cuda.Stream() for _ in range(12)]
+    xs = [pa.make([1, 30], [2000 + 100 * i, 500], 6, 2, 128, seed=50 + i, garbage=0.0) for i in range(12)]
+    args = [(x["q"].cuda(), x["kc"].cuda(), x["vc"].cuda(), pa.i32(x["table"]), pa.i32(x["cu"]), pa.i32(x["lens"])) for x in xs]
+    want = [ctx.paged_attention(*a)[0] for a in args]
+    torch.cuda.synchronize()
+    ctx.release_workspaces()
+    size = ctx.paged_attention_workspace(128, torch.bfloat16).numel()
+    assert size < 41e6
+    held = torch.cuda.memory_allocated()
+    outs = [torch.empty_like(w) for w in want]
+    for _ in range(10):
+        for s, a, out in zip(streams, args, outs):
+            ctx.paged_attention(*a, out=out, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert torch.cuda.memory_allocated() - held <= 8 * (size + (2 << 20)) + sum(w.numel() * 2 + 512 for w in want)
+    ctx.release_workspaces()
+    assert torch.cuda.memory_allocated() - held < size
