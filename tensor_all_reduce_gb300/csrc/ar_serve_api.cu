@@ -77,6 +77,9 @@ bool strides_ok(int64_t outer, int64_t os, int64_t inner, int64_t is, int64_t di
   return true;
 }
 
+// Steps of whole eights of elements (or other units); a single one has no step.
+bool eights(int64_t stride, int64_t count, int unit = 8) { return count < 2 || stride % unit == 0; }
+
 Extent cache_extent(const void* p, int64_t d, int64_t heads, int64_t hs, int64_t page, int64_t ps, int64_t blocks, int64_t bs) {
   return {p, d * 2, {hs * 2, ps * 2, bs * 2}, {heads, page, blocks}};
 }
@@ -267,14 +270,17 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   p.stall = ctx->test_stall;
   p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
   // the vector form: every row on a 16-byte boundary
-  auto row = [](const void* q, int64_t ts, int64_t hs) { return aligned(q, 16) && ts % 8 == 0 && hs % 8 == 0; };
+  auto row = [&](const void* q, int64_t ts, int64_t heads, int64_t hs) { return aligned(q, 16) && eights(ts, n) && eights(hs, heads); };
   bool vec = d % 8 == 0 && ctx->force_variant != 4;
-  if (hq) vec = vec && row(a->q, a->q_token_stride, a->q_head_stride) && row(a->q_out, a->q_out_token_stride, a->q_out_head_stride) && aligned(a->q_weight, 16);
-  if (hk) vec = vec && row(a->k, a->k_token_stride, a->k_head_stride) && aligned(a->k_weight, 16);
-  if (k_out) vec = vec && row(a->k_out, a->k_out_token_stride, a->k_out_head_stride);
+  if (hq)
+    vec = vec && row(a->q, a->q_token_stride, hq, a->q_head_stride) && row(a->q_out, a->q_out_token_stride, hq, a->q_out_head_stride) &&
+          aligned(a->q_weight, 16);
+  if (hk) vec = vec && row(a->k, a->k_token_stride, hk, a->k_head_stride) && aligned(a->k_weight, 16);
+  if (k_out) vec = vec && row(a->k_out, a->k_out_token_stride, hk, a->k_out_head_stride);
   if (cache)
-    vec = vec && row(a->v, a->v_token_stride, a->v_head_stride) && row(a->k_cache, a->k_page_stride, a->k_cache_head_stride) &&
-          row(a->v_cache, a->v_page_stride, a->v_cache_head_stride) && a->k_block_stride % 8 == 0 && a->v_block_stride % 8 == 0;
+    vec = vec && row(a->v, a->v_token_stride, hk, a->v_head_stride) && aligned(a->k_cache, 16) && aligned(a->v_cache, 16) &&
+          eights(a->k_block_stride, a->num_blocks) && eights(a->v_block_stride, a->num_blocks) && eights(a->k_page_stride, a->page_size) &&
+          eights(a->v_page_stride, a->page_size) && eights(a->k_cache_head_stride, hk) && eights(a->v_cache_head_stride, hk);
   const bool bf16 = a->dtype == AR_DTYPE_BF16;
   DeviceGuard g(ctx->device);
   ar_status st;
@@ -432,11 +438,10 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   }
   p.slopes = a->slopes;
   p.prefix = a->prefix_lens;
-  auto eight = [](int64_t x) { return x % 8 == 0; };
-  p.vec = eight(d) && eight(a->q_token_stride) && eight(a->q_head_stride) && eight(a->out_token_stride) && eight(a->out_head_stride) &&
-          eight(a->k_block_stride) && eight(a->k_page_stride) && eight(a->k_head_stride) && eight(a->v_block_stride) &&
-          eight(a->v_page_stride) && eight(a->v_head_stride) && aligned(a->q, 16) && aligned(a->out, 16) && aligned(a->k_cache, 16) &&
-          aligned(a->v_cache, 16) && ctx->force_variant != 4;
+  p.vec = d % 8 == 0 && eights(a->q_token_stride, n) && eights(a->q_head_stride, hq) && eights(a->out_token_stride, n) &&
+          eights(a->out_head_stride, hq) && eights(a->k_block_stride, a->num_blocks) && eights(a->k_page_stride, pg) && eights(a->k_head_stride, hk) &&
+          eights(a->v_block_stride, a->num_blocks) && eights(a->v_page_stride, pg) && eights(a->v_head_stride, hk) && aligned(a->q, 16) &&
+          aligned(a->out, 16) && aligned(a->k_cache, 16) && aligned(a->v_cache, 16) && ctx->force_variant != 4;
   p.status = ctx->d_status;
   p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
 
@@ -463,7 +468,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.headers = reinterpret_cast<int*>(base);
   p.part_ml = reinterpret_cast<float*>(base + w.ml);
   p.part_o = reinterpret_cast<float*>(base + w.o);
-  p.wide = d % 16 == 0 && a->out_token_stride % 16 == 0 && a->out_head_stride % 16 == 0 && aligned(a->out, 32) && aligned(base, 32);
+  p.wide = d % 16 == 0 && eights(a->out_token_stride, n, 16) && eights(a->out_head_stride, hq, 16) && aligned(a->out, 32) && aligned(base, 32);
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
   const bool bias = a->slopes || !(a->scale > 0.0f);

@@ -221,3 +221,26 @@ def test_workspaces_of_many_streams(ctx):
     assert torch.cuda.memory_allocated() - held <= 8 * (size + (2 << 20)) + sum(w.numel() * 2 + 512 for w in want)
     ctx.release_workspaces()
     assert torch.cuda.memory_allocated() - held < size
+
+
+@pytest.mark.parametrize("tokens, heads", [(1, 4), (5, 1), (1, 1)])
+def test_single_rows_with_odd_strides(ctx, tokens, heads):
+    """The stride of a dimension of one element says nothing: the aligned forms serve, with the bits of contiguous tensors."""
+    def odd(t):  # the tensor with a stride of 12345 in dimensions of one element
+        strides = [12345 if t.shape[i] == 1 else s for i, s in enumerate(t.stride())]
+        return torch.as_strided(t, t.shape, strides)
+    g = nr.on_gpu(nr.make(tokens, heads, heads, 64, "bf16", 64, seed=1))
+    q, k, v = (g[x].contiguous() for x in "qkv")
+    caches = [torch.zeros(1, 16, heads, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    slots = torch.arange(tokens, device="cuda") + 3
+    call = lambda f, kc, vc, qo: ctx.qk_norm_rope(f(q), f(k), f(v), g["pos"][0], g["freq"], q_weight=g["wq"], k_weight=g["wk"],  # noqa: E731
+                                                  k_cache=f(kc), v_cache=f(vc), slots=slots, q_out=f(qo))
+    want, kw = call(lambda t: t, *caches[:2], torch.empty_like(q))
+    got, kg = call(odd, *caches[2:], torch.empty_like(q))
+    assert ctx.last_variant == "qk_norm_rope_vec"
+    assert torch.equal(got, want) and torch.equal(kg, kw) and torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    a = (pa.i32([[0]]), pa.i32([0, tokens]), pa.i32([tokens + 3]))
+    want, wl = ctx.paged_attention(want, *caches[:2], *a, want_lse=True)
+    got, lse = ctx.paged_attention(odd(got), odd(caches[2]), odd(caches[3]), *a, want_lse=True, out=odd(torch.empty_like(got)))
+    assert ctx.last_variant == "paged_attention_tma"
+    assert torch.equal(got, want) and torch.equal(lse, wl) and ctx.device_status() == 0
