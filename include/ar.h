@@ -418,7 +418,8 @@ typedef struct {
   int64_t num_blocks;
   int page_size;                        /* 1..65536 */
   const int32_t* block_table;           /* device [requests, table_cols] */
-  int64_t table_cols, table_stride;     /* table_stride >= table_cols (0: table_cols) */
+  int64_t table_cols, table_stride;     /* table_stride >= table_cols (0: table_cols); kv_heads times the
+                                           keys that a row can name, cut to 2^30, at most 2^36 */
   const int32_t* cu_q;                  /* device [requests + 1], not decreasing */
   const int32_t* seq_lens;              /* device [requests] */
   float scale;                          /* finite */

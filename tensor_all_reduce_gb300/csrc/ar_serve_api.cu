@@ -357,6 +357,9 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
     return AR_ERR_INVALID_ARG;
   const int64_t n = a->tokens, d = a->head_dim, hq = a->q_heads, hk = a->kv_heads, r = a->requests, pg = a->page_size;
   if (n > kMaxRows || n * (hq / hk) > kMaxRows) return AR_ERR_UNSUPPORTED;
+  // the key tiles of one query tile and all heads are counted in 32 bits
+  const int64_t room = a->table_cols * pg < kMaxRows ? a->table_cols * pg : kMaxRows;
+  if (room * hk > (int64_t)1 << 36) return AR_ERR_UNSUPPORTED;
   if (n == 0 || r == 0) {
     if (!ctx) return AR_ERR_NOT_INITIALIZED;
     ctx->last_variant = "none";
@@ -419,8 +422,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.page = ar::fast_div((uint32_t)pg);
   p.table = a->block_table;
   p.table_stride = ts;
-  const int64_t room = a->table_cols * pg;
-  p.max_len = (int)(room < kMaxRows ? room : kMaxRows);
+  p.max_len = (int)room;
   p.cu_q = a->cu_q;
   p.seq_lens = a->seq_lens;
   p.causal = a->causal != 0;

@@ -83,3 +83,14 @@ def test_the_rule_never_passes_arrays_that_meet():
         b = {off + t * kt + x * ks + e for t in range(n) for x in range(g) for e in range(d)}
         assert not a & b, (n, h, g, d, hs, ks, ts, kt, off)
     assert taken > 300
+
+
+@pytest.mark.parametrize("want, heads, cols", [(NI, 64, 1 << 26), (tar.AR_ERR_UNSUPPORTED, 65, 1 << 26), (tar.AR_ERR_UNSUPPORTED, 65536, 1 << 20),
+                                               (NI, 65536, 1 << 16), (NI, 8, (1 << 31) - 1)])
+def test_tiles_that_32_bits_count(want, heads, cols):
+    """Tables that name more key tiles over all heads than the division of the work counts are refused."""
+    far = 1 << 44  # the other operands, away from so long a table and cache
+    kw = dict(q_heads=heads, kv_heads=heads, head_dim=8, tokens=4, requests=1, table_cols=cols, page_size=16, num_blocks=1,
+              q_token_stride=heads * 8, q_head_stride=8, out_token_stride=heads * 8, out_head_stride=8, k_block_stride=128 * heads, k_page_stride=8 * heads,
+              k_head_stride=8, v_block_stride=128 * heads, v_page_stride=8 * heads, v_head_stride=8, block_table=far, workspace=2 * far)
+    assert host.attention(**kw) == want
