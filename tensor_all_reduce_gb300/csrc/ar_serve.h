@@ -51,7 +51,6 @@ struct HeadRows {  // [tokens, heads, head_dim] with unit last stride
   int64_t in_ts, in_hs, out_ts, out_hs;
   const void* weight;  // NULL: no norm
   int heads;
-  FastDiv div;  // by heads
 };
 
 struct RopeParams {

@@ -238,8 +238,8 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
   memset(&p, 0, sizeof(p));
   p.tokens = n;
   p.head_dim = a->head_dim;
-  p.q = {a->q, hq ? a->q_out : nullptr, a->q_token_stride, a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride, a->q_weight, a->q_heads, ar::fast_div(hq ? (uint32_t)hq : 1)};
-  p.k = {a->k, k_out ? a->k_out : nullptr, a->k_token_stride, a->k_head_stride, a->k_out_token_stride, a->k_out_head_stride, a->k_weight, a->kv_heads, ar::fast_div(hk ? (uint32_t)hk : 1)};
+  p.q = {a->q, hq ? a->q_out : nullptr, a->q_token_stride, a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride, a->q_weight, a->q_heads};
+  p.k = {a->k, k_out ? a->k_out : nullptr, a->k_token_stride, a->k_head_stride, a->k_out_token_stride, a->k_out_head_stride, a->k_weight, a->kv_heads};
   p.v = a->v;
   p.v_ts = a->v_token_stride;
   p.v_hs = a->v_head_stride;
