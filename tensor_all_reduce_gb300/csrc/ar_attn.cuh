@@ -310,8 +310,8 @@ __device__ __forceinline__ bool visible(const Item& it, const RowView& v, int ke
 __device__ __forceinline__ float bend(const AttnParams& p, const RowView& v, float dot, int key) {
   float s = dot * p.scale_log2;
   if (p.cap_log2 > 0.0f) {
-    const float x = s * p.cap_inv;
-    if (!(fabsf(x) < 0x1p-13f)) s = p.cap_log2 * tanhf(x);  // below, tanh(x) is x to 2^-27, and x may be subnormal
+    const float x = s * p.cap_inv, bent = p.cap_log2 * tanhf(x);
+    s = fabsf(x) < 0x1p-13f ? s : bent;  // there tanh(x) is x to 2^-27, and x may be subnormal
   }
   if (p.slopes) s -= v.slope * (float)abs(v.pos - key);
   return s;
