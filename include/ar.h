@@ -325,7 +325,8 @@ ar_status ar_paged_plan(ar_ctx* ctx, const ar_paged_plan_args* args, void* strea
  *     a' = a cos theta - b sin theta,  b' = b cos theta + a sin theta
  *   pairs != 0: (y[2i], y[2i + 1]); else (y[i], y[i + rot_dim / 2]); y[rot_dim ..) stays
  *
- * theta is reduced exactly enough for any int32 position (64-bit fixed-point turns).  With
+ * theta is reduced modulo a turn in 64-bit fixed point: off by at most 2^-25 turns while
+ * |position * inv_freq| is below 2^28, by 2^-23 at any int32 position and one radian a position.  With
  * several position axes, sections[a] frequencies belong to axis a (their sum is rot_dim / 2):
  * one section after another, or, with `dealt`, dealt to the axes in turn, an axis dropping out
  * when its section is full.

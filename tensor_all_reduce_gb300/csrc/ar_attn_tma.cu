@@ -15,7 +15,7 @@
 // two halves, one half's softmax runs while the tensor core works on the other's products; with
 // one (few rows, wide heads) the two buffers hold its present and next tile, and the warpgroups
 // take tiles by turns, each with a maximum and a sum of its own, joined at the item's end (17
-// requests, one of them 700 tokens, window and cap: 56 us with one warpgroup, 53 us with both;
+// requests, two of them 700 tokens, window and cap: 56 us with one warpgroup, 53 us with both;
 // heads of more than 128 have no columns for a second sum).
 //
 // The running maximum that the weights refer to moves only when a row's maximum has grown by more
@@ -23,9 +23,9 @@
 // tensor memory is scaled.  Weights are thus at most 2^8, far inside both 16-bit ranges.
 //
 // Measured on GB300 with the joining kernel: 64 single tokens over up to 9000 keys (48 heads, 8 key
-// heads of 128, 1.4 GB) 219 us, 6.4 TB/s, where memory is the bound; 4096 tokens over 28000 (12 heads, 2
-// key heads of 128) 507 us, 1490 TFLOP/s, bound by shared memory, which feeds both operands of the
-// scores and the values, and by the exponentials; heads of 256 886 TFLOP/s, since 128 rows of an item
+// heads of 128, 1.4 GB) 213 to 220 us, 6.4 to 6.6 TB/s, where memory is the bound; 4096 tokens over 28000
+// (12 heads, 2 key heads of 128) 510 to 530 us, 1430 to 1480 TFLOP/s, bound by shared memory, which feeds both
+// operands of the scores and the values, and by the exponentials; heads of 256 928 TFLOP/s, since 128 rows of an item
 // leave twice the reads of keys and values a product; short prompts by an item's start and end.
 //
 // Every wait is bounded; one that runs out leaves code 1 in the status word, and all roles stop.
@@ -661,7 +661,9 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
           a = ex2(a);
           z = ex2(z);
           sum[j & 3] = add2(sum[j & 3], two(a, z));  // of the unrounded weights
-          w[j] = pack2<DT>(a, z);      // the second product's operand is 16-bit: half a step, relative, a weight
+          // the second product's operand is 16-bit: half a step, relative, a weight (outputs are 1.2 to 1.4
+          // times as far from the 64-bit ones as with weights of 32 bits, which would be two operands and two products)
+          w[j] = pack2<DT>(a, z);
         }
         tmem_st32(ts + part * 32, w);
         tmem_wait_st();

@@ -6,9 +6,9 @@
 // Angles: theta is needed modulo one turn only.  inv_freq / (2 pi) is held as a 64-bit
 // fixed-point fraction of a turn, and position * fraction wraps modulo 2^64 by itself, so one
 // integer product reduces exactly; the top 32 bits, as a signed fraction of a turn, go to
-// sincospi.  The fraction's error is below 2^-53 of its value (the binary64 product) plus
-// 2^-64, so at position 2^20 and one radian a position the angle is off by less than 2^-35 turns,
-// under the 2^-33 of the cut to 32 bits.
+// sincospi, which takes 24 of them: 2^-26 turns at most.  The fraction's error is below 2^-52 of
+// inv_freq / (2 pi) (the binary64 constant and the product) plus 2^-64, and the position multiplies it: 2^-34
+// turns at position 2^20 and one radian a position, as much as the cut at 2^29, 2^-23.6 at 2^31.
 #include "ar_common.cuh"
 #include "ar_fastdiv.cuh"
 #include "ar_serve.h"
@@ -154,9 +154,9 @@ enum RopeMode { kPairs = 0, kHalves8 = 1, kHalvesAny = 2 };
 // lanes fall into different banks).
 //
 // The bound is memory, with the arithmetic not far behind.  Measured on GB300 (CUDA graph, cold
-// inputs): 2800 tokens x 64 heads of 128, half rotated, 92 MB: 23.4 us, 3.9 TB/s with the launch;
+// inputs): 2800 tokens x 64 heads of 128, half rotated, 92 MB: 23.4 us, 3.9 TB/s with the launch (the general form 95 us);
 // the same without norm and rotation 18.3 us, without the stores too 13.0 us.  16384 tokens x 48
-// heads of 80, adjacent pairs, three axes, 252 MB: 57.0 us, 4.4 TB/s.  What it took to get there,
+// heads of 80, adjacent pairs, three axes, 252 MB: 57.0 us, 4.4 TB/s (the general form 600 us).  What it took to get there,
 // 2800 and 16384 tokens: rows loaded straight into registers 32 and 89 us; staged 25 and 78 us; two
 // chunks a lane instead of shuffles between partners 23 and 70 us; two floats an instruction and
 // sums unrolled for n = 5 and 6 24 and 62 us; units of up to 34 KB in two stages 23 and 57 us.
