@@ -14,7 +14,7 @@ own = False
 
 DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 E4M3 = torch.float8_e4m3fn
-LOW, HIGH = 2.0 ** -64, 2.0 ** 64  # the range of the scales
+LOW, HIGH = 2.0 ** -32, 2.0 ** 32  # the range of the scales
 
 
 def listed():
