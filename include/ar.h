@@ -438,6 +438,93 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* args, v
 /* Bytes of workspace that calls with this head_dim and dtype need (whatever their lengths). */
 ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_args* args, size_t* bytes);
 
+/* ---------------------------------------------------------------------------------------
+ * The same block over a paged cache held in 8 bits: half the bytes to keep and to read.
+ *
+ * The caches are E4M3 codes (one byte an element, strides in elements as above) with one fp32
+ * scale for each block and head: an element is its code times its block's scale.  Scales are
+ * [num_blocks, kv_heads] with any strides (in elements).
+ * ------------------------------------------------------------------------------------- */
+
+/*
+ * Append the requests' new tokens to an 8-bit cache: k with RMSNorm and rotation as in
+ * ar_qk_norm_rope (y below; fp32 inside), v as it is.  Request r owns rows cu_q[r] .. cu_q[r+1] of k
+ * and v, n of them, which become the tokens seq_lens[r] - n .. seq_lens[r] - 1 of its blocks (what
+ * ar_paged_plan gives); those below are in the cache already, the `held` ones of a block.
+ *
+ *   fresh = 2^e, the smallest power of two with |y| <= 448 * 2^e for the block's new tokens of a head,
+ *           between 2^-32 and 2^32
+ *   scale = fresh in a block without held tokens, else max(scale, fresh)
+ *   code  = e4m3(y / scale), rounded to nearest once, saturating; NaN and infinities give the NaN
+ *           code and do not count for the scale
+ *
+ * Where a scale grows, the held codes are rounded to it.  Powers of two make that exact but for
+ * codes that become subnormal, and cost an E4M3 value no precision.  A held block's scale that is no
+ * finite positive number counts as 2^-32.
+ *
+ * Not touched: blocks that get no token, places of a block behind its last token.  A request whose
+ * length is below n (or negative), tokens behind its table's columns, and tokens of a block outside the
+ * cache are dropped and leave code 2.  Two requests that add to one block in one call: what it then
+ * holds is not defined.
+ */
+typedef struct {
+  int64_t tokens;                       /* rows of k and v, >= 0 */
+  int requests;                         /* 0..AR_MAX_REQUESTS */
+  int kv_heads;                         /* >= 1 */
+  int head_dim;                         /* 1..AR_MAX_HEAD_DIM */
+  ar_dtype dtype;                       /* AR_DTYPE_BF16 or AR_DTYPE_F16: k, v and k_weight */
+  const void* k;                        /* device [tokens, kv_heads, head_dim], unit last stride */
+  const void* v;                        /* the same */
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  const void* k_weight;                 /* device [head_dim] or NULL: no norm of k */
+  float eps;                            /* finite, >= 0 */
+  int gemma;                            /* != 0: w' = 1 + w */
+  int rot_dim;                          /* 0 (no rotation) or even, at most head_dim */
+  int pairs;                            /* != 0: adjacent pairs, else halves */
+  int axes;                             /* 1..AR_MAX_ROPE_AXES (with rot_dim 0: ignored) */
+  int sections[AR_MAX_ROPE_AXES];       /* frequencies of each axis (axes = 1: ignored) */
+  int dealt;
+  const int32_t* positions;             /* device [axes, tokens], or NULL (axes = 1): each token's place in its request */
+  int64_t position_stride;              /* elements between the axes' rows (0: tokens) */
+  const float* inv_freq;                /* device fp32 [rot_dim / 2], radians a position */
+  void* k_cache;                        /* device E4M3 [num_blocks, page_size, kv_heads, head_dim], updated in place */
+  void* v_cache;
+  int64_t k_block_stride, k_page_stride, k_cache_head_stride;  /* elements between blocks, tokens of a block, heads */
+  int64_t v_block_stride, v_page_stride, v_cache_head_stride;
+  int64_t num_blocks;
+  int page_size;                        /* 1..65536 */
+  float* k_scale;                       /* device fp32 [num_blocks, kv_heads], updated in place */
+  float* v_scale;
+  int64_t k_scale_block_stride, k_scale_head_stride, v_scale_block_stride, v_scale_head_stride;
+  const int32_t* block_table;           /* device [requests, table_cols] */
+  int64_t table_cols, table_stride;     /* table_stride >= table_cols (0: table_cols) */
+  const int32_t* cu_q;                  /* device [requests + 1], not decreasing */
+  const int32_t* seq_lens;              /* device [requests] */
+} ar_paged_append_fp8_args;
+
+/* No output may overlap an input or another output (AR_ERR_OVERLAP); caches and scales may lie between each other. */
+ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* args, void* stream);
+
+/*
+ * ar_paged_attention over an 8-bit cache: k_j and v_j are codes times scales, everything else is that
+ * call's, its workspace (ar_paged_attention_workspace) too.  The scales need not be
+ * ar_paged_append_fp8's: any between 2^-32 and 2^32; others count as the nearer of the two, NaN as 2^-32.
+ * Scales of blocks that no row sees are not used; codes behind a request's length may be NaN.
+ *
+ * The products run on the 8-bit codes themselves.  q is split into E4M3 and E5M2 parts, exactly but for
+ * elements 2^-16 (bf16; fp16: 2^-14) below the row's largest, which keep an absolute error of 2^-25 of it; the weights
+ * likewise, rounded to 8 bits (bf16; fp16: 11), those 2^-23 below the row's largest product of weight and scale to
+ * nothing.  Sums are fp32.  (The general form rounds the weights to dtype instead.)
+ */
+typedef struct {
+  ar_paged_attention_args base;         /* k_cache and v_cache: E4M3 codes */
+  const float* k_scale;                 /* device fp32 [num_blocks, kv_heads] */
+  const float* v_scale;
+  int64_t k_scale_block_stride, k_scale_head_stride, v_scale_block_stride, v_scale_head_stride;  /* >= 0 */
+} ar_paged_attention_fp8_args;
+
+ar_status ar_paged_attention_fp8(ar_ctx* ctx, const ar_paged_attention_fp8_args* args, void* stream);
+
 /* Static description of a status code. */
 const char* ar_status_string(ar_status s);
 
@@ -450,7 +537,8 @@ const char* ar_last_error(const ar_ctx* ctx);
  * or norm), "reduce_rows", "fused_row_vec", "fused_cluster_vec", "fused_staged",
  * "fused_staged_cluster" (rows longer than 8192 elements split over a cluster of staged CTAs),
  * "fused_scalar", "fused_cluster_scalar", "fused_batch", "fused_batch_sequential", "paged_plan",
- * "qk_norm_rope_vec", "qk_norm_rope_scalar", "paged_attention_mma", "paged_attention_tma" or "none"
+ * "qk_norm_rope_vec", "qk_norm_rope_scalar", "paged_attention_mma", "paged_attention_tma",
+ * "paged_append_fp8_vec", "paged_append_fp8_scalar", "paged_attention_fp8_mma", "paged_attention_fp8_tma" or "none"
  * (empty call). */
 const char* ar_last_variant(const ar_ctx* ctx);
 

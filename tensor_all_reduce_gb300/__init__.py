@@ -8,7 +8,8 @@ as the C functions do; the ``Context`` methods (``reduce_sum``, ``fused_reduce_r
 ``fused_reduce_rmsnorm_batch``, ``fused_reduce_rmsnorm_host``) marshal torch tensors into
 those calls.  The attention block between two fused calls is ``ar_paged_plan``,
 ``ar_qk_norm_rope`` and ``ar_paged_attention`` (methods ``paged_plan``, ``qk_norm_rope``,
-``paged_attention``).  Every step of the computation runs in the library's CUDA kernels: there is no
+``paged_attention``), over a cache held in 8 bits ``ar_paged_append_fp8`` and
+``ar_paged_attention_fp8`` (``paged_append_fp8``, ``paged_attention_fp8``).  Every step of the computation runs in the library's CUDA kernels: there is no
 Python or PyTorch compute path, and using the package without a built ``libar.so`` raises.
 """
 from __future__ import annotations
@@ -145,15 +146,51 @@ class ArPagedAttentionArgs(ctypes.Structure):
     """)
 
 
+class ArPagedAppendFp8Args(ctypes.Structure):
+    _fields_ = _fields("""
+        l tokens
+        i requests kv_heads head_dim dtype
+        p k v
+        l k_token_stride k_head_stride v_token_stride v_head_stride
+        p k_weight
+        f eps
+        i gemma rot_dim pairs axes
+    """) + [("sections", ctypes.c_int * AR_MAX_ROPE_AXES)] + _fields("""
+        i dealt
+        p positions
+        l position_stride
+        p inv_freq k_cache v_cache
+        l k_block_stride k_page_stride k_cache_head_stride v_block_stride v_page_stride v_cache_head_stride num_blocks
+        i page_size
+        p k_scale v_scale
+        l k_scale_block_stride k_scale_head_stride v_scale_block_stride v_scale_head_stride
+        p block_table
+        l table_cols table_stride
+        p cu_q seq_lens
+    """)
+
+
+class ArPagedAttentionFp8Args(ctypes.Structure):
+    _fields_ = [("base", ArPagedAttentionArgs)] + _fields("""
+        p k_scale v_scale
+        l k_scale_block_stride k_scale_head_stride v_scale_block_stride v_scale_head_stride
+    """)
+
+
 def _packer(args):
     """pack(*values) of an argument structure's fields, as bytes that the C functions take for it
     (a third of the time of building the ctypes structure)."""
     codes = {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_size_t: "N", ctypes.c_void_p: "P",
              ctypes.c_int * AR_MAX_ROPE_AXES: f"{AR_MAX_ROPE_AXES}i"}
-    return struct.Struct("@" + "".join(codes[kind] for _, kind in args._fields_)).pack
+
+    def of(fields):
+        return "".join(codes[kind] if kind in codes else of(kind._fields_) for _, kind in fields)
+
+    return struct.Struct("@" + of(args._fields_)).pack
 
 
 _pack_plan, _pack_rope, _pack_attention = map(_packer, (ArPagedPlanArgs, ArQkNormRopeArgs, ArPagedAttentionArgs))
+_pack_append_fp8, _pack_attention_fp8 = map(_packer, (ArPagedAppendFp8Args, ArPagedAttentionFp8Args))
 _NO_SECTIONS = (0,) * AR_MAX_ROPE_AXES
 _NO_CACHES = (0, 0, 0, 0, 0, 0, 0, 0, 0, 1)
 _KEPT_WORKSPACES = 8  # streams that a context keeps a workspace for
@@ -213,12 +250,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ar_paged_attention.argtypes = [vp, ctypes.POINTER(ArPagedAttentionArgs), vp]
     lib.ar_paged_attention_workspace.argtypes = [vp, ctypes.POINTER(ArPagedAttentionArgs),
                                                  ctypes.POINTER(ctypes.c_size_t)]
+    lib.ar_paged_append_fp8.argtypes = [vp, ctypes.POINTER(ArPagedAppendFp8Args), vp]
+    lib.ar_paged_attention_fp8.argtypes = [vp, ctypes.POINTER(ArPagedAttentionFp8Args), vp]
     for f in ("ar_paged_plan", "ar_qk_norm_rope", "ar_paged_attention", "ar_paged_attention_workspace",
+              "ar_paged_append_fp8", "ar_paged_attention_fp8",
               "ar_init", "ar_destroy", "ar_reduce_sum", "ar_fused_reduce_rmsnorm", "ar_set_option",
               "ar_get_info", "ar_device_status", "ar_fused_reduce_rmsnorm_batch", "ar_fused_reduce_rmsnorm_host",
               "ar_fused_reduce_rmsnorm_noalloc"):
         getattr(lib, f).restype = c_int
-    for f in ("ar_paged_plan", "ar_qk_norm_rope", "ar_paged_attention"):
+    for f in ("ar_paged_plan", "ar_qk_norm_rope", "ar_paged_attention", "ar_paged_append_fp8", "ar_paged_attention_fp8"):
         _packed[f] = fn = lib[f]  # a function object of its own
         fn.argtypes, fn.restype = [vp, ctypes.c_char_p, vp], c_int
     _lib = lib
@@ -353,6 +393,22 @@ def ar_paged_attention(ctx: int, args: ArPagedAttentionArgs, stream: Optional[in
     return st
 
 
+def ar_paged_append_fp8(ctx: int, args: ArPagedAppendFp8Args, stream: Optional[int] = None,
+                        raise_on_error: bool = True) -> int:
+    st = (_lib or load_library()).ar_paged_append_fp8(ctx, ctypes.byref(args), stream)
+    if st != AR_OK and raise_on_error:
+        _check(ctx, st, "ar_paged_append_fp8")
+    return st
+
+
+def ar_paged_attention_fp8(ctx: int, args: ArPagedAttentionFp8Args, stream: Optional[int] = None,
+                           raise_on_error: bool = True) -> int:
+    st = (_lib or load_library()).ar_paged_attention_fp8(ctx, ctypes.byref(args), stream)
+    if st != AR_OK and raise_on_error:
+        _check(ctx, st, "ar_paged_attention_fp8")
+    return st
+
+
 def ar_paged_attention_workspace(ctx: int, args: ArPagedAttentionArgs) -> int:
     """Bytes of workspace for calls with the head size and element type of `args`."""
     n = ctypes.c_size_t()
@@ -435,6 +491,7 @@ class _Torch:
         import torch
         self.i32, self.i64, self.f32, self.u8 = torch.int32, torch.int64, torch.float32, torch.uint8
         self.codes = {torch.bfloat16: AR_DTYPE_BF16, torch.float16: AR_DTYPE_F16}
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
         self.empty, self.device, self.use_stream = torch.empty, torch.device, torch.cuda.stream
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.capturing = torch.cuda.is_current_stream_capturing
@@ -482,6 +539,24 @@ def _caches(k, v, heads, dim, dtype, device):
     if (one != 1 or one_v != 1) and dim > 1:
         raise ValueError("k_cache and v_cache must have unit stride in their last dimension")
     return k.data_ptr(), v.data_ptr(), kb, kp, kh, vb, vp, vh, shape[0], shape[1]
+
+
+def _caches_fp8(k, v, heads, dim, device):
+    """_caches of two caches of E4M3 codes (float8_e4m3fn or uint8)."""
+    if k.dtype not in _torch.e4m3 or v.dtype not in _torch.e4m3:
+        raise ValueError("k_cache and v_cache must be float8_e4m3fn (or uint8) tensors")
+    if k.dtype is not v.dtype:
+        k, v = k.view(_torch.u8), v.view(_torch.u8)
+    return _caches(k, v, heads, dim, k.dtype, device)
+
+
+def _scales(k, v, blocks, heads, device):
+    """(k address, v address, k's block and head strides, v's) of two [blocks, heads] fp32 tensors."""
+    shape = (blocks, heads)
+    for t in (k, v):
+        if t.shape != shape or t.dtype is not _torch.f32 or t.get_device() != device:
+            raise ValueError(f"k_scale and v_scale must be {list(shape)} float32 tensors on cuda:{device}")
+    return (k.data_ptr(), v.data_ptr(), *k.stride(), *v.stride())
 
 
 def _table(t, requests, device):
@@ -702,6 +777,38 @@ class Context:
         self._call("ar_paged_plan", args, stream)
         return PagedPlan(block_table, cu_q, seq_lens, slots, positions, free_count_out, info)
 
+    def _rotation(self, positions, inv_freq, sections, n, where):
+        """(frequencies, axes, sections, address and row stride of positions, address of inv_freq)."""
+        t, dev = _torch, self.device
+        half, axes, pos, pos_stride, freq = 0, 1, 0, 0, 0
+        sec = _NO_SECTIONS
+        if inv_freq is not None:
+            half = inv_freq.numel()
+            freq = _flat(inv_freq, t.f32, half, dev, "inv_freq")
+        if half and positions is not None:
+            shape = positions.shape
+            if positions.dtype is not t.i32 or positions.get_device() != dev or len(shape) not in (1, 2) or \
+                    shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
+                raise ValueError(f"positions must be a [{n}] or [axes, {n}] int32 tensor on cuda:{dev}, unit stride")
+            pos = positions.data_ptr()
+            if len(shape) == 2:
+                axes = shape[0]
+                if axes > 1:
+                    pos_stride = positions.stride(0)
+                    if axes > AR_MAX_ROPE_AXES:
+                        raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
+                    if sections is None or len(sections) != axes:
+                        raise ValueError("sections must name the frequencies of each position axis")
+                    if pos_stride:
+                        sec = (*sections, *_NO_SECTIONS[axes:])
+                    else:  # one row for all axes (an expanded view) is the rotation by one axis; the C call takes 0 for `tokens`
+                        if sum(sections) != half or min(sections) < 0:
+                            raise ArError(AR_ERR_INVALID_ARG, where, "sections must add up to the frequencies")
+                        axes = 1
+                elif axes < 1:
+                    raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
+        return half, axes, sec, pos, pos_stride, freq
+
     def qk_norm_rope(self, q, k, v, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
                      gemma: bool = False, pairs: bool = False, sections: Optional[Sequence[int]] = None,
                      dealt: bool = False, k_cache=None, v_cache=None, slots=None, q_out=None, k_out=None,
@@ -747,33 +854,7 @@ class Context:
             vp, vt, vh = _heads(v, shape, dt, dev, "v")
             caches = _caches(k_cache, v_cache, hk, d, dt, dev)
             slot = _flat(slots, t.i64, n, dev, "slots")
-        half, axes, pos, pos_stride, freq = 0, 1, 0, 0, 0
-        sec = _NO_SECTIONS
-        if inv_freq is not None:
-            half = inv_freq.numel()
-            freq = _flat(inv_freq, t.f32, half, dev, "inv_freq")
-        if half:
-            shape = positions.shape
-            if positions.dtype is not t.i32 or positions.get_device() != dev or len(shape) not in (1, 2) or \
-                    shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
-                raise ValueError(f"positions must be a [{n}] or [axes, {n}] int32 tensor on cuda:{dev}, unit stride")
-            pos = positions.data_ptr()
-            if len(shape) == 2:
-                axes = shape[0]
-                if axes > 1:
-                    pos_stride = positions.stride(0)
-                    if axes > AR_MAX_ROPE_AXES:
-                        raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
-                    if sections is None or len(sections) != axes:
-                        raise ValueError("sections must name the frequencies of each position axis")
-                    if pos_stride:
-                        sec = (*sections, *_NO_SECTIONS[axes:])
-                    else:  # one row for all axes (an expanded view) is the rotation by one axis; the C call takes 0 for `tokens`
-                        if sum(sections) != half or min(sections) < 0:
-                            raise ArError(AR_ERR_INVALID_ARG, "ar_qk_norm_rope", "sections must add up to the frequencies")
-                        axes = 1
-                elif axes < 1:
-                    raise ValueError(f"positions must have 1 to {AR_MAX_ROPE_AXES} axes")
+        half, axes, sec, pos, pos_stride, freq = self._rotation(positions, inv_freq, sections, n, "ar_qk_norm_rope")
         args = _pack_rope(
             n, hq, hk, d, code, qp, kp, vp, qt, qh, kt, kh, vt, vh, qop, kop, qot, qoh, kot, koh,
             0 if q_weight is None else _flat(q_weight, dt, d, dev, "q_weight"),
@@ -792,6 +873,20 @@ class Context:
         paged_attention_workspace; calls that may run at the same time need one each.  Where it is not
         given the context keeps one (up to 40 MB) for each of the last eight streams that called, until
         release_workspaces or close, and a captured call allocates its own."""
+        return self._attention(None, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, causal, window, softcap,
+                               slopes, prefix_lens, out, lse, want_lse, workspace, stream)
+
+    def paged_attention_fp8(self, q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, seq_lens,
+                            scale: Optional[float] = None, causal: bool = True, window: int = 0, softcap: float = 0.0,
+                            slopes=None, prefix_lens=None, out=None, lse=None, want_lse: bool = False, workspace=None,
+                            stream=None):
+        """paged_attention over a cache of E4M3 codes (float8_e4m3fn or uint8) with one fp32 scale a block
+        and head, k_scale and v_scale [blocks, kv_heads] (see ar_paged_attention_fp8)."""
+        return self._attention((k_scale, v_scale), q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, causal, window,
+                               softcap, slopes, prefix_lens, out, lse, want_lse, workspace, stream)
+
+    def _attention(self, scales, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, causal, window, softcap, slopes,
+                   prefix_lens, out, lse, want_lse, workspace, stream):
         t = _torch or _bind_torch()
         dev = self.device
         shape = q.shape
@@ -815,17 +910,51 @@ class Context:
             work, size = _flat(workspace, t.u8, None, dev, "workspace"), workspace.numel()
         qp, qt, qh = _heads(q, shape, dt, dev, "q")
         op, ot, oh = _heads(out, shape, dt, dev, "out")
-        kp, vp, kb, kt, kh, vb, vt, vh, blocks, page = _caches(k_cache, v_cache, hk, d, dt, dev)
+        kp, vp, kb, kt, kh, vb, vt, vh, blocks, page = \
+            _caches(k_cache, v_cache, hk, d, dt, dev) if scales is None else _caches_fp8(k_cache, v_cache, hk, d, dev)
         table, cols, stride = _table(block_table, r, dev)
-        args = _pack_attention(
+        args = (
             n, r, hq, hk, d, code, qp, op, qt, qh, ot, oh,
             0 if lse is None else _flat(lse, t.f32, n * hq, dev, "lse"), kp, vp, kb, kt, kh, vb, vt, vh, blocks, page,
             table, cols, stride, _flat(cu_q, t.i32, r + 1, dev, "cu_q"), _flat(seq_lens, t.i32, r, dev, "seq_lens"),
             d ** -0.5 if scale is None else scale, causal, window, softcap,
             0 if slopes is None else _flat(slopes, t.f32, hq, dev, "slopes"),
             0 if prefix_lens is None else _flat(prefix_lens, t.i32, r, dev, "prefix_lens"), work, size)
-        self._call("ar_paged_attention", args, stream)
+        if scales is None:
+            self._call("ar_paged_attention", _pack_attention(*args), stream)
+        else:
+            self._call("ar_paged_attention_fp8", _pack_attention_fp8(*args, *_scales(*scales, blocks, hk, dev)), stream)
         return out, lse
+
+    def paged_append_fp8(self, k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, seq_lens, positions=None,
+                         inv_freq=None, k_weight=None, eps: float = 1e-6, gemma: bool = False, pairs: bool = False,
+                         sections: Optional[Sequence[int]] = None, dealt: bool = False, stream=None) -> None:
+        """Appends the requests' new tokens k and v [tokens, kv_heads, head_dim] to a paged cache of E4M3 codes
+        (float8_e4m3fn or uint8) with one fp32 scale a block and head, k_scale and v_scale [blocks, kv_heads], all
+        updated in place (see ar_paged_append_fp8).  k gets RMSNorm (where k_weight is given) and the rotation of
+        qk_norm_rope (where inv_freq is given) on the way; positions default to each token's place in its
+        request.  q's norm and rotation are qk_norm_rope's, with k None."""
+        t = _torch or _bind_torch()
+        dev = self.device
+        n, hk, d = shape = k.shape
+        dt = k.dtype
+        code = t.codes.get(dt)
+        if code is None:
+            raise ValueError("k and v must be bfloat16 or float16")
+        r = seq_lens.numel()
+        kp, kt, kh = _heads(k, shape, dt, dev, "k")
+        vp, vt, vh = _heads(v, shape, dt, dev, "v")
+        caches = _caches_fp8(k_cache, v_cache, hk, d, dev)
+        if positions is None and sections is not None and len(sections) > 1:
+            raise ValueError("several position axes need positions")
+        half, axes, sec, pos, pos_stride, freq = self._rotation(positions, inv_freq, sections, n, "ar_paged_append_fp8")
+        table, cols, stride = _table(block_table, r, dev)
+        args = _pack_append_fp8(
+            n, r, hk, d, code, kp, vp, kt, kh, vt, vh, 0 if k_weight is None else _flat(k_weight, dt, d, dev, "k_weight"),
+            eps, gemma, 2 * half, pairs, axes, *sec, dealt, pos, pos_stride, freq, *caches,
+            *_scales(k_scale, v_scale, caches[8], hk, dev), table, cols, stride,
+            _flat(cu_q, t.i32, r + 1, dev, "cu_q"), _flat(seq_lens, t.i32, r, dev, "seq_lens"))
+        self._call("ar_paged_append_fp8", args, stream)
 
     def _own_workspace(self, size: int, stream):
         """`size` bytes for one call on `stream`: kept for the calls behind it on that stream, which
@@ -846,7 +975,7 @@ class Context:
         return kept
 
     def release_workspaces(self):
-        """Gives the workspaces kept for paged_attention back to torch's allocator."""
+        """Gives the workspaces kept for paged_attention and paged_attention_fp8 back to torch's allocator."""
         self._workspaces.clear()
 
     def _attention_workspace(self, head_dim: int, code: int) -> int:
@@ -857,6 +986,6 @@ class Context:
         return n
 
     def paged_attention_workspace(self, head_dim: int, dtype):
-        """A workspace for paged_attention calls with this head size and element type, of any lengths."""
+        """A workspace for paged_attention and paged_attention_fp8 calls with this head size and element type, of any lengths."""
         t = _bind_torch()
         return self._empty(self._attention_workspace(head_dim, t.codes[dtype]), t.u8, None)

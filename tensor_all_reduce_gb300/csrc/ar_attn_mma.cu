@@ -10,7 +10,10 @@
 // asynchronous.  With aligned rows and pages of 12 (of 1) tokens: 4096 tokens over 28000 (12 heads, 2 key
 // heads of 128) 6.0 (6.2) ms against 0.51 ms in pages of 64, 64 single tokens over up to 9000 keys (48
 // heads, 8 key heads) 1.05 (1.11) ms against 0.22 ms in pages of 16; element by element 8.8 and 1.26 ms.
+#include <type_traits>
+
 #include "ar_attn.cuh"
+#include "ar_e4m3.cuh"
 
 namespace ar {
 namespace {
@@ -66,7 +69,39 @@ __device__ __forceinline__ void fill_row(const AttnParams& p, uint16_t* dst, con
   }
 }
 
+// The same for a row of E4M3 codes, whose values both 16-bit types hold.
 template <int DT, int DP>
+__device__ __forceinline__ void fill_codes(const AttnParams& p, uint16_t* dst, const uint8_t* src, int part, int parts) {
+  for (int c = part; c < DP / 8; c += parts) {
+    const int e = c * 8;
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (src && e < p.head_dim) {
+      uint32_t codes[2] = {0, 0};
+      if (p.vec) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src + e);
+        codes[0] = v.x;
+        codes[1] = v.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e + i < p.head_dim) codes[i >> 2] |= (uint32_t)src[e + i] << (8 * (i & 3));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        from_e4m3x2(codes[i >> 1] >> (16 * (i & 1)), a, b);
+        w[i] = pack2<DT>(a, b);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// FP8: the cache holds E4M3 codes.  The codes are the products' operands, both 16-bit types hold them.  A
+// key's score takes its block's k scale; its v scale joins the weight, which is held relative to the largest
+// product of the two in the row, so that scales of any size neither overflow nor drown: with t = log2(vs),
+//   w_j = 2^(s_j + t_j - m),  o = sum w_j c_j,  l = sum w_j / vs_j,  out = o / l.
+template <int DT, int DP, bool FP8>
 __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ AttnParams p) {
   constexpr int LD = DP + 8;  // 16 bytes of padding: the eight rows of a matrix load fall into different banks
   extern __shared__ __align__(16) uint16_t smem[];
@@ -74,6 +109,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
   uint16_t* sk = sq + kRows * LD;
   uint16_t* sv = sk + kKeys * LD;
   __shared__ SpanShared span;
+  __shared__ float4 scales[FP8 ? kKeys : 1];  // of a key: k scale, log2 and reciprocal of the v scale
   pdl_wait_and_release();
   find_span<kRows, kKeys, kThreads>(p, span);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -106,17 +142,26 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
       __syncthreads();
       for (int r = threadIdx.x >> 2; r < kKeys; r += kThreads / 4) {
         const int key = key0 + r;
-        const uint16_t *k = nullptr, *v = nullptr;
+        using Elem = std::conditional_t<FP8, uint8_t, uint16_t>;
+        const Elem *k = nullptr, *v = nullptr;
+        float4 scale = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
         if (key < it.q.len) {
           int off;
           const int64_t b = block_of(p, it, key, off);
           if (b >= 0) {
-            k = static_cast<const uint16_t*>(p.k) + b * p.k_bs + off * p.k_ps + it.h * p.k_hs;
-            v = static_cast<const uint16_t*>(p.v) + b * p.v_bs + off * p.v_ps + it.h * p.v_hs;
+            k = static_cast<const Elem*>(p.k) + b * p.k_bs + off * p.k_ps + it.h * p.k_hs;
+            v = static_cast<const Elem*>(p.v) + b * p.v_bs + off * p.v_ps + it.h * p.v_hs;
+            if constexpr (FP8) scale = load_scales(p, b, it.h);
           }
         }
-        fill_row<DP>(p, sk + r * LD, k, threadIdx.x & 3, 4);
-        fill_row<DP>(p, sv + r * LD, v, threadIdx.x & 3, 4);
+        if constexpr (FP8) {
+          if ((threadIdx.x & 3) == 0) scales[r] = scale;
+          fill_codes<DT, DP>(p, sk + r * LD, k, threadIdx.x & 3, 4);
+          fill_codes<DT, DP>(p, sv + r * LD, v, threadIdx.x & 3, 4);
+        } else {
+          fill_row<DP>(p, sk + r * LD, k, threadIdx.x & 3, 4);
+          fill_row<DP>(p, sv + r * LD, v, threadIdx.x & 3, 4);
+        }
       }
       __syncthreads();
 
@@ -143,7 +188,12 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
         for (int e = 0; e < 4; ++e) {
           const int key = key0 + j * 8 + (lane & 3) * 2 + (e & 1);
           const RowView& w = view[e >> 1];
-          s[j][e] = visible(it, w, key) ? bend(p, w, s[j][e], key) : -INFINITY;
+          if constexpr (FP8) {
+            const float4 c = scales[j * 8 + (lane & 3) * 2 + (e & 1)];
+            s[j][e] = visible(it, w, key) ? bend(p, w, s[j][e] * c.x, key) + c.y : -INFINITY;
+          } else {
+            s[j][e] = visible(it, w, key) ? bend(p, w, s[j][e], key) : -INFINITY;
+          }
           top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
         }
       float base[2];
@@ -166,7 +216,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[j][e] = ex2(s[j][e] - base[e >> 1]);
-          l[e >> 1] += s[j][e];
+          if constexpr (FP8)
+            l[e >> 1] = fmaf(s[j][e], scales[j * 8 + (lane & 3) * 2 + (e & 1)].z, l[e >> 1]);
+          else
+            l[e >> 1] += s[j][e];
         }
       // weights rounded to the 16-bit type for the second product; their sum l is of the unrounded ones
 #pragma unroll
@@ -310,19 +363,22 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine(const __grid_consta
   }
 }
 
-template <int DT>
+template <int DT, bool FP8>
 const void* mma_of(int dp) {
   switch (dp) {
-    case 64: return reinterpret_cast<const void*>(&attn_mma<DT, 64>);
-    case 128: return reinterpret_cast<const void*>(&attn_mma<DT, 128>);
-    case 256: return reinterpret_cast<const void*>(&attn_mma<DT, 256>);
+    case 64: return reinterpret_cast<const void*>(&attn_mma<DT, 64, FP8>);
+    case 128: return reinterpret_cast<const void*>(&attn_mma<DT, 128, FP8>);
+    case 256: return reinterpret_cast<const void*>(&attn_mma<DT, 256, FP8>);
   }
   return nullptr;
 }
 
 }  // namespace
 
-const void* attn_mma_kernel(bool bf16, int padded_dim) { return bf16 ? mma_of<kBF16>(padded_dim) : mma_of<kF16>(padded_dim); }
+const void* attn_mma_kernel(bool bf16, int padded_dim, bool fp8) {
+  if (fp8) return bf16 ? mma_of<kBF16, true>(padded_dim) : mma_of<kF16, true>(padded_dim);
+  return bf16 ? mma_of<kBF16, false>(padded_dim) : mma_of<kF16, false>(padded_dim);
+}
 
 const void* attn_combine_kernel(bool bf16) {
   return bf16 ? reinterpret_cast<const void*>(&attn_combine<kBF16>) : reinterpret_cast<const void*>(&attn_combine<kF16>);

@@ -25,6 +25,7 @@ struct ar_ctx {
   int test_stall;        // test hook: make the staged kernel's first waits run out
   int prefetch;          // warm L2 with the first inputs before the grid-dependency wait
   int attn_mma_per_sm[2][3];  // resident CTAs of the general attention kernel: fp16/bf16, heads of 64/128/256
+  int attn8_mma_per_sm[2][3]; // the same over a cache in 8 bits
   void* encode_tensor_map;    // the driver's cuTensorMapEncodeTiled; NULL: the driver has none, the general form serves
   cudaError_t serve_error;    // why the attention block's kernels could not be prepared
   const char* last_variant;

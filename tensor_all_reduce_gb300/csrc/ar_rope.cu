@@ -9,6 +9,7 @@
 // sincospi, which takes 24 of them: 2^-26 turns at most.  The fraction's error is below 2^-52 of
 // inv_freq / (2 pi) (the binary64 constant and the product) plus 2^-64, and the position multiplies it: 2^-34
 // turns at position 2^20 and one radian a position, as much as the cut at 2^29, 2^-23.6 at 2^31.
+#include "ar_angle.cuh"
 #include "ar_common.cuh"
 #include "ar_fastdiv.cuh"
 #include "ar_serve.h"
@@ -26,49 +27,6 @@ constexpr int kRopeRowBytes = 16384;  // a unit of one token has no more heads t
 constexpr int kRopeSmem = 68 * 1024;  // all stages, so that three CTAs fit an SM; kRopeSkew less where halves meet in shared memory
 constexpr int kRopeSkew = kRopeWorkers * 18 * 4;
 constexpr int kRopeUnitCost = 4096;   // a unit costs as much as so many bytes besides its own
-
-// Fraction of a turn a position, in units of 2^-64 turns (modulo 1).
-__device__ __forceinline__ unsigned long long turn_of(float inv_freq) {
-  double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return (unsigned long long)(t * 18446744073709549568.0);  // t < 1; 2^64 less one ulp keeps it in range
-}
-
-__device__ __forceinline__ void angle(unsigned long long turn, int pos, float* s, float* c) {
-  const unsigned long long a = turn * (unsigned long long)(long long)pos;
-  const int top = (int)(unsigned)((a + 0x80000000ull) >> 32);  // [-0.5, 0.5) turns in units of 2^-32
-  sincospif((float)top * 0x1p-31f, s, c);                      // 2 pi turns = pi * (2 turns)
-}
-
-// The position axis of frequency i.
-__device__ __forceinline__ int axis_of(const RopeParams& p, int i) {
-  if (p.axes == 1) return 0;
-  if (!p.dealt) {
-    int a = 0;
-    for (int end = p.sections[0]; a < p.axes - 1 && i >= end;) end += p.sections[++a];
-    return a;
-  }
-  // round k deals one frequency to each axis whose section is longer than k; all rounds up to the
-  // end of the shortest section left at once
-  int left = i, done = 0;
-  for (int phase = 0; phase < p.axes; ++phase) {
-    int shortest = 0x7fffffff, open = 0;
-    for (int a = 0; a < p.axes; ++a)
-      if (p.sections[a] > done) {
-        ++open;
-        shortest = min(shortest, p.sections[a]);
-      }
-    if (open == 0) break;
-    if (left < (shortest - done) * open) {
-      int nth = left % open;
-      for (int a = 0; a < p.axes; ++a)
-        if (p.sections[a] > done && nth-- == 0) return a;
-    }
-    left -= (shortest - done) * open;
-    done = shortest;
-  }
-  return 0;
-}
 
 // Any alignment, stride and head size: one warp a head, its values as fp32 in shared memory.
 template <int DT>

@@ -77,6 +77,43 @@ struct RopeParams {
   long long wait_cycles;
 };
 
+// Scales of a cache of E4M3 codes, one a block and head.
+struct Scales {
+  float* p;
+  int64_t bs, hs;  // strides: block, head
+};
+
+// Scales outside this range count as its nearer end, NaN as the lower one.
+constexpr float kScaleLow = 0x1p-32f, kScaleHigh = 0x1p32f;
+
+struct AppendParams {
+  int64_t tokens;
+  int requests, heads, head_dim;
+  const void* k;
+  const void* v;
+  int64_t k_ts, k_hs, v_ts, v_hs;
+  const void* weight;  // of k; NULL: no norm
+  float eps, inv_dim;
+  int gemma, half, pairs, axes, dealt;  // half: frequencies, rot_dim / 2
+  FastDiv half_div;
+  int sections[AR_MAX_ROPE_AXES];
+  const int32_t* positions;  // NULL: the token's place in its request
+  int64_t pos_stride;
+  const float* inv_freq;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int64_t kc_bs, kc_ps, kc_hs, vc_bs, vc_ps, vc_hs;  // strides: block, token of a block, head
+  int64_t num_blocks;
+  FastDiv page;
+  Scales k_scale, v_scale;
+  const int32_t* table;
+  int64_t table_stride;
+  int max_len;  // tokens that a table row can name, at most 2^30
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  int* status;
+};
+
 struct AttnParams {
   int64_t tokens;
   int requests, q_heads, kv_heads, head_dim;
@@ -88,6 +125,7 @@ struct AttnParams {
   const void* k;
   const void* v;
   int64_t k_bs, k_ps, k_hs, v_bs, v_ps, v_hs;
+  Scales k_scale, v_scale;  // of a cache in 8 bits
   int64_t num_blocks;
   FastDiv page;
   const int32_t* table;
@@ -131,7 +169,8 @@ const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs);
 RopePlan rope_plan(const RopeParams& p, int sm_count);
 size_t rope_smem(const RopePlan& plan);
 size_t rope_smem_most();
-const void* attn_mma_kernel(bool bf16, int padded_dim);
+const void* append_scalar_kernel(bool bf16);
+const void* attn_mma_kernel(bool bf16, int padded_dim, bool fp8 = false);  // fp8: a cache in 8 bits
 const void* attn_combine_kernel(bool bf16);
 
 // Dynamic shared memory of the general attention kernel: 64 query rows, keys and values each,

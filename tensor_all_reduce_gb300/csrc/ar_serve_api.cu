@@ -80,8 +80,38 @@ bool strides_ok(int64_t outer, int64_t os, int64_t inner, int64_t is, int64_t di
 // Steps of whole eights of elements (or other units); a single one has no step.
 bool eights(int64_t stride, int64_t count, int unit = 8) { return count < 2 || stride % unit == 0; }
 
-Extent cache_extent(const void* p, int64_t d, int64_t heads, int64_t hs, int64_t page, int64_t ps, int64_t blocks, int64_t bs) {
-  return {p, d * 2, {hs * 2, ps * 2, bs * 2}, {heads, page, blocks}};
+// `es`: bytes of an element.
+Extent cache_extent(const void* p, int64_t d, int64_t heads, int64_t hs, int64_t page, int64_t ps, int64_t blocks, int64_t bs, int64_t es = 2) {
+  return {p, d * es, {hs * es, ps * es, bs * es}, {heads, page, blocks}};
+}
+
+Extent scale_extent(const void* p, int64_t heads, int64_t hs, int64_t blocks, int64_t bs) { return {p, 4, {hs * 4, 0, bs * 4}, {heads, 1, blocks}}; }
+
+constexpr int64_t kMostStride = (int64_t)1 << 40;
+
+bool scale_strides_ok(int64_t bs, int64_t hs) { return bs >= 0 && hs >= 0 && bs <= kMostStride && hs <= kMostStride; }
+
+// And that every block and head has a scale of its own.
+bool scale_strides_apart(int64_t blocks, int64_t bs, int64_t heads, int64_t hs) {
+  if (!scale_strides_ok(bs, hs)) return false;
+  if ((blocks > 1 && bs < 1) || (heads > 1 && hs < 1)) return false;
+  return blocks < 2 || heads < 2 || bs >= (heads - 1) * hs + 1 || hs >= (blocks - 1) * bs + 1;
+}
+
+bool rotation_ok(int rot_dim, int head_dim, int axes, const int* sections, int64_t position_stride, int64_t tokens) {
+  if (rot_dim < 0 || rot_dim > head_dim || (rot_dim & 1)) return false;
+  const int half = rot_dim / 2;
+  if (!half) return true;
+  if (axes < 1 || axes > AR_MAX_ROPE_AXES || position_stride < 0 || (position_stride && axes > 1 && position_stride < tokens) ||
+      position_stride > kMostStride)
+    return false;
+  if (axes == 1) return true;
+  int sum = 0;
+  for (int i = 0; i < axes; ++i) {
+    if (sections[i] < 0 || sections[i] > half) return false;
+    sum += sections[i];
+  }
+  return sum == half;
 }
 
 }  // namespace
@@ -159,21 +189,8 @@ ar_status ar_qk_norm_rope(ar_ctx* ctx, const ar_qk_norm_rope_args* a, void* stre
       (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
     return AR_ERR_INVALID_ARG;
   if (!(a->eps >= 0.0f) || isinf(a->eps)) return AR_ERR_INVALID_ARG;
-  if (a->rot_dim < 0 || a->rot_dim > a->head_dim || (a->rot_dim & 1)) return AR_ERR_INVALID_ARG;
+  if (!rotation_ok(a->rot_dim, a->head_dim, a->axes, a->sections, a->position_stride, a->tokens)) return AR_ERR_INVALID_ARG;
   const int half = a->rot_dim / 2;
-  if (half) {
-    if (a->axes < 1 || a->axes > AR_MAX_ROPE_AXES || a->position_stride < 0 ||
-        (a->position_stride && a->axes > 1 && a->position_stride < a->tokens) || a->position_stride > ((int64_t)1 << 40))
-      return AR_ERR_INVALID_ARG;
-    if (a->axes > 1) {
-      int sum = 0;
-      for (int i = 0; i < a->axes; ++i) {
-        if (a->sections[i] < 0 || a->sections[i] > half) return AR_ERR_INVALID_ARG;
-        sum += a->sections[i];
-      }
-      if (sum != half) return AR_ERR_INVALID_ARG;
-    }
-  }
   const int64_t n = a->tokens, d = a->head_dim, hq = a->q_heads, hk = a->kv_heads;
   if (cache && (!a->k_cache || !a->v_cache || !hk || a->num_blocks < 0 || a->page_size < 1 || a->page_size > 65536 ||
                 a->num_blocks > ((int64_t)1 << 40) / a->page_size))
@@ -320,8 +337,10 @@ Workspace workspace_of(int64_t spans, int64_t rows, int64_t part_dim) {
   return w;
 }
 
-int mma_spans(const ar_ctx* ctx, bool bf16, int dp) {
-  return ctx->sm_count * ctx->attn_mma_per_sm[bf16][dp == 64 ? 0 : dp == 128 ? 1 : 2];
+// At most as many over a cache in 8 bits, so that its workspace is the other's.
+int mma_spans(const ar_ctx* ctx, bool bf16, int dp, bool fp8 = false) {
+  const int i = dp == 64 ? 0 : dp == 128 ? 1 : 2, n = ctx->attn_mma_per_sm[bf16][i], n8 = ctx->attn8_mma_per_sm[bf16][i];
+  return ctx->sm_count * (fp8 && n8 < n ? n8 : n);
 }
 
 int part_dim(int d) { return (d + 3) / 4 * 4; }
@@ -345,8 +364,13 @@ ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_arg
   return AR_OK;
 }
 
-ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void* stream) {
-  if (!a) return AR_ERR_INVALID_ARG;
+}  // extern "C"
+
+namespace {
+
+// Both forms of the cache: scales = NULL for one of 16 bits, else that of the 8-bit call.
+ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_paged_attention_fp8_args* scales, void* stream) {
+  const int64_t es = scales ? 1 : 2;  // bytes of an element of the cache
   if (a->tokens < 0 || a->requests < 0 || a->requests > AR_MAX_REQUESTS || a->q_heads < 1 || a->kv_heads < 1 || a->q_heads % a->kv_heads ||
       a->q_heads > 65536 || a->head_dim < 1 || a->head_dim > AR_MAX_HEAD_DIM || (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
     return AR_ERR_INVALID_ARG;
@@ -368,19 +392,27 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   if (!a->q || !a->out || !a->cu_q || !a->seq_lens || (a->table_cols && !a->block_table) || (a->num_blocks && (!a->k_cache || !a->v_cache)) ||
       !a->workspace)
     return AR_ERR_INVALID_ARG;
+  if (scales && ((a->num_blocks && (!scales->k_scale || !scales->v_scale)) ||
+                 !scale_strides_ok(scales->k_scale_block_stride, scales->k_scale_head_stride) ||
+                 !scale_strides_ok(scales->v_scale_block_stride, scales->v_scale_head_stride)))
+    return AR_ERR_INVALID_ARG;
   if (!strides_ok(n, a->q_token_stride, hq, a->q_head_stride, d) || !strides_ok(n, a->out_token_stride, hq, a->out_head_stride, d) ||
       !strides_ok(a->num_blocks, a->k_block_stride, pg, a->k_page_stride, d) || !strides_ok(a->num_blocks, a->v_block_stride, pg, a->v_page_stride, d) ||
       !strides_ok(1, 0, hk, a->k_head_stride, d) || !strides_ok(1, 0, hk, a->v_head_stride, d))
     return AR_ERR_INVALID_ARG;
-  if (!aligned(a->q, 2) || !aligned(a->out, 2) || !aligned(a->lse, 4) || !aligned(a->k_cache, 2) || !aligned(a->v_cache, 2) ||
-      !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) || !aligned(a->seq_lens, 4) || !aligned(a->slopes, 4) ||
+  if (!aligned(a->q, 2) || !aligned(a->out, 2) || !aligned(a->lse, 4) || !aligned(a->k_cache, (int)es) || !aligned(a->v_cache, (int)es) ||
+      (scales && (!aligned(scales->k_scale, 4) || !aligned(scales->v_scale, 4))) || !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) || !aligned(a->seq_lens, 4) || !aligned(a->slopes, 4) ||
       !aligned(a->prefix_lens, 4) || !aligned(a->workspace, 16))
     return AR_ERR_ALIGNMENT;
   const int64_t ts = a->table_stride ? a->table_stride : a->table_cols;
   Operands c;
   c.read({a->q, d * 2, {a->q_head_stride * 2, 0, a->q_token_stride * 2}, {hq, 1, n}});
-  c.read(cache_extent(a->k_cache, d, hk, a->k_head_stride, pg, a->k_page_stride, a->num_blocks, a->k_block_stride));
-  c.read(cache_extent(a->v_cache, d, hk, a->v_head_stride, pg, a->v_page_stride, a->num_blocks, a->v_block_stride));
+  c.read(cache_extent(a->k_cache, d, hk, a->k_head_stride, pg, a->k_page_stride, a->num_blocks, a->k_block_stride, es));
+  c.read(cache_extent(a->v_cache, d, hk, a->v_head_stride, pg, a->v_page_stride, a->num_blocks, a->v_block_stride, es));
+  if (scales) {
+    c.read(scale_extent(scales->k_scale, hk, scales->k_scale_head_stride, a->num_blocks, scales->k_scale_block_stride));
+    c.read(scale_extent(scales->v_scale, hk, scales->v_scale_head_stride, a->num_blocks, scales->v_scale_block_stride));
+  }
   c.read(table(a->block_table, a->table_cols * 4, ts * 4, r));
   c.read(flat(a->cu_q, (r + 1) * 4));
   c.read(flat(a->seq_lens, r * 4));
@@ -418,6 +450,10 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   p.v_bs = a->v_block_stride;
   p.v_ps = a->v_page_stride;
   p.v_hs = a->v_head_stride;
+  if (scales) {
+    p.k_scale = {const_cast<float*>(scales->k_scale), scales->k_scale_block_stride, scales->k_scale_head_stride};
+    p.v_scale = {const_cast<float*>(scales->v_scale), scales->v_scale_block_stride, scales->v_scale_head_stride};
+  }
   p.num_blocks = a->num_blocks;
   p.page = ar::fast_div((uint32_t)pg);
   p.table = a->block_table;
@@ -440,10 +476,14 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   }
   p.slopes = a->slopes;
   p.prefix = a->prefix_lens;
+  // steps of a cache in whole units of elements, from a boundary of as many bytes
+  auto cache_steps = [&](int unit) {
+    return eights(a->k_block_stride, a->num_blocks, unit) && eights(a->k_page_stride, pg, unit) && eights(a->k_head_stride, hk, unit) &&
+           eights(a->v_block_stride, a->num_blocks, unit) && eights(a->v_page_stride, pg, unit) && eights(a->v_head_stride, hk, unit) &&
+           aligned(a->k_cache, unit * (int)es) && aligned(a->v_cache, unit * (int)es);
+  };
   p.vec = d % 8 == 0 && eights(a->q_token_stride, n) && eights(a->q_head_stride, hq) && eights(a->out_token_stride, n) &&
-          eights(a->out_head_stride, hq) && eights(a->k_block_stride, a->num_blocks) && eights(a->k_page_stride, pg) && eights(a->k_head_stride, hk) &&
-          eights(a->v_block_stride, a->num_blocks) && eights(a->v_page_stride, pg) && eights(a->v_head_stride, hk) && aligned(a->q, 16) &&
-          aligned(a->out, 16) && aligned(a->k_cache, 16) && aligned(a->v_cache, 16) && ctx->force_variant != 4;
+          eights(a->out_head_stride, hq) && cache_steps(8) && aligned(a->q, 16) && aligned(a->out, 16) && ctx->force_variant != 4;
   p.status = ctx->d_status;
   p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
 
@@ -452,7 +492,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   const int dp = padded_dim(a->head_dim);
   int box = 1;
   while (box < 128 && pg % (box * 2) == 0) box *= 2;
-  bool tma = p.vec && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
+  bool tma = !scales && p.vec && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
   CUtensorMap kmap, vmap;
   if (tma) {
     p.box_rows = box;
@@ -462,7 +502,7 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
           ar::attn_tensor_map(ctx->encode_tensor_map, &vmap, a->v_cache, bf16, d, pg, hk, a->num_blocks, a->v_page_stride, a->v_head_stride,
                               a->v_block_stride, box);
   }
-  p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp);
+  p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
   p.tile_rows = tma ? ar::attn_tma_rows(dp) : kMmaRows;
   p.part_dim = part_dim(a->head_dim);
   const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
@@ -475,13 +515,130 @@ ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void
   void* args[3] = {&p, &kmap, &vmap};
   const bool bias = a->slopes || !(a->scale > 0.0f);
   ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
-                     : launch(ctx, ar::attn_mma_kernel(bf16, dp), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
+                     : launch(ctx, ar::attn_mma_kernel(bf16, dp, scales), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
   // Blocks that may join the rows of one item: 4 where a request has few rows, else 16 (us with
   // 4, 8, 16, 32: one token 10.9, 11.0, 12.3, 15.0; 128 tokens over 3000: 54.5, 40.4, 32.7, 31.8).
   const unsigned joiners = n * (hq / hk) > 64 * r ? 16 : 4;
   st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, joiners), 256, 1, args, 0, stream);
-  if (st == AR_OK) ctx->last_variant = tma ? "paged_attention_tma" : "paged_attention_mma";
+  if (st == AR_OK)
+    ctx->last_variant = scales ? (tma ? "paged_attention_fp8_tma" : "paged_attention_fp8_mma") : tma ? "paged_attention_tma" : "paged_attention_mma";
+  return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status ar_paged_attention(ar_ctx* ctx, const ar_paged_attention_args* a, void* stream) {
+  return a ? attention(ctx, a, nullptr, stream) : AR_ERR_INVALID_ARG;
+}
+
+ar_status ar_paged_attention_fp8(ar_ctx* ctx, const ar_paged_attention_fp8_args* a, void* stream) {
+  return a ? attention(ctx, &a->base, a, stream) : AR_ERR_INVALID_ARG;
+}
+
+ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* a, void* stream) {
+  if (!a) return AR_ERR_INVALID_ARG;
+  if (a->tokens < 0 || a->tokens > kMaxRows || a->requests < 0 || a->requests > AR_MAX_REQUESTS || a->kv_heads < 1 || a->kv_heads > 65536 ||
+      a->head_dim < 1 || a->head_dim > AR_MAX_HEAD_DIM || (a->dtype != AR_DTYPE_BF16 && a->dtype != AR_DTYPE_F16))
+    return AR_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.0f) || isinf(a->eps)) return AR_ERR_INVALID_ARG;
+  if (!rotation_ok(a->rot_dim, a->head_dim, a->axes, a->sections, a->position_stride, a->tokens)) return AR_ERR_INVALID_ARG;
+  const int half = a->rot_dim / 2;
+  if (half && a->axes > 1 && !a->positions) return AR_ERR_INVALID_ARG;
+  if (a->page_size < 1 || a->page_size > 65536 || a->num_blocks < 0 || a->num_blocks > ((int64_t)1 << 40) / a->page_size || a->table_cols < 0 ||
+      a->table_cols > 0x7fffffff || a->table_stride < 0 || (a->table_stride && a->table_stride < a->table_cols) || a->table_stride > kMostStride)
+    return AR_ERR_INVALID_ARG;
+  const int64_t n = a->tokens, d = a->head_dim, hk = a->kv_heads, r = a->requests, pg = a->page_size, nb = a->num_blocks;
+  if (n == 0 || r == 0) {
+    if (!ctx) return AR_ERR_NOT_INITIALIZED;
+    ctx->last_variant = "none";
+    return AR_OK;
+  }
+  if (!a->k || !a->v || (half && !a->inv_freq) || !a->cu_q || !a->seq_lens || (a->table_cols && !a->block_table) ||
+      (nb && (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)))
+    return AR_ERR_INVALID_ARG;
+  if (!strides_ok(n, a->k_token_stride, hk, a->k_head_stride, d) || !strides_ok(n, a->v_token_stride, hk, a->v_head_stride, d) ||
+      !strides_ok(nb, a->k_block_stride, pg, a->k_page_stride, d) || !strides_ok(nb, a->v_block_stride, pg, a->v_page_stride, d) ||
+      !strides_ok(1, 0, hk, a->k_cache_head_stride, d) || !strides_ok(1, 0, hk, a->v_cache_head_stride, d) ||
+      !scale_strides_apart(nb, a->k_scale_block_stride, hk, a->k_scale_head_stride) ||
+      !scale_strides_apart(nb, a->v_scale_block_stride, hk, a->v_scale_head_stride))
+    return AR_ERR_INVALID_ARG;
+  if (!aligned(a->k, 2) || !aligned(a->v, 2) || !aligned(a->k_weight, 2) || (half && (!aligned(a->positions, 4) || !aligned(a->inv_freq, 4))) ||
+      !aligned(a->k_scale, 4) || !aligned(a->v_scale, 4) || !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) || !aligned(a->seq_lens, 4))
+    return AR_ERR_ALIGNMENT;
+  const int64_t ts = a->table_stride ? a->table_stride : a->table_cols, ps = a->position_stride ? a->position_stride : n;
+  Operands c;
+  c.read({a->k, d * 2, {a->k_head_stride * 2, 0, a->k_token_stride * 2}, {hk, 1, n}});
+  c.read({a->v, d * 2, {a->v_head_stride * 2, 0, a->v_token_stride * 2}, {hk, 1, n}});
+  c.read(flat(a->k_weight, d * 2));
+  if (half) {
+    c.read(table(a->positions, n * 4, ps * 4, a->axes));
+    c.read(flat(a->inv_freq, half * 4));
+  }
+  c.read(table(a->block_table, a->table_cols * 4, ts * 4, r));
+  c.read(flat(a->cu_q, (r + 1) * 4));
+  c.read(flat(a->seq_lens, r * 4));
+  c.write(cache_extent(a->k_cache, d, hk, a->k_cache_head_stride, pg, a->k_page_stride, nb, a->k_block_stride, 1));
+  c.write(cache_extent(a->v_cache, d, hk, a->v_cache_head_stride, pg, a->v_page_stride, nb, a->v_block_stride, 1));
+  c.write(scale_extent(a->k_scale, hk, a->k_scale_head_stride, nb, a->k_scale_block_stride));
+  c.write(scale_extent(a->v_scale, hk, a->v_scale_head_stride, nb, a->v_scale_block_stride));
+  if (!c.ok()) return AR_ERR_OVERLAP;
+  if (!ctx) return AR_ERR_NOT_INITIALIZED;
+  if (ctx->serve_error) return fail_cuda(ctx, ctx->serve_error, "the attention block's kernels");
+
+  ar::AppendParams p;
+  memset(&p, 0, sizeof(p));
+  p.tokens = n;
+  p.requests = a->requests;
+  p.heads = a->kv_heads;
+  p.head_dim = a->head_dim;
+  p.k = a->k;
+  p.v = a->v;
+  p.k_ts = a->k_token_stride;
+  p.k_hs = a->k_head_stride;
+  p.v_ts = a->v_token_stride;
+  p.v_hs = a->v_head_stride;
+  p.weight = a->k_weight;
+  p.eps = a->eps;
+  p.inv_dim = (float)(1.0 / (double)d);
+  p.gemma = a->gemma != 0;
+  p.half = half;
+  p.half_div = ar::fast_div(half ? (uint32_t)half : 1);
+  p.pairs = a->pairs != 0;
+  p.axes = half ? a->axes : 1;
+  p.dealt = a->dealt != 0;
+  for (int i = 0; i < AR_MAX_ROPE_AXES; ++i) p.sections[i] = i < p.axes ? a->sections[i] : 0;
+  p.positions = a->positions;
+  p.pos_stride = ps;
+  p.inv_freq = a->inv_freq;
+  p.k_cache = static_cast<uint8_t*>(a->k_cache);
+  p.v_cache = static_cast<uint8_t*>(a->v_cache);
+  p.kc_bs = a->k_block_stride;
+  p.kc_ps = a->k_page_stride;
+  p.kc_hs = a->k_cache_head_stride;
+  p.vc_bs = a->v_block_stride;
+  p.vc_ps = a->v_page_stride;
+  p.vc_hs = a->v_cache_head_stride;
+  p.num_blocks = nb;
+  p.page = ar::fast_div((uint32_t)pg);
+  p.k_scale = {a->k_scale, a->k_scale_block_stride, a->k_scale_head_stride};
+  p.v_scale = {a->v_scale, a->v_scale_block_stride, a->v_scale_head_stride};
+  p.table = a->block_table;
+  p.table_stride = ts;
+  p.max_len = (int)(a->table_cols * pg < kMaxRows ? a->table_cols * pg : kMaxRows);
+  p.cu_q = a->cu_q;
+  p.seq_lens = a->seq_lens;
+  p.status = ctx->d_status;
+  const bool bf16 = a->dtype == AR_DTYPE_BF16;
+  DeviceGuard g(ctx->device);
+  // blocks that can get tokens: a request's first and last one, and whole ones between
+  int64_t grid = n / pg + 2 * r < n ? n / pg + 2 * r : n;
+  if (grid > ctx->sm_count * 8) grid = ctx->sm_count * 8;
+  void* args[1] = {&p};
+  const ar_status st = launch(ctx, ar::append_scalar_kernel(bf16), (unsigned)grid, 128, 1, args, 0, stream);
+  if (st == AR_OK) ctx->last_variant = "paged_append_fp8_scalar";
   return st;
 }
 
@@ -506,13 +663,16 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
     for (int i = 0; i < 3; ++i)
       for (int ext = 0; ext < 6; ++ext)  // no cap, a cap, a wide one
         keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, (float)(ext >> 1) * 50.0f, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
-    for (int i = 0; i < 3; ++i) {
-      const int dp = 64 << i;
-      const void* f = attn_mma_kernel(b, dp);
-      keep(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_mma_smem(dp)));
-      keep(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctx->attn_mma_per_sm[b][i], f, 128, attn_mma_smem(dp)));
-      if (ctx->attn_mma_per_sm[b][i] < 1) ctx->attn_mma_per_sm[b][i] = 1;
-    }
+    keep(cudaFuncGetAttributes(&fa, append_scalar_kernel(b)));
+    for (int fp8 = 0; fp8 < 2; ++fp8)
+      for (int i = 0; i < 3; ++i) {
+        const int dp = 64 << i;
+        const void* f = attn_mma_kernel(b, dp, fp8);
+        int& per_sm = fp8 ? ctx->attn8_mma_per_sm[b][i] : ctx->attn_mma_per_sm[b][i];
+        keep(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_mma_smem(dp)));
+        keep(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f, 128, attn_mma_smem(dp)));
+        if (per_sm < 1) per_sm = 1;
+      }
   }
   cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ctx->encode_tensor_map, 12000, cudaEnableDefault, &found) != cudaSuccess ||
