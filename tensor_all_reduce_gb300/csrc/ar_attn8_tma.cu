@@ -1,0 +1,868 @@
+// Paged attention over a cache of E4M3 codes on the fifth-generation tensor cores: rows on 16-byte boundaries,
+// heads of a multiple of 16, pages of a multiple of 8 tokens.
+//
+// The division of the work, the roles of the warps and the tensor memory are those of the kernel for 16-bit
+// caches.  What differs is that the codes are never turned into 16 bits: the 8-bit matrix instructions run at
+// twice the 16-bit rate, so each 16-bit operand of theirs is given as a sum of parts of 8 bits, and two
+// products of parts cost what one of 16 bits does, with half the bytes of keys and values to bring and to hold.
+//
+//   x = hi + lo    bf16 (8 bits): hi = e4m3(x), lo = e5m2(x - hi);  fp16 (11 bits): hi + e4m3(x - hi) + e5m2(rest)
+//
+// E4M3 keeps 4 bits, E5M2 3 and reaches down to 2^-16.  A row of q is scaled by a power of two, so that its
+// largest element lies between 224 and 448: the parts are then exact but for what is 2^-17 of one unit.  A row's
+// weights take their keys' v scale, so that one reference serves both: with t_j = log2(vs_j),
+//   w_j = 2^(s_j + t_j - m),  o = sum w_j c_j,  l = sum w_j / vs_j,  out = o / l,  lse = m + log2(l)
+// and m kept so that the largest w of a row lies between 2^6 and 2^8: parts of a w are off by half a step
+// of 8 (11) bits, or by 2^-17, 2^-23 of the largest.
+//
+// A block's scales are the same for eight keys in a row at least; a warp of its own looks them up, tiles ahead, and
+// leaves the k scale, t and 1 / vs of each eight keys of a tile in a ring in shared memory.
+#include <cuda.h>
+
+#include "ar_attn.cuh"
+#include "ar_attn_tc.cuh"
+#include "ar_e4m3.cuh"
+#include "ar_staged.cuh"
+#include "ar_two.cuh"
+
+namespace ar {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kScaleWarp = 11;  // kLoadWarp + 1: values
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // of 168 a thread at launch
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168, "the split uses what the launch has");
+constexpr int kScaleTiles = 8;            // tiles of the ring of scales
+constexpr int kScaleGroups = kKeys / 8;   // entries of a tile
+
+template <int DT, int DP>
+struct Shape {
+  static constexpr int kRows = DP == 256 ? 128 : 256;   // rows of an item
+  static constexpr bool kTurns = DP == 128;             // the warpgroups take an item of one half by turns, tile by tile
+  static constexpr int kParts = DT == kBF16 ? 2 : 3;    // of a 16-bit operand
+  static constexpr int kUnits = DP / 128;               // ring slots that a tile of keys or values takes
+  static constexpr int kUnitBytes = kKeys * 128;        // 128 rows of 128 codes
+  static constexpr int kPartBytes = kUnits * kUnitBytes;   // one part of a half's queries
+  static constexpr int kHalfBytes = kParts * kPartBytes;
+  static constexpr int kQueryBytes = kRows / 128 * kHalfBytes;
+  static constexpr int kSlots = kParts == 2 ? 9 : 7;
+  static constexpr int kBytes = kQueryBytes + kSlots * kUnitBytes;
+};
+
+// As in the kernel for 16-bit caches, and the ring of scales.
+struct Bars {
+  uint64_t full[9], empty[9];
+  uint64_t q[2];
+  uint64_t s[4];
+  uint64_t p[4], p2[4];
+  uint64_t o[4];
+  uint64_t join[2];
+  uint64_t sc_full[kScaleTiles], sc_empty[kScaleTiles];  // released by 8 warps, or twice by each of 4
+  uint64_t drain;
+  uint32_t issued[9];
+  uint32_t tmem;
+  int stop;
+};
+
+// ---- parts of 8 bits ----------------------------------------------------------
+
+// Four floats -> four codes (E4M3 or E5M2), round to nearest even, saturating.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  if constexpr (E5M2)
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e5m2x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  else
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// What four E4M3 codes leave of four floats: exact, the codes being their roundings.
+__device__ __forceinline__ void minus_codes4(uint32_t codes, float& a, float& b, float& c, float& d) {
+  asm("{\n\t.reg .b16 x, y, lo, hi, one;\n\t.reg .b32 f, g;\n\tmov.b32 {x, y}, %4;\n\tmov.b16 one, 0xbc00;\n\t"
+      "cvt.rn.f16x2.e4m3x2 f, x;\n\tcvt.rn.f16x2.e4m3x2 g, y;\n\t"
+      "mov.b32 {lo, hi}, f;\n\tfma.rn.f32.f16 %0, lo, one, %0;\n\tfma.rn.f32.f16 %1, hi, one, %1;\n\t"
+      "mov.b32 {lo, hi}, g;\n\tfma.rn.f32.f16 %2, lo, one, %2;\n\tfma.rn.f32.f16 %3, hi, one, %3;\n\t}"
+      : "+f"(a), "+f"(b), "+f"(c), "+f"(d)
+      : "r"(codes));
+}
+
+template <int PARTS>
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&part)[PARTS]) {
+#pragma unroll
+  for (int i = 0; i < PARTS - 1; ++i) {
+    part[i] = codes4<false>(a, b, c, d);
+    minus_codes4(part[i], a, b, c, d);
+  }
+  part[PARTS - 1] = codes4<true>(a, b, c, d);
+}
+
+// ---- tcgen05, 8-bit operands ----------------------------------------------------
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Instruction descriptor: A in E4M3 or E5M2, B in E4M3, fp32 accumulator, 128 rows, n columns.
+__device__ __forceinline__ uint32_t instr_desc(int n, bool a_e5m2, bool b_rows_along_k) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_rows_along_k ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_count(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// ---- roles --------------------------------------------------------------------
+
+// Every role walks the CTA's items for itself and counts barrier phases the same way (n, items, pairs, d, g as in
+// the kernel for 16-bit caches; tiles: all so far, for the ring of scales).
+
+template <class S>
+__device__ __forceinline__ bool single_half(const Item& it) {
+  return S::kRows == 128 || it.rows - it.qt * S::kRows <= 128;
+}
+
+template <class S>
+__device__ void load_role(const AttnParams& p, bool keys, const CUtensorMap* map, const SpanShared& span, Bars& b, uint32_t ring) {
+  const int lane = threadIdx.x & 31;
+  const int boxes = kKeys / p.box_rows;
+  const bool one = elect_one();
+  Walk<S::kRows, kKeys> walk;
+  walk.start(span);
+  Item it = {};
+  uint32_t n = 0;
+  bool ok = true;
+  while (ok && walk.next(p, it)) {
+    const int nt = it.end - it.begin;
+    const bool ahead = single_half<S>(it);  // scores run a tile ahead
+    int block = 0, place = 0;               // block of this lane's box, and its place in the block
+    auto look_up = [&](int t) {
+      const int key = it.range.tile(it.begin + t) * kKeys + lane * p.box_rows;
+      block = -1;
+      place = 0;
+      if (lane < boxes && key < it.q.len) {
+        const int j = key / p.page;
+        place = key - j * (int)p.page.d;
+        block = p.table[(int64_t)it.r * p.table_stride + j];
+      }
+    };
+    look_up(0);
+    for (int t = 0; ok && t < nt; ++t) {
+      // ring units of the item: keys 0, then (values t, keys t + 1), or (keys t + 1, values t) where scores run ahead
+      uint32_t i;
+      if (keys)
+        i = t == 0 ? 0 : (ahead ? 2 * t - 1 : 2 * t);
+      else
+        i = ahead && t + 1 < nt ? 2 * t + 2 : 2 * t + 1;
+      i = n + i * S::kUnits;
+      // outside the cache: the copy fills with zeros
+      const int w = (unsigned)block < (unsigned)p.num_blocks ? block : (int)p.num_blocks, y = place;
+      if (t + 1 < nt) look_up(t + 1);
+      for (int u = 0; u < S::kUnits; ++u, ++i) {
+        const uint32_t slot = i % S::kSlots, round = i / S::kSlots;
+        ok = __all_sync(0xffffffffu, ok && wait_for(&b.empty[slot], (round & 1) ^ 1, b, p));
+        if (!ok) break;
+        if (one) {
+          mbar_arrive_expect_tx(&b.full[slot], S::kUnitBytes);
+          b.issued[slot] = round + 1;
+        }
+        const uint32_t dst = ring + slot * S::kUnitBytes;
+        for (int x = 0; x < boxes; ++x) {
+          const int wx = __shfl_sync(0xffffffffu, w, x), yx = __shfl_sync(0xffffffffu, y, x);
+          if (one && !(p.stall && i == 0)) tma_4d(dst + x * p.box_rows * 128, map, u * 128, yx, it.h, wx, &b.full[slot]);
+        }
+      }
+    }
+    n += 2 * nt * S::kUnits;
+  }
+}
+
+// The scales of two tiles at a time, a lane eight keys: the next blocks are looked up while the scales arrive.
+template <class S>
+__device__ void scale_role(const AttnParams& p, const SpanShared& span, Bars& b, float4 (*ring)[kScaleGroups]) {
+  const int lane = threadIdx.x & 31, second = lane >> 4, group = lane & 15;
+  Walk<S::kRows, kKeys> walk;
+  walk.start(span);
+  Item it = {};
+  uint32_t tiles = 0;
+  bool ok = true;
+  while (ok && walk.next(p, it)) {
+    const int nt = it.end - it.begin;
+    auto block_at = [&](int t) {  // -1: none, or outside the cache, which reads as zeros
+      int block = -1;
+      if (t + second < nt) {
+        const int key = it.range.tile(it.begin + t + second) * kKeys + group * 8;
+        if (key < it.q.len) block = p.table[(int64_t)it.r * p.table_stride + key / p.page];
+      }
+      return (unsigned)block < (unsigned)p.num_blocks ? block : -1;
+    };
+    int block = block_at(0);
+    for (int t = 0; ok && t < nt; t += 2) {
+      float4 v = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+      if (block >= 0) v = load_scales(p, block, it.h);
+      block = block_at(t + 2);
+      const uint32_t c = tiles + t, c1 = c + 1;
+      const bool two = t + 1 < nt;
+      ok = wait_for(&b.sc_empty[c % kScaleTiles], ((c / kScaleTiles) & 1) ^ 1, b, p) &&
+           (!two || wait_for(&b.sc_empty[c1 % kScaleTiles], ((c1 / kScaleTiles) & 1) ^ 1, b, p));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (t + second < nt) ring[(c + second) % kScaleTiles][group] = v;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&b.sc_full[c % kScaleTiles]);
+        if (two) mbar_arrive(&b.sc_full[c1 % kScaleTiles]);
+      }
+    }
+    tiles += nt;
+  }
+}
+
+template <class S>
+__device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, uint32_t queries, uint32_t ring, uint32_t tmem) {
+  const int lane = threadIdx.x & 31;
+  const int ksteps = (p.head_dim + 31) / 32;
+  const uint32_t idesc_s = instr_desc(kKeys, false, false), idesc_last = instr_desc(kKeys, true, false);
+  // descriptors differ in the address alone, in units of 16 bytes: constant offsets are added
+  const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(ring, 16), v_desc = matrix_desc(ring, S::kUnitBytes);
+  const bool one = elect_one();
+  Walk<S::kRows, kKeys> walk;
+  walk.start(span);
+  Item it = {};
+  uint32_t n = 0, items = 0, pairs = 0, d = 0, g = 0;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
+    fence_after();
+    return ok;
+  };
+  auto wait_unit = [&](uint32_t i) { return wait(&b.full[i % S::kSlots], (i / S::kSlots) & 1); };
+  // queries of half h, part by part, times the keys of unit i (column part u of the head) into score buffer `buf`
+  auto scores = [&](int buf, int h, uint32_t i, int u) {
+    const uint64_t k = k_desc + (i % S::kSlots) * (S::kUnitBytes / 16);
+#pragma unroll
+    for (int x = 0; x < S::kParts; ++x) {
+      const uint64_t a = q_desc + (h * S::kHalfBytes + x * S::kPartBytes + u * S::kUnitBytes) / 16;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (u * 4 + s < ksteps) mma_ss(tmem + buf * 128, a + s * 2, k + s * 2, x == S::kParts - 1 ? idesc_last : idesc_s, u > 0 || x > 0 || s > 0);
+    }
+  };
+  // half `part` of the tile's weights in score buffer `buf` times the values of unit i, to columns `to`
+  auto weighted = [&](int buf, uint32_t i, int u, int part, uint32_t to, bool more) {
+    const uint64_t v = v_desc + (i % S::kSlots) * (S::kUnitBytes / 16);
+    const int cols = p.head_dim - u * 128;
+    if (cols <= 0) return;
+    const uint32_t idesc_o = instr_desc(cols < 128 ? cols : 128, false, true), last_o = instr_desc(cols < 128 ? cols : 128, true, true);
+#pragma unroll
+    for (int x = 0; x < S::kParts; ++x)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        mma_ts(tmem + to + u * 128, tmem + buf * 128 + part * S::kParts * 16 + x * 16 + s * 8, v + (((part * 2 + s) * 32 * 128) >> 4),
+               x == S::kParts - 1 ? last_o : idesc_o, more || part > 0 || x > 0 || s > 0);
+  };
+  // Values behind the request's end: whole boxes came as zeros, the rest of the last box holds
+  // whatever the cache does.  Zeroed, because a weight of 0 does not cancel a NaN.
+  auto clear_tail = [&](int t, uint32_t i) {
+    const int left = it.q.len - it.range.tile(it.begin + t) * kKeys;
+    if (left >= kKeys) return;
+    const int lo = max(left, 0), hi = min((lo + p.box_rows - 1) / p.box_rows * p.box_rows, kKeys);
+    const uint32_t v = ring + (i % S::kSlots) * S::kUnitBytes;
+    for (int x = lo * 8 + lane; x < hi * 8; x += 32) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + x * 16), "r"(0) : "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  while (ok && walk.next(p, it)) {
+    const int nt = it.end - it.begin;
+    if (single_half<S>(it)) {
+      if (!wait(&b.q[0], items & 1)) break;
+      for (int i = -1; ok && i < nt; ++i) {
+        if (i + 1 < nt) {
+          const uint32_t x = (g + i + 1) & 1;
+          for (int u = 0; u < S::kUnits; ++u, ++n) {
+            if (!wait_unit(n)) break;
+            if (one) {
+              scores(x, 0, n, u);
+              mma_commit(&b.empty[n % S::kSlots]);
+            }
+          }
+          if (!ok) break;
+          if (one) mma_commit(&b.s[2 + x]);
+        }
+        if (i < 0) continue;
+        const uint32_t x = (g + i) & 1, phase = ((g + i) >> 1) & 1, sum_at = 256 + (S::kTurns ? x * 128 : 0);
+        for (int u = 0; u < S::kUnits; ++u, ++n) {
+          if (!wait_unit(n)) break;
+          clear_tail(i, n);
+          if (u == 0 && !wait(&b.p[2 + x], phase)) break;
+          if (one) weighted(x, n, u, 0, sum_at, S::kTurns ? i > 1 : i > 0);
+          if (u == 0 && !wait(&b.p2[2 + x], phase)) break;
+          if (one) {
+            weighted(x, n, u, 1, sum_at, true);
+            mma_commit(&b.empty[n % S::kSlots]);
+          }
+        }
+        if (!ok) break;
+        if (one) mma_commit(&b.o[2 + x]);
+      }
+      g += nt;
+    } else {
+      if (!wait_unit(n)) break;
+      for (int h = 0; ok && h < 2; ++h) {
+        if (!wait(&b.q[h], (h ? pairs : items) & 1)) break;
+        if (one) {
+          scores(h, h, n, 0);
+          mma_commit(&b.s[h]);
+        }
+      }
+      if (!ok) break;
+      if (one) mma_commit(&b.empty[n % S::kSlots]);
+      ++n;
+      for (int i = 0; ok && i < nt; ++i, ++d) {
+        const bool more = i + 1 < nt;
+        if (!wait_unit(n)) break;
+        clear_tail(i, n);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&b.p[h], d & 1)) break;
+          if (one) weighted(h, n, 0, 0, 256 + h * 128, i > 0);
+          if (!wait(&b.p2[h], d & 1)) break;
+          if (one) {
+            weighted(h, n, 0, 1, 256 + h * 128, true);
+            if (h == 1) mma_commit(&b.empty[n % S::kSlots]);
+          }
+          if (more) {
+            if (h == 0 && !wait_unit(n + 1)) break;
+            if (one) {
+              scores(h, h, n + 1, 0);
+              mma_commit(&b.s[h]);
+            }
+          } else if (one) {
+            mma_commit(&b.o[h]);
+          }
+        }
+        if (!ok) break;
+        if (one && more) mma_commit(&b.empty[(n + 1) % S::kSlots]);
+        n += more ? 2 : 1;
+      }
+      ++pairs;
+    }
+    ++items;
+  }
+  if (!ok) {  // matrix instructions in flight end before tensor memory is freed
+    if (one) mma_commit(&b.drain);
+    mbar_wait_bounded(&b.drain, 0, p.wait_cycles);
+  }
+}
+
+template <class S>
+struct SoftmaxState {  // of a warp
+  Walk<S::kRows, kKeys> walk;
+  Item it, later;
+};
+
+// Shared by the softmax warps: what a row of q was divided by, of an item and the next (whose queries may come
+// before the other warpgroup has looked); maxima and sums to join.
+struct RowShared {
+  float factor[2][256];
+  float2 ml[256];
+};
+
+template <int DT, int DP, int EXT>
+__device__ void softmax_role(const AttnParams& p, const SpanShared& span, SoftmaxState<Shape<DT, DP>>& state, Bars& b, RowShared& rs,
+                             const float4 (*scale_ring)[kScaleGroups], uint32_t queries, uint32_t tmem) {
+  using S = Shape<DT, DP>;
+  const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+  // A thread's scores take most of its registers: what is the same for a warp stays in shared
+  // memory.  Lane 0 alone steps the walk (a step reads and writes it), between two barriers of the warp.
+  auto& walk = state.walk;
+  Item &it = state.it, &later = state.later;
+  if (lane == 0) walk.start(span);
+  uint32_t pairs = 0, d = 0, g = 0, joined = 0, tiles = 0, items = 0;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
+    fence_after();
+    return ok;
+  };
+  auto arrive = [&](uint64_t* bar) {  // a warp's stores are done
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    __syncwarp();  // tensor memory is read and written by whole warps
+  };
+  auto next_item = [&](Item& to) {  // the next one that this warpgroup has a part in
+    __syncwarp();
+    bool found = false;
+    if (lane == 0) found = (S::kTurns || h == 0) && walk.next(p, to);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, found, 0) != 0;
+  };
+  // Queries: a warp loads, scales and splits the rows that its own lanes serve, 16 bytes a lane.  The first rows
+  // are asked for while the last product of the item before still runs.  Columns beyond the head are zero.  Rows
+  // beyond the item's keep what was there: they meet no other row, and nothing of them is stored.
+  constexpr int kRowLanes = DP / 8, kStep = 32 / kRowLanes;  // lanes of a row, rows of a round of loads
+  constexpr int kAhead = 4;                                  // rounds in flight
+  const int col = (lane % kRowLanes) * 8, sub = lane / kRowLanes;
+  uint4 raw[kAhead];
+  bool loading = false;
+  auto warp_rows = [&](const Item& it) { return min(it.rows - (it.qt * S::kRows + h * 128 + warp * 32), 32); };
+  auto fetch = [&](const Item& it, int r0) {
+    const int base = it.qt * S::kRows + h * 128 + warp * 32, rows = warp_rows(it);
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)it.q.q0 * p.q_ts + (int64_t)it.h * (int)p.group.d * p.q_hs;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = r0 + k * kStep + sub;
+      raw[k] = make_uint4(0, 0, 0, 0);
+      if (r < rows && col < p.head_dim) {
+        const int t = (base + r) / p.group, e = base + r - t * (int)p.group.d;
+        raw[k] = ld_keep(q + t * p.q_ts + e * p.q_hs + col);
+      }
+    }
+  };
+  auto load_queries = [&](const Item& it) {
+    if (h == 1 && single_half<S>(it)) return;
+    loading = true;
+    fetch(it, 0);
+  };
+  auto queries_loaded = [&](const Item& it, uint32_t item) {
+    if (!loading) return;
+    loading = false;
+    const int rows = warp_rows(it);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kAhead * kStep) {
+      if (r0) fetch(it, r0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * kStep + sub;
+        float f[8];
+        unpack8<DT>(raw[k], f);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_magnitude(f[i]));
+#pragma unroll
+        for (int o = kRowLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^(e - 127): the power of two that brings the largest element to 224 .. 448
+        const int e = max((int)((__float_as_uint(top) + 0x1fffffu) >> 23) - 8, 1);
+        const float inv = __uint_as_float((unsigned)(254 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = for_code(f[i], inv);
+        uint32_t lo[S::kParts], hi[S::kParts];
+        split4(f[0], f[1], f[2], f[3], lo);
+        split4(f[4], f[5], f[6], f[7], hi);
+        if (r < rows) {
+          const int row = warp * 32 + r;
+          const uint32_t dst = queries + h * S::kHalfBytes + (col >> 7) * S::kUnitBytes + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4) + (col & 8);
+#pragma unroll
+          for (int x = 0; x < S::kParts; ++x) sts_v2(dst + x * S::kPartBytes, lo[x], hi[x]);
+          if (col == 0) rs.factor[item & 1][h * 128 + row] = __uint_as_float((unsigned)e << 23);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.q[h]);
+  };
+  bool goes_on = false;
+  bool have = next_item(it);
+  if (have) load_queries(it);
+  queries_loaded(it, items);
+  while (have) {
+    const int nt = it.end - it.begin;
+    const bool one = single_half<S>(it);
+    const bool turns = S::kTurns && one;
+    const uint32_t to = lanes + 256 + (one && !S::kTurns ? 0 : h * 128);
+    const int half_row = (one ? 0 : h * 128) + tid, row = it.qt * S::kRows + half_row;
+    const bool busy = row - lane < it.rows;  // the warp has a row
+    RowView view = row_view(p, it, row);
+    if (row >= it.rows) {  // no row: sees all, so that the warp need not mask for it; nothing of it is stored
+      view.see_lo = 0;
+      view.see_hi = 0x7fffffff;
+    }
+    float m = -INFINITY, factor = 1.0f;  // of the scores: what q was divided by (and what turns the product to log2 units)
+    bool factor_known = false;
+    uint64_t sum[4] = {0, 0, 0, 0};  // of the weights over their v scales, eight floats: one chain of additions would take longer than the exponentials
+    const int first = turns ? (g ^ h) & 1 : 0, step = turns ? 2 : 1;
+    for (int i = first; i < nt; i += step) {
+      const uint32_t c = g + i, buf = one ? (c & 1) : h, x = one ? 2 + buf : h, phase = one ? (c >> 1) & 1 : (d + i) & 1;
+      const uint32_t ts = lanes + buf * 128, at = tiles + i, stage = at % kScaleTiles;
+      if (!wait(&b.s[x], phase)) break;
+      if (!busy) {
+        arrive(&b.p[x]);
+        arrive(&b.p2[x]);
+        if (lane == 0) mbar_arrive_count(&b.sc_empty[stage], one ? 2 : 1);
+        continue;
+      }
+      if (!factor_known) {  // scores are there, so the queries were, and the row's factor with them
+        factor_known = true;
+        factor = rs.factor[items & 1][half_row];
+        // within these bounds products of 0 stay 0, and what a k scale can add stays finite
+        if (!EXT) factor = fminf(fmaxf(factor * p.scale_log2, 0x1p-90f), 0x1p95f);
+      }
+      if (!wait(&b.sc_full[stage], (at / kScaleTiles) & 1)) break;
+      const float4* sc = scale_ring[stage];
+      // Twice over the scores: for the maximum (bent and masked scores go back to tensor memory) and
+      // for the weights, 64 at a time.
+      const int key0 = it.range.tile(it.begin + i) * kKeys, prefix = it.q.prefix;
+      const bool edge = !__all_sync(0xffffffffu, (key0 + kKeys <= view.see_hi && key0 >= view.see_lo) || key0 + kKeys <= prefix);
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto largest = [&](float a, float b, float c, float d, float e, float f, float g, float h) {
+        return fmaxf(max3(max3(max3(a, b, c), d, e), f, g), h);
+      };
+      if (!EXT && !edge) {
+        uint32_t s[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(s[k], ts + k * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          settle(s[k]);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            auto f = [&](int n) { return __uint_as_float(s[k][j + n]); };
+            const float2 e = *reinterpret_cast<const float2*>(&sc[k * 4 + j / 8]);
+            top[k] = fmaxf(top[k], fmaf(largest(f(0), f(1), f(2), f(3), f(4), f(5), f(6), f(7)), e.x * factor, e.y));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          float s[64];
+          load_scores(ts + part * 64, s);
+          if constexpr (EXT != 0) {  // to products of q and k
+#pragma unroll
+            for (int j = 0; j < 64; j += 8) {
+              const float f = sc[part * 8 + j / 8].x * factor;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) s[j + k] *= f;
+            }
+          }
+          shape_scores<EXT>(p, prefix, view, key0 + part * 64, edge, s);
+          uint32_t back[32];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) back[j] = __float_as_uint(s[k * 32 + j]);
+            tmem_st32(ts + part * 64 + k * 32, back);
+          }
+#pragma unroll
+          for (int j = 0; j < 64; j += 8) {
+            const float2 e = *reinterpret_cast<const float2*>(&sc[part * 8 + j / 8]);
+            const float high = largest(s[j], s[j + 1], s[j + 2], s[j + 3], s[j + 4], s[j + 5], s[j + 6], s[j + 7]);
+            top[j / 16] = fmaxf(top[j / 16], EXT ? high + e.y : fmaf(high, e.x * factor, e.y));
+          }
+        }
+        tmem_wait_st();
+      }
+      const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+      const bool grown = high > m + 8.0f;  // m = -inf: any finite score
+      if (__any_sync(0xffffffffu, grown)) {
+        const float shrink = grown ? ex2(m - (high - 6.0f)) : 1.0f;  // m = -inf: 0
+        if (grown) m = high - 6.0f;
+        if (i > first) {
+          // the sum holds this warpgroup's tiles so far: that is so once the scores are there, but for
+          // one warpgroup with scores that run ahead, where a barrier says so.  (Scores of tile c
+          // complete after the sum of tile c - 2, so this barrier is at most one phase behind.)
+          if (!S::kTurns && !wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            untwo(sum[k], lo, hi);
+            sum[k] = two(lo * shrink, hi * shrink);
+          }
+#pragma unroll
+          for (int k = 0; k < DP / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32(o, to + k * 32);
+            tmem_wait_ld();
+            settle(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
+            tmem_st32(to + k * 32, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        float s[64];
+        load_scores(ts + part * 64, s);
+        uint32_t w[S::kParts][16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // eight keys with the same scales
+          const float4 e = sc[part * 8 + j];
+          const uint64_t mul = two(e.x * factor, e.x * factor), add = two(e.y - base, e.y - base);
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const uint64_t v = two(s[j * 8 + k], s[j * 8 + k + 1]);
+            untwo(EXT ? add2(v, add) : fma2(v, mul, add), f[k], f[k + 1]);
+            f[k] = ex2(f[k]);
+            f[k + 1] = ex2(f[k + 1]);
+          }
+          // of the unrounded weights
+          sum[j & 3] = fma2(add2(add2(two(f[0], f[1]), two(f[2], f[3])), add2(two(f[4], f[5]), two(f[6], f[7]))), two(e.z, e.z), sum[j & 3]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t parts[S::kParts];
+            split4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], parts);
+#pragma unroll
+            for (int y = 0; y < S::kParts; ++y) w[y][j * 2 + k] = parts[y];
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < S::kParts; ++y) tmem_st16(ts + (part * S::kParts + y) * 16, w[y]);
+        tmem_wait_st();
+        arrive(part ? &b.p2[x] : &b.p[x]);  // the second product starts on the first half of the keys
+      }
+      if (lane == 0) mbar_arrive_count(&b.sc_empty[stage], one ? 2 : 1);
+    }
+    if (!ok) break;
+    const uint32_t end = g + nt - 1;  // the last tile
+    const bool other_ends = turns && (end & 1) != h;
+    if (other_ends && (h == 0 || nt > 1) && !wait(&b.s[2 + (end & 1)], (end >> 1) & 1)) break;
+    // every score of the item is computed: its queries may go
+    const bool more = next_item(later), shared = turns && nt > 1;
+    if (more) load_queries(later);
+    tiles += nt;
+    if (!one) {
+      d += nt;
+      if (!wait(&b.o[h], pairs++ & 1)) break;
+    } else {
+      g += nt;
+      // (scores of the last tile are there, so the sum's barrier is at most one phase behind)
+      if ((shared || !other_ends) && !wait(&b.o[2 + (end & 1)], (end >> 1) & 1)) break;
+    }
+    if (!shared) queries_loaded(later, items + 1);
+    const bool whole = it.first && it.last;
+    const int slot = it.first ? 1 : 0;
+    float lo, hi;
+    untwo(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
+    float l = lo + hi, scale0 = 1.0f, scale1 = 1.0f;
+    if (shared) {
+      rs.ml[threadIdx.x] = make_float2(m, l);
+      arrive(&b.join[0]);
+      if (!wait(&b.join[0], joined & 1)) break;
+      // Not before: the next item's scores would complete phases that the other warpgroup still waits for.
+      queries_loaded(later, items + 1);
+      const float2 mine = make_float2(m, l), theirs = rs.ml[threadIdx.x ^ 128];
+      m = fmaxf(m, theirs.x);
+      const float a = m == -INFINITY ? 0.0f : ex2(mine.x - m), z = m == -INFINITY ? 0.0f : ex2(theirs.x - m);
+      // in one order for both, so that they agree
+      scale0 = h ? z : a;
+      scale1 = h ? a : z;
+      l = (h ? theirs.y : mine.y) * scale0 + (h ? mine.y : theirs.y) * scale1;
+    }
+    if (busy && (shared || !other_ends)) {
+      const bool mine = row < it.rows;
+      const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw nothing gives 0
+      uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs;
+      const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * S::kRows + half_row;
+      float* part = p.part_o + at * p.part_dim;
+      // 32 columns at a time, one copy of the code.  Of a shared item each warpgroup joins half of the columns.
+      const int col0 = shared ? h * (DP / 2) : 0, cols = min(p.head_dim, shared ? col0 + DP / 2 : DP);
+#pragma unroll 1
+      for (int col = col0; col < cols; col += 32) {
+        uint32_t o[32];
+        __syncwarp();  // lanes without a row come from the last round early
+        float f[32];
+        tmem_ld32(o, (shared ? lanes + 256 : to) + col);
+        tmem_wait_ld();
+        settle(o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
+        if (shared) {
+          tmem_ld32(o, lanes + 384 + col);
+          tmem_wait_ld();
+          settle(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = f[j] * scale0 + __uint_as_float(o[j]) * scale1;
+        }
+        if (!mine) continue;
+        if (p.wide) {  // whole sectors
+#pragma unroll
+          for (int j = 0; j < 32; j += 16) {
+            if (col + j >= p.head_dim) break;
+            uint32_t v[8];
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = pack2<DT>(f[j + 2 * e] * inv, f[j + 2 * e + 1] * inv);
+              st_v8(out + col + j, v);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 16; x += 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(f[j + x + e]);
+                st_v8(part + col + j + x, v);
+              }
+            }
+          }
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          if (col + j >= p.head_dim) break;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = f[j + e];
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            st_v4(out + col + j, pack8<DT>(v));
+          } else {
+            *reinterpret_cast<float4*>(part + col + j) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(part + col + j + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        }
+      }
+      if (mine && !(shared && h == 1)) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+        else if (p.lse)
+          p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      }
+    }
+    // neither sum nor the room of m and l is written again until both warpgroups have read them
+    if (shared) {
+      arrive(&b.join[1]);
+      if (!wait(&b.join[1], joined++ & 1)) break;
+    }
+    if (it.first && !it.last) {
+      goes_on = true;
+      if (threadIdx.x == 0) write_header(p, span, &it);
+    }
+    __syncwarp();  // every lane is done with the item
+    if (lane == 0) it = later;
+    __syncwarp();
+    have = more;
+    ++items;
+  }
+  if (threadIdx.x == 0 && !goes_on) write_header(p, span, nullptr);
+}
+
+template <int DT, int DP, int EXT>
+__global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                                                         const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<DT, DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ SpanShared span;
+  __shared__ Bars b;
+  __shared__ SoftmaxState<S> states[8];
+  __shared__ RowShared rows;
+  __shared__ float4 scales[kScaleTiles][kScaleGroups];
+  uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // swizzled tiles start on 1024 bytes
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&b.full[i], 1);
+      mbar_init(&b.empty[i], 1);
+      b.issued[i] = 0;
+    }
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(&b.s[x], 1);
+      mbar_init(&b.o[x], 1);
+      mbar_init(&b.p[x], 4);  // one arrival a warp
+      mbar_init(&b.p2[x], 4);
+    }
+    for (int h = 0; h < 2; ++h) mbar_init(&b.q[h], 4);
+    for (int x = 0; x < 2; ++x) mbar_init(&b.join[x], 8);
+    for (int x = 0; x < kScaleTiles; ++x) {
+      mbar_init(&b.sc_full[x], 1);
+      mbar_init(&b.sc_empty[x], 8);
+    }
+    mbar_init(&b.drain, 1);
+    b.stop = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&b.tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&b.tmem);
+  pdl_wait_and_release();
+  find_span<S::kRows, kKeys, kThreads>(p, span);
+
+  const uint32_t queries = smem_addr(smem), ring = queries + S::kQueryBytes;
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      load_role<S>(p, true, &kmap, span, b, ring);
+    } else if (warp == kLoadWarp + 1) {
+      load_role<S>(p, false, &vmap, span, b, ring);
+      check_blocks(p);
+    } else if (warp == kMmaWarp) {
+      mma_role<S>(p, span, b, queries, ring, tmem);
+    } else if (warp == kScaleWarp) {
+      scale_role<S>(p, span, b, scales);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    softmax_role<DT, DP, EXT>(p, span, states[warp], b, rows, scales, queries, tmem);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (b.stop && warp == kLoadWarp)  // copies in flight end before the CTA does
+    for (int i = 0; i < S::kSlots; ++i)
+      if (b.issued[i] > (p.stall && i == 0 ? 1u : 0u)) mbar_wait_bounded(&b.full[i], (b.issued[i] - 1) & 1, p.wait_cycles);
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+template <int DT, int DP>
+const void* tma_of(int ext) {
+  switch (ext) {
+    case 0: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, 0>);
+    case kCap: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kCap>);
+    case kBias: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kBias>);
+    case kCap | kBias | kWide: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kCap | kBias | kWide>);
+    default: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kCap | kBias>);
+  }
+}
+
+}  // namespace
+
+const void* attn8_tma_kernel(bool bf16, int padded_dim, float cap, bool bias) {
+  const int ext = score_forms(cap, bias);
+  if (padded_dim == 256) return bf16 ? tma_of<kBF16, 256>(ext) : tma_of<kF16, 256>(ext);
+  return bf16 ? tma_of<kBF16, 128>(ext) : tma_of<kF16, 128>(ext);
+}
+
+size_t attn8_tma_smem(bool bf16, int padded_dim) {
+  static_assert(Shape<kBF16, 128>::kBytes == Shape<kBF16, 256>::kBytes && Shape<kF16, 128>::kBytes == Shape<kF16, 256>::kBytes, "one size a type");
+  return (bf16 ? Shape<kBF16, 128>::kBytes : Shape<kF16, 128>::kBytes) + 1024;
+}
+
+}  // namespace ar

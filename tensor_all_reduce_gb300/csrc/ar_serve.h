@@ -181,9 +181,13 @@ const void* attn_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  /
 size_t attn_tma_smem(int padded_dim);
 int attn_tma_rows(int padded_dim);  // query rows of an item
 
+const void* attn8_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  // over a cache in 8 bits
+size_t attn8_tma_smem(bool bf16, int padded_dim);  // (rows of an item: attn_tma_rows)
+
 // Tensor map of a cache [blocks, page, heads, dim] (strides in elements) with boxes of box_rows
-// tokens by 64 elements; `encode` is the driver's cuTensorMapEncodeTiled.
-bool attn_tensor_map(void* encode, CUtensorMap* map, const void* base, bool bf16, int64_t dim, int64_t page, int64_t heads, int64_t blocks,
+// tokens by 128 bytes; `encode` is the driver's cuTensorMapEncodeTiled.
+enum class CacheType { kF16, kBF16, kE4M3 };
+bool attn_tensor_map(void* encode, CUtensorMap* map, const void* base, CacheType type, int64_t dim, int64_t page, int64_t heads, int64_t blocks,
                      int64_t page_stride, int64_t head_stride, int64_t block_stride, int box_rows);
 
 // Function attributes, module loading and occupancies for all of the above, once per context.

@@ -487,19 +487,20 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   p.status = ctx->d_status;
   p.wait_cycles = ctx->wait_cycles ? ctx->wait_cycles : 2000000000LL;
 
-  // The tensor-core form takes aligned rows and pages that whole groups of
+  // The tensor-core form takes rows on 16-byte boundaries and pages that whole groups of
   // 8 keys (the swizzle's period) fill; the general form the rest.
   const int dp = padded_dim(a->head_dim);
   int box = 1;
   while (box < 128 && pg % (box * 2) == 0) box *= 2;
-  bool tma = !scales && p.vec && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
+  bool tma = p.vec && (!scales || (d % 16 == 0 && cache_steps(16))) && box >= 8 && a->num_blocks > 0 && a->num_blocks < 0x7fffffff && ctx->encode_tensor_map;
   CUtensorMap kmap, vmap;
   if (tma) {
     p.box_rows = box;
     p.stall = ctx->test_stall;
-    tma = ar::attn_tensor_map(ctx->encode_tensor_map, &kmap, a->k_cache, bf16, d, pg, hk, a->num_blocks, a->k_page_stride, a->k_head_stride,
+    const ar::CacheType type = scales ? ar::CacheType::kE4M3 : bf16 ? ar::CacheType::kBF16 : ar::CacheType::kF16;
+    tma = ar::attn_tensor_map(ctx->encode_tensor_map, &kmap, a->k_cache, type, d, pg, hk, a->num_blocks, a->k_page_stride, a->k_head_stride,
                               a->k_block_stride, box) &&
-          ar::attn_tensor_map(ctx->encode_tensor_map, &vmap, a->v_cache, bf16, d, pg, hk, a->num_blocks, a->v_page_stride, a->v_head_stride,
+          ar::attn_tensor_map(ctx->encode_tensor_map, &vmap, a->v_cache, type, d, pg, hk, a->num_blocks, a->v_page_stride, a->v_head_stride,
                               a->v_block_stride, box);
   }
   p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
@@ -514,7 +515,8 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
   const bool bias = a->slopes || !(a->scale > 0.0f);
-  ar_status st = tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
+  ar_status st = tma && scales ? launch(ctx, ar::attn8_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn8_tma_smem(bf16, dp), stream)
+                 : tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp, scales), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
   // Blocks that may join the rows of one item: 4 where a request has few rows, else 16 (us with
@@ -661,8 +663,11 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
         keep(cudaFuncSetAttribute(rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rope_smem_most()));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int i = 0; i < 3; ++i)
-      for (int ext = 0; ext < 6; ++ext)  // no cap, a cap, a wide one
-        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, (float)(ext >> 1) * 50.0f, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
+      for (int ext = 0; ext < 6; ++ext) {  // no cap, a cap, a wide one
+        const float cap = (float)(ext >> 1) * 50.0f;
+        keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, cap, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
+        keep(cudaFuncSetAttribute(attn8_tma_kernel(b, 64 << i, cap, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_tma_smem(b, 64 << i)));
+      }
     keep(cudaFuncGetAttributes(&fa, append_scalar_kernel(b)));
     for (int fp8 = 0; fp8 < 2; ++fp8)
       for (int i = 0; i < 3; ++i) {
