@@ -2,22 +2,26 @@
 // heads of a multiple of 16, pages of a multiple of 8 tokens.
 //
 // The division of the work, the roles of the warps and the tensor memory are those of the kernel for 16-bit
-// caches.  What differs is that the codes are never turned into 16 bits: the 8-bit matrix instructions run at
-// twice the 16-bit rate, so each 16-bit operand of theirs is given as a sum of parts of 8 bits, and two
-// products of parts cost what one of 16 bits does, with half the bytes of keys and values to bring and to hold.
+// caches.  What differs:
 //
+// Scores.  The keys' codes are operands of 8-bit matrix instructions as they are, which run at twice the 16-bit
+// rate, so that q may be a sum of parts of 8 bits at the price of a 16-bit product:
 //   x = hi + lo    bf16 (8 bits): hi = e4m3(x), lo = e5m2(x - hi);  fp16 (11 bits): hi + e4m3(x - hi) + e5m2(rest)
-//
 // E4M3 keeps 4 bits, E5M2 3 and reaches down to 2^-16.  A row of q is scaled by a power of two, so that its
-// largest element lies between 224 and 448: the parts are then exact but for what is 2^-17 of one unit.  A row's
-// weights take their keys' v scale, so that one reference serves both: with t_j = log2(vs_j),
-//   w_j = 2^(s_j + t_j - m),  o = sum w_j c_j,  l = sum w_j / vs_j,  out = o / l,  lse = m + log2(l)
-// and m kept so that the largest w of a row lies between 2^6 and 2^8: parts of a w are off by half a step
-// of 8 (11) bits, or by 2^-17, 2^-23 of the largest.
+// largest element lies between 224 and 448: the parts are then exact but for what is 2^-17 of one unit.
 //
-// A block's scales are the same for eight keys in a row at least; a warp of its own looks them up, tiles ahead, and
-// leaves the k scale, t and 1 / vs of each eight keys of a tile in a ring in shared memory.
+// Values.  A warpgroup turns their codes to fp16, exactly, tile by tile, and the weights are fp16 too whatever
+// the type of q (11 bits).  Parts of 8 bits for the weights as well, without that warpgroup, were slower: an
+// element took 10 instructions in the softmax warps (4096 tokens over 28000: 854 us, 64 single tokens 260 us).
+//
+// Scales.  A row's weights take their keys' v scale, so that one reference serves both: with t_j = log2(vs_j),
+//   w_j = 2^(s_j + t_j - m),  o = sum w_j c_j,  l = sum w_j / vs_j,  out = o / l,  lse = m + log2(l)
+// and m kept so that the largest w of a row lies between 2^6 and 2^14, inside fp16's range.  Scales are the
+// same for eight keys in a row at least; a warp of its own looks them up, tiles ahead, and leaves the k scale, t
+// and 1 / vs of each eight keys of a tile in a ring in shared memory.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "ar_attn.cuh"
 #include "ar_attn_tc.cuh"
@@ -28,11 +32,11 @@
 namespace ar {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kScaleWarp = 11;  // kLoadWarp + 1: values
+constexpr int kThreads = kAttn8Threads;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kScaleWarp = 11, kConvertWarp = 12;  // kLoadWarp + 1: values; four warps convert
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // of 168 a thread at launch
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * 168, "the split uses what the launch has");
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // of 128 a thread at launch
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "the split uses what the launch has");
 constexpr int kScaleTiles = 8;            // tiles of the ring of scales
 constexpr int kScaleGroups = kKeys / 8;   // entries of a tile
 
@@ -40,27 +44,36 @@ template <int DT, int DP>
 struct Shape {
   static constexpr int kRows = DP == 256 ? 128 : 256;   // rows of an item
   static constexpr bool kTurns = DP == 128;             // the warpgroups take an item of one half by turns, tile by tile
-  static constexpr int kParts = DT == kBF16 ? 2 : 3;    // of a 16-bit operand
+  static constexpr int kParts = DT == kBF16 ? 2 : 3;    // of an element of q
   static constexpr int kUnits = DP / 128;               // ring slots that a tile of keys or values takes
   static constexpr int kUnitBytes = kKeys * 128;        // 128 rows of 128 codes
   static constexpr int kPartBytes = kUnits * kUnitBytes;   // one part of a half's queries
   static constexpr int kHalfBytes = kParts * kPartBytes;
   static constexpr int kQueryBytes = kRows / 128 * kHalfBytes;
-  static constexpr int kSlots = kParts == 2 ? 9 : 7;
-  static constexpr int kBytes = kQueryBytes + kSlots * kUnitBytes;
+  static constexpr int kWide = 2, kWideBytes = 2 * kUnitBytes;  // units of values in fp16, in column blocks of 64
+  static constexpr int kKeySlots = kParts == 2 ? 3 : 2, kValueSlots = kParts == 2 ? 2 : 1;
+  static constexpr int kBytes = kQueryBytes + kWide * kWideBytes + (kKeySlots + kValueSlots) * kUnitBytes;
 };
 
-// As in the kernel for 16-bit caches, and the ring of scales.
+constexpr int kMostSlots = 3;
+
+struct Ring {
+  uint64_t full[kMostSlots], empty[kMostSlots];
+  uint32_t issued[kMostSlots];  // rounds whose copies were issued, a slot
+};
+
+// As in the kernel for 16-bit caches; keys and values have rings of their own.
 struct Bars {
-  uint64_t full[9], empty[9];
+  Ring k, v;                     // keys are released by the matrix instructions, values by the four warps that convert
+  uint64_t w_full[2], w_empty[2];  // values in fp16
   uint64_t q[2];
-  uint64_t s[4];
+  uint64_t s[4], s2[4];          // scores of the first and second 64 keys
   uint64_t p[4], p2[4];
   uint64_t o[4];
+  uint64_t half[4];              // first half of a tile's product complete (as p)
   uint64_t join[2];
   uint64_t sc_full[kScaleTiles], sc_empty[kScaleTiles];  // released by 8 warps, or twice by each of 4
   uint64_t drain;
-  uint32_t issued[9];
   uint32_t tmem;
   int stop;
 };
@@ -102,25 +115,35 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
   part[PARTS - 1] = codes4<true>(a, b, c, d);
 }
 
-// ---- tcgen05, 8-bit operands ----------------------------------------------------
+// ---- tcgen05 --------------------------------------------------------------------
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_16bit(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 
-// Instruction descriptor: A in E4M3 or E5M2, B in E4M3, fp32 accumulator, 128 rows, n columns.
-__device__ __forceinline__ uint32_t instr_desc(int n, bool a_e5m2, bool b_rows_along_k) {
-  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_rows_along_k ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptors, fp32 accumulator, 128 rows: scores of n keys, A in E4M3 or E5M2, B in E4M3; weighted
+// sums of n columns, A and B in fp16, B's rows along the reduction.
+__device__ __forceinline__ uint32_t scores_desc(int n, bool a_e5m2) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t sums_desc(int n) { return (1u << 4) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
@@ -129,6 +152,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// After tmem_wait_ld: keeps the uses of loaded registers behind the wait.
+__device__ __forceinline__ void settle16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
+__device__ __forceinline__ void load_columns(uint32_t addr, float (&s)[64]) { load_scores(addr, s); }
+__device__ __forceinline__ void load_columns(uint32_t addr, float (&s)[32]) {
+  uint32_t r[32];
+  tmem_ld32(r, addr);
+  tmem_wait_ld();
+  settle(r);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(r[j]);
 }
 
 __device__ __forceinline__ void mbar_arrive_count(uint64_t* bar, uint32_t count) {
@@ -144,25 +182,32 @@ __device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
 // Every role walks the CTA's items for itself and counts barrier phases the same way (n, items, pairs, d, g as in
 // the kernel for 16-bit caches; tiles: all so far, for the ring of scales).
 
+// Items of no more than 32 rows: the rows are laid out four times, a warp's lanes each, and a warp takes 32 of a
+// tile's 128 keys, so that the tile's softmax runs on all four sub-cores at once and takes a quarter of the time.
+template <class S>
+__device__ __forceinline__ bool by_quarters(const Item& it) {
+  return S::kTurns && it.rows - it.qt * S::kRows <= 32;
+}
+
 template <class S>
 __device__ __forceinline__ bool single_half(const Item& it) {
   return S::kRows == 128 || it.rows - it.qt * S::kRows <= 128;
 }
 
+// Keys or values, box by box through the block table: the lanes look the blocks up, one elected lane issues.
 template <class S>
-__device__ void load_role(const AttnParams& p, bool keys, const CUtensorMap* map, const SpanShared& span, Bars& b, uint32_t ring) {
+__device__ void load_role(const AttnParams& p, const CUtensorMap* map, const SpanShared& span, Bars& b, Ring& ring, uint32_t slots, uint32_t base, bool stall) {
   const int lane = threadIdx.x & 31;
   const int boxes = kKeys / p.box_rows;
   const bool one = elect_one();
   Walk<S::kRows, kKeys> walk;
   walk.start(span);
   Item it = {};
-  uint32_t n = 0;
+  uint32_t n = 0, slot = 0, round = 0;
   bool ok = true;
   while (ok && walk.next(p, it)) {
     const int nt = it.end - it.begin;
-    const bool ahead = single_half<S>(it);  // scores run a tile ahead
-    int block = 0, place = 0;               // block of this lane's box, and its place in the block
+    int block = 0, place = 0;  // block of this lane's box, and its place in the block
     auto look_up = [&](int t) {
       const int key = it.range.tile(it.begin + t) * kKeys + lane * p.box_rows;
       block = -1;
@@ -175,32 +220,92 @@ __device__ void load_role(const AttnParams& p, bool keys, const CUtensorMap* map
     };
     look_up(0);
     for (int t = 0; ok && t < nt; ++t) {
-      // ring units of the item: keys 0, then (values t, keys t + 1), or (keys t + 1, values t) where scores run ahead
-      uint32_t i;
-      if (keys)
-        i = t == 0 ? 0 : (ahead ? 2 * t - 1 : 2 * t);
-      else
-        i = ahead && t + 1 < nt ? 2 * t + 2 : 2 * t + 1;
-      i = n + i * S::kUnits;
       // outside the cache: the copy fills with zeros
       const int w = (unsigned)block < (unsigned)p.num_blocks ? block : (int)p.num_blocks, y = place;
       if (t + 1 < nt) look_up(t + 1);
-      for (int u = 0; u < S::kUnits; ++u, ++i) {
-        const uint32_t slot = i % S::kSlots, round = i / S::kSlots;
-        ok = __all_sync(0xffffffffu, ok && wait_for(&b.empty[slot], (round & 1) ^ 1, b, p));
+      for (int u = 0; u < S::kUnits; ++u, ++n) {
+        ok = __all_sync(0xffffffffu, ok && wait_for(&ring.empty[slot], (round & 1) ^ 1, b, p));
         if (!ok) break;
         if (one) {
-          mbar_arrive_expect_tx(&b.full[slot], S::kUnitBytes);
-          b.issued[slot] = round + 1;
+          mbar_arrive_expect_tx(&ring.full[slot], S::kUnitBytes);
+          ring.issued[slot] = round + 1;
         }
-        const uint32_t dst = ring + slot * S::kUnitBytes;
+        const uint32_t dst = base + slot * S::kUnitBytes;
         for (int x = 0; x < boxes; ++x) {
           const int wx = __shfl_sync(0xffffffffu, w, x), yx = __shfl_sync(0xffffffffu, y, x);
-          if (one && !(p.stall && i == 0)) tma_4d(dst + x * p.box_rows * 128, map, u * 128, yx, it.h, wx, &b.full[slot]);
+          if (one && !(stall && n == 0)) tma_4d(dst + x * p.box_rows * 128, map, u * 128, yx, it.h, wx, &ring.full[slot]);
+        }
+        if (++slot == slots) {
+          slot = 0;
+          ++round;
         }
       }
     }
-    n += 2 * nt * S::kUnits;
+  }
+}
+
+// Values to fp16: a thread a key, 16 elements at a time.  Both layouts have 128-byte rows in 128-byte swizzle, so
+// that eight rows' 16 bytes fall into different banks.  Keys behind the request's end become zeros: the rest of a
+// box holds whatever the cache does, and a weight of 0 does not cancel a NaN.
+template <class S>
+__device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& b, uint32_t values, uint32_t wide) {
+  const int lane = threadIdx.x & 31, row = (int)threadIdx.x - kConvertWarp * 32;
+  Walk<S::kRows, kKeys> walk;
+  walk.start(span);
+  Item it = {};
+  uint32_t n = 0, slot = 0, round = 0;
+  bool ok = true;
+  while (ok && walk.next(p, it)) {
+    const int nt = it.end - it.begin;
+    for (int t = 0; ok && t < nt; ++t) {
+      const bool there = row < it.q.len - it.range.tile(it.begin + t) * kKeys;
+      for (int u = 0; u < S::kUnits; ++u, ++n) {
+        const int chunks = min((p.head_dim - u * 128 + 15) / 16, 8);  // may be negative
+        const uint32_t to = n & 1;
+        ok = wait_for(&b.v.full[slot], round & 1, b, p) && wait_for(&b.w_empty[to], ((n >> 1) & 1) ^ 1, b, p);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t src = values + slot * S::kUnitBytes + row * 128, dst = wide + to * S::kWideBytes + row * 128;
+#pragma unroll
+        for (int c0 = 0; c0 < 8; c0 += 4) {
+          uint32_t in[4][4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < chunks)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(in[c][0]), "=r"(in[c][1]), "=r"(in[c][2]), "=r"(in[c][3])
+                           : "r"(src + (((c0 + c) ^ (row & 7)) << 4))
+                           : "memory");
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c0 + c >= chunks) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t f[4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+                    : "=r"(f[2 * i]), "=r"(f[2 * i + 1])
+                    : "r"(there ? in[c][half * 2 + i] : 0u));
+              }
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c0 / 4 * S::kUnitBytes + (((c * 2 + half) ^ (row & 7)) << 4)), "r"(f[0]),
+                           "r"(f[1]), "r"(f[2]), "r"(f[3])
+                           : "memory");
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&b.v.empty[slot]);
+          mbar_arrive(&b.w_full[to]);
+        }
+        if (++slot == S::kValueSlots) {
+          slot = 0;
+          ++round;
+        }
+      }
+    }
   }
 }
 
@@ -246,58 +351,55 @@ __device__ void scale_role(const AttnParams& p, const SpanShared& span, Bars& b,
 }
 
 template <class S>
-__device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, uint32_t queries, uint32_t ring, uint32_t tmem) {
-  const int lane = threadIdx.x & 31;
+__device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, uint32_t queries, uint32_t keys, uint32_t wide, uint32_t tmem) {
   const int ksteps = (p.head_dim + 31) / 32;
-  const uint32_t idesc_s = instr_desc(kKeys, false, false), idesc_last = instr_desc(kKeys, true, false);
   // descriptors differ in the address alone, in units of 16 bytes: constant offsets are added
-  const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(ring, 16), v_desc = matrix_desc(ring, S::kUnitBytes);
+  const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(keys, 16), v_desc = matrix_desc(wide, S::kUnitBytes);
   const bool one = elect_one();
   Walk<S::kRows, kKeys> walk;
   walk.start(span);
   Item it = {};
-  uint32_t n = 0, items = 0, pairs = 0, d = 0, g = 0;
+  uint32_t slot = 0, round = 0, n = 0;  // of the unit of keys in turn; unit of values in turn
+  uint32_t items = 0, pairs = 0, d = 0, g = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
     fence_after();
     return ok;
   };
-  auto wait_unit = [&](uint32_t i) { return wait(&b.full[i % S::kSlots], (i / S::kSlots) & 1); };
-  // queries of half h, part by part, times the keys of unit i (column part u of the head) into score buffer `buf`
-  auto scores = [&](int buf, int h, uint32_t i, int u) {
-    const uint64_t k = k_desc + (i % S::kSlots) * (S::kUnitBytes / 16);
+  auto wait_keys = [&] { return wait(&b.k.full[slot], round & 1); };
+  auto release_keys = [&] {
+    if (one) mma_commit(&b.k.empty[slot]);
+    if (++slot == S::kKeySlots) {
+      slot = 0;
+      ++round;
+    }
+  };
+  auto wait_values = [&](int u) { return wait(&b.w_full[(n + u) & 1], ((n + u) >> 1) & 1); };
+  // queries of half h, part by part, times `count` keys of those in turn from key0 on (column part u of the head)
+  // into score buffer `buf`
+  auto scores = [&](int buf, int h, int u, int key0, int count) {
+    const uint32_t idesc = scores_desc(count, false), idesc_last = scores_desc(count, true);
+    const uint64_t k = k_desc + (slot * S::kUnitBytes + key0 * 128) / 16;
 #pragma unroll
     for (int x = 0; x < S::kParts; ++x) {
       const uint64_t a = q_desc + (h * S::kHalfBytes + x * S::kPartBytes + u * S::kUnitBytes) / 16;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        if (u * 4 + s < ksteps) mma_ss(tmem + buf * 128, a + s * 2, k + s * 2, x == S::kParts - 1 ? idesc_last : idesc_s, u > 0 || x > 0 || s > 0);
+        if (u * 4 + s < ksteps) mma_8bit(tmem + buf * 128 + key0, a + s * 2, k + s * 2, x == S::kParts - 1 ? idesc_last : idesc, u > 0 || x > 0 || s > 0);
     }
   };
-  // half `part` of the tile's weights in score buffer `buf` times the values of unit i, to columns `to`
-  auto weighted = [&](int buf, uint32_t i, int u, int part, uint32_t to, bool more) {
-    const uint64_t v = v_desc + (i % S::kSlots) * (S::kUnitBytes / 16);
+  // half `part` of the tile's weights in score buffer `buf` times the values in turn (column part u), to columns `to`
+  auto weighted = [&](int buf, int u, int part, uint32_t to, bool more) {
+    const uint64_t v = v_desc + ((n + u) & 1) * (S::kWideBytes / 16);
     const int cols = p.head_dim - u * 128;
     if (cols <= 0) return;
-    const uint32_t idesc_o = instr_desc(cols < 128 ? cols : 128, false, true), last_o = instr_desc(cols < 128 ? cols : 128, true, true);
+    const uint32_t idesc_o = sums_desc(cols < 128 ? cols : 128);
 #pragma unroll
-    for (int x = 0; x < S::kParts; ++x)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        mma_ts(tmem + to + u * 128, tmem + buf * 128 + part * S::kParts * 16 + x * 16 + s * 8, v + (((part * 2 + s) * 32 * 128) >> 4),
-               x == S::kParts - 1 ? last_o : idesc_o, more || part > 0 || x > 0 || s > 0);
-  };
-  // Values behind the request's end: whole boxes came as zeros, the rest of the last box holds
-  // whatever the cache does.  Zeroed, because a weight of 0 does not cancel a NaN.
-  auto clear_tail = [&](int t, uint32_t i) {
-    const int left = it.q.len - it.range.tile(it.begin + t) * kKeys;
-    if (left >= kKeys) return;
-    const int lo = max(left, 0), hi = min((lo + p.box_rows - 1) / p.box_rows * p.box_rows, kKeys);
-    const uint32_t v = ring + (i % S::kSlots) * S::kUnitBytes;
-    for (int x = lo * 8 + lane; x < hi * 8; x += 32) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + x * 16), "r"(0) : "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
+    for (int s = 0; s < 4; ++s) {
+      const int k = part * 4 + s;
+      mma_16bit(tmem + to + u * 128, tmem + buf * 128 + part * 64 + s * 8, v + ((k * 16 * 128) >> 4), idesc_o, more || k > 0);
+    }
   };
   while (ok && walk.next(p, it)) {
     const int nt = it.end - it.begin;
@@ -306,70 +408,80 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
       for (int i = -1; ok && i < nt; ++i) {
         if (i + 1 < nt) {
           const uint32_t x = (g + i + 1) & 1;
-          for (int u = 0; u < S::kUnits; ++u, ++n) {
-            if (!wait_unit(n)) break;
-            if (one) {
-              scores(x, 0, n, u);
-              mma_commit(&b.empty[n % S::kSlots]);
-            }
+          for (int u = 0; u < S::kUnits; ++u) {
+            if (!wait_keys()) break;
+            if (one) scores(x, 0, u, 0, kKeys);
+            release_keys();
           }
           if (!ok) break;
-          if (one) mma_commit(&b.s[2 + x]);
+          if (one) {
+            mma_commit(&b.s[2 + x]);
+            mma_commit(&b.s2[2 + x]);
+          }
         }
         if (i < 0) continue;
         const uint32_t x = (g + i) & 1, phase = ((g + i) >> 1) & 1, sum_at = 256 + (S::kTurns ? x * 128 : 0);
-        for (int u = 0; u < S::kUnits; ++u, ++n) {
-          if (!wait_unit(n)) break;
-          clear_tail(i, n);
-          if (u == 0 && !wait(&b.p[2 + x], phase)) break;
-          if (one) weighted(x, n, u, 0, sum_at, S::kTurns ? i > 1 : i > 0);
-          if (u == 0 && !wait(&b.p2[2 + x], phase)) break;
-          if (one) {
-            weighted(x, n, u, 1, sum_at, true);
-            mma_commit(&b.empty[n % S::kSlots]);
-          }
+        for (int u = 0; u < S::kUnits; ++u) wait_values(u);
+        if (!wait(&b.p[2 + x], phase)) break;
+        if (one) {
+          for (int u = 0; u < S::kUnits; ++u) weighted(x, u, 0, sum_at, S::kTurns ? i > 1 : i > 0);
+          mma_commit(&b.half[2 + x]);
         }
+        if (!wait(&b.p2[2 + x], phase)) break;
+        for (int u = 0; u < S::kUnits; ++u) {
+          if (one) weighted(x, u, 1, sum_at, true);
+          if (one) mma_commit(&b.w_empty[(n + u) & 1]);
+        }
+        n += S::kUnits;
         if (!ok) break;
         if (one) mma_commit(&b.o[2 + x]);
       }
       g += nt;
     } else {
-      if (!wait_unit(n)) break;
+      // Two halves take turns, 64 keys at a time: as soon as the weights of a half's 64 keys are used, the next
+      // tile's scores take their columns, so that a half's softmax finds them when it is done with the other 64.
+      if (!wait_keys()) break;
       for (int h = 0; ok && h < 2; ++h) {
         if (!wait(&b.q[h], (h ? pairs : items) & 1)) break;
         if (one) {
-          scores(h, h, n, 0);
+          scores(h, h, 0, 0, kKeys);
           mma_commit(&b.s[h]);
+          mma_commit(&b.s2[h]);
         }
       }
       if (!ok) break;
-      if (one) mma_commit(&b.empty[n % S::kSlots]);
-      ++n;
+      release_keys();
       for (int i = 0; ok && i < nt; ++i, ++d) {
         const bool more = i + 1 < nt;
-        if (!wait_unit(n)) break;
-        clear_tail(i, n);
-        for (int h = 0; h < 2; ++h) {
+        if (!wait_values(0)) break;
+        for (int h = 0; ok && h < 2; ++h) {
           if (!wait(&b.p[h], d & 1)) break;
-          if (one) weighted(h, n, 0, 0, 256 + h * 128, i > 0);
+          if (one) {
+            weighted(h, 0, 0, 256 + h * 128, i > 0);
+            mma_commit(&b.half[h]);
+          }
+          if (!more) continue;
+          if (h == 0 && !wait_keys()) break;
+          if (one) {
+            scores(h, h, 0, 0, 64);
+            mma_commit(&b.s[h]);
+          }
+        }
+        for (int h = 0; ok && h < 2; ++h) {
           if (!wait(&b.p2[h], d & 1)) break;
           if (one) {
-            weighted(h, n, 0, 1, 256 + h * 128, true);
-            if (h == 1) mma_commit(&b.empty[n % S::kSlots]);
-          }
-          if (more) {
-            if (h == 0 && !wait_unit(n + 1)) break;
-            if (one) {
-              scores(h, h, n + 1, 0);
-              mma_commit(&b.s[h]);
-            }
-          } else if (one) {
+            weighted(h, 0, 1, 256 + h * 128, true);
             mma_commit(&b.o[h]);
+            if (h == 1) mma_commit(&b.w_empty[n & 1]);
+            if (more) {
+              scores(h, h, 0, 64, 64);
+              mma_commit(&b.s2[h]);
+            }
           }
         }
         if (!ok) break;
-        if (one && more) mma_commit(&b.empty[(n + 1) % S::kSlots]);
-        n += more ? 2 : 1;
+        ++n;
+        if (more) release_keys();
       }
       ++pairs;
     }
@@ -392,6 +504,7 @@ struct SoftmaxState {  // of a warp
 struct RowShared {
   float factor[2][256];
   float2 ml[256];
+  float inv[2][32];  // of an item by quarters: reciprocals of the sums
 };
 
 template <int DT, int DP, int EXT>
@@ -405,7 +518,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   auto& walk = state.walk;
   Item &it = state.it, &later = state.later;
   if (lane == 0) walk.start(span);
-  uint32_t pairs = 0, d = 0, g = 0, joined = 0, tiles = 0, items = 0;
+  uint32_t d = 0, g = 0, joined = 0, tiles = 0, items = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
@@ -433,9 +546,10 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   const int col = (lane % kRowLanes) * 8, sub = lane / kRowLanes;
   uint4 raw[kAhead];
   bool loading = false;
-  auto warp_rows = [&](const Item& it) { return min(it.rows - (it.qt * S::kRows + h * 128 + warp * 32), 32); };
+  auto first_row = [&](const Item& it) { return it.qt * S::kRows + (by_quarters<S>(it) ? 0 : h * 128 + warp * 32); };
+  auto warp_rows = [&](const Item& it) { return min(it.rows - first_row(it), 32); };
   auto fetch = [&](const Item& it, int r0) {
-    const int base = it.qt * S::kRows + h * 128 + warp * 32, rows = warp_rows(it);
+    const int base = first_row(it), rows = warp_rows(it);
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)it.q.q0 * p.q_ts + (int64_t)it.h * (int)p.group.d * p.q_hs;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -499,7 +613,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     const bool one = single_half<S>(it);
     const bool turns = S::kTurns && one;
     const uint32_t to = lanes + 256 + (one && !S::kTurns ? 0 : h * 128);
-    const int half_row = (one ? 0 : h * 128) + tid, row = it.qt * S::kRows + half_row;
+    const bool quarters = by_quarters<S>(it);
+    const int half_row = (one ? 0 : h * 128) + tid, row = it.qt * S::kRows + (quarters ? lane : half_row);
     const bool busy = row - lane < it.rows;  // the warp has a row
     RowView view = row_view(p, it, row);
     if (row >= it.rows) {  // no row: sees all, so that the warp need not mask for it; nothing of it is stored
@@ -516,6 +631,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       if (!wait(&b.s[x], phase)) break;
       if (!busy) {
         arrive(&b.p[x]);
+        // not before: the tile before's second weights may still be on their way, and this arrival would count for them
+        if (!wait(&b.s2[x], phase)) break;
         arrive(&b.p2[x]);
         if (lane == 0) mbar_arrive_count(&b.sc_empty[stage], one ? 2 : 1);
         continue;
@@ -527,97 +644,79 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
         if (!EXT) factor = fminf(fmaxf(factor * p.scale_log2, 0x1p-90f), 0x1p95f);
       }
       if (!wait(&b.sc_full[stage], (at / kScaleTiles) & 1)) break;
-      const float4* sc = scale_ring[stage];
-      // Twice over the scores: for the maximum (bent and masked scores go back to tensor memory) and
-      // for the weights, 64 at a time.
+      const uint32_t sc = smem_addr(scale_ring[stage]);
+      auto key_scale = [&](int group) {  // and log2 of the v scale
+        float2 e;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(e.x), "=f"(e.y) : "r"(sc + group * 16));
+        return e;
+      };
+      auto all_scales = [&](int group) {
+        float4 e;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(e.x), "=f"(e.y), "=f"(e.z), "=f"(e.w) : "r"(sc + group * 16));
+        return e;
+      };
       const int key0 = it.range.tile(it.begin + i) * kKeys, prefix = it.q.prefix;
       const bool edge = !__all_sync(0xffffffffu, (key0 + kKeys <= view.see_hi && key0 >= view.see_lo) || key0 + kKeys <= prefix);
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto largest = [&](float a, float b, float c, float d, float e, float f, float g, float h) {
-        return fmaxf(max3(max3(max3(a, b, c), d, e), f, g), h);
-      };
-      if (!EXT && !edge) {
-        uint32_t s[4][32];
+      // `count` keys from column `col` on: maximum and weights from the same registers.  `second`: of the second 64 keys
+      // of a tile whose first are on their way.  Weights of two keys a column.
+      auto weights = [&](auto count, int col, bool second, auto& w) {
+        constexpr int N = decltype(count)::value;
+        float s[N];
+        load_columns(ts + col, s);
+        if constexpr (EXT != 0) {  // to products of q and k
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(s[k], ts + k * 32);
-        tmem_wait_ld();
+          for (int j = 0; j < N; j += 8) {
+            const float f = key_scale((col + j) / 8).x * factor;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          settle(s[k]);
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            auto f = [&](int n) { return __uint_as_float(s[k][j + n]); };
-            const float2 e = *reinterpret_cast<const float2*>(&sc[k * 4 + j / 8]);
-            top[k] = fmaxf(top[k], fmaf(largest(f(0), f(1), f(2), f(3), f(4), f(5), f(6), f(7)), e.x * factor, e.y));
+            for (int k = 0; k < 8; ++k) s[j + k] *= f;
           }
         }
-      } else {
+        if (EXT || edge) shape_scores<EXT>(p, prefix, view, key0 + col, edge, s);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          float s[64];
-          load_scores(ts + part * 64, s);
-          if constexpr (EXT != 0) {  // to products of q and k
-#pragma unroll
-            for (int j = 0; j < 64; j += 8) {
-              const float f = sc[part * 8 + j / 8].x * factor;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) s[j + k] *= f;
+        for (int j = 0; j < N; j += 8) {
+          const float2 e = key_scale((col + j) / 8);
+          const float high = fmaxf(max3(max3(max3(s[j], s[j + 1], s[j + 2]), s[j + 3], s[j + 4]), s[j + 5], s[j + 6]), s[j + 7]);
+          top[j / 8 % 4] = fmaxf(top[j / 8 % 4], EXT ? high + e.y : fmaf(high, e.x * factor, e.y));
+        }
+        const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        const bool grown = high > m + 14.0f;  // m = -inf: any finite score
+        if (__any_sync(0xffffffffu, grown)) {
+          const float shrink = grown ? ex2(m - (high - 6.0f)) : 1.0f;  // m = -inf: 0
+          if (grown) m = high - 6.0f;
+          if (i > first || second) {
+            // The products so far have to be complete: of the tile's first 64 keys, or of the tile before (of this
+            // warpgroup: by turns that is so once the scores are there).  Each barrier is at most one phase behind.
+            if (second) {
+              if (!wait(&b.half[x], phase)) return;
+            } else if (!one) {
+              if (!wait(&b.o[x], phase ^ 1)) return;
+            } else if (!S::kTurns) {
+              if (!wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) return;
             }
-          }
-          shape_scores<EXT>(p, prefix, view, key0 + part * 64, edge, s);
-          uint32_t back[32];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 4; ++k) {
+              float lo, hi;
+              untwo(sum[k], lo, hi);
+              sum[k] = two(lo * shrink, hi * shrink);
+            }
+#pragma unroll 1
+            for (int k = 0; k < p.head_dim; k += 16) {
+              uint32_t o[16];
+              tmem_ld16(o, to + k);
+              tmem_wait_ld();
+              settle16(o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) back[j] = __float_as_uint(s[k * 32 + j]);
-            tmem_st32(ts + part * 64 + k * 32, back);
-          }
-#pragma unroll
-          for (int j = 0; j < 64; j += 8) {
-            const float2 e = *reinterpret_cast<const float2*>(&sc[part * 8 + j / 8]);
-            const float high = largest(s[j], s[j + 1], s[j + 2], s[j + 3], s[j + 4], s[j + 5], s[j + 6], s[j + 7]);
-            top[j / 16] = fmaxf(top[j / 16], EXT ? high + e.y : fmaf(high, e.x * factor, e.y));
-          }
-        }
-        tmem_wait_st();
-      }
-      const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-      const bool grown = high > m + 8.0f;  // m = -inf: any finite score
-      if (__any_sync(0xffffffffu, grown)) {
-        const float shrink = grown ? ex2(m - (high - 6.0f)) : 1.0f;  // m = -inf: 0
-        if (grown) m = high - 6.0f;
-        if (i > first) {
-          // the sum holds this warpgroup's tiles so far: that is so once the scores are there, but for
-          // one warpgroup with scores that run ahead, where a barrier says so.  (Scores of tile c
-          // complete after the sum of tile c - 2, so this barrier is at most one phase behind.)
-          if (!S::kTurns && !wait(&b.o[2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1)) break;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            untwo(sum[k], lo, hi);
-            sum[k] = two(lo * shrink, hi * shrink);
-          }
-#pragma unroll
-          for (int k = 0; k < DP / 32; ++k) {
-            uint32_t o[32];
-            tmem_ld32(o, to + k * 32);
-            tmem_wait_ld();
-            settle(o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
-            tmem_st32(to + k * 32, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink);
+              tmem_st16(to + k, o);
+            }
+            tmem_wait_st();
           }
         }
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        float s[64];
-        load_scores(ts + part * 64, s);
-        uint32_t w[S::kParts][16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {  // eight keys with the same scales
-          const float4 e = sc[part * 8 + j];
+        for (int j = 0; j < N / 8; ++j) {  // eight keys with the same scales
+          const float4 e = all_scales(col / 8 + j);
           const uint64_t mul = two(e.x * factor, e.x * factor), add = two(e.y - base, e.y - base);
           float f[8];
 #pragma unroll
@@ -626,35 +725,58 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
             untwo(EXT ? add2(v, add) : fma2(v, mul, add), f[k], f[k + 1]);
             f[k] = ex2(f[k]);
             f[k + 1] = ex2(f[k + 1]);
+            // the second product's operand: fp16, whose 11 bits are no fewer than the type's
+            w[j * 4 + k / 2] = pack2<kF16>(f[k], f[k + 1]);
           }
           // of the unrounded weights
           sum[j & 3] = fma2(add2(add2(two(f[0], f[1]), two(f[2], f[3])), add2(two(f[4], f[5]), two(f[6], f[7]))), two(e.z, e.z), sum[j & 3]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t parts[S::kParts];
-            split4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3], parts);
-#pragma unroll
-            for (int y = 0; y < S::kParts; ++y) w[y][j * 2 + k] = parts[y];
-          }
         }
+      };
+      if (quarters) {
+        uint32_t w[16], none[16];
+        weights(std::integral_constant<int, 32>(), warp * 32, false, w);
+        if (!ok) break;
 #pragma unroll
-        for (int y = 0; y < S::kParts; ++y) tmem_st16(ts + (part * S::kParts + y) * 16, w[y]);
+        for (int j = 0; j < 16; ++j) none[j] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // the other keys are the other warps'
+          const uint32_t to = ts + (k & 2) * 32 + (k & 1) * 16;
+          if (k == warp)
+            tmem_st16(to, w);
+          else
+            tmem_st16(to, none);
+        }
         tmem_wait_st();
-        arrive(part ? &b.p2[x] : &b.p[x]);  // the second product starts on the first half of the keys
+        arrive(&b.p[x]);
+        arrive(&b.p2[x]);
+      } else {
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          if (part && !wait(&b.s2[x], phase)) break;
+          uint32_t w[32];
+          weights(std::integral_constant<int, 64>(), part * 64, part != 0, w);
+          if (!ok) break;
+          tmem_st32(ts + part * 64, w);
+          tmem_wait_st();
+          arrive(part ? &b.p2[x] : &b.p[x]);  // the second product starts on the first half of the keys
+        }
       }
+      if (!ok) break;
       if (lane == 0) mbar_arrive_count(&b.sc_empty[stage], one ? 2 : 1);
     }
     if (!ok) break;
     const uint32_t end = g + nt - 1;  // the last tile
     const bool other_ends = turns && (end & 1) != h;
-    if (other_ends && (h == 0 || nt > 1) && !wait(&b.s[2 + (end & 1)], (end >> 1) & 1)) break;
+    // (by turns a tile's score buffer is its warpgroup's: two tiles of one have one of the other between them, so that
+    // no barrier of the other's can be two phases behind)
+    if (other_ends && (h == 0 || nt > 1 || quarters) && !wait(&b.s[2 + (end & 1)], (end >> 1) & 1)) break;
     // every score of the item is computed: its queries may go
-    const bool more = next_item(later), shared = turns && nt > 1;
+    const bool more = next_item(later), shared = turns && (nt > 1 || quarters);
     if (more) load_queries(later);
     tiles += nt;
     if (!one) {
       d += nt;
-      if (!wait(&b.o[h], pairs++ & 1)) break;
+      if (!wait(&b.o[h], (d - 1) & 1)) break;
     } else {
       g += nt;
       // (scores of the last tile are there, so the sum's barrier is at most one phase behind)
@@ -671,16 +793,92 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       arrive(&b.join[0]);
       if (!wait(&b.join[0], joined & 1)) break;
       // Not before: the next item's scores would complete phases that the other warpgroup still waits for.
-      queries_loaded(later, items + 1);
-      const float2 mine = make_float2(m, l), theirs = rs.ml[threadIdx.x ^ 128];
-      m = fmaxf(m, theirs.x);
-      const float a = m == -INFINITY ? 0.0f : ex2(mine.x - m), z = m == -INFINITY ? 0.0f : ex2(theirs.x - m);
-      // in one order for both, so that they agree
-      scale0 = h ? z : a;
-      scale1 = h ? a : z;
-      l = (h ? theirs.y : mine.y) * scale0 + (h ? mine.y : theirs.y) * scale1;
+      // (By quarters the second half's room is in use until the end.)
+      if (!quarters || h == 0) queries_loaded(later, items + 1);
+      if (quarters) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) most = fmaxf(most, rs.ml[k * 32 + lane].x);
+        auto by = [&](int k) { return rs.ml[k * 32 + lane].x == -INFINITY ? 0.0f : ex2(rs.ml[k * 32 + lane].x - most); };
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) l += rs.ml[k * 32 + lane].y * by(k);
+        scale0 = by(warp);
+        scale1 = by(4 + warp);
+        m = most;
+      } else {
+        const float2 mine = make_float2(m, l), theirs = rs.ml[threadIdx.x ^ 128];
+        m = fmaxf(m, theirs.x);
+        const float a = m == -INFINITY ? 0.0f : ex2(mine.x - m), z = m == -INFINITY ? 0.0f : ex2(theirs.x - m);
+        // in one order for both, so that they agree
+        scale0 = h ? z : a;
+        scale1 = h ? a : z;
+        l = (h ? theirs.y : mine.y) * scale0 + (h ? mine.y : theirs.y) * scale1;
+      }
     }
-    if (busy && (shared || !other_ends)) {
+    if (quarters) {
+      // The four warps' sums of a row meet in shared memory, 32 columns at a time; each warpgroup joins half of the
+      // columns.  (A warpgroup without a tile has left nothing in its columns: scale 0.)
+      const int rows = it.rows - it.qt * S::kRows, row0 = it.qt * S::kRows;
+      const int64_t at0 = ((int64_t)blockIdx.x * 2 + slot) * S::kRows;
+      const uint32_t room = queries + S::kHalfBytes + h * 16384;
+      if (warp == 0) {
+        rs.inv[h][lane] = l == 0.0f ? 0.0f : 1.0f / l;
+        if (h == 0 && lane < rows) {
+          if (!whole) {
+            *reinterpret_cast<float2*>(p.part_ml + (at0 + lane) * 2) = make_float2(m, l);
+          } else if (p.lse) {
+            const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
+            p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+          }
+        }
+      }
+#pragma unroll 1
+      for (int col = h * 64; col < min(p.head_dim, h * 64 + 64); col += 32) {
+        uint32_t o[32];
+        float f[32];
+        tmem_ld32(o, lanes + 256 + col);
+        tmem_wait_ld();
+        settle(o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = scale0 == 0.0f ? 0.0f : __uint_as_float(o[j]) * scale0;
+        tmem_ld32(o, lanes + 384 + col);
+        tmem_wait_ld();
+        settle(o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] += scale1 == 0.0f ? 0.0f : __uint_as_float(o[j]) * scale1;
+        if (lane < rows)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(room + warp * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4)), "f"(f[4 * j]),
+                         "f"(f[4 * j + 1]), "f"(f[4 * j + 2]), "f"(f[4 * j + 3])
+                         : "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+        for (int k = tid; k < rows * 8; k += 128) {
+          const int r = k >> 3, j = k & 7, e = col + j * 4;
+          if (e >= p.head_dim) continue;
+          float4 sum4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float4 v;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                         : "r"(room + y * 4096 + r * 128 + ((j ^ (r & 7)) << 4))
+                         : "memory");
+            sum4 = make_float4(sum4.x + v.x, sum4.y + v.y, sum4.z + v.z, sum4.w + v.w);
+          }
+          if (whole) {
+            const int t = (row0 + r) / p.group, head = it.h * (int)p.group.d + row0 + r - t * (int)p.group.d;
+            const float inv = rs.inv[h][r];
+            st_v2(static_cast<uint16_t*>(p.out) + (int64_t)(it.q.q0 + t) * p.o_ts + (int64_t)head * p.o_hs + e,
+                  make_uint2(pack2<DT>(sum4.x * inv, sum4.y * inv), pack2<DT>(sum4.z * inv, sum4.w * inv)));
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (at0 + r) * p.part_dim + e) = sum4;
+          }
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+      }
+    } else if (busy && (shared || !other_ends)) {
       const bool mine = row < it.rows;
       const int t = row / p.group, head = it.h * (int)p.group.d + row - t * (int)p.group.d;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw nothing gives 0
@@ -754,6 +952,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     if (shared) {
       arrive(&b.join[1]);
       if (!wait(&b.join[1], joined++ & 1)) break;
+      if (quarters && h == 1) queries_loaded(later, items + 1);
     }
     if (it.first && !it.last) {
       goes_on = true;
@@ -781,14 +980,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // swizzled tiles start on 1024 bytes
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(&b.full[i], 1);
-      mbar_init(&b.empty[i], 1);
-      b.issued[i] = 0;
+    for (int i = 0; i < kMostSlots; ++i) {
+      mbar_init(&b.k.full[i], 1);
+      mbar_init(&b.k.empty[i], 1);
+      mbar_init(&b.v.full[i], 1);
+      mbar_init(&b.v.empty[i], 4);
+      b.k.issued[i] = b.v.issued[i] = 0;
+    }
+    for (int x = 0; x < S::kWide; ++x) {
+      mbar_init(&b.w_full[x], 4);
+      mbar_init(&b.w_empty[x], 1);
     }
     for (int x = 0; x < 4; ++x) {
       mbar_init(&b.s[x], 1);
+      mbar_init(&b.s2[x], 1);
       mbar_init(&b.o[x], 1);
+      mbar_init(&b.half[x], 1);
       mbar_init(&b.p[x], 4);  // one arrival a warp
       mbar_init(&b.p2[x], 4);
     }
@@ -814,18 +1021,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
   pdl_wait_and_release();
   find_span<S::kRows, kKeys, kThreads>(p, span);
 
-  const uint32_t queries = smem_addr(smem), ring = queries + S::kQueryBytes;
+  const uint32_t queries = smem_addr(smem), wide = queries + S::kQueryBytes, keys = wide + S::kWide * S::kWideBytes,
+                 values = keys + S::kKeySlots * S::kUnitBytes;
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
-      load_role<S>(p, true, &kmap, span, b, ring);
+      load_role<S>(p, &kmap, span, b, b.k, S::kKeySlots, keys, p.stall);
     } else if (warp == kLoadWarp + 1) {
-      load_role<S>(p, false, &vmap, span, b, ring);
+      load_role<S>(p, &vmap, span, b, b.v, S::kValueSlots, values, false);
       check_blocks(p);
     } else if (warp == kMmaWarp) {
-      mma_role<S>(p, span, b, queries, ring, tmem);
+      mma_role<S>(p, span, b, queries, keys, wide, tmem);
     } else if (warp == kScaleWarp) {
       scale_role<S>(p, span, b, scales);
+    } else {
+      convert_role<S>(p, span, b, values, wide);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -835,8 +1045,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
   __syncthreads();
   fence_after();
   if (b.stop && warp == kLoadWarp)  // copies in flight end before the CTA does
-    for (int i = 0; i < S::kSlots; ++i)
-      if (b.issued[i] > (p.stall && i == 0 ? 1u : 0u)) mbar_wait_bounded(&b.full[i], (b.issued[i] - 1) & 1, p.wait_cycles);
+    for (int i = 0; i < kMostSlots; ++i) {
+      if (b.k.issued[i] > (p.stall && i == 0 ? 1u : 0u)) mbar_wait_bounded(&b.k.full[i], (b.k.issued[i] - 1) & 1, p.wait_cycles);
+      if (b.v.issued[i]) mbar_wait_bounded(&b.v.full[i], (b.v.issued[i] - 1) & 1, p.wait_cycles);
+    }
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }

@@ -138,10 +138,10 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// A row's products with the 64 keys from key0 on to scores: in log2 units where they are bent, else
+// A row's products with the N keys from key0 on to scores: in log2 units where they are bent, else
 // as they are (the caller scales); masked where `edge` says that some row of the warp does not see all.
-template <int EXT>
-__device__ __forceinline__ void shape_scores(const AttnParams& p, int prefix, const RowView& v, int key0, bool edge, float (&s)[64]) {
+template <int EXT, int N>
+__device__ __forceinline__ void shape_scores(const AttnParams& p, int prefix, const RowView& v, int key0, bool edge, float (&s)[N]) {
   if constexpr (EXT & kCap) {
     // c tanh(x) = c - 2 c / (1 + e^2x): one exponential and one reciprocal an element; an exponential that
     // overflows gives c.  The difference leaves an absolute error of 2^-22 c, whatever the score: 2^-16 at
@@ -151,7 +151,7 @@ __device__ __forceinline__ void shape_scores(const AttnParams& p, int prefix, co
     const float twice = p.cap_twice, c = p.cap_log2;
     if constexpr (EXT & kWide) {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {
+      for (int j = 0; j < N; ++j) {
         const float t = s[j] * p.scale_log2, x = t * p.cap_inv, u = x * x;
         const float far = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
         const float near = t * fmaf(fmaf(fmaf(fmaf(0.0171313444f, u, -0.0529842388f), u, 0.133247505f), u, -0.333330679f), u, 1.0f);
@@ -159,19 +159,19 @@ __device__ __forceinline__ void shape_scores(const AttnParams& p, int prefix, co
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
+      for (int j = 0; j < N; ++j) s[j] = fmaf(-2.0f * c, rcp(1.0f + ex2(s[j] * twice)), c);
     }
   }
   if constexpr (EXT & kBias) {
     const float scale = EXT & kCap ? 1.0f : p.scale_log2;
     const float far = (float)(v.pos - key0);
 #pragma unroll
-    for (int j = 0; j < 64; ++j) s[j] = fmaf(-v.slope, fabsf(far - (float)j), s[j] * scale);
+    for (int j = 0; j < N; ++j) s[j] = fmaf(-v.slope, fabsf(far - (float)j), s[j] * scale);
   }
   if (!edge) return;
   const int hi = v.see_hi - key0, lo = v.see_lo - key0, pre = prefix - key0;
 #pragma unroll
-  for (int j = 0; j < 64; ++j)
+  for (int j = 0; j < N; ++j)
     if (!(j < pre || (j < hi && j >= lo))) s[j] = -INFINITY;
 }
 

@@ -181,6 +181,7 @@ const void* attn_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  /
 size_t attn_tma_smem(int padded_dim);
 int attn_tma_rows(int padded_dim);  // query rows of an item
 
+constexpr int kAttn8Threads = 512;  // the kernel's division of registers waits for as many
 const void* attn8_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  // over a cache in 8 bits
 size_t attn8_tma_smem(bool bf16, int padded_dim);  // (rows of an item: attn_tma_rows)
 

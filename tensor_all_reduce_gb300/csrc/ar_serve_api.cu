@@ -515,7 +515,7 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
   const bool bias = a->slopes || !(a->scale > 0.0f);
-  ar_status st = tma && scales ? launch(ctx, ar::attn8_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn8_tma_smem(bf16, dp), stream)
+  ar_status st = tma && scales ? launch(ctx, ar::attn8_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, ar::kAttn8Threads, 1, args, ar::attn8_tma_smem(bf16, dp), stream)
                  : tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp, scales), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
