@@ -40,9 +40,11 @@ static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "the split uses what
 constexpr int kScaleTiles = 8;            // tiles of the ring of scales
 constexpr int kScaleGroups = kKeys / 8;   // entries of a tile
 
-template <int DT, int DP>
+// FEW: for batches of few rows a request: items of 128 rows leave half of the queries' room to the rings, whose
+// depth is what such calls are bound by.
+template <int DT, int DP, bool FEW>
 struct Shape {
-  static constexpr int kRows = DP == 256 ? 128 : 256;   // rows of an item
+  static constexpr int kRows = DP == 256 || FEW ? 128 : 256;  // rows of an item
   static constexpr bool kTurns = DP == 128;             // the warpgroups take an item of one half by turns, tile by tile
   static constexpr int kParts = DT == kBF16 ? 2 : 3;    // of an element of q
   static constexpr int kUnits = DP / 128;               // ring slots that a tile of keys or values takes
@@ -51,11 +53,15 @@ struct Shape {
   static constexpr int kHalfBytes = kParts * kPartBytes;
   static constexpr int kQueryBytes = kRows / 128 * kHalfBytes;
   static constexpr int kWide = 2, kWideBytes = 2 * kUnitBytes;  // units of values in fp16, in column blocks of 64
-  static constexpr int kKeySlots = kParts == 2 ? 3 : 2, kValueSlots = kParts == 2 ? 2 : 1;
-  static constexpr int kBytes = kQueryBytes + kWide * kWideBytes + (kKeySlots + kValueSlots) * kUnitBytes;
+  static constexpr int kSlots = (13 * kUnitBytes - kQueryBytes - kWide * kWideBytes) / kUnitBytes;
+  static constexpr int kKeySlots = (kSlots + 1) / 2, kValueSlots = kSlots / 2;
+  static constexpr int kBytes = 13 * kUnitBytes;
+  // Where the sums of a row's quarters meet: in the second half's queries, which an item of few rows has no use for,
+  // or in its own, when its scores are computed and before the next item's come.
+  static constexpr int kMeet = kRows == 256 ? kHalfBytes : 0;
 };
 
-constexpr int kMostSlots = 3;
+constexpr int kMostSlots = 4;
 
 struct Ring {
   uint64_t full[kMostSlots], empty[kMostSlots];
@@ -266,32 +272,31 @@ __device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& 
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t src = values + slot * S::kUnitBytes + row * 128, dst = wide + to * S::kWideBytes + row * 128;
+        uint32_t in[8][4];
 #pragma unroll
-        for (int c0 = 0; c0 < 8; c0 += 4) {
-          uint32_t in[4][4];
+        for (int c = 0; c < 8; ++c)
+          if (c < chunks)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(in[c][0]), "=r"(in[c][1]), "=r"(in[c][2]), "=r"(in[c][3])
+                         : "r"(src + ((c ^ (row & 7)) << 4))
+                         : "memory");
+        if (!there)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c0 + c < chunks)
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(in[c][0]), "=r"(in[c][1]), "=r"(in[c][2]), "=r"(in[c][3])
-                           : "r"(src + (((c0 + c) ^ (row & 7)) << 4))
-                           : "memory");
+          for (int c = 0; c < 8; ++c) in[c][0] = in[c][1] = in[c][2] = in[c][3] = 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c0 + c >= chunks) break;
+        for (int c = 0; c < 8; ++c) {
+          if (c >= chunks) break;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t f[4];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t f[4];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-                    : "=r"(f[2 * i]), "=r"(f[2 * i + 1])
-                    : "r"(there ? in[c][half * 2 + i] : 0u));
-              }
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c0 / 4 * S::kUnitBytes + (((c * 2 + half) ^ (row & 7)) << 4)), "r"(f[0]),
-                           "r"(f[1]), "r"(f[2]), "r"(f[3])
-                           : "memory");
-            }
+            for (int i = 0; i < 2; ++i)
+              asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+                  : "=r"(f[2 * i]), "=r"(f[2 * i + 1])
+                  : "r"(in[c][half * 2 + i]));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c / 4 * S::kUnitBytes + (((c % 4 * 2 + half) ^ (row & 7)) << 4)), "r"(f[0]),
+                         "r"(f[1]), "r"(f[2]), "r"(f[3])
+                         : "memory");
           }
         }
         fence_proxy_async_smem();
@@ -507,10 +512,9 @@ struct RowShared {
   float inv[2][32];  // of an item by quarters: reciprocals of the sums
 };
 
-template <int DT, int DP, int EXT>
-__device__ void softmax_role(const AttnParams& p, const SpanShared& span, SoftmaxState<Shape<DT, DP>>& state, Bars& b, RowShared& rs,
+template <class S, int DT, int DP, int EXT>
+__device__ void softmax_role(const AttnParams& p, const SpanShared& span, SoftmaxState<S>& state, Bars& b, RowShared& rs,
                              const float4 (*scale_ring)[kScaleGroups], uint32_t queries, uint32_t tmem) {
-  using S = Shape<DT, DP>;
   const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
   // A thread's scores take most of its registers: what is the same for a warp stays in shared
@@ -793,8 +797,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       arrive(&b.join[0]);
       if (!wait(&b.join[0], joined & 1)) break;
       // Not before: the next item's scores would complete phases that the other warpgroup still waits for.
-      // (By quarters the second half's room is in use until the end.)
-      if (!quarters || h == 0) queries_loaded(later, items + 1);
+      // (By quarters the room where the sums meet is in use until the end.)
+      if (!quarters || (S::kMeet && h == 0)) queries_loaded(later, items + 1);
       if (quarters) {
         float most = -INFINITY;
 #pragma unroll
@@ -821,7 +825,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
       // columns.  (A warpgroup without a tile has left nothing in its columns: scale 0.)
       const int rows = it.rows - it.qt * S::kRows, row0 = it.qt * S::kRows;
       const int64_t at0 = ((int64_t)blockIdx.x * 2 + slot) * S::kRows;
-      const uint32_t room = queries + S::kHalfBytes + h * 16384;
+      const uint32_t room = queries + S::kMeet + h * 16384;
       if (warp == 0) {
         rs.inv[h][lane] = l == 0.0f ? 0.0f : 1.0f / l;
         if (h == 0 && lane < rows) {
@@ -952,7 +956,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
     if (shared) {
       arrive(&b.join[1]);
       if (!wait(&b.join[1], joined++ & 1)) break;
-      if (quarters && h == 1) queries_loaded(later, items + 1);
+      queries_loaded(later, items + 1);
     }
     if (it.first && !it.last) {
       goes_on = true;
@@ -967,10 +971,10 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   if (threadIdx.x == 0 && !goes_on) write_header(p, span, nullptr);
 }
 
-template <int DT, int DP, int EXT>
+template <int DT, int DP, bool FEW, int EXT>
 __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                                                          const __grid_constant__ CUtensorMap vmap) {
-  using S = Shape<DT, DP>;
+  using S = Shape<DT, DP, FEW>;
   extern __shared__ uint8_t raw[];
   __shared__ SpanShared span;
   __shared__ Bars b;
@@ -1039,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<DT, DP, EXT>(p, span, states[warp], b, rows, scales, queries, tmem);
+    softmax_role<S, DT, DP, EXT>(p, span, states[warp], b, rows, scales, queries, tmem);
   }
   fence_before();
   __syncthreads();
@@ -1053,28 +1057,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-template <int DT, int DP>
+template <int DT, int DP, bool FEW>
 const void* tma_of(int ext) {
   switch (ext) {
-    case 0: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, 0>);
-    case kCap: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kCap>);
-    case kBias: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kBias>);
-    case kCap | kBias | kWide: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kCap | kBias | kWide>);
-    default: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, kCap | kBias>);
+    case 0: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, FEW, 0>);
+    case kCap: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, FEW, kCap>);
+    case kBias: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, FEW, kBias>);
+    case kCap | kBias | kWide: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, FEW, kCap | kBias | kWide>);
+    default: return reinterpret_cast<const void*>(&attn8_tma<DT, DP, FEW, kCap | kBias>);
   }
+}
+
+template <int DT>
+const void* tma_of(int dp, bool few, int ext) {
+  return dp == 256 ? tma_of<DT, 256, false>(ext) : few ? tma_of<DT, 128, true>(ext) : tma_of<DT, 128, false>(ext);
 }
 
 }  // namespace
 
-const void* attn8_tma_kernel(bool bf16, int padded_dim, float cap, bool bias) {
+const void* attn8_tma_kernel(bool bf16, int padded_dim, bool few, float cap, bool bias) {
   const int ext = score_forms(cap, bias);
-  if (padded_dim == 256) return bf16 ? tma_of<kBF16, 256>(ext) : tma_of<kF16, 256>(ext);
-  return bf16 ? tma_of<kBF16, 128>(ext) : tma_of<kF16, 128>(ext);
+  return bf16 ? tma_of<kBF16>(padded_dim, few, ext) : tma_of<kF16>(padded_dim, few, ext);
 }
 
-size_t attn8_tma_smem(bool bf16, int padded_dim) {
-  static_assert(Shape<kBF16, 128>::kBytes == Shape<kBF16, 256>::kBytes && Shape<kF16, 128>::kBytes == Shape<kF16, 256>::kBytes, "one size a type");
-  return (bf16 ? Shape<kBF16, 128>::kBytes : Shape<kF16, 128>::kBytes) + 1024;
-}
+size_t attn8_tma_smem() { return Shape<kBF16, 128, false>::kBytes + 1024; }  // of every form
 
 }  // namespace ar

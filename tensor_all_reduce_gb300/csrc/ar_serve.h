@@ -182,8 +182,8 @@ size_t attn_tma_smem(int padded_dim);
 int attn_tma_rows(int padded_dim);  // query rows of an item
 
 constexpr int kAttn8Threads = 512;  // the kernel's division of registers waits for as many
-const void* attn8_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  // over a cache in 8 bits
-size_t attn8_tma_smem(bool bf16, int padded_dim);  // (rows of an item: attn_tma_rows)
+const void* attn8_tma_kernel(bool bf16, int padded_dim, bool few, float cap, bool bias);  // over a cache in 8 bits; few: items of 128 rows
+size_t attn8_tma_smem();
 
 // Tensor map of a cache [blocks, page, heads, dim] (strides in elements) with boxes of box_rows
 // tokens by 128 bytes; `encode` is the driver's cuTensorMapEncodeTiled.

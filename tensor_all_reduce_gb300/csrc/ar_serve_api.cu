@@ -504,7 +504,10 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
                               a->v_block_stride, box);
   }
   p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
-  p.tile_rows = tma ? ar::attn_tma_rows(dp) : kMmaRows;
+  // Over 8 bits, batches of few rows a request take items of 128 rows (64 single tokens over up to 9000, 48/8 heads
+  // of 128: FEWTIME us, with 256 rows 302).
+  const bool few = scales && n * (hq / hk) <= 64 * r;
+  p.tile_rows = !tma ? kMmaRows : few ? 128 : ar::attn_tma_rows(dp);
   p.part_dim = part_dim(a->head_dim);
   const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
   char* base = static_cast<char*>(a->workspace);
@@ -515,7 +518,7 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
   const bool bias = a->slopes || !(a->scale > 0.0f);
-  ar_status st = tma && scales ? launch(ctx, ar::attn8_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, ar::kAttn8Threads, 1, args, ar::attn8_tma_smem(bf16, dp), stream)
+  ar_status st = tma && scales ? launch(ctx, ar::attn8_tma_kernel(bf16, dp, few, a->softcap, bias), (unsigned)p.spans, ar::kAttn8Threads, 1, args, ar::attn8_tma_smem(), stream)
                  : tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
                      : launch(ctx, ar::attn_mma_kernel(bf16, dp, scales), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
@@ -666,7 +669,8 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
       for (int ext = 0; ext < 6; ++ext) {  // no cap, a cap, a wide one
         const float cap = (float)(ext >> 1) * 50.0f;
         keep(cudaFuncSetAttribute(attn_tma_kernel(b, 64 << i, cap, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_tma_smem(64 << i)));
-        keep(cudaFuncSetAttribute(attn8_tma_kernel(b, 64 << i, cap, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_tma_smem(b, 64 << i)));
+        for (int few = 0; few < 2; ++few)
+          keep(cudaFuncSetAttribute(attn8_tma_kernel(b, 64 << i, few, cap, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_tma_smem()));
       }
     keep(cudaFuncGetAttributes(&fa, append_scalar_kernel(b)));
     for (int fp8 = 0; fp8 < 2; ++fp8)
