@@ -9,6 +9,26 @@ namespace {
 
 constexpr int kScalarThreads = 128;
 
+// Sine and cosine of `pos` times the fraction of a turn, as in the other rotations (ar_angle.cuh), and the eight bits
+// that sincospi does not take as a first-order term: off by an ulp or two, so that few codes differ from those of exact angles.
+__device__ __forceinline__ void angle_fine(unsigned long long turn, int pos, float* s, float* c) {
+  const unsigned long long a = turn * (unsigned long long)(long long)pos;
+  const int top = (int)(unsigned)((a + 0x80000000ull) >> 32);  // [-0.5, 0.5) turns in units of 2^-32
+  const float head = (float)(top & ~0xff);  // 24 bits
+  const float rest = (float)(top & 0xff) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  float s0, c0;
+  sincospif(head * 0x1p-31f, &s0, &c0);
+  *s = fmaf(c0, rest, s0);
+  *c = fmaf(-s0, rest, c0);
+}
+
+// 8 bytes that are read once.
+__device__ __forceinline__ uint2 ld_v2_once(const void* p) {
+  uint2 v;
+  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 // Any alignment, stride, head and page size: a warp a token, its values as fp32 in shared memory, computed
 // once for the scale and once more for the codes.
 template <int DT>
@@ -53,7 +73,7 @@ __global__ void __launch_bounds__(kScalarThreads) append_scalar(const __grid_con
         __syncwarp();
         for (int f = lane; f < p.half; f += 32) {
           float s, c;
-          angle(turn_of(p.inv_freq[f]), p.positions ? p.positions[axis_of(p, f) * p.pos_stride + u.row + i] : u.place + i, &s, &c);
+          angle_fine(turn_of(p.inv_freq[f]), p.positions ? p.positions[axis_of(p, f) * p.pos_stride + u.row + i] : u.place + i, &s, &c);
           const int ia = p.pairs ? 2 * f : f, ib = p.pairs ? 2 * f + 1 : f + p.half;
           const float a = x[ia], b = x[ib];
           x[ia] = a * c - b * s;
@@ -94,7 +114,329 @@ __global__ void __launch_bounds__(kScalarThreads) append_scalar(const __grid_con
   }
 }
 
+constexpr int kVecThreads = 256, kVecWarps = kVecThreads / 32;
+constexpr int kSlots = 8;  // rows that a lane holds a part of
+
+// Rows on 8-byte boundaries, heads of a multiple of 8.  A CTA works through units of all (or a share of) the heads of a
+// block, so that the angles of its tokens are computed once, into shared memory.  A task is the new keys or the new
+// values of one head: `warps` warps take it, LANES lanes a row, each with two chunks of 4 elements: neighbours, or (HALVES)
+// chunk c and the one half a rotation on, so that a lane has both elements of each pair.  All rows of a task stay in
+// registers from the loads to the codes, with the scale found in between; the next task's rows are on their way
+// meanwhile.  Blocks of more tokens than eight warps hold are gone through twice, once for the scale.
+//
+// The bound is memory: 6 bytes an element.
+template <int DT, int LANES, bool HALVES>
+struct AppendVec {
+  static constexpr int kRowsAStep = 32 / LANES, kTokens = kSlots * kRowsAStep;  // tokens of a warp
+
+  struct Shared {
+    AppendShared span;
+    unsigned long long turn[AR_MAX_HEAD_DIM / 2];
+    int axis[AR_MAX_HEAD_DIM / 2];
+    float weight[AR_MAX_HEAD_DIM];
+    float top[kVecWarps];
+  };
+
+  const AppendParams& p;
+  const AppendPlan& plan;
+  Shared& sh;
+  float* cosines;  // [tokens][pitch], then the sines
+  int lane, warp, sub, task_of_group, row_in_step, c0, c1;
+  bool there;
+  // of the task whose rows are in `raw`
+  int task;
+  uint2 raw[kSlots][2];
+  float old;
+
+  __device__ __forceinline__ int tokens_a_round() const { return plan.warps * kTokens; }
+  __device__ __forceinline__ float* sines() const { return cosines + plan.round_tokens * plan.pitch; }
+
+  __device__ __forceinline__ void angles(const AppendUnit& u, int first) {
+    if (!p.half) return;
+    const int n = min(u.n - first, tokens_a_round());
+    for (int i = threadIdx.x; i < n * p.half; i += kVecThreads) {
+      const int t = i / p.half_div, f = i - t * p.half;
+      float s, c;
+      angle_fine(sh.turn[f], p.positions ? p.positions[sh.axis[f] * p.pos_stride + u.row + first + t] : u.place + first + t, &s, &c);
+      cosines[t * plan.pitch + f] = c;
+      sines()[t * plan.pitch + f] = s;
+    }
+  }
+
+  struct Place {  // of a task in a unit
+    const uint16_t* rows;
+    uint8_t* cache;
+    float* scale;
+    int64_t ts, ps;
+  };
+  __device__ __forceinline__ Place place(const AppendUnit& u) const {
+    const bool v = task >= p.heads;
+    const int h = v ? task - p.heads : task;
+    const Scales& sc = v ? p.v_scale : p.k_scale;
+    return {static_cast<const uint16_t*>(v ? p.v : p.k) + h * (v ? p.v_hs : p.k_hs),
+            (v ? p.v_cache : p.k_cache) + u.block * (v ? p.vc_bs : p.kc_bs) + h * (v ? p.vc_hs : p.kc_hs), sc.p + u.block * sc.bs + h * sc.hs,
+            v ? p.v_ts : p.k_ts, v ? p.vc_ps : p.kc_ps};
+  }
+  __device__ __forceinline__ bool busy() const { return task < 2 * p.heads; }
+  __device__ __forceinline__ int token(int first, int slot) const { return first + sub * kTokens + slot * kRowsAStep + row_in_step; }
+
+  // Asks for the rows of a task, from token `first` of the unit on.
+  __device__ __forceinline__ void fetch(const AppendUnit& u, int group, int first) {
+    task = group * (kVecWarps / plan.warps) + task_of_group;
+    if (!busy()) return;
+    const Place at = place(u);
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int t = token(first, k);
+      raw[k][0] = raw[k][1] = make_uint2(0, 0);
+      if (t < u.n && there) {
+        const uint16_t* src = at.rows + (u.row + t) * at.ts;
+        raw[k][0] = ld_v2_once(src + c0 * 4);
+        raw[k][1] = ld_v2_once(src + c1 * 4);
+      }
+    }
+    old = u.held ? clamp_scale(*reinterpret_cast<const volatile float*>(at.scale)) : kScaleLow;
+  }
+
+  // The rows in `raw` as they are stored, and the largest magnitude among them.
+  __device__ __forceinline__ float values(const AppendUnit& u, int first, float (&f)[kSlots][8]) {
+    const bool v = task >= p.heads;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[k][4 * i] = to_f32<DT>(raw[k][i].x & 0xffffu);
+        f[k][4 * i + 1] = to_f32<DT>(raw[k][i].x >> 16);
+        f[k][4 * i + 2] = to_f32<DT>(raw[k][i].y & 0xffffu);
+        f[k][4 * i + 3] = to_f32<DT>(raw[k][i].y >> 16);
+      }
+    if (!v && p.weight) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = sh.weight[c0 * 4 + i];
+        w[4 + i] = sh.weight[c1 * 4 + i];
+      }
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        if (first + sub * kTokens + k * kRowsAStep >= u.n) break;  // no row of the warp
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(f[k][i], f[k][i], ss);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * p.inv_dim + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[k][i] = f[k][i] * r * w[i];
+      }
+    }
+    if (!v && p.half) {
+      // chunk c0's first frequency; pairs of neighbours: two a chunk
+      const int f0 = HALVES ? c0 * 4 : c0 * 2;
+      if (f0 < p.half && there)
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+          const int t = token(first, k);
+          if (t >= u.n) continue;
+          const float4 c = *reinterpret_cast<const float4*>(cosines + (t - first) * plan.pitch + f0);
+          const float4 s = *reinterpret_cast<const float4*>(sines() + (t - first) * plan.pitch + f0);
+          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (f0 + i >= p.half) continue;
+            float &a = HALVES ? f[k][i] : f[k][2 * i], &b = HALVES ? f[k][4 + i] : f[k][2 * i + 1];
+            const float x = a, y = b;
+            a = x * cs[i] - y * sn[i];
+            b = y * cs[i] + x * sn[i];
+          }
+        }
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[k][i]));
+    if (__any_sync(0xffffffffu, top > 3.402823466e38f)) {  // infinities do not count
+      top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          top = fmaxf(top, finite_magnitude(f[k][i]));
+          if (fabsf(f[k][i]) > 3.402823466e38f) f[k][i] = __uint_as_float(0x7fffffffu);  // their code is NaN's
+        }
+    }
+    return warp_max_magnitude(top);
+  }
+
+  // Largest magnitude over a task's warps.
+  __device__ __forceinline__ float over_warps(float top) {
+    if (plan.warps == 1) return top;
+    __syncthreads();
+    if (lane == 0) sh.top[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < plan.warps; ++w) top = fmaxf(top, sh.top[warp - sub + w]);
+    return top;
+  }
+
+  // Scale, and the codes that the block holds already.
+  __device__ __forceinline__ float settle_scale(const AppendUnit& u, const Place& at, float was, float top) {
+    const float now = fmaxf(was, fresh_scale(top)), inv = 1.0f / now;
+    if (sub == 0 && lane == 0) st_f32(at.scale, now);
+    if (u.held && now > was && there) {
+      const float ratio = was * inv;
+      for (int i = sub * kRowsAStep + row_in_step; i < u.held; i += plan.warps * kRowsAStep) {
+        uint8_t* row = at.cache + i * at.ps;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t* q = reinterpret_cast<uint32_t*>(row + (k ? c1 : c0) * 4);
+          float a, b, c, d;
+          from_e4m3x2(*q & 0xffffu, a, b);
+          from_e4m3x2(*q >> 16, c, d);
+          *q = e4m3x2(a * ratio, b * ratio) | (e4m3x2(c * ratio, d * ratio) << 16);
+        }
+      }
+    }
+    return inv;
+  }
+
+  __device__ __forceinline__ void store(const AppendUnit& u, const Place& at, int first, const float (&f)[kSlots][8], float inv) {
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int t = token(first, k);
+      if (t >= u.n || !there) continue;
+      uint8_t* row = at.cache + (u.held + t) * at.ps;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint32_t*>(row + (i ? c1 : c0) * 4) = e4m3x2(f[k][4 * i] * inv, f[k][4 * i + 1] * inv) | (e4m3x2(f[k][4 * i + 2] * inv, f[k][4 * i + 3] * inv) << 16);
+    }
+  }
+
+  __device__ __forceinline__ void run() {
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x >> 5;
+    sub = warp % plan.warps;
+    task_of_group = warp / plan.warps;
+    row_in_step = lane / LANES;
+    const int c = lane % LANES, hb = p.half / 4;
+    there = c * 8 < p.head_dim;
+    const bool turns = HALVES && c < hb;
+    c0 = turns ? c : 2 * c;
+    c1 = turns ? c + hb : 2 * c + 1;
+    if (!there) c0 = c1 = 0;
+    const int a_group = kVecWarps / plan.warps, groups = (2 * p.heads + a_group - 1) / a_group;
+    AppendWalk walk;
+    walk.start(p, sh.span, plan.parts);
+    AppendUnit u;
+    float f[kSlots][8];
+    while (walk.next(p, u)) {
+      if (u.block < 0) continue;
+      const int g0 = u.part * groups / plan.parts, g1 = (u.part + 1) * groups / plan.parts;
+      const bool keys = g0 * a_group < p.heads;  // the share has keys
+      if (u.n <= tokens_a_round()) {
+        fetch(u, g0, 0);
+        __syncthreads();  // the unit before is done with the angles
+        if (keys) angles(u, 0);
+        __syncthreads();
+        for (int g = g0; g < g1; ++g) {
+          const bool mine = busy();
+          const Place at = place(u);
+          const float was = old;
+          float top = mine ? values(u, 0, f) : 0.0f;
+          if (g + 1 < g1) fetch(u, g + 1, 0);
+          top = over_warps(top);
+          if (mine) store(u, at, 0, f, settle_scale(u, at, was, top));
+        }
+      } else {
+        for (int g = g0; g < g1; ++g) {
+          const bool turn = g * a_group < p.heads;
+          float top = 0.0f, inv = 0.0f;
+          for (int pass = 0; pass < 2; ++pass) {
+            for (int first = 0; first < u.n; first += tokens_a_round()) {
+              __syncthreads();
+              if (turn) angles(u, first);
+              fetch(u, g, first);
+              __syncthreads();
+              const float part = busy() ? values(u, first, f) : 0.0f;
+              if (pass == 0)
+                top = fmaxf(top, part);
+              else if (busy())
+                store(u, place(u), first, f, inv);
+            }
+            if (pass == 0) {
+              const float was = old;
+              top = over_warps(top);
+              __syncthreads();  // every warp has read the scale
+              if (busy()) inv = settle_scale(u, place(u), was, top);
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int DT, int LANES, bool HALVES>
+__global__ void __launch_bounds__(kVecThreads, 2) append_vec(const __grid_constant__ AppendParams p, const __grid_constant__ AppendPlan plan) {
+  using V = AppendVec<DT, LANES, HALVES>;
+  extern __shared__ __align__(16) float angles[];
+  __shared__ typename V::Shared sh;
+  pdl_wait_and_release();
+  for (int i = threadIdx.x; i < p.half; i += kVecThreads) {
+    sh.turn[i] = turn_of(p.inv_freq[i]);
+    sh.axis[i] = axis_of(p, i);
+  }
+  if (p.weight)
+    for (int i = threadIdx.x; i < p.head_dim; i += kVecThreads) {
+      const float w = to_f32<DT>(ld_u16(static_cast<const uint16_t*>(p.weight) + i));
+      sh.weight[i] = p.gemma ? 1.0f + w : w;
+    }
+  append_span<kVecThreads>(p, plan.parts, sh.span);
+  V{p, plan, sh, angles}.run();
+}
+
+int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
+
 }  // namespace
+
+AppendPlan append_plan(const AppendParams& p, int sm_count) {
+  AppendPlan plan;
+  const int tokens = kSlots * 32 / lanes_of(p.head_dim), page = (int)p.page.d;
+  plan.warps = 1;
+  while (plan.warps < kVecWarps && plan.warps * tokens < page) plan.warps *= 2;
+  plan.round_tokens = plan.warps * tokens < page ? plan.warps * tokens : page;
+  plan.pitch = (p.half + 3) / 4 * 4;
+  // blocks that can get tokens: a request's first and last one, and whole ones between
+  const int64_t most = p.tokens / page + 2 * (int64_t)p.requests < p.tokens ? p.tokens / page + 2 * (int64_t)p.requests : p.tokens;
+  // shares of a block's heads, until there are about four units an SM
+  const int groups = (2 * p.heads + kVecWarps / plan.warps - 1) / (kVecWarps / plan.warps);
+  const int64_t usual = p.tokens / page + p.requests < p.tokens ? p.tokens / page + p.requests : p.tokens;
+  plan.parts = 1;
+  while (plan.parts < groups && usual * plan.parts < 4 * sm_count) ++plan.parts;
+  const int64_t grid = most * plan.parts;
+  plan.ctas = (unsigned)(grid < (int64_t)sm_count * 4 ? grid : (int64_t)sm_count * 4);
+  return plan;
+}
+
+size_t append_smem(const AppendPlan& plan) { return (size_t)plan.round_tokens * plan.pitch * 8; }
+size_t append_smem_most() { return 64 * 1024; }
+
+namespace {
+
+template <int DT, bool HALVES>
+const void* vec_of(int lanes) {
+  return lanes == 8    ? reinterpret_cast<const void*>(&append_vec<DT, 8, HALVES>)
+         : lanes == 16 ? reinterpret_cast<const void*>(&append_vec<DT, 16, HALVES>)
+                       : reinterpret_cast<const void*>(&append_vec<DT, 32, HALVES>);
+}
+
+}  // namespace
+
+const void* append_vec_kernel(bool bf16, int head_dim, bool halves) {
+  const int lanes = lanes_of(head_dim);
+  if (halves) return bf16 ? vec_of<kBF16, true>(lanes) : vec_of<kF16, true>(lanes);
+  return bf16 ? vec_of<kBF16, false>(lanes) : vec_of<kF16, false>(lanes);
+}
 
 const void* append_scalar_kernel(bool bf16) {
   return bf16 ? reinterpret_cast<const void*>(&append_scalar<kBF16>) : reinterpret_cast<const void*>(&append_scalar<kF16>);

@@ -169,7 +169,19 @@ const void* rope_vec_kernel(bool bf16, int head_dim, int half, bool pairs);
 RopePlan rope_plan(const RopeParams& p, int sm_count);
 size_t rope_smem(const RopePlan& plan);
 size_t rope_smem_most();
+struct AppendPlan {  // how the vector form divides its work
+  int warps;         // of a task: the new keys or values of a head in a block
+  int parts;         // units that share a block's heads
+  int round_tokens;  // tokens whose angles are held at once
+  int pitch;         // floats between their cosines
+  unsigned ctas;
+};
+
 const void* append_scalar_kernel(bool bf16);
+const void* append_vec_kernel(bool bf16, int head_dim, bool halves);  // halves: of a multiple of 4 (else adjacent pairs, or no rotation)
+AppendPlan append_plan(const AppendParams& p, int sm_count);
+size_t append_smem(const AppendPlan& plan);
+size_t append_smem_most();
 const void* attn_mma_kernel(bool bf16, int padded_dim, bool fp8 = false);  // fp8: a cache in 8 bits
 const void* attn_combine_kernel(bool bf16);
 

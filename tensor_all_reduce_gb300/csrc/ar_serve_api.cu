@@ -638,12 +638,25 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* a, vo
   p.status = ctx->d_status;
   const bool bf16 = a->dtype == AR_DTYPE_BF16;
   DeviceGuard g(ctx->device);
-  // blocks that can get tokens: a request's first and last one, and whole ones between
-  int64_t grid = n / pg + 2 * r < n ? n / pg + 2 * r : n;
-  if (grid > ctx->sm_count * 8) grid = ctx->sm_count * 8;
-  void* args[1] = {&p};
-  const ar_status st = launch(ctx, ar::append_scalar_kernel(bf16), (unsigned)grid, 128, 1, args, 0, stream);
-  if (st == AR_OK) ctx->last_variant = "paged_append_fp8_scalar";
+  // the vector form: rows of k and v on 8-byte, of the caches on 4-byte boundaries, halves of a multiple of 4
+  auto row = [&](const void* x, int64_t ts, int64_t hs) { return aligned(x, 8) && eights(ts, n, 4) && eights(hs, hk, 4); };
+  auto cache = [&](const void* x, int64_t bs, int64_t ps, int64_t hs) { return aligned(x, 4) && eights(bs, nb, 4) && eights(ps, pg, 4) && eights(hs, hk, 4); };
+  const bool vec = d % 8 == 0 && (p.pairs || half % 4 == 0) && row(a->k, a->k_token_stride, a->k_head_stride) &&
+                   row(a->v, a->v_token_stride, a->v_head_stride) && cache(a->k_cache, a->k_block_stride, a->k_page_stride, a->k_cache_head_stride) &&
+                   cache(a->v_cache, a->v_block_stride, a->v_page_stride, a->v_cache_head_stride) && ctx->force_variant != 4;
+  ar_status st;
+  if (vec) {
+    ar::AppendPlan plan = ar::append_plan(p, ctx->sm_count);
+    void* args[2] = {&p, &plan};
+    st = launch(ctx, ar::append_vec_kernel(bf16, p.head_dim, half && !p.pairs), plan.ctas, 256, 1, args, ar::append_smem(plan), stream);
+  } else {
+    // blocks that can get tokens: a request's first and last one, and whole ones between
+    int64_t grid = n / pg + 2 * r < n ? n / pg + 2 * r : n;
+    if (grid > ctx->sm_count * 8) grid = ctx->sm_count * 8;
+    void* args[1] = {&p};
+    st = launch(ctx, ar::append_scalar_kernel(bf16), (unsigned)grid, 128, 1, args, 0, stream);
+  }
+  if (st == AR_OK) ctx->last_variant = vec ? "paged_append_fp8_vec" : "paged_append_fp8_scalar";
   return st;
 }
 
@@ -673,6 +686,9 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
           keep(cudaFuncSetAttribute(attn8_tma_kernel(b, 64 << i, few, cap, ext & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_tma_smem()));
       }
     keep(cudaFuncGetAttributes(&fa, append_scalar_kernel(b)));
+    for (int d : {64, 128, 256})
+      for (int halves = 0; halves < 2; ++halves)
+        keep(cudaFuncSetAttribute(append_vec_kernel(b, d, halves), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)append_smem_most()));
     for (int fp8 = 0; fp8 < 2; ++fp8)
       for (int i = 0; i < 3; ++i) {
         const int dp = 64 << i;

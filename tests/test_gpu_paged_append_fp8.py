@@ -390,3 +390,16 @@ def test_binding_refuses(ctx):
             bad()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(before, (kc, vc, ks, vs)))
+
+
+def test_forms(ctx):
+    """Which form serves which call."""
+    import tensor_all_reduce_gb300 as tar
+    for d, rot, pairs, want in ((128, 128, False, "vec"), (80, 80, True, "vec"), (80, 20, False, "scalar"), (80, 20, True, "vec"), (64, 0, False, "vec"),
+                                (256, 64, False, "vec"), (8, 8, False, "vec"), (36, 8, False, "scalar")):
+        check(ctx, make([3, 20], [5, 0], 2, d, rot=rot), pairs=pairs)
+        assert ctx.last_variant == "paged_append_fp8_" + want
+    ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 4)
+    check(ctx, make([3], [50], 2, 128))
+    assert ctx.last_variant == "paged_append_fp8_scalar"
+    ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 0)
