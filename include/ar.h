@@ -538,7 +538,8 @@ const char* ar_last_error(const ar_ctx* ctx);
  * "fused_staged_cluster" (rows longer than 8192 elements split over a cluster of staged CTAs),
  * "fused_scalar", "fused_cluster_scalar", "fused_batch", "fused_batch_sequential", "paged_plan",
  * "qk_norm_rope_vec", "qk_norm_rope_scalar", "paged_attention_mma", "paged_attention_tma",
- * "paged_append_fp8_vec", "paged_append_fp8_scalar", "paged_attention_fp8_mma", "paged_attention_fp8_tma" or "none"
+ * "paged_append_fp8_vec", "paged_append_fp8_scalar", "paged_attention_fp8_mma", "paged_attention_fp8_tma",
+ * "paged_attention_fp8_few" or "none"
  * (empty call). */
 const char* ar_last_variant(const ar_ctx* ctx);
 

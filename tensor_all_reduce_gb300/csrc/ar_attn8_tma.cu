@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "ar_attn.cuh"
+#include "ar_attn8.cuh"
 #include "ar_attn_tc.cuh"
 #include "ar_e4m3.cuh"
 #include "ar_staged.cuh"
@@ -37,8 +38,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kScaleWarp = 11, kConvertWarp = 12;  
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // of 128 a thread at launch
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "the split uses what the launch has");
-constexpr int kScaleTiles = 8;            // tiles of the ring of scales
-constexpr int kScaleGroups = kKeys / 8;   // entries of a tile
+constexpr int kRoomBytes = 13 * kUnitBytes;  // queries, fp16 values, rings
 
 // FEW: for batches of few rows a request: items of 128 rows leave half of the queries' room to the rings, whose
 // depth is what such calls are bound by.
@@ -48,24 +48,15 @@ struct Shape {
   static constexpr bool kTurns = DP == 128;             // the warpgroups take an item of one half by turns, tile by tile
   static constexpr int kParts = DT == kBF16 ? 2 : 3;    // of an element of q
   static constexpr int kUnits = DP / 128;               // ring slots that a tile of keys or values takes
-  static constexpr int kUnitBytes = kKeys * 128;        // 128 rows of 128 codes
   static constexpr int kPartBytes = kUnits * kUnitBytes;   // one part of a half's queries
   static constexpr int kHalfBytes = kParts * kPartBytes;
   static constexpr int kQueryBytes = kRows / 128 * kHalfBytes;
   static constexpr int kWide = 2, kWideBytes = 2 * kUnitBytes;  // units of values in fp16, in column blocks of 64
-  static constexpr int kSlots = (13 * kUnitBytes - kQueryBytes - kWide * kWideBytes) / kUnitBytes;
+  static constexpr int kSlots = (kRoomBytes - kQueryBytes - kWide * kWideBytes) / kUnitBytes;
   static constexpr int kKeySlots = (kSlots + 1) / 2, kValueSlots = kSlots / 2;
-  static constexpr int kBytes = 13 * kUnitBytes;
   // Where the sums of a row's quarters meet: in the second half's queries, which an item of few rows has no use for,
   // or in its own, when its scores are computed and before the next item's come.
   static constexpr int kMeet = kRows == 256 ? kHalfBytes : 0;
-};
-
-constexpr int kMostSlots = 4;
-
-struct Ring {
-  uint64_t full[kMostSlots], empty[kMostSlots];
-  uint32_t issued[kMostSlots];  // rounds whose copies were issued, a slot
 };
 
 // As in the kernel for 16-bit caches; keys and values have rings of their own.
@@ -78,57 +69,14 @@ struct Bars {
   uint64_t o[4];
   uint64_t half[4];              // first half of a tile's product complete (as p)
   uint64_t join[2];
+  uint64_t meet[2];              // of a warpgroup's four warps, by quarters
   uint64_t sc_full[kScaleTiles], sc_empty[kScaleTiles];  // released by 8 warps, or twice by each of 4
   uint64_t drain;
   uint32_t tmem;
   int stop;
 };
 
-// ---- parts of 8 bits ----------------------------------------------------------
-
-// Four floats -> four codes (E4M3 or E5M2), round to nearest even, saturating.
-template <bool E5M2>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  uint32_t r;
-  if constexpr (E5M2)
-    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e5m2x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
-        : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
-  else
-    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
-        : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-
-// What four E4M3 codes leave of four floats: exact, the codes being their roundings.
-__device__ __forceinline__ void minus_codes4(uint32_t codes, float& a, float& b, float& c, float& d) {
-  asm("{\n\t.reg .b16 x, y, lo, hi, one;\n\t.reg .b32 f, g;\n\tmov.b32 {x, y}, %4;\n\tmov.b16 one, 0xbc00;\n\t"
-      "cvt.rn.f16x2.e4m3x2 f, x;\n\tcvt.rn.f16x2.e4m3x2 g, y;\n\t"
-      "mov.b32 {lo, hi}, f;\n\tfma.rn.f32.f16 %0, lo, one, %0;\n\tfma.rn.f32.f16 %1, hi, one, %1;\n\t"
-      "mov.b32 {lo, hi}, g;\n\tfma.rn.f32.f16 %2, lo, one, %2;\n\tfma.rn.f32.f16 %3, hi, one, %3;\n\t}"
-      : "+f"(a), "+f"(b), "+f"(c), "+f"(d)
-      : "r"(codes));
-}
-
-template <int PARTS>
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&part)[PARTS]) {
-#pragma unroll
-  for (int i = 0; i < PARTS - 1; ++i) {
-    part[i] = codes4<false>(a, b, c, d);
-    minus_codes4(part[i], a, b, c, d);
-  }
-  part[PARTS - 1] = codes4<true>(a, b, c, d);
-}
-
 // ---- tcgen05 --------------------------------------------------------------------
-
-__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 
 __device__ __forceinline__ void mma_16bit(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -144,27 +92,6 @@ __device__ __forceinline__ uint32_t scores_desc(int n, bool a_e5m2) {
 }
 __device__ __forceinline__ uint32_t sums_desc(int n) { return (1u << 4) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-// After tmem_wait_ld: keeps the uses of loaded registers behind the wait.
-__device__ __forceinline__ void settle16(uint32_t (&r)[16]) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
 __device__ __forceinline__ void load_columns(uint32_t addr, float (&s)[64]) { load_scores(addr, s); }
 __device__ __forceinline__ void load_columns(uint32_t addr, float (&s)[32]) {
   uint32_t r[32];
@@ -173,14 +100,6 @@ __device__ __forceinline__ void load_columns(uint32_t addr, float (&s)[32]) {
   settle(r);
 #pragma unroll
   for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(r[j]);
-}
-
-__device__ __forceinline__ void mbar_arrive_count(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 // ---- roles --------------------------------------------------------------------
@@ -198,56 +117,6 @@ __device__ __forceinline__ bool by_quarters(const Item& it) {
 template <class S>
 __device__ __forceinline__ bool single_half(const Item& it) {
   return S::kRows == 128 || it.rows - it.qt * S::kRows <= 128;
-}
-
-// Keys or values, box by box through the block table: the lanes look the blocks up, one elected lane issues.
-template <class S>
-__device__ void load_role(const AttnParams& p, const CUtensorMap* map, const SpanShared& span, Bars& b, Ring& ring, uint32_t slots, uint32_t base, bool stall) {
-  const int lane = threadIdx.x & 31;
-  const int boxes = kKeys / p.box_rows;
-  const bool one = elect_one();
-  Walk<S::kRows, kKeys> walk;
-  walk.start(span);
-  Item it = {};
-  uint32_t n = 0, slot = 0, round = 0;
-  bool ok = true;
-  while (ok && walk.next(p, it)) {
-    const int nt = it.end - it.begin;
-    int block = 0, place = 0;  // block of this lane's box, and its place in the block
-    auto look_up = [&](int t) {
-      const int key = it.range.tile(it.begin + t) * kKeys + lane * p.box_rows;
-      block = -1;
-      place = 0;
-      if (lane < boxes && key < it.q.len) {
-        const int j = key / p.page;
-        place = key - j * (int)p.page.d;
-        block = p.table[(int64_t)it.r * p.table_stride + j];
-      }
-    };
-    look_up(0);
-    for (int t = 0; ok && t < nt; ++t) {
-      // outside the cache: the copy fills with zeros
-      const int w = (unsigned)block < (unsigned)p.num_blocks ? block : (int)p.num_blocks, y = place;
-      if (t + 1 < nt) look_up(t + 1);
-      for (int u = 0; u < S::kUnits; ++u, ++n) {
-        ok = __all_sync(0xffffffffu, ok && wait_for(&ring.empty[slot], (round & 1) ^ 1, b, p));
-        if (!ok) break;
-        if (one) {
-          mbar_arrive_expect_tx(&ring.full[slot], S::kUnitBytes);
-          ring.issued[slot] = round + 1;
-        }
-        const uint32_t dst = base + slot * S::kUnitBytes;
-        for (int x = 0; x < boxes; ++x) {
-          const int wx = __shfl_sync(0xffffffffu, w, x), yx = __shfl_sync(0xffffffffu, y, x);
-          if (one && !(stall && n == 0)) tma_4d(dst + x * p.box_rows * 128, map, u * 128, yx, it.h, wx, &ring.full[slot]);
-        }
-        if (++slot == slots) {
-          slot = 0;
-          ++round;
-        }
-      }
-    }
-  }
 }
 
 // Values to fp16: a thread a key, 16 elements at a time.  Both layouts have 128-byte rows in 128-byte swizzle, so
@@ -271,7 +140,7 @@ __device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& 
         ok = wait_for(&b.v.full[slot], round & 1, b, p) && wait_for(&b.w_empty[to], ((n >> 1) & 1) ^ 1, b, p);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t src = values + slot * S::kUnitBytes + row * 128, dst = wide + to * S::kWideBytes + row * 128;
+        const uint32_t src = values + slot * kUnitBytes + row * 128, dst = wide + to * S::kWideBytes + row * 128;
         uint32_t in[8][4];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -294,7 +163,7 @@ __device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& 
               asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
                   : "=r"(f[2 * i]), "=r"(f[2 * i + 1])
                   : "r"(in[c][half * 2 + i]));
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c / 4 * S::kUnitBytes + (((c % 4 * 2 + half) ^ (row & 7)) << 4)), "r"(f[0]),
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c / 4 * kUnitBytes + (((c % 4 * 2 + half) ^ (row & 7)) << 4)), "r"(f[0]),
                          "r"(f[1]), "r"(f[2]), "r"(f[3])
                          : "memory");
           }
@@ -314,52 +183,11 @@ __device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& 
   }
 }
 
-// The scales of two tiles at a time, a lane eight keys: the next blocks are looked up while the scales arrive.
-template <class S>
-__device__ void scale_role(const AttnParams& p, const SpanShared& span, Bars& b, float4 (*ring)[kScaleGroups]) {
-  const int lane = threadIdx.x & 31, second = lane >> 4, group = lane & 15;
-  Walk<S::kRows, kKeys> walk;
-  walk.start(span);
-  Item it = {};
-  uint32_t tiles = 0;
-  bool ok = true;
-  while (ok && walk.next(p, it)) {
-    const int nt = it.end - it.begin;
-    auto block_at = [&](int t) {  // -1: none, or outside the cache, which reads as zeros
-      int block = -1;
-      if (t + second < nt) {
-        const int key = it.range.tile(it.begin + t + second) * kKeys + group * 8;
-        if (key < it.q.len) block = p.table[(int64_t)it.r * p.table_stride + key / p.page];
-      }
-      return (unsigned)block < (unsigned)p.num_blocks ? block : -1;
-    };
-    int block = block_at(0);
-    for (int t = 0; ok && t < nt; t += 2) {
-      float4 v = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-      if (block >= 0) v = load_scales(p, block, it.h);
-      block = block_at(t + 2);
-      const uint32_t c = tiles + t, c1 = c + 1;
-      const bool two = t + 1 < nt;
-      ok = wait_for(&b.sc_empty[c % kScaleTiles], ((c / kScaleTiles) & 1) ^ 1, b, p) &&
-           (!two || wait_for(&b.sc_empty[c1 % kScaleTiles], ((c1 / kScaleTiles) & 1) ^ 1, b, p));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (t + second < nt) ring[(c + second) % kScaleTiles][group] = v;
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&b.sc_full[c % kScaleTiles]);
-        if (two) mbar_arrive(&b.sc_full[c1 % kScaleTiles]);
-      }
-    }
-    tiles += nt;
-  }
-}
-
 template <class S>
 __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, uint32_t queries, uint32_t keys, uint32_t wide, uint32_t tmem) {
   const int ksteps = (p.head_dim + 31) / 32;
   // descriptors differ in the address alone, in units of 16 bytes: constant offsets are added
-  const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(keys, 16), v_desc = matrix_desc(wide, S::kUnitBytes);
+  const uint64_t q_desc = matrix_desc(queries, 16), k_desc = matrix_desc(keys, 16), v_desc = matrix_desc(wide, kUnitBytes);
   const bool one = elect_one();
   Walk<S::kRows, kKeys> walk;
   walk.start(span);
@@ -385,10 +213,10 @@ __device__ void mma_role(const AttnParams& p, const SpanShared& span, Bars& b, u
   // into score buffer `buf`
   auto scores = [&](int buf, int h, int u, int key0, int count) {
     const uint32_t idesc = scores_desc(count, false), idesc_last = scores_desc(count, true);
-    const uint64_t k = k_desc + (slot * S::kUnitBytes + key0 * 128) / 16;
+    const uint64_t k = k_desc + (slot * kUnitBytes + key0 * 128) / 16;
 #pragma unroll
     for (int x = 0; x < S::kParts; ++x) {
-      const uint64_t a = q_desc + (h * S::kHalfBytes + x * S::kPartBytes + u * S::kUnitBytes) / 16;
+      const uint64_t a = q_desc + (h * S::kHalfBytes + x * S::kPartBytes + u * kUnitBytes) / 16;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         if (u * 4 + s < ksteps) mma_8bit(tmem + buf * 128 + key0, a + s * 2, k + s * 2, x == S::kParts - 1 ? idesc_last : idesc, u > 0 || x > 0 || s > 0);
@@ -522,7 +350,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
   auto& walk = state.walk;
   Item &it = state.it, &later = state.later;
   if (lane == 0) walk.start(span);
-  uint32_t d = 0, g = 0, joined = 0, tiles = 0, items = 0;
+  uint32_t d = 0, g = 0, joined = 0, met = 0, tiles = 0, items = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, b, p));
@@ -597,7 +425,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
         split4(f[4], f[5], f[6], f[7], hi);
         if (r < rows) {
           const int row = warp * 32 + r;
-          const uint32_t dst = queries + h * S::kHalfBytes + (col >> 7) * S::kUnitBytes + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4) + (col & 8);
+          const uint32_t dst = queries + h * S::kHalfBytes + (col >> 7) * kUnitBytes + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4) + (col & 8);
 #pragma unroll
           for (int x = 0; x < S::kParts; ++x) sts_v2(dst + x * S::kPartBytes, lo[x], hi[x]);
           if (col == 0) rs.factor[item & 1][h * 128 + row] = __uint_as_float((unsigned)e << 23);
@@ -857,7 +685,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(room + warp * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4)), "f"(f[4 * j]),
                          "f"(f[4 * j + 1]), "f"(f[4 * j + 2]), "f"(f[4 * j + 3])
                          : "memory");
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+        arrive(&b.meet[h]);
+        if (!wait(&b.meet[h], met++ & 1)) break;
         for (int k = tid; k < rows * 8; k += 128) {
           const int r = k >> 3, j = k & 7, e = col + j * 4;
           if (e >= p.head_dim) continue;
@@ -880,7 +709,8 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
             *reinterpret_cast<float4*>(p.part_o + (at0 + r) * p.part_dim + e) = sum4;
           }
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+        arrive(&b.meet[h]);
+        if (!wait(&b.meet[h], met++ & 1)) break;
       }
     } else if (busy && (shared || !other_ends)) {
       const bool mine = row < it.rows;
@@ -1004,7 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
       mbar_init(&b.p2[x], 4);
     }
     for (int h = 0; h < 2; ++h) mbar_init(&b.q[h], 4);
-    for (int x = 0; x < 2; ++x) mbar_init(&b.join[x], 8);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&b.join[x], 8);
+      mbar_init(&b.meet[x], 4);
+    }
     for (int x = 0; x < kScaleTiles; ++x) {
       mbar_init(&b.sc_full[x], 1);
       mbar_init(&b.sc_empty[x], 8);
@@ -1026,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
   find_span<S::kRows, kKeys, kThreads>(p, span);
 
   const uint32_t queries = smem_addr(smem), wide = queries + S::kQueryBytes, keys = wide + S::kWide * S::kWideBytes,
-                 values = keys + S::kKeySlots * S::kUnitBytes;
+                 values = keys + S::kKeySlots * kUnitBytes;
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
@@ -1080,6 +913,6 @@ const void* attn8_tma_kernel(bool bf16, int padded_dim, bool few, float cap, boo
   return bf16 ? tma_of<kBF16>(padded_dim, few, ext) : tma_of<kF16>(padded_dim, few, ext);
 }
 
-size_t attn8_tma_smem() { return Shape<kBF16, 128, false>::kBytes + 1024; }  // of every form
+size_t attn8_tma_smem() { return kRoomBytes + 1024; }
 
 }  // namespace ar

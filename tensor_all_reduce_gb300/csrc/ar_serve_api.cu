@@ -348,7 +348,9 @@ int part_dim(int d) { return (d + 3) / 4 * 4; }
 int64_t workspace_need(const ar_ctx* ctx, bool bf16, int d) {
   const int64_t general = workspace_of(mma_spans(ctx, bf16, padded_dim(d)), kMmaRows, part_dim(d)).bytes;
   const int64_t tma = workspace_of(ctx->sm_count, ar::attn_tma_rows(padded_dim(d)), part_dim(d)).bytes;
-  return tma > general ? tma : general;
+  const int64_t few = workspace_of(2 * ctx->sm_count, ar::kAttn8FewRows, part_dim(d)).bytes;
+  const int64_t most = tma > general ? tma : general;
+  return few > most ? few : most;
 }
 
 }  // namespace
@@ -503,11 +505,11 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
           ar::attn_tensor_map(ctx->encode_tensor_map, &vmap, a->v_cache, type, d, pg, hk, a->num_blocks, a->v_page_stride, a->v_head_stride,
                               a->v_block_stride, box);
   }
-  p.spans = tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
-  // Over 8 bits, batches of few rows a request take items of 128 rows (64 single tokens over up to 9000, 48/8 heads
-  // of 128: FEWTIME us, with 256 rows 302).
-  const bool few = scales && n * (hq / hk) <= 64 * r;
-  p.tile_rows = !tma ? kMmaRows : few ? 128 : ar::attn_tma_rows(dp);
+  // Over 8 bits: batches of few rows a request take the kernel for them, then items of 128 rows.
+  const int64_t rows = n * (hq / hk);
+  const bool few = tma && scales && rows <= ar::kAttn8FewRows * r, half = scales && rows <= 64 * r;
+  p.spans = few ? 2 * ctx->sm_count : tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
+  p.tile_rows = !tma ? kMmaRows : few ? ar::kAttn8FewRows : half ? 128 : ar::attn_tma_rows(dp);
   p.part_dim = part_dim(a->head_dim);
   const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
   char* base = static_cast<char*>(a->workspace);
@@ -518,16 +520,23 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   DeviceGuard g(ctx->device);
   void* args[3] = {&p, &kmap, &vmap};
   const bool bias = a->slopes || !(a->scale > 0.0f);
-  ar_status st = tma && scales ? launch(ctx, ar::attn8_tma_kernel(bf16, dp, few, a->softcap, bias), (unsigned)p.spans, ar::kAttn8Threads, 1, args, ar::attn8_tma_smem(), stream)
-                 : tma ? launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), (unsigned)p.spans, 384, 1, args, ar::attn_tma_smem(dp), stream)
-                     : launch(ctx, ar::attn_mma_kernel(bf16, dp, scales), (unsigned)p.spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
+  const unsigned spans = (unsigned)p.spans;
+  ar_status st;
+  if (few)
+    st = launch(ctx, ar::attn8_few_kernel(bf16, dp), spans, ar::kAttn8FewThreads, 1, args, ar::attn8_few_smem(dp), stream);
+  else if (tma && scales)
+    st = launch(ctx, ar::attn8_tma_kernel(bf16, dp, half, a->softcap, bias), spans, ar::kAttn8Threads, 1, args, ar::attn8_tma_smem(), stream);
+  else if (tma)
+    st = launch(ctx, ar::attn_tma_kernel(bf16, dp, a->softcap, bias), spans, 384, 1, args, ar::attn_tma_smem(dp), stream);
+  else
+    st = launch(ctx, ar::attn_mma_kernel(bf16, dp, scales), spans, 128, 1, args, ar::attn_mma_smem(dp), stream);
   if (st != AR_OK) return st;
   // Blocks that may join the rows of one item: 4 where a request has few rows, else 16 (us with
   // 4, 8, 16, 32: one token 10.9, 11.0, 12.3, 15.0; 128 tokens over 3000: 54.5, 40.4, 32.7, 31.8).
   const unsigned joiners = n * (hq / hk) > 64 * r ? 16 : 4;
   st = launch(ctx, ar::attn_combine_kernel(bf16), dim3((unsigned)p.spans, joiners), 256, 1, args, 0, stream);
   if (st == AR_OK)
-    ctx->last_variant = scales ? (tma ? "paged_attention_fp8_tma" : "paged_attention_fp8_mma") : tma ? "paged_attention_tma" : "paged_attention_mma";
+    ctx->last_variant = scales ? (few ? "paged_attention_fp8_few" : tma ? "paged_attention_fp8_tma" : "paged_attention_fp8_mma") : tma ? "paged_attention_tma" : "paged_attention_mma";
   return st;
 }
 
@@ -678,6 +687,8 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
       for (int mode = 0; mode < 3; ++mode)
         keep(cudaFuncSetAttribute(rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rope_smem_most()));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
+    for (int dp : {128, 256})
+      keep(cudaFuncSetAttribute(attn8_few_kernel(b, dp), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_few_smem(dp)));
     for (int i = 0; i < 3; ++i)
       for (int ext = 0; ext < 6; ++ext) {  // no cap, a cap, a wide one
         const float cap = (float)(ext >> 1) * 50.0f;

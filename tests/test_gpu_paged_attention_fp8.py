@@ -540,25 +540,28 @@ def test_binding_refuses(ctx):
 def test_forms(ctx):
     """Which form serves which call."""
     import tensor_all_reduce_gb300 as tar
-    for d, page, want in ((128, 16, "tma"), (64, 128, "tma"), (80, 24, "tma"), (16, 8, "tma"), (256, 16, "tma"), (128, 4, "mma"), (72, 16, "mma"),
+    for d, page, want in ((128, 16, "few"), (64, 128, "few"), (80, 24, "few"), (16, 8, "few"), (256, 16, "few"), (128, 4, "mma"), (72, 16, "mma"),
                           (36, 16, "mma"), (256, 7, "mma")):
-        check(ctx, make([3], [50], 4, 2, d, page=page))
+        check(ctx, make([8], [50], 4, 2, d, page=page))
         assert ctx.last_variant == "paged_attention_fp8_" + want
+        check(ctx, make([9], [50], 4, 2, d, page=page))
+        assert ctx.last_variant == "paged_attention_fp8_" + want.replace("few", "tma")
     ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 4)
     check(ctx, make([3], [50], 4, 2, 128))
     assert ctx.last_variant == "paged_attention_fp8_mma"
     ctx.set_option(tar.AR_OPT_FORCE_VARIANT, 0)
 
 
-def test_a_wait_that_runs_out_ends_the_call(ctx):
+@pytest.mark.parametrize("new, form", [([40, 1], "tma"), ([300, 1], "tma"), ([1, 2], "few")])
+def test_a_wait_that_runs_out_ends_the_call(ctx, new, form):
     """The first copy of each CTA is held back: the call ends with code 1, and the next one is right."""
     import tensor_all_reduce_gb300 as tar
-    x = make([40, 1], [500, 3000], 4, 2, 128, seed=17, garbage=0)
+    x = make(new, [500, 3000], 4, 2, 128, seed=17, garbage=0)
     ctx.set_option(tar.AR_OPT_TEST_STALL, 1)
     ctx.set_option(tar.AR_OPT_WAIT_CYCLES, 2000000)
     try:
         run(ctx, x)
-        assert ctx.last_variant == "paged_attention_fp8_tma"
+        assert ctx.last_variant == "paged_attention_fp8_" + form
         assert ctx.device_status() == 1
     finally:
         ctx.set_option(tar.AR_OPT_TEST_STALL, 0)
