@@ -1,19 +1,19 @@
 // Paged attention over a cache of E4M3 codes for few rows a request (single tokens, drafts): the products turned
 // around, so that keys and values, not queries, are the 128-row operand.
 //
-// An item is up to 16 query rows of one request and key head.  With X = hi + mid / 16 + lo / 256 in three E4M3
-// parts (14 bits), side by side as 48 columns, a tile of 128 keys is two products of 8-bit matrix instructions:
-//   scores   S[key, (part, row)] = K[key, d] Q[(part, row), d]          128 x 48 x head
-//   sums     O[d, (part, row)]  += V[key, d]^T W[(part, row), key]      128 x 48 x 128, for each 128 of the head
+// An item is up to 8 (or 16) query rows of one request and key head.  With X = hi + mid / 16 + lo / 256 in three
+// E4M3 parts (14 bits), side by side as 32 (48) columns, a tile of 128 keys is two products of 8-bit matrix instructions:
+//   scores   S[key, (part, row)] = K[key, d] Q[(part, row), d]          128 x 32 x head
+//   sums     O[d, (part, row)]  += V[key, d]^T W[(part, row), key]      128 x 32 x 128, for each 128 of the head
 // Each byte of keys and values is thus read from shared memory once, as it came, and the tensor core's time and
 // the softmax's do not count 128 rows where there are six.  The kernel that keeps queries as the 128-row operand
 // reads keys twice (two parts), turns values to fp16 and was bound by that traffic in shared memory: 64 single
 // tokens over up to 9000 keys, 48 heads, 8 key heads of 128: 273 us.
 //
 // A thread of the softmax warpgroup owns a key: it adds up the parts of the key's scores, and its weights, times
-// the v scale as in ar_attn8_tma.cu, go to shared memory as parts.  The references m of the 16 rows are the same
+// the v scale as in ar_attn8_tma.cu, go to shared memory as parts.  The references m of the rows are the same
 // in all threads; they move only when some weight of a tile would exceed 2^8 (one vote a tile), and then so that
-// the largest becomes 2^6, which keeps weights down to 2^-24 of the largest.
+// the row's largest becomes 2^6, which keeps weights down to 2^-24 of the largest.
 //
 // Two CTAs an SM, 256 threads each: a warpgroup for the softmax; warps for the matrix instructions, keys, values
 // and scales.  Work division, parts of split items and their joining are the other kernels'.  Every wait is bounded.
@@ -25,18 +25,21 @@
 namespace ar {
 namespace {
 
-constexpr int kRows = kAttn8FewRows, kParts = 3, kColumns = kParts * kRows;
+constexpr int kParts = 3;
 constexpr int kThreads = 256;
 constexpr int kMmaWarp = 4, kLoadWarp = 5;  // kLoadWarp + 1: values; the last: scales
 constexpr uint32_t kTmemCols = 256;                         // two score buffers and two sums, 64 columns each
-constexpr int kOperandBytes = kColumns * 128;               // queries (of 128 elements) or weights: rows of 128 bytes
 constexpr float kPart = 16.0f, kPartInv = 0.0625f;          // a part holds the rest of the one before, times 16
 
-template <int DP>
+// ROWS: 8 or 16 rows of an item.
+template <int DP, int ROWS>
 struct Few {
-  static constexpr int kRows = ar::kAttn8FewRows;
+  static constexpr int kRows = ROWS;
+  static constexpr int kColumns = (kParts * ROWS + 15) / 16 * 16;  // what the matrix instructions take; those behind the parts hold anything
+  static constexpr int kOperandBytes = kColumns * 128;             // queries (of 128 elements) or weights: rows of 128 bytes
   static constexpr int kUnits = DP / 128;
-  static constexpr int kKeySlots = 3, kValueSlots = 2;  // two CTAs' fill an SM's shared memory
+  // What two CTAs of an SM have room for.  (Boxes asked into L2 some tiles ahead besides: 3 tiles 207 -> 221 us, 6 227.)
+  static constexpr int kKeySlots = 3, kValueSlots = DP == 128 && ROWS == 8 ? 3 : 2;
   static constexpr int kBytes = (kUnits + 2) * kOperandBytes + (kKeySlots + kValueSlots) * kUnitBytes;
 };
 
@@ -46,20 +49,25 @@ struct Bars {
   uint64_t s[2];       // scores ready
   uint64_t p[2];       // weights stored
   uint64_t o[2];       // sum complete, of a tile
+  uint64_t vote[2];    // a tile's scores have been looked at by the four softmax warps
+  uint64_t meet;       // of these warps
   uint64_t sc_full[kScaleTiles], sc_empty[kScaleTiles];
   uint64_t drain;
   uint32_t tmem;
   int stop;
 };
 
+template <int ROWS>
 struct FewShared {
   SpanShared span;
   Bars b;
   float4 scales[kScaleTiles][kScaleGroups];
-  float factor[kRows];           // of a row: what q was divided by
-  int see_lo[kRows], see_hi[kRows], pos[kRows];
-  float slope[kRows];
-  float top[4][kRows];           // of a warp
+  alignas(16) float factor[ROWS];  // of a row: what q was divided by
+  int see_lo[ROWS], see_hi[ROWS], pos[ROWS];
+  float slope[ROWS];
+  alignas(16) float m[ROWS];        // what a row's weights refer to
+  float top[4][ROWS];           // of a warp
+  uint32_t grown[2];             // the last tile (counted from 1) whose scores outgrew the references
 };
 
 // The three parts of four floats.
@@ -73,17 +81,17 @@ __device__ __forceinline__ void parts4(float a, float b, float c, float d, uint3
   }
 }
 
+template <class S>
 __device__ __forceinline__ uint32_t few_desc(bool a_rows_along_k) {
-  return (1u << 4) | ((a_rows_along_k ? 1u : 0u) << 15) | ((uint32_t)(kColumns >> 3) << 17) | ((128u >> 4) << 24);
+  return (1u << 4) | ((a_rows_along_k ? 1u : 0u) << 15) | ((uint32_t)(S::kColumns >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-template <int DP>
-__device__ void few_mma_role(const AttnParams& p, FewShared& sh, uint32_t queries, uint32_t weights, uint32_t keys, uint32_t values, uint32_t tmem) {
-  using S = Few<DP>;
+template <class S>
+__device__ void few_mma_role(const AttnParams& p, FewShared<S::kRows>& sh, uint32_t queries, uint32_t weights, uint32_t keys, uint32_t values, uint32_t tmem) {
   Bars& b = sh.b;
   const int lane = threadIdx.x & 31;
   const int ksteps = (p.head_dim + 31) / 32;
-  const uint32_t idesc_s = few_desc(false), idesc_o = few_desc(true);
+  const uint32_t idesc_s = few_desc<S>(false), idesc_o = few_desc<S>(true);
   const uint64_t q_desc = matrix_desc(queries, 16), w_desc = matrix_desc(weights, 16), k_desc = matrix_desc(keys, 16), v_desc = matrix_desc(values, kUnitBytes);
   const bool one = elect_one();
   Walk<S::kRows, kKeys> walk;
@@ -101,7 +109,7 @@ __device__ void few_mma_role(const AttnParams& p, FewShared& sh, uint32_t querie
     for (int u = 0; u < S::kUnits; ++u) {
       if (!wait(&b.k.full[ks], kr & 1)) return;
       if (one) {
-        const uint64_t a = k_desc + ks * (kUnitBytes / 16), q = q_desc + u * (kOperandBytes / 16);
+        const uint64_t a = k_desc + ks * (kUnitBytes / 16), q = q_desc + u * (S::kOperandBytes / 16);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           if (u * 4 + s < ksteps) mma_8bit(tmem + x * 64, a + s * 2, q + s * 2, idesc_s, u > 0 || s > 0);
@@ -134,7 +142,7 @@ __device__ void few_mma_role(const AttnParams& p, FewShared& sh, uint32_t querie
         if (!wait(&b.v.full[vs], vr & 1)) break;
         clear_tail(it.q.len - it.range.tile(it.begin + i) * kKeys);
         if (one) {
-          const uint64_t a = v_desc + vs * (kUnitBytes / 16), w = w_desc + x * (kOperandBytes / 16);
+          const uint64_t a = v_desc + vs * (kUnitBytes / 16), w = w_desc + x * (S::kOperandBytes / 16);
           if (u * 128 < p.head_dim)
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_8bit(tmem + 128 + u * 64, a + ((s * 32 * 128) >> 4), w + s * 2, idesc_o, i > 0 || s > 0);
@@ -154,8 +162,8 @@ __device__ void few_mma_role(const AttnParams& p, FewShared& sh, uint32_t querie
   }
 }
 
-// 48 columns of tensor memory: the parts of 16 rows, added up.
-__device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[kRows]) {
+// The parts of the rows in tensor memory, added up.
+__device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[16]) {
   uint32_t a[32], c[16];
   tmem_ld32(a, addr);
   tmem_ld16(c, addr + 32);
@@ -163,13 +171,20 @@ __device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[kRows]) {
   settle(a);
   settle16(c);
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
-    f[r] = fmaf(fmaf(__uint_as_float(c[r]), kPartInv, __uint_as_float(a[kRows + r])), kPartInv, __uint_as_float(a[r]));
+  for (int r = 0; r < 16; ++r) f[r] = fmaf(fmaf(__uint_as_float(c[r]), kPartInv, __uint_as_float(a[16 + r])), kPartInv, __uint_as_float(a[r]));
+}
+__device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[8]) {
+  uint32_t a[32];
+  tmem_ld32(a, addr);
+  tmem_wait_ld();
+  settle(a);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) f[r] = fmaf(fmaf(__uint_as_float(a[16 + r]), kPartInv, __uint_as_float(a[8 + r])), kPartInv, __uint_as_float(a[r]));
 }
 
-template <int DT, int DP>
-__device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t queries, uint32_t weights, uint32_t tmem) {
-  using S = Few<DP>;
+template <int DT, int DP, class S>
+__device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, uint32_t queries, uint32_t weights, uint32_t tmem) {
+  constexpr int kRows = S::kRows;
   Bars& b = sh.b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
@@ -183,11 +198,20 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
     fence_after();
     return ok;
   };
-  auto together = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-  auto any = [](bool x) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbar.red.or.pred b, 2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}" : "=r"(r) : "r"((uint32_t)x) : "memory");
-    return r != 0;
+  auto four = [](const float* x) {  // read anew at each use: kept in registers they spilled
+    float4 f;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(smem_addr(x)) : "memory");
+    return f;
+  };
+  uint32_t met = 0;
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    __syncwarp();
+  };
+  auto together = [&] {  // the four warps, with the others' bound
+    arrive(&b.meet);
+    return wait(&b.meet, met++ & 1);
   };
   // Queries, 16 bytes a lane; the rows of the next item are asked for before the last sums of this one are read.
   constexpr int kRowLanes = DP / 8, kStep = 32 / kRowLanes, kRounds = kRows / 4 / kStep;
@@ -229,7 +253,7 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
 #pragma unroll
       for (int x = 0; x < kParts; ++x) {
         const int n = x * kRows + r;
-        sts_v2(queries + (col >> 7) * kOperandBytes + n * 128 + ((((col & 127) >> 4) ^ (n & 7)) << 4) + (col & 8), lo[x], hi[x]);
+        sts_v2(queries + (col >> 7) * S::kOperandBytes + n * 128 + ((((col & 127) >> 4) ^ (n & 7)) << 4) + (col & 8), lo[x], hi[x]);
       }
       if (col == 0) {
         const RowView v = row_view(p, it, it.qt * S::kRows + r);
@@ -241,41 +265,38 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
         const bool there = it.qt * S::kRows + r < it.rows;  // else: sees all, so that a tile need not be masked for it
         sh.see_lo[r] = there ? v.see_lo : 0;
         sh.see_hi[r] = there ? v.see_hi : 0x7fffffff;
+        sh.m[r] = -INFINITY;
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.q);
-    together();  // what the rows see is there for all
+    return together();  // what the rows see is there for all
   };
   Item it = {}, later = {};
   bool have = walk.next(p, it);
   if (have) {
     fetch(it);
-    queries_loaded(it);
+    have = queries_loaded(it);
   }
   while (have) {
     const int nt = it.end - it.begin, row0 = it.qt * S::kRows, rows = min(it.rows - row0, S::kRows);
-    float m[kRows], l[kRows], factor[kRows];
+    float l[kRows];
     int lo = 0, hi = 0x7fffffff;  // keys that all rows see
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      m[r] = -INFINITY;
       l[r] = 0.0f;
-      factor[r] = sh.factor[r];
       lo = max(lo, sh.see_lo[r]);
       hi = min(hi, sh.see_hi[r]);
     }
-    for (int i = 0; i < nt; ++i) {
-      const uint32_t c = g + i, x = c & 1, phase = (c >> 1) & 1, stage = c % kScaleTiles;
-      // (The four warps meet at barriers that do not run out, so they leave together: a wait that ran out is part of
-      // the next vote.)
-      wait(&b.s[x], phase);
-      wait(&b.sc_full[stage], (c / kScaleTiles) & 1);
+    // A tile's scores in log2 units with log2 of the v scale, masked; e_z: 1 / v scale.  The warps say whether some
+    // outgrow the references, and look at the answer a tile later, so that nobody waits for it.
+    auto prepare = [&](int i, float (&s)[kRows], float& e_z) {
+      const uint32_t c = g + i, x = c & 1, stage = c % kScaleTiles;
+      if (!wait(&b.s[x], (c >> 1) & 1) || !wait(&b.sc_full[stage], (c / kScaleTiles) & 1)) return;
       const float4 e = sh.scales[stage][tid >> 3];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.sc_empty[stage]);
-      float s[kRows];
+      arrive(&b.sc_empty[stage]);
+      e_z = e.z;
       load_rows(lanes + x * 64, s);
       const int key0 = it.range.tile(it.begin + i) * kKeys, key = key0 + tid, prefix = it.q.prefix;
       const bool edge = !((key0 + kKeys <= hi && key0 >= lo) || key0 + kKeys <= prefix);
@@ -285,11 +306,17 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
           RowView v;
           v.pos = sh.pos[r];
           v.slope = sh.slope[r];
-          s[r] = bend(p, v, s[r] * (factor[r] * e.x), key) + e.y;
+          s[r] = bend(p, v, s[r] * (sh.factor[r] * e.x), key) + e.y;
         }
       } else {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) s[r] = fmaf(s[r], factor[r] * e.x, e.y);
+        for (int r = 0; r < kRows; r += 4) {
+          const float4 f = four(&sh.factor[r]);
+          s[r] = fmaf(s[r], f.x * e.x, e.y);
+          s[r + 1] = fmaf(s[r + 1], f.y * e.x, e.y);
+          s[r + 2] = fmaf(s[r + 2], f.z * e.x, e.y);
+          s[r + 3] = fmaf(s[r + 3], f.w * e.x, e.y);
+        }
       }
       if (edge)
 #pragma unroll
@@ -297,12 +324,19 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
           if (!(key < prefix || (key < sh.see_hi[r] && key >= sh.see_lo[r]))) s[r] = -INFINITY;
       bool grown = false;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) grown = grown || s[r] > m[r] + 8.0f;  // m = -inf: any finite score
-      if (any(grown || !ok)) {
-        if (any(!ok)) {
-          ok = false;
-          break;
-        }
+      for (int r = 0; r < kRows; r += 4) {
+        const float4 m = four(&sh.m[r]);  // -inf: any finite score
+        grown = grown || s[r] > m.x + 8.0f || s[r + 1] > m.y + 8.0f || s[r + 2] > m.z + 8.0f || s[r + 3] > m.w + 8.0f;
+      }
+      if (grown) *reinterpret_cast<volatile uint32_t*>(&sh.grown[x]) = c + 1;
+      arrive(&b.vote[x]);
+    };
+    float s[kRows], e_z = 1.0f;
+    prepare(0, s, e_z);
+    for (int i = 0; ok && i < nt; ++i) {
+      const uint32_t c = g + i, x = c & 1;
+      if (!wait(&b.vote[x], (c >> 1) & 1)) break;
+      if (*reinterpret_cast<volatile uint32_t*>(&sh.grown[x]) == c + 1) {
         float shrink[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
@@ -311,62 +345,68 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == r) sh.top[warp][r] = top;
         }
-        together();
+        if (!together()) break;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           const float high = fmaxf(fmaxf(sh.top[0][r], sh.top[1][r]), fmaxf(sh.top[2][r], sh.top[3][r]));
-          const bool moves = high > m[r] + 8.0f;
-          shrink[r] = moves ? ex2(m[r] - (high - 6.0f)) : 1.0f;  // m = -inf: 0
-          if (moves) m[r] = high - 6.0f;
+          const float m = sh.m[r];
+          const bool moves = high > m + 8.0f;
+          shrink[r] = moves ? ex2(m - (high - 6.0f)) : 1.0f;  // m = -inf: 0
           l[r] *= shrink[r];
         }
-        together();  // before the maxima are written again
+        if (!together()) break;  // every warp has read the maxima and references
+        if (warp == 0 && lane < kRows) {
+          const float high = fmaxf(fmaxf(sh.top[0][lane], sh.top[1][lane]), fmaxf(sh.top[2][lane], sh.top[3][lane]));
+          if (high > sh.m[lane] + 8.0f) sh.m[lane] = high - 6.0f;
+        }
+        if (!together()) break;  // before the maxima are written again
         if (i > 0) {
           // (scores of tile c complete after the sum of tile c - 2, so this barrier is at most one phase behind)
-          wait(&b.o[x ^ 1], ((c - 1) >> 1) & 1);
-          if (any(!ok)) {
-            ok = false;
-            break;
-          }
+          if (!wait(&b.o[x ^ 1], ((c - 1) >> 1) & 1)) break;
 #pragma unroll 1
-          for (int y = 0; y < S::kUnits * kParts; ++y) {
-            const uint32_t at = lanes + 128 + y / kParts * 64 + y % kParts * kRows;
+          for (int y = 0; y < S::kUnits * (S::kColumns / 16); ++y) {
+            const uint32_t at = lanes + 128 + y / (S::kColumns / 16) * 64 + y % (S::kColumns / 16) * 16;
             uint32_t o[16];
             tmem_ld16(o, at);
             tmem_wait_ld();
             settle16(o);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * shrink[r]);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * shrink[j % kRows]);
             tmem_st16(at, o);
           }
           tmem_wait_st();
         }
       }
+      float w[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; r += 4) {
-        float w[4];
+        const float4 m = four(&sh.m[r]);
+        const float base[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          w[k] = ex2(s[r + k] - (m[r + k] == -INFINITY ? 0.0f : m[r + k]));
-          l[r + k] = fmaf(w[k], e.z, l[r + k]);
+          w[r + k] = ex2(s[r + k] - (base[k] == -INFINITY ? 0.0f : base[k]));
+          l[r + k] = fmaf(w[r + k], e_z, l[r + k]);
         }
+      }
+      if (i + 1 < nt) prepare(i + 1, s, e_z);
+      if (!ok) break;
+#pragma unroll
+      for (int r = 0; r < kRows; r += 4) {
         uint32_t part[kParts];
-        parts4(w[0], w[1], w[2], w[3], part);
+        parts4(w[r], w[r + 1], w[r + 2], w[r + 3], part);
 #pragma unroll
         for (int y = 0; y < kParts; ++y)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int n = y * kRows + r + k;
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(weights + x * kOperandBytes + n * 128 + (((tid >> 4) ^ (n & 7)) << 4) + (tid & 15)),
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(weights + x * S::kOperandBytes + n * 128 + (((tid >> 4) ^ (n & 7)) << 4) + (tid & 15)),
                          "r"(part[y] >> (8 * k))
                          : "memory");
           }
       }
       fence_proxy_async_smem();
       fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.p[x]);
-      __syncwarp();
+      arrive(&b.p[x]);
     }
     if (!ok) break;
     const uint32_t end = g + nt - 1;
@@ -380,12 +420,13 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
       l[r] = warp_sum(l[r]);
       if (lane == r) sh.top[warp][r] = l[r];
     }
-    together();
+    if (!together()) break;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) l[r] = (sh.top[0][r] + sh.top[1][r]) + (sh.top[2][r] + sh.top[3][r]);
-    together();  // (also: what the rows see has been read)
-    if (more) queries_loaded(later);
-    wait(&b.o[end & 1], (end >> 1) & 1);  // one that ran out leaves the outputs incomplete; the next item's first vote ends the loop
+    const float m = sh.m[lane % kRows];
+    if (!together()) break;  // (also: what the rows see has been read)
+    if (more && !queries_loaded(later)) break;
+    if (!wait(&b.o[end & 1], (end >> 1) & 1)) break;
     const bool whole = it.first && it.last;
     const int slot = it.first ? 1 : 0;
     const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * S::kRows;
@@ -414,10 +455,10 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
       for (int r = 0; r < kRows; ++r)
         if (lane == r && r < rows) {
           if (!whole) {
-            *reinterpret_cast<float2*>(p.part_ml + (at + r) * 2) = make_float2(m[r], l[r]);
+            *reinterpret_cast<float2*>(p.part_ml + (at + r) * 2) = make_float2(m, l[r]);
           } else if (p.lse) {
             const int t = (row0 + r) / p.group, head = it.h * (int)p.group.d + row0 + r - t * (int)p.group.d;
-            p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * 0.69314718055994531f;
+            p.lse[(int64_t)(it.q.q0 + t) * p.q_heads + head] = l[r] == 0.0f ? -INFINITY : (m + log2f(l[r])) * 0.69314718055994531f;
           }
         }
     }
@@ -431,12 +472,12 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared& sh, uint32_t qu
   if (tid == 0 && !goes_on) write_header(p, sh.span, nullptr);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int ROWS>
 __global__ void __launch_bounds__(kThreads, 2) attn8_few(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                                                          const __grid_constant__ CUtensorMap vmap) {
-  using S = Few<DP>;
+  using S = Few<DP, ROWS>;
   extern __shared__ uint8_t raw[];
-  __shared__ FewShared sh;
+  __shared__ FewShared<ROWS> sh;
   Bars& b = sh.b;
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);  // swizzled tiles start on 1024 bytes
   const int warp = threadIdx.x >> 5;
@@ -452,8 +493,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn8_few(const __grid_constant__
       mbar_init(&b.s[x], 1);
       mbar_init(&b.o[x], 1);
       mbar_init(&b.p[x], 4);  // one arrival a warp
+      mbar_init(&b.vote[x], 4);
     }
     mbar_init(&b.q, 4);
+    mbar_init(&b.meet, 4);
+    sh.grown[0] = sh.grown[1] = 0;
     for (int x = 0; x < kScaleTiles; ++x) {
       mbar_init(&b.sc_full[x], 1);
       mbar_init(&b.sc_empty[x], 4);
@@ -474,17 +518,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn8_few(const __grid_constant__
   pdl_wait_and_release();
   find_span<S::kRows, kKeys, kThreads>(p, sh.span);
 
-  const uint32_t queries = smem_addr(smem), weights = queries + S::kUnits * kOperandBytes, keys = weights + 2 * kOperandBytes,
+  const uint32_t queries = smem_addr(smem), weights = queries + S::kUnits * S::kOperandBytes, keys = weights + 2 * S::kOperandBytes,
                  values = keys + S::kKeySlots * kUnitBytes;
   if (warp < kMmaWarp) {
-    few_softmax_role<DT, DP>(p, sh, queries, weights, tmem);
+    few_softmax_role<DT, DP, S>(p, sh, queries, weights, tmem);
   } else if (warp == kLoadWarp) {
     load_role<S>(p, &kmap, sh.span, b, b.k, S::kKeySlots, keys, p.stall);
   } else if (warp == kLoadWarp + 1) {
     load_role<S>(p, &vmap, sh.span, b, b.v, S::kValueSlots, values, false);
     check_blocks(p);
   } else if (warp == kMmaWarp) {
-    few_mma_role<DP>(p, sh, queries, weights, keys, values, tmem);
+    few_mma_role<S>(p, sh, queries, weights, keys, values, tmem);
   } else {
     scale_role<S>(p, sh.span, b, sh.scales);
   }
@@ -500,15 +544,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn8_few(const __grid_constant__
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-template <int DT>
+template <int DT, int ROWS>
 const void* few_of(int dp) {
-  return dp == 256 ? reinterpret_cast<const void*>(&attn8_few<DT, 256>) : reinterpret_cast<const void*>(&attn8_few<DT, 128>);
+  return dp == 256 ? reinterpret_cast<const void*>(&attn8_few<DT, 256, ROWS>) : reinterpret_cast<const void*>(&attn8_few<DT, 128, ROWS>);
 }
 
 }  // namespace
 
-const void* attn8_few_kernel(bool bf16, int padded_dim) { return bf16 ? few_of<kBF16>(padded_dim) : few_of<kF16>(padded_dim); }
+const void* attn8_few_kernel(bool bf16, int padded_dim, int rows) {
+  if (rows == 8) return bf16 ? few_of<kBF16, 8>(padded_dim) : few_of<kF16, 8>(padded_dim);
+  return bf16 ? few_of<kBF16, 16>(padded_dim) : few_of<kF16, 16>(padded_dim);
+}
 
-size_t attn8_few_smem(int padded_dim) { return (padded_dim == 256 ? Few<256>::kBytes : Few<128>::kBytes) + 1024; }
+size_t attn8_few_smem(int padded_dim, int rows) {
+  if (rows == 8) return (padded_dim == 256 ? Few<256, 8>::kBytes : Few<128, 8>::kBytes) + 1024;
+  return (padded_dim == 256 ? Few<256, 16>::kBytes : Few<128, 16>::kBytes) + 1024;
+}
 
 }  // namespace ar

@@ -193,9 +193,9 @@ const void* attn_tma_kernel(bool bf16, int padded_dim, float cap, bool bias);  /
 size_t attn_tma_smem(int padded_dim);
 int attn_tma_rows(int padded_dim);  // query rows of an item
 
-constexpr int kAttn8FewRows = 16, kAttn8FewThreads = 256;  // rows of an item; two CTAs an SM
-const void* attn8_few_kernel(bool bf16, int padded_dim);  // for few rows a request
-size_t attn8_few_smem(int padded_dim);
+constexpr int kAttn8FewRows = 16, kAttn8FewThreads = 256;  // most rows of an item; two CTAs an SM
+const void* attn8_few_kernel(bool bf16, int padded_dim, int rows);  // for few rows a request: items of 8 or 16
+size_t attn8_few_smem(int padded_dim, int rows);
 constexpr int kAttn8Threads = 512;  // the kernel's division of registers waits for as many
 const void* attn8_tma_kernel(bool bf16, int padded_dim, bool few, float cap, bool bias);  // over a cache in 8 bits; few: items of 128 rows
 size_t attn8_tma_smem();

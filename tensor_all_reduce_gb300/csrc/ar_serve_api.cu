@@ -509,7 +509,7 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   const int64_t rows = n * (hq / hk);
   const bool few = tma && scales && rows <= ar::kAttn8FewRows * r, half = scales && rows <= 64 * r;
   p.spans = few ? 2 * ctx->sm_count : tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
-  p.tile_rows = !tma ? kMmaRows : few ? ar::kAttn8FewRows : half ? 128 : ar::attn_tma_rows(dp);
+  p.tile_rows = !tma ? kMmaRows : few ? (rows <= 8 * r ? 8 : ar::kAttn8FewRows) : half ? 128 : ar::attn_tma_rows(dp);
   p.part_dim = part_dim(a->head_dim);
   const Workspace w = workspace_of(p.spans, p.tile_rows, p.part_dim);
   char* base = static_cast<char*>(a->workspace);
@@ -523,7 +523,7 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
   const unsigned spans = (unsigned)p.spans;
   ar_status st;
   if (few)
-    st = launch(ctx, ar::attn8_few_kernel(bf16, dp), spans, ar::kAttn8FewThreads, 1, args, ar::attn8_few_smem(dp), stream);
+    st = launch(ctx, ar::attn8_few_kernel(bf16, dp, p.tile_rows), spans, ar::kAttn8FewThreads, 1, args, ar::attn8_few_smem(dp, p.tile_rows), stream);
   else if (tma && scales)
     st = launch(ctx, ar::attn8_tma_kernel(bf16, dp, half, a->softcap, bias), spans, ar::kAttn8Threads, 1, args, ar::attn8_tma_smem(), stream);
   else if (tma)
@@ -688,7 +688,8 @@ cudaError_t serve_prepare(ar_ctx* ctx) {
         keep(cudaFuncSetAttribute(rope_vec_kernel(b, d, mode == 1 ? 8 : 4, mode == 0), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rope_smem_most()));
     keep(cudaFuncGetAttributes(&fa, attn_combine_kernel(b)));
     for (int dp : {128, 256})
-      keep(cudaFuncSetAttribute(attn8_few_kernel(b, dp), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_few_smem(dp)));
+      for (int rows : {8, 16})
+        keep(cudaFuncSetAttribute(attn8_few_kernel(b, dp, rows), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn8_few_smem(dp, rows)));
     for (int i = 0; i < 3; ++i)
       for (int ext = 0; ext < 6; ++ext) {  // no cap, a cap, a wide one
         const float cap = (float)(ext >> 1) * 50.0f;
