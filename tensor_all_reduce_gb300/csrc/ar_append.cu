@@ -3,6 +3,7 @@
 #include "ar_angle.cuh"
 #include "ar_append.cuh"
 #include "ar_staged.cuh"
+#include "ar_two.cuh"
 
 namespace ar {
 namespace {
@@ -185,85 +186,106 @@ struct AppendVec {
     task = group * (kVecWarps / plan.warps) + task_of_group;
     if (!busy()) return;
     const Place at = place(u);
+    const int t0 = token(first, 0), left = there ? u.n - t0 : 0;
+    const uint16_t* src = at.rows + (u.row + t0) * at.ts + c0 * 4;
+    const int64_t step = kRowsAStep * at.ts;
+    const int other = (c1 - c0) * 4;
 #pragma unroll
-    for (int k = 0; k < kSlots; ++k) {
-      const int t = token(first, k);
+    for (int k = 0; k < kSlots; ++k, src += step) {
       raw[k][0] = raw[k][1] = make_uint2(0, 0);
-      if (t < u.n && there) {
-        const uint16_t* src = at.rows + (u.row + t) * at.ts;
-        raw[k][0] = ld_v2_once(src + c0 * 4);
-        raw[k][1] = ld_v2_once(src + c1 * 4);
+      if (k * kRowsAStep < left) {
+        raw[k][0] = ld_v2_once(src);
+        raw[k][1] = ld_v2_once(src + other);
       }
     }
     old = u.held ? clamp_scale(*reinterpret_cast<const volatile float*>(at.scale)) : kScaleLow;
   }
 
-  // The rows in `raw` as they are stored, and the largest magnitude among them.
-  __device__ __forceinline__ float values(const AppendUnit& u, int first, float (&f)[kSlots][8]) {
+  // The rows in `raw` as they are stored, two elements a register pair, and the largest magnitude among them.
+  __device__ __forceinline__ float values(const AppendUnit& u, int first, uint64_t (&f)[kSlots][4]) {
     const bool v = task >= p.heads;
+    const int t0 = token(first, 0), rows = u.n - first - sub * kTokens;  // rows of the warp
 #pragma unroll
     for (int k = 0; k < kSlots; ++k)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        f[k][4 * i] = to_f32<DT>(raw[k][i].x & 0xffffu);
-        f[k][4 * i + 1] = to_f32<DT>(raw[k][i].x >> 16);
-        f[k][4 * i + 2] = to_f32<DT>(raw[k][i].y & 0xffffu);
-        f[k][4 * i + 3] = to_f32<DT>(raw[k][i].y >> 16);
+        f[k][2 * i] = two(to_f32<DT>(raw[k][i].x & 0xffffu), to_f32<DT>(raw[k][i].x >> 16));
+        f[k][2 * i + 1] = two(to_f32<DT>(raw[k][i].y & 0xffffu), to_f32<DT>(raw[k][i].y >> 16));
       }
     if (!v && p.weight) {
-      float w[8];
+      uint64_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = sh.weight[c0 * 4 + i];
-        w[4 + i] = sh.weight[c1 * 4 + i];
+      for (int i = 0; i < 2; ++i) {
+        w[i] = two(sh.weight[c0 * 4 + 2 * i], sh.weight[c0 * 4 + 2 * i + 1]);
+        w[2 + i] = two(sh.weight[c1 * 4 + 2 * i], sh.weight[c1 * 4 + 2 * i + 1]);
       }
 #pragma unroll
       for (int k = 0; k < kSlots; ++k) {
-        if (first + sub * kTokens + k * kRowsAStep >= u.n) break;  // no row of the warp
-        float ss = 0.0f;
+        if (k * kRowsAStep >= rows) break;
+        uint64_t s2 = mul2(f[k][0], f[k][0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[k][i], f[k][i], ss);
+        for (int i = 1; i < 4; ++i) s2 = fma2(f[k][i], f[k][i], s2);
+        float a, b;
+        untwo(s2, a, b);
+        float ss = a + b;
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float r = rsqrtf(ss * p.inv_dim + p.eps);
+        const uint64_t r2 = two(r, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[k][i] = f[k][i] * r * w[i];
+        for (int i = 0; i < 4; ++i) f[k][i] = mul2(mul2(f[k][i], r2), w[i]);
       }
     }
     if (!v && p.half) {
       // chunk c0's first frequency; pairs of neighbours: two a chunk
       const int f0 = HALVES ? c0 * 4 : c0 * 2;
-      if (f0 < p.half && there)
+      if (f0 < p.half && there) {
+        const float* at = cosines + (t0 - first) * plan.pitch + f0;
+        const int to_sines = plan.round_tokens * plan.pitch;
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-          const int t = token(first, k);
-          if (t >= u.n) continue;
-          const float4 c = *reinterpret_cast<const float4*>(cosines + (t - first) * plan.pitch + f0);
-          const float4 s = *reinterpret_cast<const float4*>(sines() + (t - first) * plan.pitch + f0);
-          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        for (int k = 0; k < kSlots; ++k, at += kRowsAStep * plan.pitch) {
+          if (t0 + k * kRowsAStep >= u.n) break;
+          if constexpr (HALVES) {  // of a multiple of 4
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(at), s = *reinterpret_cast<const ulonglong2*>(at + to_sines);
+            const uint64_t x0 = f[k][0], x1 = f[k][1], y0 = f[k][2], y1 = f[k][3], minus = two(-1.0f, -1.0f);
+            f[k][0] = fma2(x0, c.x, mul2(mul2(y0, minus), s.x));
+            f[k][1] = fma2(x1, c.y, mul2(mul2(y1, minus), s.y));
+            f[k][2] = fma2(y0, c.x, mul2(x0, s.x));
+            f[k][3] = fma2(y1, c.y, mul2(x1, s.y));
+          } else {
+            const float4 c = *reinterpret_cast<const float4*>(at), s = *reinterpret_cast<const float4*>(at + to_sines);
+            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (f0 + i >= p.half) continue;
-            float &a = HALVES ? f[k][i] : f[k][2 * i], &b = HALVES ? f[k][4 + i] : f[k][2 * i + 1];
-            const float x = a, y = b;
-            a = x * cs[i] - y * sn[i];
-            b = y * cs[i] + x * sn[i];
+            for (int i = 0; i < 4; ++i) {
+              if (f0 + i >= p.half) continue;  // an element that does not turn keeps its value, infinities included
+              float x, y;
+              untwo(f[k][i], x, y);
+              f[k][i] = two(x * cs[i] - y * sn[i], y * cs[i] + x * sn[i]);
+            }
           }
         }
+      }
     }
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < kSlots; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[k][i]));
-    if (__any_sync(0xffffffffu, top > 3.402823466e38f)) {  // infinities do not count
+      for (int i = 0; i < 4; ++i) {
+        float x, y;
+        untwo(f[k][i], x, y);
+        top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+      }
+    if (__any_sync(0xffffffffu, top > 3.402823466e38f)) {  // infinities do not count, and their code is NaN's
       top = 0.0f;
+      const float nan = __uint_as_float(0x7fffffffu);
 #pragma unroll
       for (int k = 0; k < kSlots; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          top = fmaxf(top, finite_magnitude(f[k][i]));
-          if (fabsf(f[k][i]) > 3.402823466e38f) f[k][i] = __uint_as_float(0x7fffffffu);  // their code is NaN's
+        for (int i = 0; i < 4; ++i) {
+          float x, y;
+          untwo(f[k][i], x, y);
+          top = fmaxf(top, fmaxf(finite_magnitude(x), finite_magnitude(y)));
+          f[k][i] = two(fabsf(x) > 3.402823466e38f ? nan : x, fabsf(y) > 3.402823466e38f ? nan : y);
         }
     }
     return warp_max_magnitude(top);
@@ -300,15 +322,21 @@ struct AppendVec {
     return inv;
   }
 
-  __device__ __forceinline__ void store(const AppendUnit& u, const Place& at, int first, const float (&f)[kSlots][8], float inv) {
+  __device__ __forceinline__ void store(const AppendUnit& u, const Place& at, int first, const uint64_t (&f)[kSlots][4], float inv) {
+    const int t0 = token(first, 0), left = there ? u.n - t0 : 0, other = (c1 - c0) * 4;
+    uint8_t* dst = at.cache + (u.held + t0) * at.ps + c0 * 4;
+    const int64_t step = kRowsAStep * at.ps;
+    const uint64_t inv2 = two(inv, inv);
 #pragma unroll
-    for (int k = 0; k < kSlots; ++k) {
-      const int t = token(first, k);
-      if (t >= u.n || !there) continue;
-      uint8_t* row = at.cache + (u.held + t) * at.ps;
+    for (int k = 0; k < kSlots; ++k, dst += step) {
+      if (k * kRowsAStep >= left) break;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<uint32_t*>(row + (i ? c1 : c0) * 4) = e4m3x2(f[k][4 * i] * inv, f[k][4 * i + 1] * inv) | (e4m3x2(f[k][4 * i + 2] * inv, f[k][4 * i + 3] * inv) << 16);
+      for (int i = 0; i < 2; ++i) {
+        float a, b, c, d;
+        untwo(mul2(f[k][2 * i], inv2), a, b);
+        untwo(mul2(f[k][2 * i + 1], inv2), c, d);
+        *reinterpret_cast<uint32_t*>(dst + (i ? other : 0)) = e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+      }
     }
   }
 
@@ -328,7 +356,7 @@ struct AppendVec {
     AppendWalk walk;
     walk.start(p, sh.span, plan.parts);
     AppendUnit u;
-    float f[kSlots][8];
+    uint64_t f[kSlots][4];
     while (walk.next(p, u)) {
       if (u.block < 0) continue;
       const int g0 = u.part * groups / plan.parts, g1 = (u.part + 1) * groups / plan.parts;
@@ -408,13 +436,13 @@ AppendPlan append_plan(const AppendParams& p, int sm_count) {
   plan.pitch = (p.half + 3) / 4 * 4;
   // blocks that can get tokens: a request's first and last one, and whole ones between
   const int64_t most = p.tokens / page + 2 * (int64_t)p.requests < p.tokens ? p.tokens / page + 2 * (int64_t)p.requests : p.tokens;
-  // shares of a block's heads, until there are about four units an SM
+  // shares of a block's heads, until there are about six units a resident CTA (16384 video tokens with two 107 us)
   const int groups = (2 * p.heads + kVecWarps / plan.warps - 1) / (kVecWarps / plan.warps);
   const int64_t usual = p.tokens / page + p.requests < p.tokens ? p.tokens / page + p.requests : p.tokens;
   plan.parts = 1;
-  while (plan.parts < groups && usual * plan.parts < 4 * sm_count) ++plan.parts;
+  while (plan.parts < groups && usual * plan.parts < 12 * sm_count) ++plan.parts;
   const int64_t grid = most * plan.parts;
-  plan.ctas = (unsigned)(grid < (int64_t)sm_count * 4 ? grid : (int64_t)sm_count * 4);
+  plan.ctas = (unsigned)(grid < (int64_t)sm_count * 2 ? grid : (int64_t)sm_count * 2);
   return plan;
 }
 
