@@ -36,8 +36,8 @@ namespace {
 constexpr int kThreads = kAttn8Threads;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kScaleWarp = 11, kConvertWarp = 12;  // kLoadWarp + 1: values; four warps convert
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // of 128 a thread at launch
-static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "the split uses what the launch has");
+constexpr int kSoftmaxRegs = 176, kIssueRegs = 104, kConvertRegs = 56;  // of 128 a thread at launch
+static_assert(2 * kSoftmaxRegs + kIssueRegs + kConvertRegs == 4 * 128, "the split uses what the launch has");
 constexpr int kRoomBytes = 13 * kUnitBytes;  // queries, fp16 values, rings
 
 // FEW: for batches of few rows a request: items of 128 rows leave half of the queries' room to the rings, whose
@@ -860,8 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
 
   const uint32_t queries = smem_addr(smem), wide = queries + S::kQueryBytes, keys = wide + S::kWide * S::kWideBytes,
                  values = keys + S::kKeySlots * kUnitBytes;
-  if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp >= kConvertWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+    convert_role<S>(p, span, b, values, wide);
+  } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == kLoadWarp) {
       load_role<S>(p, &kmap, span, b, b.k, S::kKeySlots, keys, p.stall);
     } else if (warp == kLoadWarp + 1) {
@@ -869,10 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tma(const __grid_constant__
       check_blocks(p);
     } else if (warp == kMmaWarp) {
       mma_role<S>(p, span, b, queries, keys, wide, tmem);
-    } else if (warp == kScaleWarp) {
-      scale_role<S>(p, span, b, scales);
     } else {
-      convert_role<S>(p, span, b, values, wide);
+      scale_role<S>(p, span, b, scales);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
