@@ -93,7 +93,7 @@ struct AppendParams {
   const void* v;
   int64_t k_ts, k_hs, v_ts, v_hs;
   const void* weight;  // of k; NULL: no norm
-  float eps, inv_dim;
+  float eps;
   int gemma, half, pairs, axes, dealt;  // half: frequencies, rot_dim / 2
   FastDiv half_div;
   int sections[AR_MAX_ROPE_AXES];

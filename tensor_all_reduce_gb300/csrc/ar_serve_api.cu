@@ -616,7 +616,6 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* a, vo
   p.v_hs = a->v_head_stride;
   p.weight = a->k_weight;
   p.eps = a->eps;
-  p.inv_dim = (float)(1.0 / (double)d);
   p.gemma = a->gemma != 0;
   p.half = half;
   p.half_div = ar::fast_div(half ? (uint32_t)half : 1);
