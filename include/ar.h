@@ -460,7 +460,8 @@ ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_arg
  *
  * Where a scale grows, the held codes are rounded to it.  Powers of two make that exact but for
  * codes that become subnormal, and cost an E4M3 value no precision.  A held block's scale that is no
- * finite positive number counts as 2^-32.
+ * finite positive number counts as 2^-32 (a held scale that is no power of two stays as long as it is large enough; y is
+ * then multiplied by its fp32 reciprocal).
  *
  * Not touched: blocks that get no token, places of a block behind its last token.  A request whose
  * length is below n (or negative), tokens behind its table's columns, and tokens of a block outside the
@@ -511,10 +512,10 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* args,
  * ar_paged_append_fp8's: any between 2^-32 and 2^32; others count as the nearer of the two, NaN as 2^-32.
  * Scales of blocks that no row sees are not used; codes behind a request's length may be NaN.
  *
- * The products run on the 8-bit codes themselves.  q is split into E4M3 and E5M2 parts, exactly but for
- * elements 2^-16 (bf16; fp16: 2^-14) below the row's largest, which keep an absolute error of 2^-25 of it; the weights
- * likewise, rounded to 8 bits (bf16; fp16: 11), those 2^-23 below the row's largest product of weight and scale to
- * nothing.  Sums are fp32.  (The general form rounds the weights to dtype instead.)
+ * The scores' products run on the 8-bit codes themselves: q is split into parts of 8 bits, exactly but for elements
+ * far below the row's largest, which keep an absolute error of 2^-24 of it.  A weight is held times its v scale:
+ * rounded to fp16 or to 14 bits (by the general form to dtype), and to nothing 2^-24 below the row's largest such
+ * product.  Sums are fp32.
  */
 typedef struct {
   ar_paged_attention_args base;         /* k_cache and v_cache: E4M3 codes */

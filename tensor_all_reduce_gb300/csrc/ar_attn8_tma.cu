@@ -19,6 +19,13 @@
 // and m kept so that the largest w of a row lies between 2^6 and 2^14, inside fp16's range.  Scales are the
 // same for eight keys in a row at least; a warp of its own looks them up, tiles ahead, and leaves the k scale, t
 // and 1 / vs of each eight keys of a tile in a ring in shared memory.
+//
+// Measured on GB300 with the joining kernel: 4096 tokens over 28000 (12 heads, 2 key heads of 128, bf16) 742 to 750 us,
+// 1010 TFLOP/s (16-bit cache 510 to 530); 2 x 1024 tokens over 8000 (heads of 256) 250 us (154); six prompts of up to
+// 1500 81 us (48); 17 requests, two of 700 tokens, window and cap 71 us (47).  The bound is the hand-over between the
+// warps: 297 tiles an SM whose matrix instructions and softmax are left out still take 445 us, with the matrix
+// instructions 640, with the softmax and without the conversion 715.  What the 16-bit kernel has over it: a third less
+// for a softmax warp to issue (scales), and no warps that convert beside it.
 #include <cuda.h>
 
 #include <type_traits>
@@ -40,8 +47,8 @@ constexpr int kSoftmaxRegs = 176, kIssueRegs = 104, kConvertRegs = 56;  // of 12
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kConvertRegs == 4 * 128, "the split uses what the launch has");
 constexpr int kRoomBytes = 13 * kUnitBytes;  // queries, fp16 values, rings
 
-// FEW: for batches of few rows a request: items of 128 rows leave half of the queries' room to the rings, whose
-// depth is what such calls are bound by.
+// FEW: for batches of 17 to 64 rows a request: items of 128 rows leave half of the queries' room to the rings (64
+// single tokens of 48 heads over up to 9000, before they had a kernel of their own: 302 us, with items of 128 rows 273).
 template <int DT, int DP, bool FEW>
 struct Shape {
   static constexpr int kRows = DP == 256 || FEW ? 128 : 256;  // rows of an item

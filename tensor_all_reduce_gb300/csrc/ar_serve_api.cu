@@ -505,7 +505,8 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
           ar::attn_tensor_map(ctx->encode_tensor_map, &vmap, a->v_cache, type, d, pg, hk, a->num_blocks, a->v_page_stride, a->v_head_stride,
                               a->v_block_stride, box);
   }
-  // Over 8 bits: batches of few rows a request take the kernel for them, then items of 128 rows.
+  // Over 8 bits: batches of up to 16 rows a request take the kernel for them, then items of 128 rows (64 single tokens of
+  // 48 heads, 8 key heads of 128, over up to 9000: 168 us in items of 8 rows, 273 in those of 128, 302 of 256).
   const int64_t rows = n * (hq / hk);
   const bool few = tma && scales && rows <= ar::kAttn8FewRows * r, half = scales && rows <= 64 * r;
   p.spans = few ? 2 * ctx->sm_count : tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
