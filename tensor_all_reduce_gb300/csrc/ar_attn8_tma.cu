@@ -41,7 +41,7 @@ namespace ar {
 namespace {
 
 constexpr int kThreads = kAttn8Threads;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kScaleWarp = 11, kConvertWarp = 12;  // kLoadWarp + 1: values; four warps convert
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 12;  // kLoadWarp + 1: values; 11 is idle; four warps convert
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftmaxRegs = 176, kIssueRegs = 104, kConvertRegs = 56;  // of 128 a thread at launch
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kConvertRegs == 4 * 128, "the split uses what the launch has");
