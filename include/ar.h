@@ -510,7 +510,10 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* args,
  * ar_paged_attention over an 8-bit cache: k_j and v_j are codes times scales, everything else is that
  * call's, its workspace (ar_paged_attention_workspace) too.  The scales need not be
  * ar_paged_append_fp8's: any between 2^-32 and 2^32; others count as the nearer of the two, NaN as 2^-32.
- * Scales of blocks that no row sees are not used; codes behind a request's length may be NaN.
+ * Scales of blocks that no row sees are not used, and their codes of keys and values may be NaN (a block that has left
+ * every row's window may be another request's by now), as may all codes behind a request's length.  A NaN value of
+ * a token that some row sees (ar_paged_append_fp8 stores infinities and NaN as such) makes that row NaN, and may make
+ * others of the same request NaN that do not see it.
  *
  * The scores' products run on the 8-bit codes themselves: q is split into parts of 8 bits, exactly but for elements
  * far below the row's largest, which keep an absolute error of 2^-24 of it.  A weight is held times its v scale:

@@ -75,10 +75,16 @@ struct TileRange {
   __device__ __forceinline__ int tile(int i) const { return i < pre ? i : lo + (i - pre); }
 };
 
+// The keys that some row of a query tile sees.
+template <int ROWS>
+__device__ __forceinline__ KeyRange tile_keys(const AttnParams& p, const Request& q, int qt) {
+  const int row0 = qt * ROWS, rows = q.n * (int)p.group.d;  // at most 2^30
+  return key_range(p, q, row0 / p.group, (min(row0 + ROWS, rows) - 1) / p.group + 1);
+}
+
 template <int ROWS, int KT>
 __device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Request& q, int qt) {
-  const int row0 = qt * ROWS, rows = q.n * (int)p.group.d;  // at most 2^30
-  const KeyRange k = key_range(p, q, row0 / p.group, (min(row0 + ROWS, rows) - 1) / p.group + 1);
+  const KeyRange k = tile_keys<ROWS>(p, q, qt);
   TileRange t;
   t.pre = (q.prefix + KT - 1) / KT;
   t.lo = max(k.low / KT, t.pre);

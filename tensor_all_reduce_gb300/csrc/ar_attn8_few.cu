@@ -126,28 +126,35 @@ __device__ void few_mma_role(const AttnParams& p, FewShared<S::kRows>& sh, uint3
     }
     if (one) mma_commit(&b.s[x]);
   };
-  // Values behind the request's end become zeros: the rest of a box holds whatever the cache does, and a weight
-  // of 0 does not cancel a NaN.
-  auto clear_tail = [&](int left) {
-    if (left >= kKeys) return;
-    const int lo = max(left, 0), hi = min((lo + p.box_rows - 1) / p.box_rows * p.box_rows, kKeys);
+  // Values of keys that no row of the item sees become zeros: in blocks that have left every row's window, and in the
+  // last box behind the request's end (boxes behind it come as zeros), the cache holds anything, and a weight of 0 does
+  // not cancel a NaN.
+  KeyRange seen = {0, 0};
+  auto has_unseen = [&](int key0) { return key0 + kKeys > it.q.prefix && (key0 + kKeys > seen.high || max(key0, it.q.prefix) < seen.low); };
+  auto clear_unseen = [&](int key0) {
+    const int pre = max(it.q.prefix - key0, 0), lo = min(seen.low - key0, kKeys), hi = min(max(seen.high - key0, 0), kKeys);
+    const int end = min((max(it.q.len - key0, 0) + p.box_rows - 1) / p.box_rows * p.box_rows, kKeys);
     const uint32_t v = values + vs * kUnitBytes;
-    for (int x = lo * 8 + lane; x < hi * 8; x += 32) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + x * 16), "r"(0) : "memory");
+    for (int x = pre * 8 + lane; x < end * 8; x += 32)
+      if (x < lo * 8 || x >= hi * 8) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + x * 16), "r"(0) : "memory");
     fence_proxy_async_smem();
     __syncwarp();
   };
   while (ok && walk.next(p, it)) {
     const int nt = it.end - it.begin;
+    seen = tile_keys<S::kRows>(p, it.q, it.qt);
     if (!wait(&b.q, items & 1)) break;
     scores(g & 1);
     for (int i = 0; ok && i < nt; ++i) {
       if (i + 1 < nt) scores((g + i + 1) & 1);
       if (!ok) break;
       const uint32_t x = (g + i) & 1;
+      const int key0 = it.range.tile(it.begin + i) * kKeys;
+      const bool unseen = has_unseen(key0);
       if (!wait(&b.p[x], ((g + i) >> 1) & 1)) break;
       for (int u = 0; u < S::kUnits; ++u) {
         if (!wait(&b.v.full[vs], vr & 1)) break;
-        clear_tail(it.q.len - it.range.tile(it.begin + i) * kKeys);
+        if (unseen) clear_unseen(key0);
         if (one) {
           const uint64_t a = v_desc + vs * (kUnitBytes / 16), w = w_desc + x * (S::kOperandBytes / 16);
           if (u * 128 < p.head_dim)

@@ -127,8 +127,9 @@ __device__ __forceinline__ bool single_half(const Item& it) {
 }
 
 // Values to fp16: a thread a key, 16 elements at a time.  Both layouts have 128-byte rows in 128-byte swizzle, so
-// that eight rows' 16 bytes fall into different banks.  Keys behind the request's end become zeros: the rest of a
-// box holds whatever the cache does, and a weight of 0 does not cancel a NaN.
+// that eight rows' 16 bytes fall into different banks.  Keys that no row of the item sees become zeros: behind the
+// request's end and in blocks that have left every row's window the cache holds anything, and a weight of 0 does not
+// cancel a NaN.
 template <class S>
 __device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& b, uint32_t values, uint32_t wide) {
   const int lane = threadIdx.x & 31, row = (int)threadIdx.x - kConvertWarp * 32;
@@ -139,8 +140,11 @@ __device__ void convert_role(const AttnParams& p, const SpanShared& span, Bars& 
   bool ok = true;
   while (ok && walk.next(p, it)) {
     const int nt = it.end - it.begin;
+    const KeyRange seen = tile_keys<S::kRows>(p, it.q, it.qt);
     for (int t = 0; ok && t < nt; ++t) {
-      const bool there = row < it.q.len - it.range.tile(it.begin + t) * kKeys;
+      const int key0 = it.range.tile(it.begin + t) * kKeys;
+      const int lo = seen.low - key0, hi = seen.high - key0, pre = it.q.prefix - key0;
+      const bool there = row < pre || (row < hi && row >= lo);
       for (int u = 0; u < S::kUnits; ++u, ++n) {
         const int chunks = min((p.head_dim - u * 128 + 15) / 16, 8);  // may be negative
         const uint32_t to = n & 1;

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
 #pragma unroll
     for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    const KeyRange keys = tile_keys<kRows>(p, it.q, it.qt);
 
     for (int ti = it.begin; ti < it.end; ++ti) {
       const int key0 = it.range.tile(ti) * kKeys;
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma(const __grid_constant__ Att
         using Elem = std::conditional_t<FP8, uint8_t, uint16_t>;
         const Elem *k = nullptr, *v = nullptr;
         float4 scale = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-        if (key < it.q.len) {
+        if (keys.sees(it.q, key)) {  // the others are zeros: a weight of 0 does not cancel a NaN
           int off;
           const int64_t b = block_of(p, it, key, off);
           if (b >= 0) {
