@@ -320,7 +320,7 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, u
           RowView v;
           v.pos = sh.pos[r];
           v.slope = sh.slope[r];
-          s[r] = bend(p, v, s[r] * (sh.factor[r] * e.x), key) + e.y;
+          s[r] = bend(p, v, s[r] * finite_product(e.x, sh.factor[r]), key) + e.y;
         }
       } else {
 #pragma unroll

@@ -509,7 +509,7 @@ __device__ void softmax_role(const AttnParams& p, const SpanShared& span, Softma
         if constexpr (EXT != 0) {  // to products of q and k
 #pragma unroll
           for (int j = 0; j < N; j += 8) {
-            const float f = key_scale((col + j) / 8).x * factor;
+            const float f = finite_product(key_scale((col + j) / 8).x, factor);
 #pragma unroll
             for (int k = 0; k < 8; ++k) s[j + k] *= f;
           }

@@ -29,6 +29,9 @@ __device__ __forceinline__ void from_e4m3x2(uint32_t codes, float& a, float& b) 
   b = to_f32<kF16>(h >> 16);
 }
 
+// Of a k scale and what a row of q was divided by: finite, so that a product of 0 stays 0 under it.
+__device__ __forceinline__ float finite_product(float k, float q) { return fminf(k * q, 3.402823466e38f); }
+
 // What attention needs of a block's scales: the k scale, log2 and reciprocal of the v scale.
 __device__ __forceinline__ float4 load_scales(const AttnParams& p, int64_t block, int h) {
   const float k = clamp_scale(p.k_scale.p[block * p.k_scale.bs + h * p.k_scale.hs]);

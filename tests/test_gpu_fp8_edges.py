@@ -1,7 +1,12 @@
-"""ar_paged_attention_fp8 where a product of 0 is easily lost: NaN codes in blocks that no row sees."""
+"""ar_paged_attention_fp8 where a product of 0 is easily lost: NaN codes in blocks that no row sees, rows of huge
+queries."""
+import math
+
 import pytest
 import torch
 
+import serve8_ref as ref8
+import serve_ref as ref
 import test_gpu_paged_attention_fp8 as pa8
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +60,41 @@ def test_released_blocks_may_hold_nan(ctx, form, batch, prefix, page, d, dtype):
     if page > 1:
         served_by(ctx, form, name)
     pa8.check(ctx, x, causal=False, **kw)
+
+
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("d", [128, 256])
+def test_products_of_zero_with_huge_queries(ctx, form, batch, d):
+    """A key of zeros scores 0 against a row of any size under a scale of its own of any size, whatever bends the scores: its weight is
+    that of a score of 0, beside keys whose scores the cap bounds.  Scores are 0 and the cap, in 32 bits up to 2^-18 of log2
+    units (a cap of 5: 2^-22 of it, tanh from an exponential and a reciprocal), so weights to 2^-18 relative, then rounded."""
+    new, name = batch
+    lens = [n + 90 for n in new]
+    x = pa8.make(new, lens, 4, 2, d, "bf16", seed=3, garbage=0, even=True)
+    x["q"] = torch.where(torch.rand(x["q"].shape, generator=torch.Generator().manual_seed(1)) < 0.5, 2.0 ** 120, 2.0 ** 119).to(x["q"].dtype)
+    x["ks"].fill_(2.0 ** 16)
+    zero = x["kc"].clone().zero_()
+    slopes = torch.tensor([0.5, 0.25, 0.0, 1.5])
+    for kw in (dict(slopes=slopes), dict(softcap=5.0), dict(softcap=100.0), dict(softcap=5.0, slopes=slopes), dict(scale=-0.3), dict(scale=0.0)):
+        pa8.check(ctx, dict(x, kc=zero), **kw)
+        served_by(ctx, form, name)
+    # every third key points along the queries: scores of 0 and of the cap
+    x["kc"] = zero.clone()
+    flat = torch.zeros(x["kc"].shape[0], x["kc"].shape[1], dtype=torch.bool)
+    for row, length in zip(x["table"], lens):
+        for j in range(0, length, 3):
+            flat[row[j // 16], j % 16] = True
+    x["kc"][flat] = pa8.code(2.0)
+    out, _ = pa8.run(ctx, x, scale=d ** -0.5, softcap=5.0)
+    u = ref.half_step(torch.bfloat16)
+    for r, length in enumerate(lens):
+        j = torch.arange(length)
+        at = torch.tensor(x["table"][r])[j // 16], j % 16
+        v = x["vc"][at].view(ref8.E4M3).double() * x["vs"].double()[at[0]][..., None]  # [length, 2, d]
+        pos = torch.arange(length - new[r], length)[:, None]
+        w = torch.where(j <= pos, torch.where(j % 3 == 0, math.exp(5.0), 1.0).double(), 0.0)
+        p = w / w.sum(-1, keepdim=True)
+        for h in range(4):
+            o, spread = p @ v[:, h // 2], p @ v[:, h // 2].abs()
+            got = out[x["cu"][r]:x["cu"][r + 1], h].double()
+            assert ((got - o).abs() <= u * o.abs() + (1 + u) * (u + 2.0 ** -16) * spread + ref.smallest(torch.bfloat16)).all()
