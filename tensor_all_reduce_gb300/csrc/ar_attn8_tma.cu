@@ -7,8 +7,9 @@
 // Scores.  The keys' codes are operands of 8-bit matrix instructions as they are, which run at twice the 16-bit
 // rate, so that q may be a sum of parts of 8 bits at the price of a 16-bit product:
 //   x = hi + lo    bf16 (8 bits): hi = e4m3(x), lo = e5m2(x - hi);  fp16 (11 bits): hi + e4m3(x - hi) + e5m2(rest)
-// E4M3 keeps 4 bits, E5M2 3 and reaches down to 2^-16.  A row of q is scaled by a power of two, so that its
-// largest element lies between 224 and 448: the parts are then exact but for what is 2^-17 of one unit.
+// E4M3 keeps 4 bits, with steps of 2^-9 at least, E5M2 3.  A row of q is scaled by a power of two, so that its
+// largest element lies between 224 and 448: bf16 elements from 2^-6 on (fp16 from 2^-3) are then exact, smaller ones, whose
+// rests of up to 2^-10 have more than 3 bits, off by up to 2^-14, 2^-21.8 of the largest.
 //
 // Values.  A warpgroup turns their codes to fp16, exactly, tile by tile, and the weights are fp16 too whatever
 // the type of q (11 bits).  Parts of 8 bits for the weights as well, without that warpgroup, were slower: an
