@@ -518,8 +518,8 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* args,
  * The scores' products run on the 8-bit codes themselves: q is split into parts of 8 bits, exactly but for elements
  * far below the row's largest (2^-14 of it in bf16, 2^-11 in fp16), which keep an absolute error of up to 2^-21.8 of it
  * (2^-25.8 in the form for few rows a request; the general form splits nothing).  A weight is held times its v scale:
- * rounded to fp16 or to 14 bits (by the general form to dtype), and to nothing 2^-24 below the row's largest such
- * product.  Sums are fp32.
+ * rounded to fp16, for few rows a request to 18 bits (by the general form to dtype), and off by up to 2^-31 of the
+ * row's largest such product where it is far smaller.  Sums are fp32.
  */
 typedef struct {
   ar_paged_attention_args base;         /* k_cache and v_cache: E4M3 codes */

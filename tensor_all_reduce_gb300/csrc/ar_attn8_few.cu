@@ -1,10 +1,11 @@
 // Paged attention over a cache of E4M3 codes for few rows a request (single tokens, drafts): the products turned
 // around, so that keys and values, not queries, are the 128-row operand.
 //
-// An item is up to 8 (or 16) query rows of one request and key head.  With X = hi + mid / 16 + lo / 256 in three
-// E4M3 parts (14 bits), side by side as 32 (48) columns, a tile of 128 keys is two products of 8-bit matrix instructions:
-//   scores   S[key, (part, row)] = K[key, d] Q[(part, row), d]          128 x 32 x head
-//   sums     O[d, (part, row)]  += V[key, d]^T W[(part, row), key]      128 x 32 x 128, for each 128 of the head
+// An item is up to 8 (or 16) query rows of one request and key head.  With Q = hi + mid / 16 + lo / 256 in three
+// E4M3 parts (14 bits) and weights in four, each of the rest of the one before times 32 (18 bits and more), side by side as
+// columns, a tile of 128 keys is two products of 8-bit matrix instructions:
+//   scores   S[key, (part, row)] = K[key, d] Q[(part, row), d]          128 x 32 (48) x head
+//   sums     O[d, (part, row)]  += V[key, d]^T W[key, (part, row)]      128 x 32 (64) x 128, for each 128 of the head
 // Each byte of keys and values is thus read from shared memory once, as it came, and the tensor core's time and
 // the softmax's do not count 128 rows where there are six.  The kernel that keeps queries as the 128-row operand
 // reads keys twice (two parts), turns values to fp16 and was bound by that traffic in shared memory: 64 single
@@ -13,14 +14,18 @@
 // A thread of the softmax warpgroup owns a key: it adds up the parts of the key's scores, and its weights, times
 // the v scale as in ar_attn8_tma.cu, go to shared memory as parts.  The references m of the rows are the same
 // in all threads; they move only when some weight of a tile would exceed 2^8 (one vote a tile), and then so that
-// the row's largest becomes 2^6, which keeps weights down to 2^-24 of the largest.
+// the row's largest becomes 2^6.  The fourth part's steps are 2^-24, so that a weight is off by 2^-31 of the largest
+// at most: many small ones under one that is 2^20 times each keep their sum.  (Three parts a factor of 16 apart held weights
+// to 2^-24 of the largest: of 160000 equal ones that are 2^-20 of it the sum came out 1 % off, at 2^-24 10 to 20 %.)
+// A key's row of weights lies along its parts and rows, 32 (64) bytes that its thread writes 16 at a time.  (As rows along
+// the keys, a byte at a time, the fourth part took the 64 single tokens below from 169 to 189 us.)
 //
-// Measured on GB300 with the joining kernel (48 heads, 8 key heads of 128, bf16, pages of 16): the 64 tokens above 168 us,
-// 4.0 TB/s (676 MB; over a 16-bit cache of twice the bytes 213 to 220 us); pages of 64 164 us, 16 rows a request 296,
-// heads of 64, 96 and 256 175, 186 and 274.  The copies alone take 154 us: a row of 128 bytes lies 1 KB from the next one's,
+// Measured on GB300 with the joining kernel (48 heads, 8 key heads of 128, bf16, pages of 16): the 64 tokens above 162 us,
+// 4.2 TB/s (676 MB; over a 16-bit cache of twice the bytes 213 to 230 us); 12 rows a request 273,
+// heads of 64 and 256 165 and 272.  The copies alone take 154 us: a row of 128 bytes lies 1 KB from the next one's,
 // between the other heads' (where there is one key head 125 us).  The rest is a tile's way through the softmax's one
 // warpgroup, whose instructions wait on each other and on their own fetching.  What it took from 209 us on: the vote
-// looked at a tile later, references in shared memory, 8 rows where 16 are not needed.
+// looked at a tile later, references in shared memory, 8 rows where 16 are not needed, weights in rows of a key.
 //
 // Two CTAs an SM, 256 threads each: a warpgroup for the softmax; warps for the matrix instructions, keys, values
 // and scales.  Work division, parts of split items and their joining are the other kernels'.  Every wait is bounded.
@@ -32,22 +37,25 @@
 namespace ar {
 namespace {
 
-constexpr int kParts = 3;
+constexpr int kParts = 3, kWeightParts = 4;
 constexpr int kThreads = 256;
 constexpr int kMmaWarp = 4, kLoadWarp = 5;  // kLoadWarp + 1: values; the last: scales
 constexpr uint32_t kTmemCols = 256;                         // two score buffers and two sums, 64 columns each
-constexpr float kPart = 16.0f, kPartInv = 0.0625f;          // a part holds the rest of the one before, times 16
+// A part holds the rest of the one before, times this: rests are at most 2^4 for queries (up to 448), 2^3 for weights (up to 256).
+constexpr float kPart = 16.0f, kWeightPart = 32.0f;
 
 // ROWS: 8 or 16 rows of an item.
 template <int DP, int ROWS>
 struct Few {
   static constexpr int kRows = ROWS;
-  static constexpr int kColumns = (kParts * ROWS + 15) / 16 * 16;  // what the matrix instructions take; those behind the parts hold anything
-  static constexpr int kOperandBytes = kColumns * 128;             // queries (of 128 elements) or weights: rows of 128 bytes
+  static constexpr int kScoreColumns = (kParts * ROWS + 15) / 16 * 16;  // what the matrix instructions take; those behind the parts hold anything
+  static constexpr int kSumColumns = kWeightParts * ROWS;
+  static constexpr int kQueryBytes = kScoreColumns * 128;  // of 128 elements: rows of 128 bytes
+  static constexpr int kWeightBytes = kKeys * kSumColumns;  // a row is a key
   static constexpr int kUnits = DP / 128;
   // What two CTAs of an SM have room for.  (Boxes asked into L2 three or six tiles ahead besides: 207 -> 221, 227 us.)
   static constexpr int kKeySlots = 3, kValueSlots = DP == 128 && ROWS == 8 ? 3 : 2;
-  static constexpr int kBytes = (kUnits + 2) * kOperandBytes + (kKeySlots + kValueSlots) * kUnitBytes;
+  static constexpr int kBytes = kUnits * kQueryBytes + 2 * kWeightBytes + (kKeySlots + kValueSlots) * kUnitBytes;
 };
 
 struct Bars {
@@ -77,7 +85,7 @@ struct FewShared {
   uint32_t grown[2];             // the last tile (counted from 1) whose scores outgrew the references
 };
 
-// The three parts of four floats.
+// The parts of four elements of a query.
 __device__ __forceinline__ void parts4(float a, float b, float c, float d, uint32_t (&part)[kParts]) {
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
@@ -88,9 +96,14 @@ __device__ __forceinline__ void parts4(float a, float b, float c, float d, uint3
   }
 }
 
+// Instruction descriptors, fp32 accumulator, 128 rows, E4M3: scores; sums, both of whose operands have rows along the reduction.
+__device__ __forceinline__ uint32_t scores_desc(int columns) { return (1u << 4) | ((uint32_t)(columns >> 3) << 17) | ((128u >> 4) << 24); }
+__device__ __forceinline__ uint32_t sums_desc(int columns) { return scores_desc(columns) | (1u << 15) | (1u << 16); }
+
+// Weights: a row of kSumColumns (32 or 64) bytes a key, eight rows after another, swizzled by as many bytes.
 template <class S>
-__device__ __forceinline__ uint32_t few_desc(bool a_rows_along_k) {
-  return (1u << 4) | ((a_rows_along_k ? 1u : 0u) << 15) | ((uint32_t)(S::kColumns >> 3) << 17) | ((128u >> 4) << 24);
+__device__ __forceinline__ uint64_t weights_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(S::kSumColumns * 8 >> 4) << 32) | (1ull << 46) | ((S::kSumColumns == 32 ? 6ull : 4ull) << 61);
 }
 
 template <class S>
@@ -98,8 +111,8 @@ __device__ void few_mma_role(const AttnParams& p, FewShared<S::kRows>& sh, uint3
   Bars& b = sh.b;
   const int lane = threadIdx.x & 31;
   const int ksteps = (p.head_dim + 31) / 32;
-  const uint32_t idesc_s = few_desc<S>(false), idesc_o = few_desc<S>(true);
-  const uint64_t q_desc = matrix_desc(queries, 16), w_desc = matrix_desc(weights, 16), k_desc = matrix_desc(keys, 16), v_desc = matrix_desc(values, kUnitBytes);
+  const uint32_t idesc_s = scores_desc(S::kScoreColumns), idesc_o = sums_desc(S::kSumColumns);
+  const uint64_t q_desc = matrix_desc(queries, 16), w_desc = weights_desc<S>(weights), k_desc = matrix_desc(keys, 16), v_desc = matrix_desc(values, kUnitBytes);
   const bool one = elect_one();
   Walk<S::kRows, kKeys> walk;
   walk.start(sh.span);
@@ -116,7 +129,7 @@ __device__ void few_mma_role(const AttnParams& p, FewShared<S::kRows>& sh, uint3
     for (int u = 0; u < S::kUnits; ++u) {
       if (!wait(&b.k.full[ks], kr & 1)) return;
       if (one) {
-        const uint64_t a = k_desc + ks * (kUnitBytes / 16), q = q_desc + u * (S::kOperandBytes / 16);
+        const uint64_t a = k_desc + ks * (kUnitBytes / 16), q = q_desc + u * (S::kQueryBytes / 16);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           if (u * 4 + s < ksteps) mma_8bit(tmem + x * 64, a + s * 2, q + s * 2, idesc_s, u > 0 || s > 0);
@@ -156,10 +169,10 @@ __device__ void few_mma_role(const AttnParams& p, FewShared<S::kRows>& sh, uint3
         if (!wait(&b.v.full[vs], vr & 1)) break;
         if (unseen) clear_unseen(key0);
         if (one) {
-          const uint64_t a = v_desc + vs * (kUnitBytes / 16), w = w_desc + x * (S::kOperandBytes / 16);
+          const uint64_t a = v_desc + vs * (kUnitBytes / 16), w = w_desc + x * (S::kWeightBytes / 16);
           if (u * 128 < p.head_dim)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) mma_8bit(tmem + 128 + u * 64, a + ((s * 32 * 128) >> 4), w + s * 2, idesc_o, i > 0 || s > 0);
+            for (int s = 0; s < 4; ++s) mma_8bit(tmem + 128 + u * 64, a + ((s * 32 * 128) >> 4), w + ((s * 32 * S::kSumColumns) >> 4), idesc_o, i > 0 || s > 0);
           mma_commit(&b.v.empty[vs]);
         }
         if (++vs == S::kValueSlots) vs = 0, ++vr;
@@ -176,8 +189,8 @@ __device__ void few_mma_role(const AttnParams& p, FewShared<S::kRows>& sh, uint3
   }
 }
 
-// The parts of the rows in tensor memory, added up.
-__device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[16]) {
+// The parts of the rows in tensor memory, added up: of scores and of weighted sums.
+__device__ __forceinline__ void load_scores(uint32_t addr, float (&f)[16]) {
   uint32_t a[32], c[16];
   tmem_ld32(a, addr);
   tmem_ld16(c, addr + 32);
@@ -185,15 +198,32 @@ __device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[16]) {
   settle(a);
   settle16(c);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) f[r] = fmaf(fmaf(__uint_as_float(c[r]), kPartInv, __uint_as_float(a[16 + r])), kPartInv, __uint_as_float(a[r]));
+  for (int r = 0; r < 16; ++r) f[r] = fmaf(fmaf(__uint_as_float(c[r]), 1.0f / kPart, __uint_as_float(a[16 + r])), 1.0f / kPart, __uint_as_float(a[r]));
 }
-__device__ __forceinline__ void load_rows(uint32_t addr, float (&f)[8]) {
+__device__ __forceinline__ void load_scores(uint32_t addr, float (&f)[8]) {
   uint32_t a[32];
   tmem_ld32(a, addr);
   tmem_wait_ld();
   settle(a);
 #pragma unroll
-  for (int r = 0; r < 8; ++r) f[r] = fmaf(fmaf(__uint_as_float(a[16 + r]), kPartInv, __uint_as_float(a[8 + r])), kPartInv, __uint_as_float(a[r]));
+  for (int r = 0; r < 8; ++r) f[r] = fmaf(fmaf(__uint_as_float(a[16 + r]), 1.0f / kPart, __uint_as_float(a[8 + r])), 1.0f / kPart, __uint_as_float(a[r]));
+}
+template <int ROWS>
+__device__ __forceinline__ void load_sums(uint32_t addr, float (&f)[ROWS]) {
+#pragma unroll
+  for (int at = kWeightParts * ROWS - 32; at >= 0; at -= 32) {  // the last parts first
+    uint32_t a[32];
+    tmem_ld32(a, addr + at);
+    tmem_wait_ld();
+    settle(a);
+#pragma unroll
+    for (int y = 32 / ROWS - 1; y >= 0; --y)
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const float part = __uint_as_float(a[y * ROWS + r]);
+        f[r] = at + y * ROWS == (kWeightParts - 1) * ROWS ? part : fmaf(f[r], 1.0f / kWeightPart, part);
+      }
+  }
 }
 
 template <int DT, int DP, class S>
@@ -267,7 +297,7 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, u
 #pragma unroll
       for (int x = 0; x < kParts; ++x) {
         const int n = x * kRows + r;
-        sts_v2(queries + (col >> 7) * S::kOperandBytes + n * 128 + ((((col & 127) >> 4) ^ (n & 7)) << 4) + (col & 8), lo[x], hi[x]);
+        sts_v2(queries + (col >> 7) * S::kQueryBytes + n * 128 + ((((col & 127) >> 4) ^ (n & 7)) << 4) + (col & 8), lo[x], hi[x]);
       }
       if (col == 0) {
         const RowView v = row_view(p, it, it.qt * S::kRows + r);
@@ -311,7 +341,7 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, u
       const float4 e = sh.scales[stage][tid >> 3];
       arrive(&b.sc_empty[stage]);
       e_z = e.z;
-      load_rows(lanes + x * 64, s);
+      load_scores(lanes + x * 64, s);
       const int key0 = it.range.tile(it.begin + i) * kKeys, key = key0 + tid, prefix = it.q.prefix;
       const bool edge = !((key0 + kKeys <= hi && key0 >= lo) || key0 + kKeys <= prefix);
       if (bent) {
@@ -378,8 +408,8 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, u
           // (scores of tile c complete after the sum of tile c - 2, so this barrier is at most one phase behind)
           if (!wait(&b.o[x ^ 1], ((c - 1) >> 1) & 1)) break;
 #pragma unroll 1
-          for (int y = 0; y < S::kUnits * (S::kColumns / 16); ++y) {
-            const uint32_t at = lanes + 128 + y / (S::kColumns / 16) * 64 + y % (S::kColumns / 16) * 16;
+          for (int y = 0; y < S::kUnits * (S::kSumColumns / 16); ++y) {
+            const uint32_t at = lanes + 128 + y / (S::kSumColumns / 16) * 64 + y % (S::kSumColumns / 16) * 16;
             uint32_t o[16];
             tmem_ld16(o, at);
             tmem_wait_ld();
@@ -404,19 +434,24 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, u
       }
       if (i + 1 < nt) prepare(i + 1, s, e_z);
       if (!ok) break;
+      // the key's row, 16 bytes at a time: two parts of 8 rows, or one of 16
+      const uint32_t row = weights + x * S::kWeightBytes + tid * S::kSumColumns;
 #pragma unroll
-      for (int r = 0; r < kRows; r += 4) {
-        uint32_t part[kParts];
-        parts4(w[r], w[r + 1], w[r + 2], w[r + 3], part);
+      for (int chunk = 0; chunk < S::kSumColumns / 16; ++chunk) {
+        uint32_t part[4];
 #pragma unroll
-        for (int y = 0; y < kParts; ++y)
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 4 % kRows;
+          part[k] = codes4<false>(w[r], w[r + 1], w[r + 2], w[r + 3]);
+          if (chunk * 16 + k * 4 < (kWeightParts - 1) * kRows) {
+            minus_codes4(part[k], w[r], w[r + 1], w[r + 2], w[r + 3]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int n = y * kRows + r + k;
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(weights + x * S::kOperandBytes + n * 128 + (((tid >> 4) ^ (n & 7)) << 4) + (tid & 15)),
-                         "r"(part[y] >> (8 * k))
-                         : "memory");
+            for (int e = 0; e < 4; ++e) w[r + e] *= kWeightPart;
           }
+        }
+        const int swizzle = S::kSumColumns == 32 ? (tid >> 2) & 1 : (tid >> 1) & 3;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((chunk ^ swizzle) << 4)), "r"(part[0]), "r"(part[1]), "r"(part[2]), "r"(part[3])
+                     : "memory");
       }
       fence_proxy_async_smem();
       fence_before();
@@ -447,7 +482,7 @@ __device__ void few_softmax_role(const AttnParams& p, FewShared<S::kRows>& sh, u
 #pragma unroll 1
     for (int u = 0; u < S::kUnits; ++u) {
       float o[kRows];
-      load_rows(lanes + 128 + u * 64, o);
+      load_sums(lanes + 128 + u * 64, o);
       const int d = u * 128 + tid;
       if (d < p.head_dim) {
 #pragma unroll
@@ -532,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn8_few(const __grid_constant__
   pdl_wait_and_release();
   find_span<S::kRows, kKeys, kThreads>(p, sh.span);
 
-  const uint32_t queries = smem_addr(smem), weights = queries + S::kUnits * S::kOperandBytes, keys = weights + 2 * S::kOperandBytes,
+  const uint32_t queries = smem_addr(smem), weights = queries + S::kUnits * S::kQueryBytes, keys = weights + 2 * S::kWeightBytes,
                  values = keys + S::kKeySlots * kUnitBytes;
   if (warp < kMmaWarp) {
     few_softmax_role<DT, DP, S>(p, sh, queries, weights, tmem);

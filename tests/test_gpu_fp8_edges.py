@@ -1,5 +1,5 @@
-"""ar_paged_attention_fp8 where a product of 0 is easily lost: NaN codes in blocks that no row sees, rows of huge
-queries."""
+"""ar_paged_attention_fp8 where a product of 0 or a small weight is easily lost: NaN codes in blocks that no row sees, rows of huge
+queries, one weight far above very many others."""
 import math
 
 import pytest
@@ -98,3 +98,44 @@ def test_products_of_zero_with_huge_queries(ctx, form, batch, d):
             o, spread = p @ v[:, h // 2], p @ v[:, h // 2].abs()
             got = out[x["cu"][r]:x["cu"][r + 1], h].double()
             assert ((got - o).abs() <= u * o.abs() + (1 + u) * (u + 2.0 ** -16) * spread + ref.smallest(torch.bfloat16)).all()
+
+
+# the relative error of a weight, by form
+def weight_step(dtype, form, name):
+    return {"few": 2.0 ** -18, "tma": 2.0 ** -11, "mma": ref.half_step(ref.DT[dtype])}["mma" if form == "general" else name]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("batch", [([1, 1], "few"), ([9, 2], "few"), ([40, 3], "tma"), ([300, 2], "tma")])
+@pytest.mark.parametrize("form", ["auto"], indirect=True)
+@pytest.mark.parametrize("gap", [14.3, 20.3, 24.3, 28.3])
+def test_small_weights_keep_their_share(ctx, form, batch, dtype, gap):
+    """A first token whose weight is 2^gap times each other's, with values of 0, over 160000 keys of equal values: the output is
+    what the others' weights add up to.  A weight is off by a half step of what holds it, or 2^-31 of the largest (half of
+    the smallest step, 2^-24, where the largest is 2^6); sums of equal terms in 32 bits lose up to 2^-24 a step, over at most 160000 / 16 steps."""
+    new, name = batch
+    length, page, d, dt = 160000, 64, 64, ref.DT[dtype]
+    cu = [0, new[0], sum(new)]
+    lens = [length, 5000]
+    blocks = length // page
+    q = torch.ones(sum(new), 2, d, dtype=dt)
+    kc = torch.zeros(blocks, page, 1, d, dtype=torch.uint8)
+    vc = torch.full_like(kc, pa8.code(112.0))
+    kc[0, 0] = pa8.code(64.0)
+    vc[0, 0] = 0
+    scales = torch.ones(blocks, 1)
+    scale = gap * math.log(2.0) / (64.0 * d)
+    table = torch.arange(blocks, dtype=torch.int32).repeat(2, 1)
+    out, lse = ctx.paged_attention_fp8(q.cuda(), kc.cuda(), vc.cuda(), scales.cuda(), scales.cuda(), table.cuda(), pa8.i32(cu), pa8.i32(lens),
+                                       scale=scale, want_lse=True)
+    served_by(ctx, form, name)
+    u, step = ref.half_step(dt), weight_step(dtype, form, name)
+    for r in range(2):
+        seen = torch.arange(lens[r] - new[r] + 1, lens[r] + 1).double()[:, None, None]
+        small = (seen - 1) * 2.0 ** -gap
+        want = 112.0 * small / (1.0 + small)
+        rel = u + step + 2.0 ** (gap - 31) + length / 16 * 2.0 ** -24
+        got = out[cu[r]:cu[r + 1]].cpu().double()
+        assert ((got - want).abs() <= rel * want + ref.smallest(dt)).all(), ((got / want - 1).abs().max(), rel)
+        log = torch.log1p(small[..., 0]) + gap * math.log(2.0)
+        assert ((lse[cu[r]:cu[r + 1]].cpu().double() - log).abs() <= 2.0 ** -10 + 2.0 ** -20 * log).all()
