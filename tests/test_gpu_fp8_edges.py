@@ -107,7 +107,6 @@ def weight_step(dtype, form, name):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("batch", [([1, 1], "few"), ([9, 2], "few"), ([40, 3], "tma"), ([300, 2], "tma")])
-@pytest.mark.parametrize("form", ["auto"], indirect=True)
 @pytest.mark.parametrize("gap", [14.3, 20.3, 24.3, 28.3])
 def test_small_weights_keep_their_share(ctx, form, batch, dtype, gap):
     """A first token whose weight is 2^gap times each other's, with values of 0, over 160000 keys of equal values: the output is
