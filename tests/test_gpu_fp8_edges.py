@@ -1,5 +1,5 @@
 """ar_paged_attention_fp8 where a product of 0 or a small weight is easily lost: NaN codes in blocks that no row sees, rows of huge
-queries, one weight far above very many others."""
+queries, one weight far above very many others, errors over long contexts."""
 import math
 
 import pytest
@@ -138,3 +138,22 @@ def test_small_weights_keep_their_share(ctx, form, batch, dtype, gap):
         assert ((got - want).abs() <= rel * want + ref.smallest(dt)).all(), ((got / want - 1).abs().max(), rel)
         log = torch.log1p(small[..., 0]) + gap * math.log(2.0)
         assert ((lse[cu[r]:cu[r + 1]].cpu().double() - log).abs() <= 2.0 ** -10 + 2.0 ** -20 * log).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("batch, length", [(([1], "few"), 20000), (([6], "few"), 9000), (([30], "tma"), 20000), (([300], "tma"), 9000)])
+def test_errors_over_long_contexts(ctx, form, batch, length, dtype):
+    """Root of the mean square error against 64 bits, relative to the outputs': of the output's rounding (a half step at most, so
+    1 / sqrt(3) of it), of each weight's (half a step of what holds it, independent, so in the mean of the same share), and the
+    scores' in 32 bits, which turn up in the weights: (2 d + 16) 2^-24 times sum |q k| scale at most, about a quarter of that in the mean.
+    A fifth more for the spread of a sample and sums in 32 bits."""
+    (new, name), d, dt = batch, 128, ref.DT[dtype]
+    x = pa8.make(new, [length], 8, 4, d, dtype, seed=length, low=-8, high=-7)
+    wo = pa8.want_of(x, d ** -0.5)[0]
+    out, _ = pa8.run(ctx, x, scale=d ** -0.5)
+    served_by(ctx, form, name)
+    u, step = ref.half_step(dt), weight_step(dtype, form, name)
+    size = 0.8 * 0.8 * 100 * 2.0 ** -7.5 * d * d ** -0.5  # of sum |q k| scale
+    limit = 1.2 * math.sqrt(u * u / 3 + step * step / 3 + (0.25 * (2 * d + 16) * 2.0 ** -24 * size) ** 2)
+    err = ((out.double() - wo).square().mean() / wo.square().mean()).sqrt().item()
+    assert err <= limit, (err, limit)
