@@ -562,7 +562,6 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* a, vo
   if (!(a->eps >= 0.0f) || isinf(a->eps)) return AR_ERR_INVALID_ARG;
   if (!rotation_ok(a->rot_dim, a->head_dim, a->axes, a->sections, a->position_stride, a->tokens)) return AR_ERR_INVALID_ARG;
   const int half = a->rot_dim / 2;
-  if (half && a->axes > 1 && !a->positions) return AR_ERR_INVALID_ARG;
   if (a->page_size < 1 || a->page_size > 65536 || a->num_blocks < 0 || a->num_blocks > ((int64_t)1 << 40) / a->page_size || a->table_cols < 0 ||
       a->table_cols > 0x7fffffff || a->table_stride < 0 || (a->table_stride && a->table_stride < a->table_cols) || a->table_stride > kMostStride)
     return AR_ERR_INVALID_ARG;
@@ -572,7 +571,7 @@ ar_status ar_paged_append_fp8(ar_ctx* ctx, const ar_paged_append_fp8_args* a, vo
     ctx->last_variant = "none";
     return AR_OK;
   }
-  if (!a->k || !a->v || (half && !a->inv_freq) || !a->cu_q || !a->seq_lens || (a->table_cols && !a->block_table) ||
+  if (!a->k || !a->v || (half && (!a->inv_freq || (a->axes > 1 && !a->positions))) || !a->cu_q || !a->seq_lens || (a->table_cols && !a->block_table) ||
       (nb && (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)))
     return AR_ERR_INVALID_ARG;
   if (!strides_ok(n, a->k_token_stride, hk, a->k_head_stride, d) || !strides_ok(n, a->v_token_stride, hk, a->v_head_stride, d) ||
