@@ -459,9 +459,10 @@ ar_status ar_paged_attention_workspace(ar_ctx* ctx, const ar_paged_attention_arg
  *           code and do not count for the scale
  *
  * Where a scale grows, the held codes are rounded to it.  Powers of two make that exact but for
- * codes that become subnormal, and cost an E4M3 value no precision.  A held block's scale that is no
- * finite positive number counts as 2^-32 (a held scale that is no power of two stays as long as it is large enough; y is
- * then multiplied by its fp32 reciprocal).
+ * codes that become subnormal, and cost an E4M3 value no precision.  A held block's scale outside 2^-32 .. 2^32
+ * counts as the nearer of the two (infinity as 2^32; 0, negative numbers and NaN as 2^-32) and becomes it, the held
+ * codes staying as they are.  One inside that is no power of two stays as long as it is large enough; y is then
+ * multiplied by its fp32 reciprocal.
  *
  * Not touched: blocks that get no token, places of a block behind its last token.  A request whose
  * length is below n (or negative), tokens behind its table's columns, and tokens of a block outside the
