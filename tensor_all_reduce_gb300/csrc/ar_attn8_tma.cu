@@ -21,9 +21,10 @@
 // same for eight keys in a row at least; a warp of its own looks them up, tiles ahead, and leaves the k scale, t
 // and 1 / vs of each eight keys of a tile in a ring in shared memory.
 //
-// Measured on GB300 with the joining kernel: 4096 tokens over 28000 (12 heads, 2 key heads of 128, bf16) 742 to 750 us,
-// 1010 TFLOP/s (16-bit cache 510 to 530); 2 x 1024 tokens over 8000 (heads of 256) 250 us (154); six prompts of up to
-// 1500 81 us (48); 17 requests, two of 700 tokens, window and cap 71 us (47).  The bound is the hand-over between the
+// Measured on GB300 with the joining kernel: 4096 tokens over 28000 (12 heads, 2 key heads of 128, bf16) 737 to 750 us,
+// 1010 TFLOP/s (16-bit cache 510 to 530); in fp16 945 to 950 us (515), whose three parts of q leave the values one slot, so
+// that none are on their way while a tile's are converted; 2 x 1024 tokens over 8000 (heads of 256) 258 us (154); six
+// prompts of up to 1500 83 us (48); 17 requests, two of 700 tokens, window and cap 72 us (47).  The bound is the hand-over between the
 // warps: 297 tiles an SM whose matrix instructions and softmax are left out still take 445 us, with the matrix
 // instructions 640, with the softmax and without the conversion 715.  What the 16-bit kernel has over it: a third less
 // for a softmax warp to issue (scales), and no warps that convert beside it.
@@ -42,7 +43,7 @@ namespace ar {
 namespace {
 
 constexpr int kThreads = kAttn8Threads;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 12;  // kLoadWarp + 1: values; 11 is idle; four warps convert
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 12;  // kLoadWarp + 1: values; 11: scales; four warps convert
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftmaxRegs = 176, kIssueRegs = 104, kConvertRegs = 56;  // of 128 a thread at launch
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kConvertRegs == 4 * 128, "the split uses what the launch has");

@@ -10,7 +10,7 @@
 // asynchronous.  With aligned rows and pages of 12 (of 1) tokens: 4096 tokens over 28000 (12 heads, 2 key
 // heads of 128) 6.0 (6.2) ms against 0.51 ms in pages of 64, 64 single tokens over up to 9000 keys (48
 // heads, 8 key heads) 1.05 (1.11) ms against 0.22 ms in pages of 16; element by element 8.8 and 1.26 ms.
-// Over 8-bit caches 8.9 and 1.35 ms in pages of 12, element by element 10.6 and 1.6 ms.
+// Over 8-bit caches 9.0 and 1.36 ms in pages of 12, element by element 10.8 and 1.6 ms.
 #include <type_traits>
 
 #include "ar_attn.cuh"

@@ -506,8 +506,13 @@ ar_status attention(ar_ctx* ctx, const ar_paged_attention_args* a, const ar_page
                               a->v_block_stride, box);
   }
   // Over 8 bits: batches of up to 16 rows a request take the kernel for them, then items of 128 rows (64 single tokens of
-  // 48 heads, 8 key heads of 128, over up to 9000: 168 us in items of 8 rows, 273 in those of 128, 302 of 256; five
-  // tokens each over 9000, 30 rows: 394 us in items of 128, 738 in two of 16).
+  // 48 heads, 8 key heads of 128, over up to 9000: 162 us in items of 8 rows, 273 in those of 128, 302 of 256; five
+  // tokens each over 9000, 30 rows: 394 us in items of 128, 738 in two of 16, before weights were stored by keys).
+  // What a request has is in device memory, so that the rule is by the average over the rows of q, those that belong to
+  // nobody among them, and over all requests, those that wait too.  Where requests differ it costs (us, two calls' sum in
+  // brackets): the 64 tokens with a chunk of 512 over 9000 500 (326), of 2048 1316 (762); 255 single tokens of 8 heads over up
+  // to 4000 with one of 203 over 7000 399 (363), of 2000, then in items of 16 rows, 990 (444).  And at a border one row more counts: 64
+  // tokens of 64 heads 156, with a row of nobody's 230 (128 heads 246 and 298).
   const int64_t rows = n * (hq / hk);
   const bool few = tma && scales && rows <= ar::kAttn8FewRows * r, half = scales && rows <= 64 * r;
   p.spans = few ? 2 * ctx->sm_count : tma ? ctx->sm_count : mma_spans(ctx, bf16, dp, scales);
